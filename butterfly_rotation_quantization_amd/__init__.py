@@ -38,7 +38,9 @@ EXPORTED = (
     "brq_profile_read", "brq_set_path", "brq_harp_blocks", "brq_harp_blocks_batch", "brq_plan_create_harp",
     "brq_plan_serialize", "brq_plan_deserialize", "brq_requant_workspace_bytes", "brq_requant",
     "brq_qlinear_workspace_bytes", "brq_qlinear", "brq_orp_geo_quantize", "brq_orp_geo_dequant",
-    "brq_qlinear_noalloc_limit", "brq_qlinear_noalloc",
+    "brq_qlinear_noalloc_limit", "brq_qlinear_noalloc", "brq_mx_quantize", "brq_mx_dequantize",
+    "brq_mx_matmul_workspace_bytes", "brq_mx_matmul", "brq_kv_page_bytes", "brq_kv_append",
+    "brq_kv_read", "brq_paged_attention_workspace_bytes", "brq_paged_attention",
 )
 
 
@@ -162,6 +164,26 @@ def bind(lib):
         lib.brq_plan_serialize.restype = i32
         lib.brq_plan_deserialize.argtypes = [ctypes.POINTER(vp), vp, sz]
         lib.brq_plan_deserialize.restype = i32
+    if hasattr(lib, "brq_mx_quantize"):
+        lib.brq_mx_quantize.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp, vp]
+        lib.brq_mx_quantize.restype = i32
+        lib.brq_mx_dequantize.argtypes = [vp, vp, vp, i64, i64, vp, i32, i64, vp]
+        lib.brq_mx_dequantize.restype = i32
+        lib.brq_mx_matmul_workspace_bytes.argtypes = [i64, i64, i64]
+        lib.brq_mx_matmul_workspace_bytes.restype = sz
+        lib.brq_mx_matmul.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, i32, i64, vp, sz, vp]
+        lib.brq_mx_matmul.restype = i32
+        lib.brq_kv_page_bytes.argtypes = [i32, i32]
+        lib.brq_kv_page_bytes.restype = sz
+        lib.brq_kv_append.argtypes = [vp, vp, i64, vp, i64, i32, vp, i64, i32, i32, i32, i64, vp, vp]
+        lib.brq_kv_append.restype = i32
+        lib.brq_kv_read.argtypes = [vp, vp, vp, i64, i32, i32, i32, i64, vp, i64, vp, i64, i32, vp]
+        lib.brq_kv_read.restype = i32
+        lib.brq_paged_attention_workspace_bytes.argtypes = [i64, i32, i32, i32]
+        lib.brq_paged_attention_workspace_bytes.restype = sz
+        lib.brq_paged_attention.argtypes = [vp, vp, i64, i32, vp, i64, vp, i64, vp, i64, i32, i32, i32,
+                                            i32, ctypes.c_float, i32, vp, i64, vp, vp, sz, vp]
+        lib.brq_paged_attention.restype = i32
     if hasattr(lib, "brq_set_path"):  # libraries built before the path switch lack it
         lib.brq_set_path.argtypes = [i32]
         lib.brq_set_path.restype = i32
@@ -517,6 +539,186 @@ def orp_geo_dequant(codes, signs, coef, m: int, n: int, bits: int, group: int, s
     q = Orp(bits, group, stride)
     check(lib().brq_orp_geo_dequant(_ptr(codes), _ptr(signs), _ptr(coef), ctypes.byref(q), int(m),
                                     int(n), _ptr(out), dtype_code(out), _ld(out), _stream(stream)))
+    return out
+
+
+# ---------------------------------------------------------------- microscaled 4-bit rows
+
+def _rows(t) -> tuple:
+    """(rows, n, leading dimension) of a 2-D tensor of contiguous rows."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("expected a 2-D tensor with unit column stride")
+    rows, n = t.shape
+    return rows, n, (t.stride(0) if rows > 1 else max(t.stride(0), n))
+
+
+def _packed(t, dtype, shape, what):
+    """Check a contiguous tensor of the library's own layout."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def mx_quantize(right: Optional[Plan], x, codes=None, scales=None, stream=None):
+    """Round the rows of x [rows, n] (f32, bf16 or f16; n a multiple of 32) to
+    the microscaled 4-bit format, after the Hadamard plan `right` (d = 32..256)
+    or none (brq_mx_quantize).  Returns (codes uint8 [rows, n/2], scales uint8
+    [rows, n/32])."""
+    import torch
+    rows, n, ld = _rows(x)
+    if codes is None:
+        codes = torch.empty((rows, n // 2), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((rows, n // 32), dtype=torch.uint8, device=x.device)
+    check(lib().brq_mx_quantize(_h(right), x.data_ptr(), dtype_code(x), ld, rows, n,
+                                _packed(codes, torch.uint8, (rows, n // 2), "codes"),
+                                _packed(scales, torch.uint8, (rows, n // 32), "scales"), _stream(stream)))
+    return codes, scales
+
+
+def mx_dequantize(right: Optional[Plan], codes, scales, out=None, out_dtype=None, stream=None):
+    """The values of microscaled 4-bit rows, with the plan `right` undone
+    (brq_mx_dequantize).  Returns out [rows, n] (float32 by default)."""
+    import torch
+    rows, n = codes.shape[0], codes.shape[1] * 2
+    if out is None:
+        out = torch.empty((rows, n), dtype=out_dtype or torch.float32, device=codes.device)
+    if tuple(out.shape) != (rows, n):
+        raise ValueError(f"out: expected shape {(rows, n)}, got {tuple(out.shape)}")
+    check(lib().brq_mx_dequantize(_h(right), _packed(codes, torch.uint8, (rows, n // 2), "codes"),
+                                  _packed(scales, torch.uint8, (rows, n // 32), "scales"), rows, n,
+                                  out.data_ptr(), dtype_code(out), _rows(out)[2], _stream(stream)))
+    return out
+
+
+def mx_matmul_workspace(T: int, m: int, n: int, device="cuda"):
+    """A device workspace for mx_matmul of these sizes (None if it needs none)."""
+    import torch
+    nb = lib().brq_mx_matmul_workspace_bytes(int(T), int(m), int(n))
+    return torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+
+
+def mx_matmul(a_codes, a_scales, b_codes, b_scales, y=None, out_dtype=None, ws=None, stream=None):
+    """y[t, o] = sum_k a[t, k] b[o, k] of two microscaled 4-bit matrices
+    (brq_mx_matmul): activations [T, n] times a weight [m, n] kept by output
+    rows.  Returns y [T, m] (bfloat16 by default)."""
+    import torch
+    T, n, m = a_codes.shape[0], a_codes.shape[1] * 2, b_codes.shape[0]
+    if y is None:
+        y = torch.empty((T, m), dtype=out_dtype or torch.bfloat16, device=a_codes.device)
+    if tuple(y.shape) != (T, m):
+        raise ValueError(f"y: expected shape {(T, m)}, got {tuple(y.shape)}")
+    if ws is None:
+        ws = mx_matmul_workspace(T, m, n, a_codes.device)
+    wp, wb = _ws_args(ws)
+    u8 = torch.uint8
+    check(lib().brq_mx_matmul(_packed(a_codes, u8, (T, n // 2), "a_codes"),
+                              _packed(a_scales, u8, (T, n // 32), "a_scales"),
+                              _packed(b_codes, u8, (m, n // 2), "b_codes"),
+                              _packed(b_scales, u8, (m, n // 32), "b_scales"), T, m, n,
+                              y.data_ptr(), dtype_code(y), _rows(y)[2], wp, wb, _stream(stream)))
+    return y
+
+
+# ---------------------------------------------------------------- paged 4-bit key-value cache
+
+def kv_cache(pages: int, heads: int, head_dim: int, page: int, device="cuda"):
+    """A zeroed cache: uint8 [pages, heads, bytes of one head's page]."""
+    import torch
+    nb = lib().brq_kv_page_bytes(int(head_dim), int(page))
+    if nb == 0:
+        raise BrqError(2, lib().brq_last_error().decode())
+    return torch.zeros((pages, heads, nb), dtype=torch.uint8, device=device)
+
+
+def _heads(t, D, what) -> tuple:
+    """(tokens, heads, leading dimension) of a [tokens, heads, D] tensor whose
+    heads follow one another."""
+    if t.dim() != 3 or t.shape[2] != D or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+        raise ValueError(f"{what}: expected [tokens, heads, {D}] with the heads of a token contiguous, "
+                         f"got {tuple(t.shape)} with strides {tuple(t.stride())}")
+    n, h = t.shape[0], t.shape[1]
+    return n, h, (t.stride(0) if n > 1 else max(t.stride(0), h * D))
+
+
+def _cache_ptr(cache, heads, D, page):
+    import torch
+    return _packed(cache, torch.uint8, (cache.shape[0], heads, page * (D + D // 16)), "cache")
+
+
+def kv_append(plan: Optional[Plan], k, v, slots, cache, page: int, stream=None):
+    """Rotate, quantize and write the keys and values [tokens, heads, D] of new
+    tokens to cache slots int64 [tokens] (brq_kv_append; a slot outside the
+    cache is skipped).  Returns cache."""
+    import torch
+    D = k.shape[-1]
+    n, h, ldk = _heads(k, D, "k")
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must have the same shape and dtype")
+    check(lib().brq_kv_append(_h(plan), k.data_ptr(), ldk, v.data_ptr(), _heads(v, D, "v")[2],
+                              dtype_code(k), _packed(slots, torch.int64, (n,), "slots"), n, h, D,
+                              int(page), cache.shape[0], _cache_ptr(cache, h, D, int(page)),
+                              _stream(stream)))
+    return cache
+
+
+def kv_read(plan: Optional[Plan], cache, slots, head_dim: int, page: int, k=None, v=None,
+            out_dtype=None, stream=None):
+    """Keys and values of the given slots, dequantized and unrotated
+    (brq_kv_read).  Returns (k, v), each [tokens, heads, head_dim] (bfloat16 by
+    default); a slot outside the cache reads as zeros."""
+    import torch
+    n, h, D = slots.shape[0], cache.shape[1], int(head_dim)
+    if k is None:
+        k = torch.empty((n, h, D), dtype=out_dtype or torch.bfloat16, device=cache.device)
+    if v is None:
+        v = torch.empty_like(k)
+    if tuple(k.shape) != (n, h, D) or v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError(f"k and v must have shape {(n, h, D)} and the same dtype")
+    check(lib().brq_kv_read(_h(plan), _cache_ptr(cache, h, D, int(page)),
+                            _packed(slots, torch.int64, (n,), "slots"), n, h, D, int(page),
+                            cache.shape[0], k.data_ptr(), _heads(k, D, "k")[2], v.data_ptr(),
+                            _heads(v, D, "v")[2], dtype_code(k), _stream(stream)))
+    return k, v
+
+
+def paged_attention_workspace(batch: int, q_heads: int, heads: int, head_dim: int, device="cuda"):
+    """A device workspace for paged_attention of these sizes (None if it needs none)."""
+    import torch
+    nb = lib().brq_paged_attention_workspace_bytes(int(batch), int(q_heads), int(heads), int(head_dim))
+    return torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+
+
+def paged_attention(plan: Optional[Plan], q, cache, table, lens, page: int, scale=None, window: int = 0,
+                    out=None, lse=None, ws=None, stream=None):
+    """Attention of one new token per sequence over the paged 4-bit cache
+    (brq_paged_attention): q [batch, q_heads, D] (f32, bf16 or f16), table int32
+    [batch, pages of a sequence], lens int32 [batch]; scale defaults to
+    1/sqrt(D), window 0 sees every cached token; lse, if given, is a float32
+    [batch, q_heads] output.  Returns out, like q."""
+    import torch
+    B, hq, D = q.shape
+    h = cache.shape[1]
+    if out is None:
+        out = torch.empty((B, hq, D), dtype=q.dtype, device=q.device)
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and dtype")
+    if ws is None:
+        ws = paged_attention_workspace(B, hq, h, D, q.device)
+    wp, wb = _ws_args(ws)
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table: expected int32 [{B}, pages] with unit column stride")
+    ldt = table.shape[1] if B == 1 else table.stride(0)
+    if ldt != table.shape[1]:
+        raise ValueError("table must be contiguous")
+    check(lib().brq_paged_attention(
+        _h(plan), q.data_ptr(), _heads(q, D, "q")[2], dtype_code(q),
+        _cache_ptr(cache, h, D, int(page)), cache.shape[0], table.data_ptr(), ldt,
+        _packed(lens, torch.int32, (B,), "lens"), B, hq, h, D, int(page),
+        D ** -0.5 if scale is None else float(scale), int(window), out.data_ptr(),
+        _heads(out, D, "out")[2], None if lse is None else _packed(lse, torch.float32, (B, hq), "lse"),
+        wp, wb, _stream(stream)))
     return out
 
 

@@ -50,6 +50,7 @@ brq_status hip_fail(hipError_t e, const char* what) {
 }  // namespace
 
 brq_status report_error(brq_status s, const char* msg) { return fail(s, "%s", msg); }
+void clear_error() { g_last_error.clear(); }
 
 namespace {
 
@@ -281,6 +282,15 @@ brq_status check_plan_device(const Plan* p) {
                 p->device, dev);
   return BRQ_OK;
 }
+
+}  // namespace
+
+brq_status plan_data(const brq_plan* plan, const Plan** out) {
+  *out = plan ? &plan->p : nullptr;
+  return check_plan_device(*out);
+}
+
+namespace {
 
 brq_status check_quant(const brq_quant* q, int64_t n) {
   if (!q) return fail(BRQ_ERR_INVALID_ARGUMENT, "quantizer is NULL");

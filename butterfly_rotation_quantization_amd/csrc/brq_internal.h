@@ -120,6 +120,11 @@ void rt_free(void* p);
 // Set this thread's brq_last_error text and return `s` (for entry points
 // defined outside the host layer's file).
 brq_status report_error(brq_status s, const char* msg);
+// Empty this thread's brq_last_error text (at the start of an entry point).
+void clear_error();
+// A plan's data, checked to be on the current device: *out is null for a null
+// plan.
+brq_status plan_data(const brq_plan* plan, const Plan** out);
 
 // Kernel timing (brq_profile_*): bracket a launch with events on its stream
 // when profiling is enabled; both calls are no-ops otherwise.

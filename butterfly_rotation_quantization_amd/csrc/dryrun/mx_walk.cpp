@@ -1,0 +1,108 @@
+// Dry-run walks of the microscaled 4-bit operators: every lane's reads and
+// writes of rows, codes, scales, cache pages and partial results, from the
+// index functions the kernels use.
+#include <vector>
+
+#include "mx.h"
+
+namespace brq {
+
+bool dry_violation(const char* fmt, long long a, long long b);
+void dry_launch();
+
+static hipError_t bad(const char* fmt, long long a, long long b) {
+  dry_violation(fmt, a, b);
+  return hipErrorInvalidValue;
+}
+
+static hipError_t walk_mx(const MxArgs& a, int64_t ld) {
+  dry_launch();
+  const int64_t n = (int64_t)a.lpr * kMxPerLane;
+  if (n % kMxBlock || a.lanes != (uint64_t)a.rows * a.lpr || ld < n || (a.d && n % a.d))
+    return bad("mx geometry (row of %lld, d %lld)", n, a.d);
+  if (a.lanes / kMxThreads >= ((uint64_t)1 << 31)) return bad("mx grid of %lld lanes", (long long)a.lanes, 0);
+  if (a.lanes > (1 << 22)) return hipSuccess;  // walked in full at test sizes
+  std::vector<uint8_t> cover((size_t)(a.rows * n), 0);
+  for (uint64_t li = 0; li < a.lanes; ++li) {
+    int64_t row, col;
+    mx_lane(a.lpr, li, &row, &col);
+    if (row < 0 || row >= a.rows || col < 0 || col + kMxPerLane > n) return bad("mx lane at (%lld, %lld)", row, col);
+    if ((row * n + col) / kMxPerLane != (int64_t)li) return bad("mx codes word %lld of lane %lld", row * n + col, li);
+    if ((li & 3) == 0 && col % kMxBlock) return bad("mx block at column %lld", col, 0);
+    for (int e = 0; e < kMxPerLane; ++e) cover[(size_t)(row * n + col + e)]++;
+  }
+  for (size_t i = 0; i < cover.size(); ++i)
+    if (cover[i] != 1) return bad("mx value %lld handled %lld times", (long long)i, cover[i]);
+  return hipSuccess;
+}
+
+hipError_t launch_mx_quant(const MxArgs& a, hipStream_t) { return walk_mx(a, a.ldx); }
+hipError_t launch_mx_dequant(const MxArgs& a, hipStream_t) { return walk_mx(a, a.ldy); }
+
+hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t) {
+  dry_launch();
+  if (a.T < 1 || a.m < 1 || a.n % kMxBlock || a.ldy < a.m) return bad("mx matmul geometry (%lld x %lld)", a.T, a.m);
+  return hipSuccess;
+}
+
+// Every byte of a page is written by exactly one lane of one token, and every
+// access is aligned to its width.
+static hipError_t walk_page(const KvPage& pg) {
+  const int D = pg.D, P = pg.P;
+  std::vector<uint8_t> cover((size_t)pg.bytes(), 0);
+  auto put = [&](int64_t at, int w) {
+    if (at < 0 || at + w > pg.bytes() || at % w) return false;
+    for (int i = 0; i < w; ++i) cover[(size_t)(at + i)]++;
+    return true;
+  };
+  for (int t = 0; t < P; ++t)
+    for (int c = 0; c < D; c += kMxPerLane) {
+      bool ok = put(pg.kcode(t) + c / 2, 4);
+      if (D == 64) ok = ok && put(pg.vcode(t, c / 4), 2) && put(pg.vcode(t, c / 4 + 1), 2);
+      else ok = ok && put(pg.vcode(t, c / (D / 16)) + (c % (D / 16)) / 2, 4);
+      if (c % kMxBlock == 0) ok = ok && put(pg.kscale(t) + c / 32, 1) && put(pg.vscale(t, c / 32), 1);
+      if (!ok) return bad("cache page access of token %lld, value %lld", t, c);
+    }
+  for (size_t i = 0; i < cover.size(); ++i)
+    if (cover[i] != 1) return bad("cache page byte %lld written %lld times", (long long)i, cover[i]);
+  return hipSuccess;
+}
+
+static hipError_t walk_kv(const KvArgs& a) {
+  dry_launch();
+  if ((1 << a.lgP) != a.pg.P || a.ldk < (int64_t)a.heads * a.pg.D || a.ldv < (int64_t)a.heads * a.pg.D ||
+      (a.d && a.d != a.pg.D))
+    return bad("cache geometry (page %lld, D %lld)", a.pg.P, a.pg.D);
+  return walk_page(a.pg);
+}
+
+hipError_t launch_kv_append(const KvArgs& a, hipStream_t) { return walk_kv(a); }
+hipError_t launch_kv_read(const KvArgs& a, hipStream_t) { return walk_kv(a); }
+
+hipError_t launch_paged_attention(const AtArgs& a, hipStream_t) {
+  dry_launch();
+  const KvPage& pg = a.pg;
+  const int D = pg.D;
+  if ((1 << a.lgP) != pg.P || a.group * a.heads != a.q_heads || a.ht * a.nt * kAtCols < a.group ||
+      (int64_t)a.cap > a.ldt << a.lgP || a.cap > kAtMaxKeys || a.splits < 1 || (a.splits > 1 && !a.part))
+    return bad("attention geometry (group %lld, splits %lld)", a.group, a.splits);
+  // the wide loads of 16 keys at every place of a page
+  for (int p = 0; p < pg.P; p += 16)
+    for (int lane = 0; lane < 64; ++lane) {
+      const int c = lane & 15, g = lane >> 4, w = D / 8;
+      const int64_t kc = pg.kcode(p + c) + g * w, vc = pg.vcode(p + 4 * g, c);
+      const int64_t ks = pg.kscale(p + c) + (int64_t)g * D / 128, vs = pg.vscale(p + 4 * g, c * D / 512);
+      const int wide = w < 16 ? w : 16, kb = D == 256 ? 2 : 1;
+      if (kc % wide || vc % wide || kc + w > pg.vcode(0, 0) || vc + w > pg.kscale(0))
+        return bad("attention codes of lane %lld at token %lld", lane, p);
+      if (ks % kb || ks + kb > pg.vscale(0, 0) || vs % 4 || vs + 4 > pg.bytes())
+        return bad("attention scales of lane %lld at token %lld", lane, p);
+      // the four keys of a lane's values follow one another, as do their scales
+      for (int i = 0; i < 4; ++i)
+        if (pg.vcode(p + 4 * g + i, c) != vc + i * (D / 32) || pg.vscale(p + 4 * g + i, c * D / 512) != vs + i)
+          return bad("attention values of lane %lld, key %lld", lane, i);
+    }
+  return walk_page(pg);
+}
+
+}  // namespace brq

@@ -1,0 +1,152 @@
+// Microscaled 4-bit rows (MX4): launch arguments and the index arithmetic
+// shared by the kernels (mx.hip, mx_matmul.hip, kv.hip, kv_attn.hip) and the
+// host dry-run checker.
+//
+// Element lanes: a lane holds kMxPerLane consecutive values of a row, so a
+// block of 32 spans 4 lanes and a transform of d values d / 8 lanes; both are
+// aligned, since rows are whole blocks (whole transforms).
+#pragma once
+
+#include "brq_internal.h"
+
+namespace brq {
+
+constexpr int kMxBlock = 32;      // values that share a scale
+constexpr int kMxPerLane = 8;
+constexpr int kMxThreads = 256;   // four wavefronts per workgroup
+
+// ---- quantize / dequantize (mx.hip)
+
+struct MxArgs {
+  const void* x;         // quantize input [rows][ldx]
+  int xt;
+  int64_t ldx;
+  void* y;               // dequantize output [rows][ldy]
+  int yt;
+  int64_t ldy;
+  int64_t rows;
+  uint32_t lpr;          // lanes per row: n / kMxPerLane
+  uint64_t lanes;        // rows * lpr
+  uint8_t* codes;        // [rows][n/2]
+  uint8_t* scales;       // [rows][n/32]
+  const float* signs;    // the transform's signs, or null
+  int d;                 // transform length (0: none)
+  float rnorm;           // fl(1 / sqrt(d))
+};
+
+// Row and first column of lane li (li < a.lanes).
+__host__ __device__ inline void mx_lane(uint32_t lpr, uint64_t li, int64_t* row, int64_t* col) {
+  const uint64_t r = (li >> 32) ? li / lpr : (uint64_t)((uint32_t)li / lpr);
+  *row = (int64_t)r;
+  *col = (int64_t)(li - r * lpr) * kMxPerLane;
+}
+
+hipError_t launch_mx_quant(const MxArgs& a, hipStream_t s);
+hipError_t launch_mx_dequant(const MxArgs& a, hipStream_t s);
+
+// ---- product (mx_matmul.hip)
+
+struct MmArgs {
+  const uint8_t* a;      // [T][n/2]
+  const uint8_t* as;     // [T][n/32]
+  const uint8_t* b;      // [m][n/2]
+  const uint8_t* bs;     // [m][n/32]
+  int64_t T, m, n;
+  void* y;
+  int yt;
+  int64_t ldy;
+};
+
+hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t s);
+
+// ---- paged cache (kv.hip) and attention (kv_attn.hip)
+
+constexpr int kKvQuad = 4;        // tokens whose value codes are interleaved
+constexpr int kKvRuns = 16;       // runs of D / 16 dimensions
+
+// Layout of one head's page for head dimension D and P tokens (bytes).
+struct KvPage {
+  int D, P;
+  __host__ __device__ int64_t bytes() const { return (int64_t)P * (D + D / 16); }
+  // keys' codes of token t (D / 2 bytes)
+  __host__ __device__ int64_t kcode(int t) const { return (int64_t)t * (D / 2); }
+  // values' codes of run r of token t (D / 32 bytes)
+  __host__ __device__ int64_t vcode(int t, int r) const {
+    return (int64_t)P * (D / 2) + (int64_t)(t / kKvQuad) * (2 * D) + r * (D / 8) + (t % kKvQuad) * (D / 32);
+  }
+  // keys' scales of token t (D / 32 bytes)
+  __host__ __device__ int64_t kscale(int t) const { return (int64_t)P * D + (int64_t)t * (D / 32); }
+  // values' scale of block e of token t
+  __host__ __device__ int64_t vscale(int t, int e) const {
+    return (int64_t)P * D + (int64_t)P * (D / 32) + (int64_t)(t / kKvQuad) * (D / 8) + e * kKvQuad + t % kKvQuad;
+  }
+};
+
+struct KvArgs {
+  const void* k;         // append: inputs; read: outputs
+  const void* v;
+  int64_t ldk, ldv;
+  int t;                 // their type
+  const int64_t* slots;
+  int64_t tokens;
+  int heads;
+  KvPage pg;
+  int lgP;               // log2 of the page's tokens
+  int64_t pages;
+  uint8_t* cache;
+  const float* signs;
+  int d;                 // transform length: 0 or the head dimension
+  float rnorm;
+};
+
+hipError_t launch_kv_append(const KvArgs& a, hipStream_t s);
+hipError_t launch_kv_read(const KvArgs& a, hipStream_t s);
+
+constexpr int kAtWaves = 4;       // wavefronts of an attention workgroup
+constexpr int kAtThreads = 64 * kAtWaves;
+constexpr int kAtKeys = 32;       // keys a wavefront takes at a time
+constexpr int kAtTile = kAtWaves * kAtKeys;
+constexpr int kAtCols = 8;        // query heads per 16 matrix columns (each as a high and a low part)
+
+constexpr int kAtMaxKeys = 1 << 30;
+constexpr int kAtMaxSplits = 64;
+
+// Parts a sequence's keys are split into when there are few sequences and
+// heads: enough workgroups for every compute unit to hold four.
+inline int at_splits(int64_t units) {
+  const int64_t s = units > 0 ? 1024 / units : 1;
+  return (int)(s < 1 ? 1 : (s < kAtMaxSplits ? s : kAtMaxSplits));
+}
+
+struct AtArgs {
+  const void* q;
+  int64_t ldq;
+  void* out;
+  int64_t ldo;
+  int qt;
+  const uint8_t* cache;
+  int64_t pages;
+  KvPage pg;
+  int lgP;
+  const int32_t* table;
+  int64_t ldt;
+  const int32_t* lens;
+  int cap;               // tokens a sequence may have: ldt * P, at most kAtMaxKeys
+  int64_t batch;
+  int q_heads, heads;
+  int group;             // query heads per key-value head
+  int nt;                // column tiles per workgroup (1 or 2)
+  int ht;                // workgroups of query heads per key-value head
+  float scale;
+  int window;
+  float* lse;
+  const float* signs;
+  int d;
+  float rnorm;
+  int splits;            // parts a sequence's keys are split into
+  float* part;           // [unit][splits][nt * kAtCols][D + 4]: o, then m and l
+};
+
+hipError_t launch_paged_attention(const AtArgs& a, hipStream_t s);
+
+}  // namespace brq

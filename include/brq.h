@@ -4,7 +4,8 @@
  * C ABI of libbrq.so.  Every data pointer passed to a hot call is a DEVICE
  * pointer owned by the caller; the library never frees or keeps it.  Hot calls
  * (brq_rotate*, brq_rotate_quantize_pack, brq_dequant_unrotate, brq_requant,
- * brq_qlinear, brq_orp_geo_*) are asynchronous on the caller's HIP stream
+ * brq_qlinear, brq_orp_geo_*, brq_mx_*, brq_kv_*, brq_paged_attention) are
+ * asynchronous on the caller's HIP stream
  * (`stream` is a hipStream_t, NULL = the default stream), never allocate and
  * never synchronise; a fault inside a kernel shows up at the caller's next
  * synchronisation.  A hot call issues nothing but kernel launches on
@@ -372,6 +373,129 @@ brq_status brq_orp_geo_quantize(const void* w, int32_t wt, int64_t m, int64_t n,
 brq_status brq_orp_geo_dequant(const uint8_t* codes, const uint8_t* signs, const float* coef,
                                const brq_orp* q, int64_t m, int64_t n, void* out, int32_t ot,
                                int64_t ldo, void* stream);
+
+/*
+ * Microscaled 4-bit rows ("MX4"): what the matrix cores of gfx950 multiply
+ * directly.  A row of n values (n a multiple of 32) is cut into blocks of 32.
+ * A block whose largest magnitude is A > 0 has the scale 2^e, e = floor(log2 A)
+ * - 2 limited to [-127, 127], stored as the byte e + 127 (a block of zeros: 0;
+ * a block that holds an infinity or a NaN: 255, its codes 0, and it stands for
+ * NaN throughout).  A value v becomes the 4-bit code of v / 2^e rounded to the
+ * nearest of 0, 1/2, 1, 3/2, 2, 3, 4, 6 (codes 0..7; a tie goes to the even
+ * code; above 6: 6), plus 8 if its sign bit is set.
+ *   codes:  [rows][n/2] bytes, value 2j of a row in the low half of its byte j;
+ *   scales: [rows][n/32] bytes.
+ *
+ * brq_mx_quantize rounds the rows of x to that format, after the right-side
+ * transform `right` (NULL: none).  right must be a Hadamard plan with d = 32,
+ * 64, 128 or 256 dividing n; every d values v of a row become H_d D v / sqrt(d)
+ * with the additions in float32 in the order of the fast transform (strides 1,
+ * 2, 4, ..., d/2), then one product with fl(1/sqrt(d)).  That order is fixed:
+ * the codes are the same bits on every call and for every shape.  Larger or
+ * other plans: brq_rotate first.
+ *   x: device [rows][ldx] of type xt, 16-byte aligned rows.
+ *   codes: 16-byte aligned; scales: 4-byte aligned.
+ * brq_mx_dequantize is its inverse: the values (code times scale, exact in
+ * float32 and bfloat16), then the inverse of `right` in float32 (the same
+ * order, then the product and the signs), rounded once to ot.
+ *   out: device [rows][ldo], 16-byte aligned rows.
+ * Errors of both: INVALID_ARGUMENT (dtype, shapes, n not a multiple of 32 or
+ * of d, NULLs, plan of another device), UNSUPPORTED (the plan; rows * n above
+ * 2^36), ALIGNMENT, HIP.  rows == 0 or n == 0 is a no-op. */
+brq_status brq_mx_quantize(const brq_plan* right, const void* x, int32_t xt, int64_t ldx,
+                           int64_t rows, int64_t n, uint8_t* codes, uint8_t* scales,
+                           void* stream);
+brq_status brq_mx_dequantize(const brq_plan* right, const uint8_t* codes, const uint8_t* scales,
+                             int64_t rows, int64_t n, void* out, int32_t ot, int64_t ldo,
+                             void* stream);
+
+/*
+ * Product of two MX4 matrices: y[t][o] = sum_k a[t][k] b[o][k] (activations
+ * times a weight stored by output rows), accumulated in float32 by the scaled
+ * matrix instructions, rounded once to yt.  Row t of `a` holding a NaN block
+ * makes row t of y NaN, row o of `b` column o.
+ *   a_codes [T][n/2], a_scales [T][n/32], b_codes [m][n/2], b_scales [m][n/32]
+ *     (codes 16-byte, scales 4-byte aligned); y: device [T][ldy].
+ *   ws: device workspace of brq_mx_matmul_workspace_bytes(T, m, n) bytes (16-byte
+ *     aligned; may be NULL if that is 0): partial sums when the long axis n is
+ *     split among workgroups.  The split depends on the sizes only, and the
+ *     parts are added in order: a call's result does not vary.
+ * T, m >= 0, n a multiple of 32 (n == 0: y = 0).  Errors: INVALID_ARGUMENT
+ * (dtype, shapes, NULLs), UNSUPPORTED (T, m or n above 2^31 - 1), ALIGNMENT,
+ * WORKSPACE, HIP. */
+size_t brq_mx_matmul_workspace_bytes(int64_t T, int64_t m, int64_t n);
+brq_status brq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                         const uint8_t* b_scales, int64_t T, int64_t m, int64_t n, void* y,
+                         int32_t yt, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * A paged key-value cache in MX4.  The cache is a device array of `pages` pages
+ * of `page` tokens; a page holds, for each of `heads` key-value heads, the keys
+ * and values of its tokens in brq_kv_page_bytes(head_dim, page) bytes:
+ *   keys' codes   [page][D/2]            (D = head_dim),
+ *   values' codes [page/4][16][4][D/32]: for every four tokens and each of 16
+ *                 runs of D/16 dimensions, the four tokens' codes of the run
+ *                 one after the other (what one lane of the attention kernel
+ *                 multiplies is contiguous),
+ *   keys' scales   [page][D/32],
+ *   values' scales [page/4][D/32][4].
+ * The whole cache is [pages][heads][brq_kv_page_bytes].  Token slot s is token
+ * s % page of page s / page.  head_dim 64, 128 or 256; page a power of two in
+ * 16..1024.
+ *
+ * brq_kv_append rotates (plan: NULL, or a Hadamard plan with d == head_dim) and
+ * quantizes the keys and values of `tokens` tokens as brq_mx_quantize does and
+ * writes token i to slot slots[i]; a slot outside [0, pages * page) is skipped
+ * (padding).  Two tokens of one call must not share a slot.
+ *   k, v: device [tokens][ldk], [tokens][ldv] of type xt: head h of token i at
+ *         element i * ld + h * head_dim; 16-byte aligned rows.
+ *   slots: device int64 [tokens].
+ * brq_kv_read is the inverse for any list of slots: dequantized, the plan
+ * undone, rounded once to ot; a slot outside the cache reads as zeros.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (head_dim, page, the plan; more than
+ * 2^31 - 1 rows tokens * heads), ALIGNMENT (rows, cache 16 bytes), HIP.
+ * tokens == 0 is a no-op. */
+size_t brq_kv_page_bytes(int32_t head_dim, int32_t page);
+brq_status brq_kv_append(const brq_plan* plan, const void* k, int64_t ldk, const void* v,
+                         int64_t ldv, int32_t xt, const int64_t* slots, int64_t tokens,
+                         int32_t heads, int32_t head_dim, int32_t page, int64_t pages,
+                         uint8_t* cache, void* stream);
+brq_status brq_kv_read(const brq_plan* plan, const uint8_t* cache, const int64_t* slots,
+                       int64_t tokens, int32_t heads, int32_t head_dim, int32_t page,
+                       int64_t pages, void* k, int64_t ldk, void* v, int64_t ldv, int32_t ot,
+                       void* stream);
+
+/*
+ * Attention of one new token per sequence over the paged cache: for sequence b
+ * with n = lens[b] cached tokens and query head i (key-value head i / (q_heads
+ * / heads)), over its visible keys j (j < n, and j >= n - window if window > 0)
+ *   s_j = scale <q', k_j>,  p = softmax(s),  out = M^T sum_j p_j v_j,
+ * q' = M q with M the plan's transform that the cache was appended with (NULL:
+ * none); k_j, v_j the cache's values.  Token j of sequence b sits in page
+ * table[b * ldt + j / page].  With no visible key, out = 0 and lse = -infinity.
+ *   q, out: device [batch][ldq], [batch][ldo] of type qt, head i at element
+ *           b * ld + i * head_dim; 16-byte aligned rows.  out may be q.
+ *   table: device int32 [batch][ldt]; entries past a sequence's last page are
+ *          not read; a sequence is limited to ldt * page (and 2^30) tokens, and the
+ *          tokens of a page outside [0, pages) are invisible.
+ *   lens: device int32 [batch]; lse: device float32 [batch][q_heads], the
+ *         natural logarithm of the sum of exp(s_j), or NULL.
+ *   ws: device workspace of brq_paged_attention_workspace_bytes(...) bytes
+ *       (16-byte aligned): partial results where a sequence's length is split.
+ * Lengths and tables are read on the device at each call, so a captured call
+ * can be replayed while sequences grow.  Queries, probabilities and sums are
+ * held in float32 (in pairs of bfloat16 where they enter the matrix units).
+ * Errors: INVALID_ARGUMENT (q_heads not a multiple of heads, NULLs, scale not
+ * finite, window < 0), UNSUPPORTED (head_dim, page, the plan; more than 2^24
+ * sequences times query heads), ALIGNMENT, WORKSPACE, HIP.  batch == 0 is a no-op. */
+size_t brq_paged_attention_workspace_bytes(int64_t batch, int32_t q_heads, int32_t heads,
+                                           int32_t head_dim);
+brq_status brq_paged_attention(const brq_plan* plan, const void* q, int64_t ldq, int32_t qt,
+                               const uint8_t* cache, int64_t pages, const int32_t* table,
+                               int64_t ldt, const int32_t* lens, int64_t batch, int32_t q_heads,
+                               int32_t heads, int32_t head_dim, int32_t page, float scale,
+                               int32_t window, void* out, int64_t ldo, float* lse, void* ws,
+                               size_t ws_bytes, void* stream);
 
 /*
  * Host helper: the 2^bits Lloyd-Max centroids for N(0,1), ascending, rounded

@@ -34,9 +34,11 @@ Modules:
 * ``orp`` -- ORP's GEO mode: a power-of-two primary basis, an orthogonal
   secondary basis by stride exchange and sign flips, least-squares scales
   ([ORPQuant] section 2).
+* ``mx`` -- microscaled 4-bit rows, their product, the paged key-value cache
+  and the attention that reads it (definitions in include/brq.h).
 
 Readings of points the pages leave open are stated where they are used and
 listed together in the design notes of the repository.
 """
 
-from . import transform, quant, lloydmax, harp, chain, linear, orp  # noqa: F401
+from . import transform, quant, lloydmax, harp, chain, linear, orp, mx  # noqa: F401

@@ -1,0 +1,283 @@
+"""GPU parity of the microscaled 4-bit rows and their product against the
+oracle (oracle/mx.py).
+
+Codes, scales and values without a transform are compared bit for bit.  Where
+float32 sums are rounded the bounds are derived: a transform of d values does
+log2(d) additions and a product, each within 2^-24 of its result, so its error
+is at most (log2(d) + 2) 2^-24 sqrt(d) max|v|; a product of rows of n has exact
+terms and at most n additions, each within 2^-23 (the matrix unit may truncate)
+of the sum of magnitudes; then one rounding to the output type."""
+
+import numpy as np
+import pytest
+
+import synthetic as S
+from gpu_util import announce, from_dev, lib_plan, to_dev, torch_dtype
+from oracle import mx as X
+
+pytestmark = pytest.mark.gpu
+
+HALF_ULP = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+
+
+def rht(d, seed=0):
+    side = S.random_plan(np.random.default_rng(seed + d), (2,) * (d.bit_length() - 1), "hadamard")
+    return lib_plan(side), side.signs
+
+
+def dev_rows(x, dtype, ld=None):
+    """(device tensor with leading dimension ld, its values as float32)"""
+    import torch
+    t = torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).to(torch_dtype(dtype)).cuda()
+    if ld is not None:
+        wide = torch.full((x.shape[0], ld), 7.0, dtype=t.dtype, device="cuda")
+        wide[:, :x.shape[1]] = t
+        t = wide[:, :x.shape[1]]
+    return t, t.float().cpu().numpy()
+
+
+def heavy(rng, rows, n):
+    """Heavy-tailed values of widely different magnitudes from block to block."""
+    x = rng.standard_t(3, size=(rows, n))
+    return x * np.exp2(rng.integers(-30, 30, size=(rows, n // 32))).repeat(32, axis=1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,n,d,pad", [(1, 32, 0, 0), (1, 4096, 0, 0), (3, 4000, 32, 8), (37, 96, 0, 0),
+                                          (7, 11008, 128, 0), (513, 768, 256, 24), (2, 64, 64, 0), (129, 2048, 64, 0)])
+def test_quantize(rows, n, d, pad, dtype):
+    import butterfly_rotation_quantization_amd as brq
+    announce(f"mx quantize {rows}x{n} d={d} {dtype}")
+    rng = np.random.default_rng(rows + n + d)
+    x = heavy(rng, rows, n) if dtype != "f16" else rng.standard_t(3, size=(rows, n))
+    t, host = dev_rows(x, dtype, n + pad if pad else None)
+    plan, signs = rht(d) if d else (None, None)
+    codes, scales = brq.mx_quantize(plan, t)
+    want = X.quantize(X.hadamard32(host, signs, d) if d else host)
+    assert np.array_equal(scales.cpu().numpy(), want[1])
+    assert np.array_equal(codes.cpu().numpy(), want[0])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quantize_special_values(dtype):
+    """Zeros of both signs, ties, saturation, subnormals, the largest values,
+    infinities and NaN, each in a block of its own, with ordinary neighbours."""
+    import butterfly_rotation_quantization_amd as brq
+    announce(f"mx quantize special values {dtype}")
+    heads = [[0.0], [-0.0, 0.0], [4, .25, .75, 1.25, 1.75, 2.5, 3.5, 5, -5, -.25], [7.99, 6.9, -7.5, 0.01],
+             [2.0 ** -126, 2.0 ** -127, -2.0 ** -128], [2.0 ** -133, 2.0 ** -130], [3.38e38, -1e38, 1e30, 1e-30],
+             [np.inf, 1.0], [-np.inf], [np.nan, 2.0], [np.nan, np.inf], [1.0, 2.0 ** -60], [2.0 ** -124, 2.0 ** -126]]
+    x = np.zeros((2, 32 * len(heads)), np.float32)
+    for i, h in enumerate(heads):
+        x[0, 32 * i:32 * i + len(h)] = h
+        x[1, 32 * i + 31] = h[0]
+        x[1, 32 * i] = 1.5
+    t, host = dev_rows(x, dtype)
+    codes, scales = brq.mx_quantize(None, t)
+    want = X.quantize(host)
+    assert np.array_equal(scales.cpu().numpy(), want[1])
+    assert np.array_equal(codes.cpu().numpy(), want[0])
+    got = from_dev(brq.mx_dequantize(None, codes, scales))
+    assert np.array_equal(got, X.values(*want), equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,n,d,pad", [(1, 32, 0, 0), (5, 4000, 32, 0), (33, 768, 256, 8), (4, 11008, 128, 0),
+                                          (65, 192, 64, 0)])
+def test_dequantize(rows, n, d, pad, dtype):
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce(f"mx dequantize {rows}x{n} d={d} {dtype}")
+    rng = np.random.default_rng(rows + n + d + 1)
+    codes = rng.integers(0, 256, (rows, n // 2), dtype=np.int64).astype(np.uint8)
+    scales = rng.integers(120, 132, (rows, n // 32), dtype=np.int64).astype(np.uint8)
+    wide = torch.full((rows, n + pad), 7.0, dtype=torch_dtype(dtype), device="cuda")
+    plan, signs = rht(d) if d else (None, None)
+    got = from_dev(brq.mx_dequantize(plan, to_dev(codes, "u8"), to_dev(scales, "u8"), out=wide[:, :n]))
+    v = X.values(codes, scales)
+    if not d:
+        import torch as T
+        assert np.array_equal(got, from_dev(T.from_numpy(v).to(torch_dtype(dtype))))
+    else:
+        want = (v.reshape(-1, d) @ X.hadamard64(d, signs)).reshape(v.shape)
+        bound = (np.log2(d) + 2) * 2.0 ** -24 * np.sqrt(d) * np.abs(v).max() + HALF_ULP[dtype] * np.abs(want) + 2.0 ** -25
+        assert (np.abs(got - want) <= bound).all()
+    assert (wide[:, n:] == 7).all()
+
+
+def test_dequantize_every_scale_byte():
+    import butterfly_rotation_quantization_amd as brq
+    announce("mx dequantize, scale bytes 0..255")
+    codes = np.arange(16, dtype=np.uint8) * 16 + np.arange(16, dtype=np.uint8)[::-1]
+    codes = np.tile(codes, (1, 256))
+    scales = np.arange(256, dtype=np.uint8).reshape(1, 256)
+    got = from_dev(brq.mx_dequantize(None, to_dev(codes, "u8"), to_dev(scales, "u8")))
+    with np.errstate(over="ignore"):
+        want = X.values(codes, scales).astype(np.float32).astype(np.float64)
+    assert np.array_equal(got, want, equal_nan=True)
+
+
+def test_quantize_beyond_32_bit_offsets():
+    """More than 2^32 values: the last rows are where they belong."""
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce("mx quantize 65538 x 65568 bf16")
+    rows, n = 65538, 65568
+    x = torch.zeros((rows, n), dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn((3, n), device="cuda").to(torch.bfloat16)
+    x[-3:] = tail
+    codes, scales = brq.mx_quantize(None, x)
+    del x
+    want = X.quantize(tail.float().cpu().numpy())
+    assert np.array_equal(codes[-3:].cpu().numpy(), want[0])
+    assert np.array_equal(scales[-3:].cpu().numpy(), want[1])
+    assert not codes[:-3].any() and not scales[:-3].any()
+    y = brq.mx_dequantize(None, codes, scales, out_dtype=torch.bfloat16)
+    assert np.array_equal(from_dev(y[-3:]), X.values(*want)) and not y[:-3].any()
+
+
+def operands(rng, T, m, n, lo=118, hi=134):
+    mk = lambda r: (rng.integers(0, 256, (r, n // 2), dtype=np.int64).astype(np.uint8),  # noqa: E731
+                    rng.integers(lo, hi, (r, n // 32), dtype=np.int64).astype(np.uint8))
+    return mk(T), mk(m)
+
+
+def check_product(got, a, b, n, dtype):
+    va, vb = X.values(*a), X.values(*b)
+    want = va @ vb.T
+    bound = (n + 2) * 2.0 ** -23 * (np.abs(va) @ np.abs(vb).T) + HALF_ULP[dtype] * np.abs(want) + 2.0 ** -25
+    over = np.abs(got - want) > bound
+    assert not over.any(), f"{int(over.sum())} outputs beyond the bound, first at {np.argwhere(over)[:3].tolist()}"
+
+
+SHAPES = [(1, 1, 32), (1, 4096, 4096), (1, 300, 28672), (2, 129, 96), (7, 256, 160), (16, 11008, 4000), (17, 64, 1024),
+          (31, 1000, 352), (33, 48, 8192), (64, 512, 512), (65, 513, 544), (128, 256, 1376), (200, 384, 2048),
+          (256, 256, 256), (257, 770, 288), (333, 4096, 11008), (512, 1024, 768), (1030, 520, 640)]
+
+
+@pytest.mark.parametrize("T,m,n", SHAPES)
+def test_matmul(T, m, n):
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    rng = np.random.default_rng(T + m + n)
+    # magnitudes that stay inside float16 and outside its subnormals
+    a, b = operands(rng, T, m, n, 121, 128)
+    ad, bd = [[to_dev(z, "u8") for z in y] for y in (a, b)]
+    for dtype, pad in (("f32", 0), ("bf16", 5), ("f16", 0)):
+        announce(f"mx matmul {T}x{m}x{n} {dtype}")
+        y = torch.full((T, m + pad), 7.0, dtype=torch_dtype(dtype), device="cuda")
+        brq.mx_matmul(*ad, *bd, y=y[:, :m])
+        check_product(from_dev(y[:, :m]), a, b, n, dtype)
+        assert (y[:, m:] == 7).all()
+        again = brq.mx_matmul(*ad, *bd, out_dtype=torch_dtype(dtype))
+        assert torch.equal(again, y[:, :m]), "a second call differs"
+
+
+@pytest.mark.parametrize("T", [1, 5, 40, 300])
+def test_matmul_keeps_nan_rows_apart(T):
+    """A NaN block makes its row (its column) NaN and nothing else; rows beyond
+    the matrices and blocks beyond a row never count."""
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce(f"mx matmul NaN rows T={T}")
+    rng = np.random.default_rng(T)
+    m, n = 270, 416
+    a, b = operands(rng, T, m, n, 121, 128)
+    a[1][T // 2, 3] = 255
+    b[1][m - 1, 0] = 255
+    a[0][T // 2, 48:64] = 0
+    b[0][m - 1, 0:16] = 0
+    # neighbours in memory that hold NaN scales
+    guard = torch.full((T + 64, n // 32), 255, dtype=torch.uint8, device="cuda")
+    guard[:T] = to_dev(a[1], "u8")
+    y = from_dev(brq.mx_matmul(to_dev(a[0], "u8"), guard[:T], to_dev(b[0], "u8"), to_dev(b[1], "u8"),
+                               out_dtype=torch.float32))
+    nan = np.isnan(y)
+    want = np.zeros_like(nan)
+    want[T // 2], want[:, m - 1] = True, True
+    assert np.array_equal(nan, want)
+    rows, cols = np.arange(T) != T // 2, np.arange(m) != m - 1
+    check_product(y[rows][:, cols], [z[rows] for z in a], [z[cols] for z in b], n, "f32")
+
+
+def test_matmul_wide_scales():
+    """Scales over the whole range whose products stay in float32."""
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce("mx matmul wide scales")
+    rng = np.random.default_rng(3)
+    a, b = operands(rng, 20, 40, 256, 0, 254)
+    b[1][:] = (254 - a[1][0]).astype(np.uint8)[None]  # 2^e times 2^-e for row 0
+    y = from_dev(brq.mx_matmul(*[to_dev(z, "u8") for z in (a[0][:1], a[1][:1])], *[to_dev(z, "u8") for z in b],
+                               out_dtype=torch.float32))
+    check_product(y, (a[0][:1], a[1][:1]), b, 256, "f32")
+
+
+def test_matmul_empty_sizes():
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce("mx matmul empty sizes")
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    y = torch.full((3, 5), 7.0, device="cuda")
+    brq.mx_matmul(u8(3, 0), u8(3, 0), u8(5, 0), u8(5, 0), y=y)
+    assert not y.any()
+    assert brq.mx_matmul(u8(0, 16), u8(0, 1), u8(5, 16), u8(5, 1)).shape == (0, 5)
+    assert brq.mx_matmul(u8(3, 16), u8(3, 1), u8(0, 16), u8(0, 1)).shape == (3, 0)
+    c, s = brq.mx_quantize(None, torch.zeros((0, 64), device="cuda"))
+    assert c.shape == (0, 32) and s.shape == (0, 2)
+    torch.cuda.synchronize()
+
+
+def test_another_stream_and_a_graph():
+    """Quantize, multiply and dequantize on a stream of the caller's, then the
+    same captured and replayed on new inputs between eager work."""
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce("mx graph")
+    plan, _ = rht(128)
+    for T, m, n in ((1, 512, 8192), (300, 512, 1024)):
+        w = brq.mx_quantize(None, torch.randn((m, n), device="cuda"))
+        x = torch.empty((T, n), device="cuda", dtype=torch.bfloat16)
+        ws = brq.mx_matmul_workspace(T, m, n)
+        codes, scales = brq.mx_quantize(plan, x.zero_())
+        y = torch.empty((T, m), device="cuda", dtype=torch.bfloat16)
+
+        def step():
+            brq.mx_quantize(plan, x, codes, scales)
+            brq.mx_matmul(codes, scales, *w, y=y, ws=ws)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            step()
+        for r in range(3):
+            new = torch.randn((T, n), device="cuda").to(torch.bfloat16)
+            eager = brq.mx_matmul(*brq.mx_quantize(plan, new), *w)
+            x.copy_(new)
+            y.zero_()
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, eager), f"replay {r} differs"
+
+
+def test_binding_refuses_other_layouts():
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    x = torch.zeros((4, 64), device="cuda")
+    c, s = brq.mx_quantize(None, x)
+    with pytest.raises(ValueError):
+        brq.mx_quantize(None, x.t())
+    with pytest.raises(ValueError):
+        brq.mx_quantize(None, x, codes=c[:, :16])
+    with pytest.raises(ValueError):
+        brq.mx_dequantize(None, c, s[:, :1])
+    with pytest.raises(ValueError):
+        brq.mx_matmul(c, s, c, s.int())
+    with pytest.raises(ValueError):
+        brq.mx_matmul(c, s, c, s, y=torch.zeros((4, 5), device="cuda"))
+    with pytest.raises(brq.BrqError):
+        brq.mx_quantize(None, torch.zeros((4, 48), device="cuda"))
