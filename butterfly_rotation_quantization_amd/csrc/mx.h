@@ -55,6 +55,10 @@ struct MmArgs {
   void* y;
   int yt;
   int64_t ldy;
+  int wide;              // four consecutive outputs may be stored at once
+  int gt, go;            // tiles along tokens and outputs
+  int band;              // rows of tiles taken together
+  int64_t per_xcd;       // tiles per XCD
 };
 
 hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t s);

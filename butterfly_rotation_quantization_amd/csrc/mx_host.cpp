@@ -166,6 +166,7 @@ brq_status brq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const 
   a.y = y;
   a.yt = yt;
   a.ldy = ldy;
+  a.wide = ldy % 4 == 0 && !misaligned(y, 4 * dtype_size(yt));
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int tok = prof_begin("mx matmul", s);
   const hipError_t e = launch_mx_matmul(a, s);
