@@ -56,10 +56,49 @@ struct MmArgs {
   int yt;
   int64_t ldy;
   int wide;              // four consecutive outputs may be stored at once
-  int gt, go;            // tiles along tokens and outputs
+  // tiles (tile > 0)
+  int tile;              // rows and columns of a workgroup's tile: 256, 128; 0: no tiles
+  int stages;            // of kMmK values
+  int64_t gt, go;        // tiles along tokens and outputs
   int band;              // rows of tiles taken together
   int64_t per_xcd;       // tiles per XCD
+  int splits, per;       // parts of the long axis, stages per part
+  uint8_t *ts, *os;      // scale images of the operands, in the workspace
+  float* part;           // [splits][T][m] partial sums, in the workspace
 };
+
+constexpr int kMmK = 256;  // values of a row per stage
+
+// Kernel and workspace of a product (a.T, a.m, a.n set): returns the
+// workspace bytes.
+inline size_t mm_plan(MmArgs& a, uint8_t* ws) {
+  a.tile = 0;
+  a.splits = 1;
+  if (a.n < kMmK || a.T <= 16 || a.n > (1 << 23)) return 0;
+  auto tiles = [&](int64_t t) { return ((a.T + t - 1) / t) * ((a.m + t - 1) / t); };
+  // One 256 x 256 tile per compute unit at a time, two of 128 x 128; such a
+  // pair takes about 2/3 of a large tile's time for half its work.
+  const int64_t large = (tiles(256) + 255) / 256 * 3, small = (tiles(128) + 511) / 512 * 2;
+  a.tile = large <= small ? 256 : 128;
+  a.stages = (int)((a.n + kMmK - 1) / kMmK);
+  a.gt = (a.T + a.tile - 1) / a.tile;
+  a.go = (a.m + a.tile - 1) / a.tile;
+  // Too few tiles for the chip: the long axis in parts of eight stages or more.
+  a.per = a.stages;
+  if (a.tile == 128 && tiles(128) <= 256) {
+    const int64_t want = 512 / tiles(128), most = a.stages / 8;
+    const int64_t parts = want < most ? want : most;
+    if (parts > 1) a.per = (int)((a.stages + parts - 1) / parts);
+  }
+  a.splits = (a.stages + a.per - 1) / a.per;
+  a.per_xcd = (a.gt * a.go * a.splits + 7) / 8;
+  a.band = 4;
+  const int64_t image = (int64_t)a.stages * (kMmK / kMxBlock) * a.tile;
+  a.ts = ws;
+  a.os = ws + a.gt * image;
+  a.part = reinterpret_cast<float*>(a.os + a.go * image);
+  return (size_t)((a.gt + a.go) * image) + (a.splits > 1 ? (size_t)a.splits * a.T * a.m * sizeof(float) : 0);
+}
 
 hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t s);
 

@@ -9,6 +9,7 @@ namespace brq {
 
 typedef float mxf2 __attribute__((ext_vector_type(2)));
 typedef float mxf4 __attribute__((ext_vector_type(4)));
+typedef float mxf16 __attribute__((ext_vector_type(16)));
 typedef int mxi4 __attribute__((ext_vector_type(4)));
 typedef int mxi8 __attribute__((ext_vector_type(8)));
 typedef __bf16 mxb2 __attribute__((ext_vector_type(2)));

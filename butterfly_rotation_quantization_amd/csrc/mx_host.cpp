@@ -129,8 +129,14 @@ brq_status brq_mx_dequantize(const brq_plan* right, const uint8_t* codes, const 
 }
 
 size_t brq_mx_matmul_workspace_bytes(int64_t T, int64_t m, int64_t n) {
-  (void)T, (void)m, (void)n;
-  return 0;
+  const int64_t most = ((int64_t)1 << 31) - 1;
+  if (T <= 0 || m <= 0 || n <= 0 || T > most || m > most || n > most || n % kMxBlock) return 0;
+  MmArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.T = T;
+  a.m = m;
+  a.n = n;
+  return mm_plan(a, nullptr);
 }
 
 brq_status brq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
@@ -166,6 +172,7 @@ brq_status brq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const 
   a.y = y;
   a.yt = yt;
   a.ldy = ldy;
+  mm_plan(a, static_cast<uint8_t*>(ws));
   a.wide = ldy % 4 == 0 && !misaligned(y, 4 * dtype_size(yt));
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int tok = prof_begin("mx matmul", s);

@@ -48,19 +48,19 @@ __global__ __launch_bounds__(64) void mm_simple_kernel(MmArgs a) {
 // c += a b with byte SA of sa and SB of sb as the scales; c stays in the
 // accumulation registers.  Written out because with all 256 of them in use the
 // register allocator moved sums to and fro between the two files (90 moves in
-// a stage of 128 products).  The hardware orders these among themselves and
+// a stage of 128 products of 16 x 16 x 128).  The hardware orders these among themselves and
 // after the loads of their operands; mm_settle comes before other reads of c.
 template <int SA, int SB>
-__device__ __forceinline__ void mm_mfma(mxi4 a, mxi4 b, mxf4& c, int sa, int sb) {
+__device__ __forceinline__ void mm_mfma(mxi4 a, mxi4 b, mxf16& c, int sa, int sb) {
   asm volatile(
-      "v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%6,0] op_sel_hi:[%7,%8,0] cbsz:4 blgp:4"
+      "v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%6,0] op_sel_hi:[%7,%8,0] cbsz:4 blgp:4"
       : "+a"(c)
       : "v"(a), "v"(b), "v"(sa), "v"(sb), "n"(SA & 1), "n"(SB & 1), "n"(SA >> 1), "n"(SB >> 1));
 }
 // More wait states than any product needs until its result can be read.
 __device__ __forceinline__ void mm_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 // byte ia of sa and byte ib of sb (constants once the loops are unrolled)
-__device__ __forceinline__ void mm_step(mxi4 a, mxi4 b, mxf4& c, int sa, int ia, int sb, int ib) {
+__device__ __forceinline__ void mm_step(mxi4 a, mxi4 b, mxf16& c, int sa, int ia, int sb, int ib) {
   switch ((ia & 3) * 4 + (ib & 3)) {
     case 0: return mm_mfma<0, 0>(a, b, c, sa, sb);
     case 1: return mm_mfma<0, 1>(a, b, c, sa, sb);
@@ -98,242 +98,401 @@ __device__ __forceinline__ void mm_store4(void* y, int yt, int64_t off, mxf4 v, 
     if (i < valid) mm_store(y, yt, off + i, v[i]);
 }
 
-constexpr int kMmK = 256;           // values of a row per stage
-constexpr int kMmKB = kMmK / 2;     // their code bytes
+constexpr int kMmKB = kMmK / 2;     // code bytes of a row in a stage
 constexpr int kMmKS = kMmK / kMxBlock;
 
 __device__ const uint4 kMmZero = {0u, 0u, 0u, 0u};
 
-// Byte g of the words of lanes c, c + 16, c + 32, c + 48 (g = lane / 16,
-// c = lane % 16): a transpose of 4 x 4 bytes over the four rows of lanes.
-__device__ __forceinline__ uint32_t mm_transpose(uint32_t w, uint32_t sel) {
-  const auto h = __builtin_amdgcn_permlane32_swap(w, w, false, false);       // rows 0 1 0 1, 2 3 2 3
-  const auto p = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);  // row 0, row 1
-  const auto q = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);  // row 2, row 3
-  const uint32_t lo = __builtin_amdgcn_perm(p[1], p[0], sel), hi = __builtin_amdgcn_perm(q[1], q[0], sel);
-  return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
-}
-
-// 16 bytes per lane from p straight to LDS, lane l's to dst + l (dst uniform
-// over the wavefront).  Written out because the compiler, which takes any LDS
+// 16 bytes per lane from p straight to LDS, lane l's to byte at + 16 l (at
+// uniform over the wavefront).  Written out because the compiler, which takes any LDS
 // read to depend on such a load, would wait for it before the next one; the
 // kernel waits for vmcnt(0) and a barrier before it reads what was brought.
-__device__ __forceinline__ void mm_to_lds(const void* p, uint4* dst) {
-  const uint32_t at = __builtin_amdgcn_readfirstlane(
-      (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)dst));
+__device__ __forceinline__ void mm_to_lds(const void* p, uint32_t at) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(p) : "memory");
 }
+// The same from base + (off + step), to byte at + to; off is left there.
+template <int TO>
+__device__ __forceinline__ void mm_to_lds(const void* base, uint32_t& off, uint32_t step, uint32_t at) {
+  asm volatile("s_add_u32 m0, %3, %4\n\tv_add_u32 %0, %2, %0\n\tglobal_load_lds_dwordx4 %0, %1"
+               : "+v"(off)
+               : "s"(base), "s"(step), "s"(at), "n"(TO)
+               : "memory", "scc");
+}
 
-// Operands of one matrix step of 128 values.
+// Scales of one operand in the order the tiles take them: for each tile of R
+// rows and each stage, [block][row % 32][row / 32], so that a stage's are one
+// run of 8 R bytes, fetched straight to LDS, in which a lane finds those of
+// its tiles in one word.  Read from the rows they are 8 bytes out of a line
+// for each row and stage (measured at 4096x8192x28672, rows read by the tile
+// kernel: 15% of its time; this pass: 1.5%).  Rows and blocks past the end
+// get zeros (2^-127, times codes of zero).  One workgroup: a tile, kMmRun
+// stages.
+constexpr int kMmRun = 4;
+template <int R>
+__device__ __forceinline__ void mm_scale_tile(const uint8_t* src, int64_t rows, int64_t nb, int stages, int64_t tile,
+                                              int s0, uint8_t* out) {
+  constexpr int W = kMmRun * kMmKS, LD = W + 4;
+  __shared__ uint8_t lds[R][LD];
+  const int tid = threadIdx.x;
+  const int64_t k0 = (int64_t)s0 * kMmKS;
+  if (nb % 4 == 0) {  // whole words (the base is aligned)
+    for (int e = tid; e < R * (W / 4); e += kMxThreads) {
+      const int r = e / (W / 4), c = 4 * (e % (W / 4));
+      const int64_t row = tile * R + r;
+      *reinterpret_cast<uint32_t*>(&lds[r][c]) =
+          row < rows && k0 + c < nb ? *reinterpret_cast<const uint32_t*>(src + row * nb + k0 + c) : 0u;
+    }
+  } else {
+    for (int e = tid; e < R * W; e += kMxThreads) {
+      const int r = e / W, c = e % W;
+      const int64_t row = tile * R + r;
+      lds[r][c] = row < rows && k0 + c < nb ? src[row * nb + k0 + c] : 0;
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < kMmRun * kMmKS * 32; e += kMxThreads) {
+    const int r = e & 31, c = e >> 5, s = s0 + c / kMmKS;  // block c of the run
+    if (s >= stages) break;
+    uint8_t* d = out + (tile * stages + s) * (8 * R) + (c % kMmKS * 32 + r) * (R / 32);
+#pragma unroll
+    for (int q = 0; q < R / 128; ++q) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w |= (uint32_t)lds[r + 32 * (4 * q + j)][c] << (8 * j);
+      reinterpret_cast<uint32_t*>(d)[q] = w;
+    }
+  }
+}
+template <int BT, int BO>
+__global__ __launch_bounds__(kMxThreads) void mm_scales_kernel(MmArgs a) {
+  const int64_t nb = a.n / kMxBlock;
+  const int stages = (int)((nb + kMmKS - 1) / kMmKS), s0 = (int)blockIdx.y * kMmRun;
+  if ((int64_t)blockIdx.x < a.gt) mm_scale_tile<BT>(a.as, a.T, nb, stages, blockIdx.x, s0, a.ts);
+  else mm_scale_tile<BO>(a.bs, a.m, nb, stages, (int64_t)blockIdx.x - a.gt, s0, a.os);
+}
+
+// Operands of a step of 128 values: two of 64, and the scales of the tiles.
 template <int TT, int TO>
 struct MmFrag {
-  mxi4 x[TT], w[TO];
-  int xs[(TT + 3) / 4], ws[(TO + 3) / 4];
+  mxi4 x[2][TT], w[2][TO];
+  int xs[2], ws[2];
 };
 
-// WT x WO wavefronts, each TT x TO tiles of 16 tokens x 16 outputs.
-template <int WT, int WO, int TT, int TO>
-__global__ __launch_bounds__(64 * WT * WO, 1) void mm_tile_kernel(MmArgs a) {
-  constexpr int NTH = 64 * WT * WO;
-  constexpr int BT = 16 * TT * WT, BO = 16 * TO * WO, ROWS = BT + BO;
-  constexpr int NL = ROWS * (kMmKB / 16) / NTH;  // 16-byte pieces per thread and stage
-  constexpr int RS = NTH / 8;                    // rows between a thread's pieces
-  constexpr int NR = ROWS / NTH;                 // rows whose scales a thread brings
-  constexpr int NTT = BT / 16, NTO = BO / 16;
+// One workgroup's tile, WT x WO wavefronts of TT x TO tiles of 32 tokens x 32
+// outputs.  FULL: no row of the tile is past the end and rows are whole
+// stages, so that a piece takes three instructions to fetch.
+template <int WT, int WO, int TT, int TO, bool FULL>
+struct MmTile {
+  static constexpr int NTH = 64 * WT * WO;
+  static constexpr int BT = 32 * TT * WT, BO = 32 * TO * WO, ROWS = BT + BO;
+  static constexpr int NL = ROWS * (kMmKB / 16) / NTH;  // 16-byte pieces per thread and stage
+  static constexpr int NL1 = NL * 3 / 4;                // of them, fetched in a stage's second step
+  static constexpr int RS = NTH / 8;                    // rows between a thread's pieces
+  static constexpr int NTT = BT / 32, NTO = BO / 32;
+  static constexpr int NM = 2 * TT * TO;                // products of a step
+  static constexpr int NG = 2 * (TT + TO);              // operand reads of a step
   static_assert(ROWS % NTH == 0 && BT % RS == 0 && BT % 64 == 0 && BO % 64 == 0, "whole rows per thread and wavefront");
-  __shared__ uint4 codes[2][ROWS * 8];           // piece c of row r at r * 8 + (c ^ (r & 7))
-  __shared__ uint8_t scales[2][ROWS * 8];        // [block][row % 16][tile], tokens first
+  using Frag = MmFrag<TT, TO>;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int lr = lane & 15, lg = lane >> 4;
-  const int wt = wave % WT, wo = wave / WT;
-  // tile of this workgroup
-  const int64_t p = (int64_t)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
-  if (p >= (int64_t)a.gt * a.go) return;
-  const int64_t band = p / ((int64_t)a.band * a.go);
-  const int64_t q = p - band * a.band * a.go;
-  const int64_t h = a.gt - band * a.band < a.band ? a.gt - band * a.band : a.band;  // rows of tiles in this band
-  const int64_t t0 = (band * a.band + q % h) * BT, o0 = q / h * BO;
+  struct Lds {
+    uint4 codes[2][ROWS * 8];     // piece c of row r at r * 8 + (c ^ (r & 7))
+    uint8_t scales[2][ROWS * 8];  // [block][row % 32][tile], tokens first
+  };
 
-  const int64_t nb = a.n / kMxBlock, ld = a.n / 2;
-  const int stages = (int)((nb + kMmKS - 1) / kMmKS);
+  const MmArgs& a;
+  Lds& lds;
+  const int tid, lane, wave, lr, lg, wt, wo;
+  const int64_t t0, o0, nb, ld;
+  const int first, stages;  // the part's first stage, its number of stages
+  // where the sums go: the output, or the part's float32 partial sums
+  void* y;
+  int yt;
+  int64_t ldy;
+  bool wide;
   // The thread's LDS slots: row pr + j RS, piece pc of the row.  Rows past the
   // end repeat the last one (their products are not stored).
-  const int pr = tid >> 3, pc = (tid & 7) ^ (pr & 7);
-  const int lt = (int)(a.T - t0 < BT ? a.T - t0 : BT) - 1, lo = (int)(a.m - o0 < BO ? a.m - o0 : BO) - 1;
-  const uint8_t* ab = a.a + t0 * ld + 16 * pc;
-  const uint8_t* bb = a.b + o0 * ld + 16 * pc;
-  const uint8_t* sp[NR];
-#pragma unroll
-  for (int j = 0; j < NR; ++j) {
-    const int r = tid + j * NTH;
-    sp[j] = r < BT ? a.as + (t0 + (r < lt ? r : lt)) * nb : a.bs + (o0 + (r - BT < lo ? r - BT : lo)) * nb;
-  }
-  const uint32_t tsel = (uint32_t)lg | (uint32_t)(4 + lg) << 8 | 0x0c0c0000u;
+  const int pr, pc, lt, lo;
+  const uint8_t *ab, *bb;
+  const uint32_t base, at;  // LDS addresses: of the workgroup, of the wavefront's first piece
+  uint32_t off0;
+  mxf16 acc[TO][TT];
 
-  // Pieces of stage s: straight to LDS; past the end of a row (the ragged last
-  // stage, stages that do not exist) zeros are fetched instead.
+  __device__ __forceinline__ MmTile(const MmArgs& a_, Lds& l, int64_t t0_, int64_t o0_, int part)
+      : a(a_), lds(l), tid(threadIdx.x), lane(tid & 63), wave(tid >> 6), lr(lane & 31), lg(lane >> 5), wt(wave % WT),
+        wo(wave / WT), t0(t0_), o0(o0_), nb(a_.n / kMxBlock), ld(a_.n / 2),
+        first(part * a_.per), stages(a_.stages - first < a_.per ? a_.stages - first : a_.per), pr(tid >> 3), pc((tid & 7) ^ (pr & 7)),
+        lt((int)(a_.T - t0_ < BT ? a_.T - t0_ : BT) - 1), lo((int)(a_.m - o0_ < BO ? a_.m - o0_ : BO) - 1),
+        base((uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)&l)),
+        at(__builtin_amdgcn_readfirstlane(base + 16 * (tid & ~63))) {
+    const bool whole = a.splits == 1;
+    y = whole ? a.y : a.part + (int64_t)part * a.T * a.m;
+    yt = whole ? a.yt : (int)BRQ_F32;
+    ldy = whole ? a.ldy : a.m;
+    wide = whole ? a.wide != 0 : a.m % 4 == 0;
+    ab = a.a + t0 * ld;
+    bb = a.b + o0 * ld;
+    off0 = (uint32_t)(pr * (int)ld + 16 * pc) - (uint32_t)(RS * (int)ld);
+  }
+
+  // Where the pieces of stage s come from.  Past the end of a row (the ragged
+  // last stage, stages that do not exist) zeros are fetched instead; with FULL
+  // only whole stages exist, and the last one is fetched again after it.
   struct Source {
     const uint8_t *x, *w;
     unsigned ld;
     int row;
+    uint32_t off;
   };
-  auto source = [&](int s) {
-    const int64_t kb = (int64_t)s * kMmKB;
-    const bool in = kb + 16 * pc < ld;
+  __device__ __forceinline__ Source source(int s) const {
     Source f;
-    f.x = in ? ab + kb : reinterpret_cast<const uint8_t*>(&kMmZero);
-    f.w = in ? bb + kb : reinterpret_cast<const uint8_t*>(&kMmZero);
-    f.ld = in ? (unsigned)ld : 0u;
-    f.row = pr;
-    asm volatile("" : "+v"(f.row));  // offsets are computed at each use, or NL of them would be kept
+    if constexpr (FULL) {
+      const int64_t kb = (int64_t)(first + (s < stages ? s : stages - 1)) * kMmKB;
+      f.x = ab + kb;
+      f.w = bb + kb;
+      f.ld = (unsigned)(RS * (int)ld);
+      f.row = 0;
+    } else {
+      const int64_t kb = (int64_t)(first + s) * kMmKB + 16 * pc;
+      const bool in = kb < ld;
+      f.x = in ? ab + kb : reinterpret_cast<const uint8_t*>(&kMmZero);
+      f.w = in ? bb + kb : reinterpret_cast<const uint8_t*>(&kMmZero);
+      f.ld = in ? (unsigned)ld : 0u;
+      f.row = pr;
+      asm volatile("" : "+v"(f.row));  // offsets are computed at each use, or NL of them would be kept
+    }
+    f.off = off0;
     return f;
-  };
-  auto fetch = [&](const Source& f, int buf, int j) {  // row < 256 and ld < 2^23: a 24-bit product
-    const int r = j * RS < BT ? f.row + j * RS : f.row + j * RS - BT, last = j * RS < BT ? lt : lo;
-    const uint8_t* g = (j * RS < BT ? f.x : f.w) + __umul24((unsigned)(r < last ? r : last), f.ld);
-    mm_to_lds(g, &codes[buf][(tid & ~63) + j * NTH]);
-  };
-  auto fetch_scales = [&](int s, uint64_t (&v)[NR]) {
-    // the row's last eight bytes where the stage is ragged, moved into place:
-    // zeros (2^-127, times codes of zero) follow
-    const int64_t k0 = (int64_t)s * kMmKS, k = k0 < nb - kMmKS ? k0 : nb - kMmKS;
-    const int sh = k0 - k < kMmKS ? 8 * (int)(k0 - k) : 8 * (kMmKS - 1);
-#pragma unroll
-    for (int j = 0; j < NR; ++j) {
-      __builtin_memcpy(&v[j], sp[j] + k, 8);
-    }
-    return sh;
-  };
-  auto put_scales = [&](int buf, const uint64_t (&v)[NR], int sh) {
-#pragma unroll
-    for (int j = 0; j < NR; ++j) {  // 64 rows of one operand: four tiles; lane (lr, lg) stores blocks lg and lg + 4
-      const int r0 = (tid & ~63) + j * NTH;
-      const int nt = r0 < BT ? NTT : NTO;
-      uint8_t* d = &scales[buf][r0 < BT ? 0 : 8 * BT] + (lg * 16 + lr) * nt + (r0 < BT ? r0 : r0 - BT) / 16;
-      *reinterpret_cast<uint32_t*>(d) = mm_transpose((uint32_t)(v[j] >> sh), tsel);
-      *reinterpret_cast<uint32_t*>(d + 64 * nt) = mm_transpose((uint32_t)(v[j] >> sh >> 32), tsel);
-    }
-  };
-  using Frag = MmFrag<TT, TO>;
-  const int xr = 16 * TT * wt + lr, wr = BT + 16 * TO * wo + lr;  // LDS rows of the lane's first tiles
-  // operand tile e of step k2 (tokens first), and the scales
-  auto read = [&](Frag& f, int buf, int k2, int e) {
-    const int c = (4 * k2 + lg) ^ (lr & 7);
-    if (e < TT) f.x[e] = *reinterpret_cast<const mxi4*>(&codes[buf][(xr + 16 * e) * 8 + c]);
-    else f.w[e - TT] = *reinterpret_cast<const mxi4*>(&codes[buf][(wr + 16 * (e - TT)) * 8 + c]);
-  };
-  auto read_scales = [&](Frag& f, int buf, int k2) {
-    const uint8_t* xq = &scales[buf][((4 * k2 + lg) * 16 + lr) * NTT + TT * wt];
-    const uint8_t* wq = &scales[buf][8 * BT + ((4 * k2 + lg) * 16 + lr) * NTO + TO * wo];
-#pragma unroll
-    for (int j = 0; j < (TT + 3) / 4; ++j)
-      f.xs[j] = TT >= 4 ? reinterpret_cast<const int*>(xq)[j] : *reinterpret_cast<const uint16_t*>(xq);
-#pragma unroll
-    for (int i = 0; i < (TO + 3) / 4; ++i)
-      f.ws[i] = TO >= 4 ? reinterpret_cast<const int*>(wq)[i] : *reinterpret_cast<const uint16_t*>(wq);
-  };
-
-  mxf4 acc[TO][TT];
-#pragma unroll
-  for (int i = 0; i < TO; ++i)
-#pragma unroll
-    for (int j = 0; j < TT; ++j) acc[i][j] = mxf4{0.f, 0.f, 0.f, 0.f};
-  constexpr int NG = TT + TO, PER = (TT * TO + NG - 1) / NG;  // groups of one operand read and PER products
-  auto products = [&](const Frag& f, int e) {
-#pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const int x = e * PER + u, i = x / TT, j = x % TT;
-      if (x < TT * TO) mm_step(f.w[i], f.x[j], acc[i][j], f.ws[i / 4], i, f.xs[j / 4], j);
-    }
-  };
-
-  // Stage s's first step multiplies while its second step's operands come from
-  // LDS; then, once every wavefront has them and stage s + 1 has arrived, the
-  // second step multiplies while stage s + 2 is fetched over stage s and the
-  // first step's operands of stage s + 1 are read.
-  uint64_t sv[NR];
-  int sh;
-  {
-    const Source f = source(0);
-#pragma unroll
-    for (int j = 0; j < NL; ++j) fetch(f, 0, j);
-    sh = fetch_scales(0, sv);
-    put_scales(0, sv, sh);
-    sh = fetch_scales(1, sv);
-    put_scales(1, sv, sh);
-    const Source g = source(1);
-#pragma unroll
-    for (int j = 0; j < NL; ++j) fetch(g, 1, j);
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  Frag f0, f1;
-  read_scales(f0, 0, 0);
-#pragma unroll
-  for (int e = 0; e < NG; ++e) read(f0, 0, 0, e);
-  for (int s = 0; s < stages; ++s) {
-    const int buf = s & 1;
-    sh = fetch_scales(s + 2, sv);
-    __builtin_amdgcn_sched_barrier(0);
-    read_scales(f1, buf, 1);
-#pragma unroll
-    for (int e = 0; e < NG; ++e) {
-      read(f1, buf, 1, e);
-      products(f0, e);
-      __builtin_amdgcn_sched_barrier(0);
+  template <int BUF, int J>
+  __device__ __forceinline__ void fetch(Source& f) const {
+    constexpr int to = (int)sizeof(lds.codes[0]) * BUF + J * NTH * 16;
+    if constexpr (FULL) {
+      if constexpr (J == BT / RS) f.off = off0;
+      mm_to_lds<to>(J * RS < BT ? f.x : f.w, f.off, f.ld, at);
+    } else {  // row < 256 and ld < 2^23: a 24-bit product
+      const int r = J * RS < BT ? f.row + J * RS : f.row + J * RS - BT, last = J * RS < BT ? lt : lo;
+      mm_to_lds((J * RS < BT ? f.x : f.w) + __umul24((unsigned)(r < last ? r : last), f.ld), at + to);
     }
+  }
+  // Scales of stage s, from their image (mm_scales_kernel): the wavefronts
+  // bring 1 KB each, in turn from the start when there are fewer pieces.
+  template <int BUF>
+  __device__ __forceinline__ void fetch_scales(int s) const {
+    constexpr int from = (int)sizeof(lds.codes) + BUF * (int)sizeof(lds.scales[0]);
+    const int piece = __builtin_amdgcn_readfirstlane(wave % (8 * ROWS / 1024)) * 1024;
+    const int64_t st = first + (s < stages ? s : stages - 1);
+    const uint8_t* g = piece < 8 * BT ? a.ts + (t0 / BT * a.stages + st) * (8 * BT) + piece
+                                      : a.os + (o0 / BO * a.stages + st) * (8 * BO) + (piece - 8 * BT);
+    mm_to_lds(g + 16 * lane, base + from + piece);
+  }
+  template <int E>  // operand E of step k2: the first 64 values, tokens first, then the second
+  __device__ __forceinline__ void read(Frag& f, int buf, int k2) const {
+    constexpr int u = E / (TT + TO), e = E % (TT + TO);
+    const int c = (4 * k2 + 2 * u + lg) ^ (lr & 7);
+    if constexpr (e < TT) f.x[u][e] = *reinterpret_cast<const mxi4*>(&lds.codes[buf][(32 * (TT * wt + e) + lr) * 8 + c]);
+    else f.w[u][e - TT] = *reinterpret_cast<const mxi4*>(&lds.codes[buf][(BT + 32 * (TO * wo + e - TT) + lr) * 8 + c]);
+  }
+  __device__ __forceinline__ void read_scales(Frag& f, int buf, int k2) const {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int at = (4 * k2 + 2 * u + lg) * 32 + lr;
+      const uint8_t* xq = &lds.scales[buf][at * NTT + TT * wt];
+      const uint8_t* wq = &lds.scales[buf][8 * BT + at * NTO + TO * wo];
+      f.xs[u] = TT == 4 ? *reinterpret_cast<const int*>(xq) : *reinterpret_cast<const uint16_t*>(xq);
+      f.ws[u] = TO == 4 ? *reinterpret_cast<const int*>(wq) : *reinterpret_cast<const uint16_t*>(wq);
+    }
+  }
+
+  // One step of 128 values: the products of f, and between them, a few
+  // instructions at a time so that the matrix unit is never left waiting for
+  // this wavefront's next issue, the reads of g (step K2G of buffer BG) and,
+  // the pieces of a later stage into buffer BF.
+  template <int BG, int K2G, bool FETCH, int BF, int X>
+  __device__ __forceinline__ void step(const Frag& f, Frag& g, Source& src) {
+    if constexpr (X < NM) {
+      // reads are spread evenly over the products; of the pieces three
+      // quarters go into the second step and the rest into the first half of
+      // the next stage's first step (FETCH false)
+      constexpr int e0 = X * NG / NM, e1 = (X + 1) * NG / NM;
+      constexpr int n = FETCH ? NL1 : NL - NL1, len = FETCH ? NM : NM / 2;
+      constexpr int x0 = X < len ? X : len, x1 = X + 1 < len ? X + 1 : len;
+      constexpr int j0 = (FETCH ? 0 : NL1) + x0 * n / len, j1 = (FETCH ? 0 : NL1) + x1 * n / len;
+      constexpr int u = X / (TT * TO), i = X % (TT * TO) / TT, j = X % TT;
+      mm_step(f.w[u][i], f.x[u][j], acc[i][j], f.ws[u], i, f.xs[u], j);
+      if constexpr (e1 > e0) read<e0>(g, BG, K2G);
+      if constexpr (e1 > e0 + 1) read<e0 + 1>(g, BG, K2G);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (j1 > j0) fetch<BF, j0>(src);
+      if constexpr (j1 > j0 + 1) fetch<BF, j0 + 1>(src);
+      static_assert(j1 <= j0 + 2 && e1 <= e0 + 2, "pieces and reads per product");
+      __builtin_amdgcn_sched_barrier(0);
+      step<BG, K2G, FETCH, BF, X + 1>(f, g, src);
+    }
+  }
+  template <int BUF, int J>
+  __device__ __forceinline__ void fetch_all(Source& f) const {
+    if constexpr (J < NL) {
+      fetch<BUF, J>(f);
+      fetch_all<BUF, J + 1>(f);
+    }
+  }
+  template <int BUF, int J>
+  __device__ __forceinline__ void fetch_some(Source& f) const {
+    if constexpr (J < NL1) {
+      fetch<BUF, J>(f);
+      fetch_some<BUF, J + 1>(f);
+    }
+  }
+  template <int E>
+  __device__ __forceinline__ void read_all(Frag& f, int buf, int k2) const {
+    if constexpr (E < NG) {
+      read<E>(f, buf, k2);
+      read_all<E + 1>(f, buf, k2);
+    }
+  }
+
+  // Stage s, in buffer BUF.  Its first step multiplies while its second step's
+  // operands come from LDS; then, once every wavefront has them and stage
+  // s + 1 has arrived, the second step multiplies while stage s + 2 is fetched
+  // over stage s and the first operands of stage s + 1 are read.
+  template <int BUF>
+  __device__ __forceinline__ void stage(int s, Frag& f0, Frag& f1, Source& src) {
+    read_scales(f1, BUF, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    step<BUF, 1, false, BUF ^ 1, 0>(f0, f1, src);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < NR; ++j) asm volatile("" : "+v"(sv[j]));  // they are here: the compiler's own wait belongs here
-    const Source f = source(s + 2);
+    src = source(s + 2);
+    fetch_scales<BUF>(s + 2);
+    read_scales(f0, BUF ^ 1, 0);
     __builtin_amdgcn_sched_barrier(0);
-    read_scales(f0, buf ^ 1, 0);
+    step<BUF ^ 1, 0, true, BUF, 0>(f1, f0, src);
+  }
+
+  __device__ __forceinline__ void run() {
 #pragma unroll
-    for (int e = 0; e < NG; ++e) {
+    for (int i = 0; i < TO; ++i)
 #pragma unroll
-      for (int j = e * NL / NG; j < (e + 1) * NL / NG; ++j) fetch(f, buf, j);
-      read(f0, buf ^ 1, 0, e);
-      products(f1, e);
-      if (e == NG / 2) put_scales(buf, sv, sh);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < TT; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+    Source src = source(0);
+    fetch_all<0, 0>(src);
+    fetch_scales<0>(0);
+    fetch_scales<1>(1);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    Frag f0, f1;
+    read_scales(f0, 0, 0);
+    read_all<0>(f0, 0, 0);
+    src = source(1);
+    fetch_some<1, 0>(src);
+    int s = 0;
+    for (; s + 1 < stages; s += 2) {
+      stage<0>(s, f0, f1, src);
+      stage<1>(s + 1, f0, f1, src);
+    }
+    if (s < stages) stage<0>(s, f0, f1, src);
+    mm_settle();
+    // LDS is about to hold the sums: the last pieces, fetched for no stage,
+    // have to be in it before, and every wavefront's reads done
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    store<0>();
+  }
+
+  // The sums of 32 tokens at a time through the wavefront's part of LDS, so
+  // that a row's outputs leave in runs of 128 TO bytes and more, by code small
+  // enough to stay in the instruction cache (one store a register, unrolled,
+  // cost 25 us of fetching instructions).
+  template <int J>
+  __device__ __forceinline__ void store() {
+    if constexpr (J < TT) {
+      constexpr int LD = 32 * TO + 4, LPR = 8 * TO;  // floats a row, lanes a row
+      static_assert(32 * LD * 4 * WT * WO <= (int)sizeof(Lds), "sums of 32 tokens of every wavefront");
+      float* my = reinterpret_cast<float*>(&lds) + wave * (32 * LD);
+#pragma unroll
+      for (int i = 0; i < TO; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)  // D: outputs 8 e + 4 lg .. + 3 of tile i, token lr of tile J
+          *reinterpret_cast<mxf4*>(&my[lr * LD + 32 * i + 8 * e + 4 * lg]) =
+              mxf4{acc[i][J][4 * e], acc[i][J][4 * e + 1], acc[i][J][4 * e + 2], acc[i][J][4 * e + 3]};
+      __builtin_amdgcn_wave_barrier();
+      const int64_t o = o0 + 32 * TO * wo + 4 * (lane % LPR), left = a.m - o;
+      const int64_t tj = t0 + 32 * (TT * wt + J);
+#pragma unroll 1
+      for (int r = lane / LPR; r < 32; r += 64 / LPR) {
+        const mxf4 v = *reinterpret_cast<const mxf4*>(&my[r * LD + 4 * (lane % LPR)]);
+        if (tj + r < a.T && left > 0) mm_store4(y, yt, (tj + r) * ldy + o, v, left < 4 ? (int)left : 4, wide);
+      }
+      __builtin_amdgcn_wave_barrier();
+      store<J + 1>();
     }
   }
-  mm_settle();
-  // D: outputs 4 lg .. + 3 of tile i, token lr of tile j
-#pragma unroll
-  for (int j = 0; j < TT; ++j) {
-    const int64_t t = t0 + 16 * (TT * wt + j) + lr;
-    if (t >= a.T) continue;
-#pragma unroll
-    for (int i = 0; i < TO; ++i) {
-      const int64_t o = o0 + 16 * (TO * wo + i) + 4 * lg;
-      const int64_t left = a.m - o;
-      if (left > 0) mm_store4(a.y, a.yt, t * a.ldy + o, acc[i][j], left < 4 ? (int)left : 4, a.wide);
-    }
+};
+
+template <int WT, int WO, int TT, int TO>
+__global__ __launch_bounds__(64 * WT * WO, 1) void mm_tile_kernel(MmArgs a) {
+  using Full = MmTile<WT, WO, TT, TO, true>;
+  using Any = MmTile<WT, WO, TT, TO, false>;
+  __shared__ typename Full::Lds lds;
+  // the workgroup's tile: consecutive ones, which share operands, on one XCD
+  int64_t p = (int64_t)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
+  if (p >= a.gt * a.go * a.splits) return;
+  const int part = (int)(p / (a.gt * a.go));
+  p -= part * (a.gt * a.go);
+  const int64_t band = p / ((int64_t)a.band * a.go);
+  const int64_t q = p - band * a.band * a.go;
+  const int64_t h = a.gt - band * a.band < a.band ? a.gt - band * a.band : a.band;  // rows of tiles in this band
+  const int64_t t0 = (band * a.band + q % h) * Full::BT, o0 = q / h * Full::BO;
+  if (t0 + Full::BT <= a.T && o0 + Full::BO <= a.m && a.n % kMmK == 0) Full(a, lds, t0, o0, part).run();
+  else Any(a, reinterpret_cast<typename Any::Lds&>(lds), t0, o0, part).run();
+}
+
+// Parts of the long axis, added in order.  W: outputs per thread.
+template <int W>
+__global__ __launch_bounds__(kMxThreads) void mm_join_kernel(MmArgs a) {
+  const int64_t per = a.m / W, i = (int64_t)blockIdx.x * kMxThreads + threadIdx.x;
+  if (i >= a.T * per) return;
+  const int64_t t = i / per, o = (i - t * per) * W, step = a.T * a.m;
+  const float* p = a.part + t * a.m + o;
+  if constexpr (W == 4) {
+    mxf4 v = *reinterpret_cast<const mxf4*>(p);
+    for (int s = 1; s < a.splits; ++s) v += *reinterpret_cast<const mxf4*>(p + s * step);
+    mm_store4(a.y, a.yt, t * a.ldy + o, v, 4, a.wide);
+  } else {
+    float v = *p;
+    for (int s = 1; s < a.splits; ++s) v += p[s * step];
+    mm_store(a.y, a.yt, t * a.ldy + o, v);
   }
 }
 
-template <int WT, int WO, int TT, int TO>
-hipError_t mm_tiles(MmArgs a, hipStream_t s) {
-  constexpr int BT = 16 * TT * WT, BO = 16 * TO * WO;
-  a.gt = (int)((a.T + BT - 1) / BT);
-  a.go = (int)((a.m + BO - 1) / BO);
-  const int64_t total = (int64_t)a.gt * a.go;
-  a.per_xcd = (total + 7) / 8;
-  a.band = 4;
-  mm_tile_kernel<WT, WO, TT, TO><<<dim3((unsigned)(8 * a.per_xcd)), 64 * WT * WO, 0, s>>>(a);
+hipError_t mm_join(const MmArgs& a, hipStream_t s) {
+  const int64_t n = a.T * (a.m % 4 ? a.m : a.m / 4);
+  const dim3 grid((unsigned)((n + kMxThreads - 1) / kMxThreads));
+  if (a.m % 4) mm_join_kernel<1><<<grid, kMxThreads, 0, s>>>(a);
+  else mm_join_kernel<4><<<grid, kMxThreads, 0, s>>>(a);
   return hipGetLastError();
+}
+
+template <int WT, int WO, int TT, int TO>
+hipError_t mm_tiles(const MmArgs& a, hipStream_t s) {
+  constexpr int BT = 32 * TT * WT, BO = 32 * TO * WO;
+  static_assert(BT == BO && (BT == 128 || BT == 256), "mm_plan's tiles");
+  const int runs = (a.stages + kMmRun - 1) / kMmRun;
+  mm_scales_kernel<BT, BO><<<dim3((unsigned)(a.gt + a.go), (unsigned)runs), kMxThreads, 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  mm_tile_kernel<WT, WO, TT, TO><<<dim3((unsigned)(8 * a.per_xcd)), 64 * WT * WO, 0, s>>>(a);
+  e = hipGetLastError();
+  return e != hipSuccess || a.splits == 1 ? e : mm_join(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t s) {
-  if (a.n >= kMmK && a.T > 16 && a.n <= (1 << 23)) {
-    if (a.T > 512 && a.m > 512) return mm_tiles<2, 2, 8, 8>(a, s);
-    return mm_tiles<2, 2, 4, 4>(a, s);
-  }
+  if (a.tile == 256) return mm_tiles<2, 2, 4, 4>(a, s);
+  if (a.tile == 128) return mm_tiles<2, 2, 2, 2>(a, s);
   const dim3 grid((unsigned)((a.m + 15) / 16), (unsigned)((a.T + 15) / 16));
   mm_simple_kernel<<<grid, 64, 0, s>>>(a);
   return hipGetLastError();
