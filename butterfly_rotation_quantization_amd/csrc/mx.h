@@ -74,7 +74,7 @@ constexpr int kMmK = 256;  // values of a row per stage
 inline size_t mm_plan(MmArgs& a, uint8_t* ws) {
   a.tile = 0;
   a.splits = 1;
-  if (a.n < kMmK || a.T <= 16 || a.n > (1 << 23)) return 0;
+  if (a.n < kMmK || a.T <= 64 || a.n > (1 << 23)) return 0;
   auto tiles = [&](int64_t t) { return ((a.T + t - 1) / t) * ((a.m + t - 1) / t); };
   // One 256 x 256 tile per compute unit at a time, two of 128 x 128; such a
   // pair takes about 2/3 of a large tile's time for half its work.

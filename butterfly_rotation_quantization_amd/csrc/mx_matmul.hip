@@ -43,6 +43,104 @@ __global__ __launch_bounds__(64) void mm_simple_kernel(MmArgs a) {
 }
 
 
+// ---- few tokens: a stream over the weight
+
+constexpr int kMmWaves = 8;      // wavefronts of a workgroup, which share its rows
+constexpr int kMmChunk = 512;    // values of a row a wavefront takes at a time
+
+// 512 values of 16 rows: lane l holds blocks 4 s + l / 16 of row l % 16.
+struct MmChunk {
+  mxi4 c[4];
+  uint4 s;  // the 16 scales of the row
+};
+// row: the lane's row of codes at its block l / 16; srow: of scales.  k: the
+// chunk's first block, nb: blocks of a row.  Past the end of a row: zeros.
+__device__ __forceinline__ void mm_chunk(MmChunk& f, const uint8_t* row, const uint8_t* srow, int64_t k, int64_t nb,
+                                         int lg) {
+  if (k + kMmChunk / kMxBlock <= nb) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) f.c[s] = *reinterpret_cast<const mxi4*>(row + (k + 4 * s) * 16);
+    __builtin_memcpy(&f.s, srow + k, 16);
+  } else {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      f.c[s] = mxi4{0, 0, 0, 0};
+      const int64_t b = k + 4 * s + lg;
+      if (b < nb) {
+        f.c[s] = *reinterpret_cast<const mxi4*>(row + (k + 4 * s) * 16);
+        w[s] = (uint32_t)srow[b] << (8 * lg);
+      }
+    }
+    f.s = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+// The scale of step s for this lane, in the lowest byte.
+__device__ __forceinline__ int mm_scale_of(const uint4& v, int s, int sh) {
+  const uint32_t w = s == 0 ? v.x : s == 1 ? v.y : s == 2 ? v.z : v.w;
+  return (int)(w >> sh);
+}
+
+// 16 outputs, up to 16 TT tokens.  The workgroup's wavefronts take chunks of
+// its weight rows in turn, 2 KB of each row in flight at a time, and join
+// their sums in LDS: the weight is read once, in one launch.
+template <int TT>
+__global__ __launch_bounds__(64 * kMmWaves) void mm_rows_kernel(MmArgs a) {
+  __shared__ float sums[kMmWaves][TT][16][17];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lr = lane & 15, lg = lane >> 4, sh = 8 * lg;
+  const int64_t o0 = (int64_t)blockIdx.x * 16, nb = a.n / kMxBlock;
+  const int64_t o = o0 + lr < a.m ? o0 + lr : a.m - 1;  // rows past the end: the last one, not stored
+  const uint8_t* wrow = a.b + (o * nb + lg) * 16;
+  const uint8_t* wsrow = a.bs + o * nb;
+  const uint8_t *xrow[TT], *xsrow[TT];
+#pragma unroll
+  for (int j = 0; j < TT; ++j) {
+    const int64_t t = 16 * j + lr < a.T ? 16 * j + lr : a.T - 1;
+    xrow[j] = a.a + (t * nb + lg) * 16;
+    xsrow[j] = a.as + t * nb;
+  }
+  mxf4 acc[TT];
+#pragma unroll
+  for (int j = 0; j < TT; ++j) acc[j] = mxf4{0.f, 0.f, 0.f, 0.f};
+  constexpr int B = kMmChunk / kMxBlock;
+  MmChunk w, x[TT];
+  int64_t k = (int64_t)wave * B;
+  if (k < nb) mm_chunk(w, wrow, wsrow, k, nb, lg);
+  while (k < nb) {
+    const int64_t next = k + kMmWaves * B;
+    MmChunk wn;
+#pragma unroll
+    for (int j = 0; j < TT; ++j) mm_chunk(x[j], xrow[j], xsrow[j], k, nb, lg);
+    if (next < nb) mm_chunk(wn, wrow, wsrow, next, nb, lg);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const mxi8 W = {w.c[s][0], w.c[s][1], w.c[s][2], w.c[s][3], 0, 0, 0, 0};
+      const int sw = mm_scale_of(w.s, s, sh);
+#pragma unroll
+      for (int j = 0; j < TT; ++j) {
+        const mxi8 X = {x[j].c[s][0], x[j].c[s][1], x[j].c[s][2], x[j].c[s][3], 0, 0, 0, 0};
+        acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(W, X, acc[j], 4, 4, 0, sw, 0,
+                                                                  mm_scale_of(x[j].s, s, sh));
+      }
+    }
+    w = wn;
+    k = next;
+  }
+#pragma unroll
+  for (int j = 0; j < TT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[wave][j][lr][4 * lg + i] = acc[j][i];  // token lr, output 4 lg + i
+  __syncthreads();
+  for (int e = tid; e < 256 * TT; e += 64 * kMmWaves) {
+    const int j = e >> 8, t = (e >> 4) & 15, c = e & 15;
+    float v = sums[0][j][t][c];
+#pragma unroll
+    for (int u = 1; u < kMmWaves; ++u) v += sums[u][j][t][c];
+    if (16 * j + t < a.T && o0 + c < a.m) mm_store(a.y, a.yt, (16 * j + t) * a.ldy + o0 + c, v);
+  }
+}
+
 // ---- tiles through LDS
 
 // c += a b with byte SA of sa and SB of sb as the scales; c stays in the
@@ -186,7 +284,6 @@ struct MmTile {
   static constexpr int NTH = 64 * WT * WO;
   static constexpr int BT = 32 * TT * WT, BO = 32 * TO * WO, ROWS = BT + BO;
   static constexpr int NL = ROWS * (kMmKB / 16) / NTH;  // 16-byte pieces per thread and stage
-  static constexpr int NL1 = NL * 3 / 4;                // of them, fetched in a stage's second step
   static constexpr int RS = NTH / 8;                    // rows between a thread's pieces
   static constexpr int NTT = BT / 32, NTO = BO / 32;
   static constexpr int NM = 2 * TT * TO;                // products of a step
@@ -303,44 +400,59 @@ struct MmTile {
     }
   }
 
-  // One step of 128 values: the products of f, and between them, a few
-  // instructions at a time so that the matrix unit is never left waiting for
-  // this wavefront's next issue, the reads of g (step K2G of buffer BG) and,
-  // the pieces of a later stage into buffer BF.
-  template <int BG, int K2G, bool FETCH, int BF, int X>
-  __device__ __forceinline__ void step(const Frag& f, Frag& g, Source& src) {
+  // A stage's first step: the products of f, and spread between them, so that
+  // the matrix unit is not left waiting for this wavefront's next issue, the
+  // reads of g, the operands of the second step.
+  template <int BUF, int X>
+  __device__ __forceinline__ void first_step(const Frag& f, Frag& g) {
     if constexpr (X < NM) {
-      // reads are spread evenly over the products; of the pieces three
-      // quarters go into the second step and the rest into the first half of
-      // the next stage's first step (FETCH false)
       constexpr int e0 = X * NG / NM, e1 = (X + 1) * NG / NM;
-      constexpr int n = FETCH ? NL1 : NL - NL1, len = FETCH ? NM : NM / 2;
-      constexpr int x0 = X < len ? X : len, x1 = X + 1 < len ? X + 1 : len;
-      constexpr int j0 = (FETCH ? 0 : NL1) + x0 * n / len, j1 = (FETCH ? 0 : NL1) + x1 * n / len;
-      constexpr int u = X / (TT * TO), i = X % (TT * TO) / TT, j = X % TT;
-      mm_step(f.w[u][i], f.x[u][j], acc[i][j], f.ws[u], i, f.xs[u], j);
-      if constexpr (e1 > e0) read<e0>(g, BG, K2G);
-      if constexpr (e1 > e0 + 1) read<e0 + 1>(g, BG, K2G);
+      multiply<X>(f);
+      if constexpr (e1 > e0) read<e0>(g, BUF, 1);
+      if constexpr (e1 > e0 + 1) read<e0 + 1>(g, BUF, 1);
+      static_assert(e1 <= e0 + 2, "reads per product");
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (j1 > j0) fetch<BF, j0>(src);
-      if constexpr (j1 > j0 + 1) fetch<BF, j0 + 1>(src);
-      static_assert(j1 <= j0 + 2 && e1 <= e0 + 2, "pieces and reads per product");
-      __builtin_amdgcn_sched_barrier(0);
-      step<BG, K2G, FETCH, BF, X + 1>(f, g, src);
+      first_step<BUF, X + 1>(f, g);
     }
+  }
+  // Its second step: the products of g; between them, the pieces of the stage
+  // after next into buffer BUF; half way, once the next stage has arrived (all
+  // but this step's fetches so far), the reads of f, the operands of its first
+  // step.  Waiting this late leaves a fetch 3/4 of a stage at least (half
+  // way through the stage, with the reads spread over the step: 488 us where
+  // this took 473 at 4096x8192x28672).
+  template <int BUF, int X>
+  __device__ __forceinline__ void second_step(const Frag& g, Frag& f, Source& src) {
+    if constexpr (X < NM) {
+      constexpr int H = NM / 2, Y = X < H ? 0 : X - H;
+      constexpr int e0 = Y * NG / H, e1 = X < H ? 0 : (Y + 1) * NG / H;
+      constexpr int j0 = X * NL / NM, j1 = (X + 1) * NL / NM;
+      if constexpr (X == H) {
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(1 + NL / 2) : "memory");
+        __syncthreads();
+        read_scales(f, BUF ^ 1, 0);
+      }
+      multiply<X>(g);
+      if constexpr (e1 > e0) read<e0>(f, BUF ^ 1, 0);
+      if constexpr (e1 > e0 + 1) read<e0 + 1>(f, BUF ^ 1, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (j1 > j0) fetch<BUF, j0>(src);
+      if constexpr (j1 > j0 + 1) fetch<BUF, j0 + 1>(src);
+      static_assert(j1 <= j0 + 2 && e1 <= e0 + 2 && NL % 2 == 0, "pieces and reads per product");
+      __builtin_amdgcn_sched_barrier(0);
+      second_step<BUF, X + 1>(g, f, src);
+    }
+  }
+  template <int X>
+  __device__ __forceinline__ void multiply(const Frag& f) {
+    constexpr int u = X / (TT * TO), i = X % (TT * TO) / TT, j = X % TT;
+    mm_step(f.w[u][i], f.x[u][j], acc[i][j], f.ws[u], i, f.xs[u], j);
   }
   template <int BUF, int J>
   __device__ __forceinline__ void fetch_all(Source& f) const {
     if constexpr (J < NL) {
       fetch<BUF, J>(f);
       fetch_all<BUF, J + 1>(f);
-    }
-  }
-  template <int BUF, int J>
-  __device__ __forceinline__ void fetch_some(Source& f) const {
-    if constexpr (J < NL1) {
-      fetch<BUF, J>(f);
-      fetch_some<BUF, J + 1>(f);
     }
   }
   template <int E>
@@ -351,22 +463,18 @@ struct MmTile {
     }
   }
 
-  // Stage s, in buffer BUF.  Its first step multiplies while its second step's
-  // operands come from LDS; then, once every wavefront has them and stage
-  // s + 1 has arrived, the second step multiplies while stage s + 2 is fetched
-  // over stage s and the first operands of stage s + 1 are read.
+  // Stage s, in buffer BUF, which is free for stage s + 2 once every wavefront
+  // has its second step's operands.
   template <int BUF>
   __device__ __forceinline__ void stage(int s, Frag& f0, Frag& f1, Source& src) {
     read_scales(f1, BUF, 1);
     __builtin_amdgcn_sched_barrier(0);
-    step<BUF, 1, false, BUF ^ 1, 0>(f0, f1, src);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    first_step<BUF, 0>(f0, f1);
     __syncthreads();
     src = source(s + 2);
     fetch_scales<BUF>(s + 2);
-    read_scales(f0, BUF ^ 1, 0);
     __builtin_amdgcn_sched_barrier(0);
-    step<BUF ^ 1, 0, true, BUF, 0>(f1, f0, src);
+    second_step<BUF, 0>(f1, f0, src);
   }
 
   __device__ __forceinline__ void run() {
@@ -379,14 +487,14 @@ struct MmTile {
     Source src = source(0);
     fetch_all<0, 0>(src);
     fetch_scales<0>(0);
-    fetch_scales<1>(1);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     Frag f0, f1;
     read_scales(f0, 0, 0);
     read_all<0>(f0, 0, 0);
     src = source(1);
-    fetch_some<1, 0>(src);
+    fetch_scales<1>(1);
+    fetch_all<1, 0>(src);
     int s = 0;
     for (; s + 1 < stages; s += 2) {
       stage<0>(s, f0, f1, src);
@@ -493,6 +601,19 @@ hipError_t mm_tiles(const MmArgs& a, hipStream_t s) {
 hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t s) {
   if (a.tile == 256) return mm_tiles<2, 2, 4, 4>(a, s);
   if (a.tile == 128) return mm_tiles<2, 2, 2, 2>(a, s);
+  const dim3 rows((unsigned)((a.m + 15) / 16));
+  if (a.T <= 16) {
+    mm_rows_kernel<1><<<rows, 64 * kMmWaves, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  if (a.T <= 32) {
+    mm_rows_kernel<2><<<rows, 64 * kMmWaves, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  if (a.T <= 64) {
+    mm_rows_kernel<4><<<rows, 64 * kMmWaves, 0, s>>>(a);
+    return hipGetLastError();
+  }
   const dim3 grid((unsigned)((a.m + 15) / 16), (unsigned)((a.T + 15) / 16));
   mm_simple_kernel<<<grid, 64, 0, s>>>(a);
   return hipGetLastError();
