@@ -81,64 +81,92 @@ __device__ __forceinline__ int mm_scale_of(const uint4& v, int s, int sh) {
   return (int)(w >> sh);
 }
 
-// 16 outputs, up to 16 TT tokens.  The workgroup's wavefronts take chunks of
-// its weight rows in turn, 2 KB of each row in flight at a time, and join
-// their sums in LDS: the weight is read once, in one launch.
-template <int TT>
+// 16 RT outputs, up to 16 TT tokens.  The workgroup's wavefronts take chunks
+// of its weight rows in turn, 2 KB of each row in flight at a time, and join
+// their sums in LDS: the weight is read once, in one launch.  Bound by memory:
+// one token at 8192x28672 24 us, 5.2 TB/s of the weight.
+template <int TT, int RT>
 __global__ __launch_bounds__(64 * kMmWaves) void mm_rows_kernel(MmArgs a) {
-  __shared__ float sums[kMmWaves][TT][16][17];
+  __shared__ float sums[kMmWaves][RT][TT][16][17];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lg = lane >> 4, sh = 8 * lg;
-  const int64_t o0 = (int64_t)blockIdx.x * 16, nb = a.n / kMxBlock;
-  const int64_t o = o0 + lr < a.m ? o0 + lr : a.m - 1;  // rows past the end: the last one, not stored
-  const uint8_t* wrow = a.b + (o * nb + lg) * 16;
-  const uint8_t* wsrow = a.bs + o * nb;
-  const uint8_t *xrow[TT], *xsrow[TT];
+  const int64_t o0 = (int64_t)blockIdx.x * (16 * RT), nb = a.n / kMxBlock;
+  const uint8_t *wrow[RT], *wsrow[RT], *xrow[TT], *xsrow[TT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {  // rows past the end: the last one, not stored
+    const int64_t o = o0 + 16 * i + lr < a.m ? o0 + 16 * i + lr : a.m - 1;
+    wrow[i] = a.b + (o * nb + lg) * 16;
+    wsrow[i] = a.bs + o * nb;
+  }
 #pragma unroll
   for (int j = 0; j < TT; ++j) {
     const int64_t t = 16 * j + lr < a.T ? 16 * j + lr : a.T - 1;
     xrow[j] = a.a + (t * nb + lg) * 16;
     xsrow[j] = a.as + t * nb;
   }
-  mxf4 acc[TT];
+  mxf4 acc[RT][TT];
 #pragma unroll
-  for (int j = 0; j < TT; ++j) acc[j] = mxf4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < TT; ++j) acc[i][j] = mxf4{0.f, 0.f, 0.f, 0.f};
   constexpr int B = kMmChunk / kMxBlock;
-  MmChunk w, x[TT];
+  MmChunk w[RT], x[TT];
   int64_t k = (int64_t)wave * B;
-  if (k < nb) mm_chunk(w, wrow, wsrow, k, nb, lg);
+  if (k < nb)
+#pragma unroll
+    for (int i = 0; i < RT; ++i) mm_chunk(w[i], wrow[i], wsrow[i], k, nb, lg);
   while (k < nb) {
     const int64_t next = k + kMmWaves * B;
-    MmChunk wn;
+    MmChunk wn[RT];
 #pragma unroll
     for (int j = 0; j < TT; ++j) mm_chunk(x[j], xrow[j], xsrow[j], k, nb, lg);
-    if (next < nb) mm_chunk(wn, wrow, wsrow, next, nb, lg);
+    if (next < nb)
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const mxi8 W = {w.c[s][0], w.c[s][1], w.c[s][2], w.c[s][3], 0, 0, 0, 0};
-      const int sw = mm_scale_of(w.s, s, sh);
+      for (int i = 0; i < RT; ++i) mm_chunk(wn[i], wrow[i], wsrow[i], next, nb, lg);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
       for (int j = 0; j < TT; ++j) {
         const mxi8 X = {x[j].c[s][0], x[j].c[s][1], x[j].c[s][2], x[j].c[s][3], 0, 0, 0, 0};
-        acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(W, X, acc[j], 4, 4, 0, sw, 0,
-                                                                  mm_scale_of(x[j].s, s, sh));
+        const int sx = mm_scale_of(x[j].s, s, sh);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const mxi8 W = {w[i].c[s][0], w[i].c[s][1], w[i].c[s][2], w[i].c[s][3], 0, 0, 0, 0};
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(W, X, acc[i][j], 4, 4, 0,
+                                                                       mm_scale_of(w[i].s, s, sh), 0, sx);
+        }
       }
-    }
-    w = wn;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) w[i] = wn[i];
     k = next;
   }
 #pragma unroll
-  for (int j = 0; j < TT; ++j)
+  for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sums[wave][j][lr][4 * lg + i] = acc[j][i];  // token lr, output 4 lg + i
+    for (int j = 0; j < TT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sums[wave][i][j][lr][4 * lg + e] = acc[i][j][e];  // token lr, output 4 lg + e
   __syncthreads();
-  for (int e = tid; e < 256 * TT; e += 64 * kMmWaves) {
-    const int j = e >> 8, t = (e >> 4) & 15, c = e & 15;
-    float v = sums[0][j][t][c];
+  for (int e = tid; e < 256 * TT * RT; e += 64 * kMmWaves) {
+    const int c = e & 15, i = (e >> 4) % RT, t = (e >> 4) / RT, j = t >> 4;  // a token's outputs on consecutive lanes
+    float v = sums[0][i][j][t & 15][c];
 #pragma unroll
-    for (int u = 1; u < kMmWaves; ++u) v += sums[u][j][t][c];
-    if (16 * j + t < a.T && o0 + c < a.m) mm_store(a.y, a.yt, (16 * j + t) * a.ldy + o0 + c, v);
+    for (int u = 1; u < kMmWaves; ++u) v += sums[u][i][j][t & 15][c];
+    const int64_t o = o0 + 16 * i + c;
+    if (t < a.T && o < a.m) mm_store(a.y, a.yt, t * a.ldy + o, v);
   }
+}
+
+template <int TT>
+hipError_t mm_rows(const MmArgs& a, hipStream_t s) {
+  // 32 rows to a workgroup where that still gives every compute unit one: the
+  // activations are read half as often (8192x28672: 16 tokens 37 -> 30 us, 64
+  // tokens 83 -> 53 us).
+  const bool two = a.m >= 32 * 256;
+  const dim3 grid((unsigned)((a.m + (two ? 31 : 15)) / (two ? 32 : 16)));
+  if (two) mm_rows_kernel<TT, 2><<<grid, 64 * kMmWaves, 0, s>>>(a);
+  else mm_rows_kernel<TT, 1><<<grid, 64 * kMmWaves, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 // ---- tiles through LDS
@@ -601,19 +629,9 @@ hipError_t mm_tiles(const MmArgs& a, hipStream_t s) {
 hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t s) {
   if (a.tile == 256) return mm_tiles<2, 2, 4, 4>(a, s);
   if (a.tile == 128) return mm_tiles<2, 2, 2, 2>(a, s);
-  const dim3 rows((unsigned)((a.m + 15) / 16));
-  if (a.T <= 16) {
-    mm_rows_kernel<1><<<rows, 64 * kMmWaves, 0, s>>>(a);
-    return hipGetLastError();
-  }
-  if (a.T <= 32) {
-    mm_rows_kernel<2><<<rows, 64 * kMmWaves, 0, s>>>(a);
-    return hipGetLastError();
-  }
-  if (a.T <= 64) {
-    mm_rows_kernel<4><<<rows, 64 * kMmWaves, 0, s>>>(a);
-    return hipGetLastError();
-  }
+  if (a.T <= 16) return mm_rows<1>(a, s);
+  if (a.T <= 32) return mm_rows<2>(a, s);
+  if (a.T <= 64) return mm_rows<4>(a, s);
   const dim3 grid((unsigned)((a.m + 15) / 16), (unsigned)((a.T + 15) / 16));
   mm_simple_kernel<<<grid, 64, 0, s>>>(a);
   return hipGetLastError();
