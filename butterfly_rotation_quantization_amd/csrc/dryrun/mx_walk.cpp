@@ -84,8 +84,40 @@ hipError_t launch_paged_attention(const AtArgs& a, hipStream_t) {
   const KvPage& pg = a.pg;
   const int D = pg.D;
   if ((1 << a.lgP) != pg.P || a.group * a.heads != a.q_heads || a.ht * a.nt * kAtCols < a.group ||
-      (int64_t)a.cap > a.ldt << a.lgP || a.cap > kAtMaxKeys || a.splits < 1 || (a.splits > 1 && !a.part))
-    return bad("attention geometry (group %lld, splits %lld)", a.group, a.splits);
+      (int64_t)a.cap > a.ldt << a.lgP || a.cap > kAtMaxKeys || a.wgs < 0 || (a.wgs > 0 && !a.part))
+    return bad("attention geometry (group %lld, workgroups %lld)", a.group, a.wgs);
+  // the deal of tiles to workgroups for some lengths: every part has a slot of
+  // its own, and the join finds the workgroups that have one
+  for (int seed = 0; a.wgs && a.batch <= 64 && seed < 6; ++seed) {
+    std::vector<int> tiles;
+    int64_t total = 0, units = (int64_t)a.heads * a.ht;
+    for (int64_t b = 0; b < a.batch; ++b) {
+      const int64_t n = seed == 0 ? 0 : seed == 1 ? a.cap : (b * 7919 + seed * 104729) % (a.cap + 1) >> (seed * b % 5);
+      tiles.push_back(at_tiles((int)n, seed == 3 ? 100 : 0));
+      total += tiles.back() * units;
+    }
+    if (!total) continue;
+    const int wgs = at_dealt(total, a.wgs);
+    std::vector<int> owner, uses(2 * (size_t)wgs, 0);
+    for (int w = 0; w < wgs; ++w)
+      for (int64_t g = at_start(w, total, wgs); g < at_start(w + 1, total, wgs); ++g) owner.push_back(w);
+    if ((int64_t)owner.size() != total || at_start(wgs, total, wgs) != total)
+      return bad("attention deal of %lld tiles covers %lld", total, owner.size());
+    int64_t g0 = 0;
+    for (int64_t b = 0; b < a.batch; ++b)
+      for (int64_t u = 0; u < units && tiles[(size_t)b]; ++u, g0 += tiles[(size_t)b]) {
+        const int64_t g1 = g0 + tiles[(size_t)b] - 1;
+        if (at_owner(g0, total, wgs) != owner[(size_t)g0] || at_owner(g1, total, wgs) != owner[(size_t)g1])
+          return bad("attention owner of tile %lld of %lld", g0, total);
+        int last = -1;
+        for (int64_t g = g0; owner[(size_t)g0] != owner[(size_t)g1] && g <= g1; ++g)
+          if (owner[(size_t)g] != last) {
+            last = owner[(size_t)g];
+            if (uses[(size_t)at_slot(last, g0, total, wgs)]++)
+              return bad("attention slot of workgroup %lld used twice (tile %lld)", last, g);
+          }
+      }
+  }
   // the wide loads of 16 keys at every place of a page
   for (int p = 0; p < pg.P; p += 16)
     for (int lane = 0; lane < 64; ++lane) {

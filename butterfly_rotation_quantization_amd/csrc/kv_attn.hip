@@ -74,10 +74,24 @@ __device__ __forceinline__ int at_length(const AtArgs& a, int64_t b) {
   return n < 0 ? 0 : (n < a.cap ? n : a.cap);
 }
 
-// One workgroup: the query heads of one column group, one part of one
-// sequence's keys; its wavefronts take 32 keys at a time in turn.
+// Sum over the workgroup's threads (every thread gets it); scratch: one value
+// per wavefront.
+__device__ __forceinline__ int64_t at_block_sum(int64_t x, int64_t* scratch) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = x;
+  __syncthreads();
+  int64_t s = 0;
+#pragma unroll
+  for (int w = 0; w < kAtWaves; ++w) s += scratch[w];
+  return s;
+}
+
+// One workgroup: its share of the tiles of all units (or, without a deal, the
+// unit of its number); its wavefronts take 32 keys at a time in turn.
 template <int D, int NT>
-__global__ __launch_bounds__(kAtThreads) void at_kernel(AtArgs a) {
+__global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_kernel(AtArgs a) {
   constexpr int KW = D / 32;          // words of codes a lane holds per key (of the scores) or four keys (values)
   constexpr int NS = D / 32;          // matrix steps of a score
   constexpr int R = D / 16;           // dimensions of a run = output tiles
@@ -86,24 +100,84 @@ __global__ __launch_bounds__(kAtThreads) void at_kernel(AtArgs a) {
   constexpr int LPH = D / kMxPerLane; // lanes of a head's row
   __shared__ float os[kAtWaves][H][LD];
   __shared__ float ms[kAtWaves][H], ls[kAtWaves][H];
+  __shared__ int64_t sums[kAtWaves];
+  __shared__ int found[1];
+  __shared__ int64_t found_base[1];
   float (*qs)[LD] = os[0];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c = lane & 15, g = lane >> 4;
-  const uint32_t unit = blockIdx.x / (uint32_t)a.splits;
-  const int sp = (int)(blockIdx.x - unit * (uint32_t)a.splits);
-  const uint32_t bh = unit / (uint32_t)a.ht;
-  const int h0 = (int)(unit - bh * (uint32_t)a.ht) * H;  // first query head within the group
-  const int64_t b = bh / (uint32_t)a.heads;
-  const int h = (int)(bh - (uint32_t)b * (uint32_t)a.heads);
-
-  // the part's keys
+  const int units = a.heads * a.ht;   // of a sequence
+  int64_t total = 0, pos = 0, end = 0, base = 0;  // tiles: all, this workgroup's, before sequence b
+  int64_t b = 0;
+  int wgs = 0;
+  if (a.wgs) {
+    int64_t mine = 0;
+    for (int64_t i = tid; i < a.batch; i += kAtThreads) mine += at_tiles(at_length(a, i), a.window);
+    total = at_block_sum(mine, sums) * units;
+    wgs = at_dealt(total, a.wgs);
+    if ((int)blockIdx.x >= wgs) return;
+    pos = at_start(blockIdx.x, total, wgs);
+    end = at_start((int64_t)blockIdx.x + 1, total, wgs);
+    // the sequence that has tile pos
+    for (int64_t i0 = 0;; i0 += kAtThreads) {
+      const int64_t i = i0 + tid;
+      const int64_t n = i < a.batch ? (int64_t)at_tiles(at_length(a, i), a.window) * units : 0;
+      int64_t x = n;  // inclusive sum over the threads before
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int64_t y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+      }
+      __syncthreads();
+      if (lane == 63) sums[wave] = x;
+      __syncthreads();
+      int64_t all = 0;
+#pragma unroll
+      for (int w = 0; w < kAtWaves; ++w) {
+        if (w < wave) x += sums[w];
+        all += sums[w];
+      }
+      if (pos >= base + x - n && pos < base + x) {
+        found[0] = (int)i;
+        found_base[0] = base + x - n;
+      }
+      __syncthreads();
+      if (pos < base + all) break;  // it is one of these: pos < total
+      base += all;
+    }
+    b = found[0];
+    base = found_base[0];
+  } else {
+    b = blockIdx.x / (uint32_t)units;
+    const int tiles = at_tiles(at_length(a, b), a.window);
+    pos = (int64_t)(blockIdx.x - (uint32_t)b * (uint32_t)units) * tiles;
+    end = pos + tiles;
+    if (pos == end) {  // no key: the unit's rows get what an empty sum gives
+      const int u = (int)(blockIdx.x - (uint32_t)b * (uint32_t)units);
+      for (int r = tid / LPH; r < H; r += kAtThreads / LPH) {
+        const int in = u % a.ht * H + r;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (in < a.group) at_finish(a, b, u / a.ht * a.group + in, (tid % LPH) * kMxPerLane, lane, v, 0.f, 0.f);
+      }
+      return;
+    }
+  }
+  while (pos < end) {
+  // the part's keys: tiles [tb, te) of unit u of sequence b
   const int n = at_length(a, b);
   const int first = a.window > 0 && n > a.window ? n - a.window : 0;
-  const int s0 = first & ~(kAtKeys - 1);
-  const int tiles = (n - s0 + kAtTile - 1) / kAtTile;
-  const int per = (tiles + a.splits - 1) / a.splits;
-  const int tb = sp * per, te = tb + per < tiles ? tb + per : tiles;
+  const int s0 = at_skip(n, a.window), tiles = at_tiles(n, a.window);
+  if (pos >= base + (int64_t)tiles * units) {  // on to the next sequence (one without keys has no tiles)
+    base += (int64_t)tiles * units;
+    ++b;
+    continue;
+  }
+  const int u = (int)((pos - base) / tiles);
+  const int64_t g0 = base + (int64_t)u * tiles;
+  const int tb = (int)(pos - g0), te = (int)(end - g0 < tiles ? end - g0 : tiles);
+  pos = g0 + te;
+  const int h = u / a.ht, h0 = (u - h * a.ht) * H;  // key-value head; first query head within its group
 
   // queries: rotated, in float32, then as pairs
   for (int r = tid / LPH; r < H; r += kAtThreads / LPH) {
@@ -143,7 +217,7 @@ __global__ __launch_bounds__(kAtThreads) void at_kernel(AtArgs a) {
   const int64_t pbytes = a.pg.bytes();
   for (int tile = tb; tile < te; ++tile) {
     const int k0 = s0 + tile * kAtTile + wave * kAtKeys;
-    if (k0 >= n) break;
+    if (k0 >= n) break;  // only in the last tile
     uint32_t kw[2][KW], vw[2][KW], ks[2][(KW + 3) / 4], vs[2];
     bool ok[2];
 #pragma unroll
@@ -318,55 +392,95 @@ __global__ __launch_bounds__(kAtThreads) void at_kernel(AtArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += os[w][r][e0 + e] * f;
     }
-    if (a.splits == 1) {
+    if (tb == 0 && te == tiles) {
       at_finish(a, b, h * a.group + h0 + r, e0, lane, v, M, L);
     } else {
-      float* p = a.part + ((int64_t)blockIdx.x * H + r) * (D + 4);
+      float* p = a.part + (at_slot(blockIdx.x, g0, total, wgs) * H + r) * (D + 4);
       mx_store8<BRQ_F32>(p, e0, v);
       if (e0 == 0) *reinterpret_cast<float2*>(p + D) = make_float2(M, L);
     }
   }
+  __syncthreads();  // the next part's queries go where these sums were
+  }
 }
 
-// The parts of one query head, added in order.
+// Joins the parts of units that span workgroups, in order, and writes the rows
+// of sequences without keys.  ROWS query heads of one unit to a workgroup;
+// each has G groups of D / 8 lanes, which take its parts in turn and are
+// joined in LDS.
 template <int D>
-__global__ __launch_bounds__(64) void at_join_kernel(AtArgs a) {
+__global__ __launch_bounds__(kAtThreads) void at_join_kernel(AtArgs a, int rows) {
   constexpr int LPH = D / kMxPerLane;
-  const int lane = threadIdx.x;
-  const int H = kAtCols * a.nt;
-  const int64_t row = (int64_t)blockIdx.x * (64 / LPH) + lane / LPH;  // sequence, then query head
-  if (row >= a.batch * a.q_heads) return;
-  const int64_t b = row / a.q_heads;
-  const int head = (int)(row - b * a.q_heads);
-  const int h = head / a.group, in = head - h * a.group;
-  const int64_t unit = (b * a.heads + h) * a.ht + in / H;
-  const int e0 = (lane % LPH) * kMxPerLane;
-  const float* p0 = a.part + (unit * a.splits * H + in % H) * (D + 4);
-  const int64_t step = (int64_t)H * (D + 4);
-  float M = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) M = fmaxf(M, p0[s * step + D]);
-  const float base = M == -INFINITY ? 0.f : M;
-  float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < a.splits; ++s) {
-    const float f = __builtin_amdgcn_exp2f(p0[s * step + D] - base);
-    L += p0[s * step + D + 1] * f;
-    float v[8];
-    mx_load8<BRQ_F32>(p0, s * step + e0, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] += v[e] * f;
+  constexpr int LD = D + 4;
+  __shared__ float os[kAtThreads / LPH][LD];
+  __shared__ int64_t sums[kAtWaves];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int H = kAtCols * a.nt, units = a.heads * a.ht, per = H / rows;
+  const int64_t ub = blockIdx.x / (uint32_t)per;
+  const int r0 = (int)(blockIdx.x - (uint32_t)ub * (uint32_t)per) * rows;
+  const int64_t b = ub / units;
+  const int u = (int)(ub - b * units);
+  const int tiles = at_tiles(at_length(a, b), a.window);
+  const int h = u / a.ht, h0 = (u - h * a.ht) * H;
+  const int r = r0 + tid / LPH % rows, grp = tid / (LPH * rows), groups = kAtThreads / (LPH * rows);
+  const int e0 = (tid % LPH) * kMxPerLane;
+  const bool mine = h0 + r < a.group;
+  int64_t before = 0, all = 0;
+  for (int64_t i = tid; i < a.batch; i += kAtThreads) {
+    const int t = at_tiles(at_length(a, i), a.window);
+    all += t;
+    if (i < b) before += t;
   }
-  at_finish(a, b, head, e0, lane, o, M, L);
+  const int64_t total = at_block_sum(all, sums) * units;
+  const int64_t g0 = at_block_sum(before, sums) * units + (int64_t)u * tiles;
+  float M = -INFINITY, L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (tiles > 0) {
+    const int wgs = at_dealt(total, a.wgs);
+    const int w0 = at_owner(g0, total, wgs), w1 = at_owner(g0 + tiles - 1, total, wgs);
+    if (w0 == w1) return;  // finished by its workgroup
+    for (int w = w0 + grp; w <= w1; w += groups) {
+      const float* p = a.part + (at_slot(w, g0, total, wgs) * H + r) * (int64_t)LD;
+      const float2 ml = *reinterpret_cast<const float2*>(p + D);
+      float v[8];
+      mx_load8<BRQ_F32>(p, e0, v);
+      const float m = fmaxf(M, ml.x), base = m == -INFINITY ? 0.f : m;
+      const float f = __builtin_amdgcn_exp2f(M - base), q = __builtin_amdgcn_exp2f(ml.x - base);
+      M = m;
+      L = L * f + ml.y * q;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = o[e] * f + v[e] * q;
+    }
+  }
+  mx_store8<BRQ_F32>(&os[tid / LPH][0], e0, o);
+  if (e0 == 0) *reinterpret_cast<float2*>(&os[tid / LPH][D]) = make_float2(M, L);
+  __syncthreads();
+  if (grp != 0 || !mine) return;
+  for (int s = 1; s < groups; ++s) {
+    const float* p = os[tid / LPH + s * rows];
+    const float2 ml = *reinterpret_cast<const float2*>(p + D);
+    const float m = fmaxf(M, ml.x), base = m == -INFINITY ? 0.f : m;
+    const float f = __builtin_amdgcn_exp2f(M - base), q = __builtin_amdgcn_exp2f(ml.x - base);
+    M = m;
+    L = L * f + ml.y * q;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = o[e] * f + p[e0 + e] * q;
+  }
+  at_finish(a, b, h * a.group + h0 + r, e0, lane, o, M, L);
 }
 
 template <int D>
 hipError_t at_launch(const AtArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.batch * a.heads * a.ht * a.splits));
+  const int64_t units = a.batch * a.heads * a.ht;
+  const dim3 grid((unsigned)(a.wgs ? a.wgs : units));
   if (a.nt == 1) at_kernel<D, 1><<<grid, kAtThreads, 0, s>>>(a);
   else at_kernel<D, 2><<<grid, kAtThreads, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
-  constexpr int rows = 64 / (D / kMxPerLane);
-  at_join_kernel<D><<<dim3((unsigned)((a.batch * a.q_heads + rows - 1) / rows)), 64, 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.wgs) return e;
+  // few units: each has many parts, and a workgroup for every row; many: most
+  // were finished in one place, and a workgroup looks after several rows
+  const int H = kAtCols * a.nt, most = kAtThreads / (D / kMxPerLane);
+  const int rows = units * H <= 2048 ? 1 : (H < most ? H : most);
+  at_join_kernel<D><<<dim3((unsigned)(units * (H / rows))), kAtThreads, 0, s>>>(a, rows);
   return hipGetLastError();
 }
 

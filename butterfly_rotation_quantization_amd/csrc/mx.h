@@ -74,7 +74,11 @@ constexpr int kMmK = 256;  // values of a row per stage
 inline size_t mm_plan(MmArgs& a, uint8_t* ws) {
   a.tile = 0;
   a.splits = 1;
-  if (a.n < kMmK || a.T <= 64 || a.n > (1 << 23)) return 0;
+  if (a.n < kMmK || a.n > (1 << 23)) return 0;
+  // The stream over the weight up to 64 tokens; above 32 only while the tiles'
+  // three launches weigh more (64 tokens: 8192x28672 stream 53 us, tiles 47;
+  // 16384x8192 35 and 31; 4096x4096 10 and 16).
+  if (a.T <= 32 || (a.T <= 64 && a.m * a.n < ((int64_t)1 << 27))) return 0;
   auto tiles = [&](int64_t t) { return ((a.T + t - 1) / t) * ((a.m + t - 1) / t); };
   // One 256 x 256 tile per compute unit at a time, two of 128 x 128; such a
   // pair takes about 2/3 of a large tile's time for half its work.
@@ -154,11 +158,37 @@ constexpr int kAtCols = 8;        // query heads per 16 matrix columns (each as 
 constexpr int kAtMaxKeys = 1 << 30;
 constexpr int kAtMaxSplits = 64;
 
-// Parts a sequence's keys are split into when there are few sequences and
-// heads: enough workgroups for every compute unit to hold four.
-inline int at_splits(int64_t units) {
-  const int64_t s = units > 0 ? 1024 / units : 1;
-  return (int)(s < 1 ? 1 : (s < kAtMaxSplits ? s : kAtMaxSplits));
+constexpr int kAtMaxBatch = 4096;  // sequences whose tiles are dealt out evenly
+
+// A unit is the group of query heads of one workgroup over one sequence's
+// keys, in tiles of kAtTile keys.  Up to kAtMaxBatch sequences the tiles of
+// all units, in order, are dealt out evenly to a fixed number of workgroups
+// that the chip holds at once, whatever the lengths: workgroup w takes tiles
+// [at_start(w), at_start(w + 1)).  A unit within one workgroup is finished
+// there; the parts of the others go to the workspace, two slots a workgroup
+// (a part that begins its range, one that ends it), and are joined in order.
+// Workgroups that get tiles: no more than there are tiles, so each has one.
+__host__ __device__ inline int at_dealt(int64_t total, int wgs) { return total < wgs ? (int)total : wgs; }
+__host__ __device__ inline int64_t at_start(int64_t w, int64_t total, int wgs) { return w * total / wgs; }
+// The workgroup that has tile g.
+__host__ __device__ inline int at_owner(int64_t g, int64_t total, int wgs) {
+  return (int)(((g + 1) * wgs - 1) / total);
+}
+// Slot of the part that workgroup w has of a unit beginning at tile g0.
+__host__ __device__ inline int64_t at_slot(int64_t w, int64_t g0, int64_t total, int wgs) {
+  return 2 * w + (at_start(w, total, wgs) < g0 ? 1 : 0);
+}
+// Keys before the first tile of n keys with a window, and their tiles.
+__host__ __device__ inline int at_skip(int n, int window) {
+  return window > 0 && n > window ? (n - window) & ~(kAtKeys - 1) : 0;
+}
+__host__ __device__ inline int at_tiles(int n, int window) {
+  return (n - at_skip(n, window) + kAtTile - 1) / kAtTile;
+}
+// Workgroups that the chip holds at once, by the registers of their kernel.
+constexpr int at_workgroups(int head_dim, int nt) {
+  if (head_dim == 256) return nt == 1 ? 512 : 256;
+  return nt == 1 ? 1024 : head_dim == 64 ? 768 : 512;
 }
 
 struct AtArgs {
@@ -186,8 +216,8 @@ struct AtArgs {
   const float* signs;
   int d;
   float rnorm;
-  int splits;            // parts a sequence's keys are split into
-  float* part;           // [unit][splits][nt * kAtCols][D + 4]: o, then m and l
+  int wgs;               // workgroups the tiles are dealt out to (0: one for each unit)
+  float* part;           // [2 wgs][nt * kAtCols][D + 4]: o, then m and l
 };
 
 hipError_t launch_paged_attention(const AtArgs& a, hipStream_t s);

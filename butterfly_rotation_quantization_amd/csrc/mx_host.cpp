@@ -283,9 +283,8 @@ size_t brq_paged_attention_workspace_bytes(int64_t batch, int32_t q_heads, int32
   if (batch <= 0 || heads < 1 || q_heads < heads || q_heads % heads || head_dim < 1) return 0;
   int nt, ht;
   at_shape(q_heads, heads, &nt, &ht);
-  const int64_t units = batch * heads * ht;
-  const int splits = at_splits(units);
-  return splits == 1 ? 0 : (size_t)units * splits * nt * kAtCols * (head_dim + 4) * sizeof(float);
+  if (batch > kAtMaxBatch) return 0;
+  return (size_t)2 * at_workgroups(head_dim, nt) * nt * kAtCols * (head_dim + 4) * sizeof(float);
 }
 
 brq_status brq_paged_attention(const brq_plan* plan, const void* q, int64_t ldq, int32_t qt, const uint8_t* cache,
@@ -342,7 +341,7 @@ brq_status brq_paged_attention(const brq_plan* plan, const void* q, int64_t ldq,
   a.scale = scale;
   a.window = window;
   a.lse = lse;
-  a.splits = at_splits(batch * heads * a.ht);
+  a.wgs = batch <= kAtMaxBatch ? at_workgroups(head_dim, a.nt) : 0;
   a.part = static_cast<float*>(ws);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int tok = prof_begin("paged attention", s);
