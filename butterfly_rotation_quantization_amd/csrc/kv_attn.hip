@@ -68,6 +68,40 @@ __device__ __forceinline__ void at_finish(const AtArgs& a, int64_t b, int head, 
     a.lse[b * a.q_heads + head] = l != 0.0f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
+// A query enters the scores as four 8-bit floating-point pieces, each the
+// rounding of what the ones before it left (4 bits each: together within
+// 2^-17 of its block's largest magnitude), with a scale for each block of 32.
+// The eight values of a lane (its block is four lanes): the pieces' words and
+// scale bytes.
+__device__ __forceinline__ void at_pieces(float (&v)[8], uint2 (&piece)[4], int (&byte)[4]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+  top = max(top, mx_xor<1>(top));
+  top = max(top, mx_xor<2>(top));
+  const int ex = (int)(top >> 23);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    // times 2^(7 - 4 k) of the largest exponent: the first piece lies below
+    // 256, what is left of it below 128; an infinity or a NaN: a NaN scale
+    const int x = ex - 7 - 4 * k;
+    byte[k] = ex == 255 ? 255 : x > 0 ? x : 0;
+    const float inv = __uint_as_float((uint32_t)(254 - (x > 0 ? x : 0)) << 23);
+    const float back = __uint_as_float(x > 0 ? (uint32_t)x << 23 : 0x400000u);
+    int w[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      w[e] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * e] * inv, v[4 * e + 1] * inv, w[e], false);
+      w[e] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * e + 2] * inv, v[4 * e + 3] * inv, w[e], true);
+      v[4 * e] -= __builtin_amdgcn_cvt_f32_fp8(w[e], 0) * back;
+      v[4 * e + 1] -= __builtin_amdgcn_cvt_f32_fp8(w[e], 1) * back;
+      v[4 * e + 2] -= __builtin_amdgcn_cvt_f32_fp8(w[e], 2) * back;
+      v[4 * e + 3] -= __builtin_amdgcn_cvt_f32_fp8(w[e], 3) * back;
+    }
+    piece[k] = make_uint2((uint32_t)w[0], (uint32_t)w[1]);
+  }
+}
+
 // Tokens of sequence b that the table has room for.
 __device__ __forceinline__ int at_length(const AtArgs& a, int64_t b) {
   const int n = a.lens[b];
@@ -93,20 +127,26 @@ __device__ __forceinline__ int64_t at_block_sum(int64_t x, int64_t* scratch) {
 template <int D, int NT>
 __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_kernel(AtArgs a) {
   constexpr int KW = D / 32;          // words of codes a lane holds per key (of the scores) or four keys (values)
-  constexpr int NS = D / 32;          // matrix steps of a score
+  constexpr int NQ = D == 256 ? 2 : 1;  // matrix steps of 128 values of a score
+  constexpr int NP = D == 64 ? 1 : 2;   // products of a step: two of a query's four pieces each (D = 64: all four)
   constexpr int R = D / 16;           // dimensions of a run = output tiles
   constexpr int H = kAtCols * NT;     // query heads
   constexpr int LD = D + 4;
   constexpr int LPH = D / kMxPerLane; // lanes of a head's row
-  __shared__ float os[kAtWaves][H][LD];
+  __shared__ __align__(16) float os[kAtWaves][H][LD];
   __shared__ float ms[kAtWaves][H], ls[kAtWaves][H];
   __shared__ int64_t sums[kAtWaves];
   __shared__ int found[1];
   __shared__ int64_t found_base[1];
-  float (*qs)[LD] = os[0];
+  __shared__ uint8_t qb[H][4][D / 32];
+  uint8_t (*qs)[4][D] = reinterpret_cast<uint8_t (*)[4][D]>(&os[0]);
+  static_assert(sizeof(uint8_t[H][4][D]) <= sizeof(os), "the pieces lie where the sums will");
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
+  const uint32_t low = c < 8 ? 0u : 0xffff0000u;
+  const uint32_t one2 = 0x3f803f80u;
+  const mxb8 ones = __builtin_bit_cast(mxb8, make_uint4(one2, one2, one2, one2));
   const int units = a.heads * a.ht;   // of a sequence
   int64_t total = 0, pos = 0, end = 0, base = 0;  // tiles: all, this workgroup's, before sequence b
   int64_t b = 0;
@@ -179,7 +219,8 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
   pos = g0 + te;
   const int h = u / a.ht, h0 = (u - h * a.ht) * H;  // key-value head; first query head within its group
 
-  // queries: rotated, in float32, then as pairs
+  // queries: rotated, times the scale, in pieces
+  const float sl = a.scale * 1.44269504088896341f;  // scores in units of log2
   for (int r = tid / LPH; r < H; r += kAtThreads / LPH) {
     const int e0 = (tid % LPH) * kMxPerLane;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -188,102 +229,134 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
       if (a.d) mx_rotate(v, a.signs, a.d, a.rnorm, e0, lane);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) qs[r][e0 + e] = v[e];
+    for (int e = 0; e < 8; ++e) v[e] *= sl;
+    uint2 piece[4];
+    int byte[4];
+    at_pieces(v, piece, byte);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      *reinterpret_cast<uint2*>(&qs[r][k][e0]) = piece[k];
+      if ((e0 & 31) == 0) qb[r][k][e0 / 32] = (uint8_t)byte[k];
+    }
   }
   __syncthreads();
-  const float sl = a.scale * 1.44269504088896341f;  // scores in units of log2
-  mxb8 qf[NT][NS];
+  // The B operand: column c < 8 holds pieces 1 and 3 of query head c, column
+  // c + 8 its pieces 2 and 4; product w takes the first or the second.  A
+  // lane's words hold dimensions 16 g .. + 15 and 64 + 16 g .. + 15 of a step,
+  // and its scale is that of block g.  With D = 64 one product takes all: the
+  // second half of the words repeats dimensions 16 g .. with pieces 3 and 4,
+  // as the keys' lanes repeat theirs.
+  mxi8 qf[NT][NQ][NP];
+  int qsc[NT][NQ][NP];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
+    for (int e = 0; e < NQ; ++e)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = qs[8 * t + (c & 7)][g * (D / 4) + 8 * s + j] * sl;
-        const __bf16 hi = (__bf16)x;
-        qf[t][s][j] = c < 8 ? hi : (__bf16)(x - (float)hi);
+      for (int w = 0; w < NP; ++w) {
+        const int r = 8 * t + (c & 7), k = (c >> 3) + 2 * w;
+        const mxi4 x = *reinterpret_cast<const mxi4*>(&qs[r][k][128 * e + 16 * g]);
+        const mxi4 y = D == 64 ? *reinterpret_cast<const mxi4*>(&qs[r][k + 2][16 * g])
+                               : *reinterpret_cast<const mxi4*>(&qs[r][k][128 * e + 64 + 16 * g]);
+        qf[t][e][w] = mxi8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+        qsc[t][e][w] = D == 64 ? qb[r][k + 2 * (g >> 1)][g & 1] : qb[r][k][4 * e + g];
       }
   __syncthreads();
 
-  mxf4 o[NT][R];
-  float m[NT], l[NT];
+  mxf4 o[NT][R], l[NT];
+  float m[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     m[t] = -INFINITY;
-    l[t] = 0.f;
+    l[t] = mxf4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < R; ++j) o[t][j] = mxf4{0.f, 0.f, 0.f, 0.f};
   }
   const int64_t pbytes = a.pg.bytes();
-  for (int tile = tb; tile < te; ++tile) {
-    const int k0 = s0 + tile * kAtTile + wave * kAtKeys;
-    if (k0 >= n) break;  // only in the last tile
-    uint32_t kw[2][KW], vw[2][KW], ks[2][(KW + 3) / 4], vs[2];
+  const int32_t* row = a.table + b * a.ldt;
+  // the pages of 32 keys (16 of them share one); -1: no key there, or no page
+  int page[2];
+  auto look_up = [&](int k0) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int kk = k0 + 16 * t;
+      page[t] = kk < n ? row[kk >> a.lgP] : -1;
+    }
+  };
+  int k0 = s0 + tb * kAtTile + wave * kAtKeys;
+  const int kend = s0 + te * kAtTile < n ? s0 + te * kAtTile : n;
+  if (k0 < kend) look_up(k0);
+  for (; k0 < kend; k0 += kAtTile) {
+    int pg[2];
     bool ok[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int kk = k0 + 16 * t;  // 16 keys of one page
-      int64_t page = -1;
-      if (kk < n) page = a.table[b * a.ldt + (kk >> a.lgP)];
-      ok[t] = page >= 0 && page < a.pages;
+      pg[t] = __builtin_amdgcn_readfirstlane(page[t]);
+      ok[t] = pg[t] >= 0 && pg[t] < a.pages;
+    }
+    mxi4 kw[2][NQ];
+    uint32_t vw[2][KW], vs[2];
+    int ks[2][NQ];
+    auto load = [&](int t) {
+      const uint8_t* pb = a.cache + ((int64_t)pg[t] * a.heads + h) * pbytes;
+      const int p = (k0 + 16 * t) & (a.pg.P - 1);
 #pragma unroll
-      for (int i = 0; i < KW; ++i) kw[t][i] = vw[t][i] = 0u;
-      ks[t][0] = 127u;
-      if constexpr (D == 256) ks[t][1] = 127u;
-      vs[t] = 0x7f7f7f7fu;
-      if (ok[t]) {
-        const uint8_t* pb = a.cache + (page * a.heads + h) * pbytes;
-        const int p = kk & (a.pg.P - 1);
-        const uint8_t* kp = pb + a.pg.kcode(p + c) + g * (D / 8);
-        const uint8_t* vp = pb + a.pg.vcode(p + 4 * g, c);
-        if constexpr (D == 64) {
-          const uint2 x = *reinterpret_cast<const uint2*>(kp), y = *reinterpret_cast<const uint2*>(vp);
-          kw[t][0] = x.x; kw[t][1] = x.y;
-          vw[t][0] = y.x; vw[t][1] = y.y;
-          ks[t][0] = pb[a.pg.kscale(p + c) + (g >> 1)];
-        } else {
+      for (int e = 0; e < NQ; ++e) {
+        const int blk = D == 64 ? (g & 1) : 4 * e + g;  // D = 64: both halves of the lanes hold the 64 values
+        kw[t][e] = *reinterpret_cast<const mxi4*>(pb + a.pg.kcode(p) + (uint32_t)(c * (D / 2) + 16 * blk));
+        ks[t][e] = pb[a.pg.kscale(p) + (uint32_t)(c * (D / 32) + blk)];
+      }
+      const uint8_t* vp = pb + a.pg.vcode(p, 0) + (uint32_t)(g * (2 * D) + c * (D / 8));
+      if constexpr (D == 64) {
+        const uint2 y = *reinterpret_cast<const uint2*>(vp);
+        vw[t][0] = y.x; vw[t][1] = y.y;
+      } else {
 #pragma unroll
-          for (int q = 0; q < KW / 4; ++q) {
-            const uint4 x = reinterpret_cast<const uint4*>(kp)[q], y = reinterpret_cast<const uint4*>(vp)[q];
-            kw[t][4 * q] = x.x; kw[t][4 * q + 1] = x.y; kw[t][4 * q + 2] = x.z; kw[t][4 * q + 3] = x.w;
-            vw[t][4 * q] = y.x; vw[t][4 * q + 1] = y.y; vw[t][4 * q + 2] = y.z; vw[t][4 * q + 3] = y.w;
-          }
-          if constexpr (D == 128) {
-            ks[t][0] = pb[a.pg.kscale(p + c) + g];
-          } else {
-            const uint32_t x = *reinterpret_cast<const uint16_t*>(pb + a.pg.kscale(p + c) + 2 * g);
-            ks[t][0] = x & 255u;
-            ks[t][1] = x >> 8;
-          }
+        for (int q = 0; q < KW / 4; ++q) {
+          const uint4 y = reinterpret_cast<const uint4*>(vp)[q];
+          vw[t][4 * q] = y.x; vw[t][4 * q + 1] = y.y; vw[t][4 * q + 2] = y.z; vw[t][4 * q + 3] = y.w;
         }
-        vs[t] = *reinterpret_cast<const uint32_t*>(pb + a.pg.vscale(p + 4 * g, c * D / 512));
+      }
+      vs[t] = *reinterpret_cast<const uint32_t*>(pb + a.pg.vscale(p, 0) + (uint32_t)(g * (D / 8) + (c * D / 512) * 4));
+    };
+    if (ok[0] && ok[1]) {
+      load(0);
+      load(1);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int e = 0; e < NQ; ++e) {
+          kw[t][e] = mxi4{0, 0, 0, 0};
+          ks[t][e] = 127;
+        }
+#pragma unroll
+        for (int i = 0; i < KW; ++i) vw[t][i] = 0u;
+        vs[t] = 0x7f7f7f7fu;
+        if (ok[t]) load(t);
       }
     }
-    // scores: column c, keys kk + 4 g + i
+    if (k0 + kAtTile < kend) look_up(k0 + kAtTile);  // the next keys' pages, ahead of their use
+    // scores: column c, keys 16 t + 4 g + i
     float s[NT][2][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      mxf4 acc[NT];
 #pragma unroll
-      for (int u = 0; u < NT; ++u) acc[u] = mxf4{0.f, 0.f, 0.f, 0.f};
+      for (int u = 0; u < NT; ++u) {
+        mxf4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int q = 0; q < NS; ++q) {
-        const float sc = mx_scale(ks[t][D == 256 ? q / 4 : 0]);
-        uint4 w;
-        w.x = at_bits(at_pair(kw[t][q], sc, 0));
-        w.y = at_bits(at_pair(kw[t][q], sc, 1));
-        w.z = at_bits(at_pair(kw[t][q], sc, 2));
-        w.w = at_bits(at_pair(kw[t][q], sc, 3));
+        for (int e = 0; e < NQ; ++e) {
+          const mxi8 K = {kw[t][e][0], kw[t][e][1], kw[t][e][2], kw[t][e][3], 0, 0, 0, 0};
 #pragma unroll
-        for (int u = 0; u < NT; ++u)
-          acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(mxb8, w), qf[u][q], acc[u], 0, 0, 0);
+          for (int w = 0; w < NP; ++w)
+            acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(K, qf[u][e][w], acc, 4, 0, 0, ks[t][e], 0,
+                                                                   qsc[u][e][w]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[u][t][i] = acc[i] + at_ror8(acc[i]);
       }
-#pragma unroll
-      for (int u = 0; u < NT; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[u][t][i] = acc[u][i] + at_ror8(acc[u][i]);
     }
-    // a tile with masked keys: scores to -infinity, values to zero
+    // masked keys: scores to -infinity, values to zero
     if (k0 < first || k0 + kAtKeys > n || !ok[0] || !ok[1]) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -306,37 +379,44 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
     mxb8 pf[NT];
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
-      float mx = s[u][0][0];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[u][t][i]);
+      float mx = fmaxf(fmaxf(s[u][0][0], s[u][0][1]), fmaxf(s[u][0][2], s[u][0][3]));
+      mx = fmaxf(mx, fmaxf(fmaxf(s[u][1][0], s[u][1][1]), fmaxf(s[u][1][2], s[u][1][3])));
       mx = fmaxf(at_colmax(mx), m[u]);
       const float base = mx == -INFINITY ? 0.f : mx;
-      const float f = __builtin_amdgcn_exp2f(m[u] - base);
-      m[u] = mx;
-      float sum = 0.f;
+      if (__builtin_amdgcn_ballot_w64(mx != m[u])) {  // seldom after the first tiles
+        const float f = __builtin_amdgcn_exp2f(m[u] - base);
+        m[u] = mx;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+        for (int i = 0; i < 4; ++i) l[u][i] *= f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = __builtin_amdgcn_exp2f(s[u][t][i] - base);
-          sum += p;
-          const __bf16 hi = (__bf16)p;
-          pf[u][4 * t + i] = c < 8 ? hi : (__bf16)(p - (float)hi);
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[u][j][i] *= f;
+      }
+      // columns 0..7 take a probability's upper 16 bits, columns 8..15 the
+      // rest, rounded toward zero to 8 bits (2^-16 of the probability); the sum
+      // below is of what the products use
+      uint32_t w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float x[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float p = __builtin_amdgcn_exp2f(s[u][q / 2][2 * (q & 1) + e] - base);
+          x[e] = p - __uint_as_float(__float_as_uint(p) & low);
         }
-      l[u] = l[u] * f + sum;
-#pragma unroll
-      for (int j = 0; j < R; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[u][j][i] *= f;
+        w[q] = __builtin_amdgcn_perm(__float_as_uint(x[1]), __float_as_uint(x[0]), 0x07060302u);
+      }
+      pf[u] = __builtin_bit_cast(mxb8, make_uint4(w[0], w[1], w[2], w[3]));
+      l[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pf[u], l[u], 0, 0, 0);
     }
-    // values: keys in pairs, one run of dimensions per lane
+    // values: keys in pairs, one run of dimensions per lane (of a scale the
+    // conversion reads the exponent, so byte 0 is 2^-127 and 255 NaN)
     float vsc[2][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) vsc[t][i] = mx_scale((vs[t] >> (8 * i)) & 255u);
+      for (int i = 0; i < 4; ++i) vsc[t][i] = __uint_as_float(i == 3 ? vs[t] >> 24 << 23 : (vs[t] >> (8 * i) & 255u) << 23);
 #pragma unroll
     for (int q = 0; q < R / 2; ++q) {  // dimensions 2 q and 2 q + 1 of the run
       uint32_t lo[4], hi[4];
@@ -363,10 +443,10 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
   // join the wavefronts: all parts to the common maximum, summed in order
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    l[t] = at_colsum(l[t]);
+    const float sum = l[t][0] + at_ror8(l[t][0]);  // every row of the product is the column's sum
     if (lane < 8) {
       ms[wave][8 * t + lane] = m[t];
-      ls[wave][8 * t + lane] = l[t];
+      ls[wave][8 * t + lane] = sum;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
