@@ -94,7 +94,7 @@ hipError_t launch_paged_attention(const AtArgs& a, hipStream_t) {
     for (int64_t b = 0; b < a.batch; ++b) {
       const int64_t n = seed == 0 ? 0 : seed == 1 ? a.cap : (b * 7919 + seed * 104729) % (a.cap + 1) >> (seed * b % 5);
       tiles.push_back(at_tiles((int)n, seed == 3 ? 100 : 0));
-      total += tiles.back() * units;
+      total += at_cost(tiles.back()) * units;
     }
     if (!total) continue;
     const int wgs = at_dealt(total, a.wgs);
@@ -106,6 +106,7 @@ hipError_t launch_paged_attention(const AtArgs& a, hipStream_t) {
     int64_t g0 = 0;
     for (int64_t b = 0; b < a.batch; ++b)
       for (int64_t u = 0; u < units && tiles[(size_t)b]; ++u, g0 += tiles[(size_t)b]) {
+        g0 += kAtLead;  // the lead's places come before the first tile
         const int64_t g1 = g0 + tiles[(size_t)b] - 1;
         if (at_owner(g0, total, wgs) != owner[(size_t)g0] || at_owner(g1, total, wgs) != owner[(size_t)g1])
           return bad("attention owner of tile %lld of %lld", g0, total);

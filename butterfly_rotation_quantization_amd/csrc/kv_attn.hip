@@ -148,21 +148,19 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
   const uint32_t one2 = 0x3f803f80u;
   const mxb8 ones = __builtin_bit_cast(mxb8, make_uint4(one2, one2, one2, one2));
   const int units = a.heads * a.ht;   // of a sequence
-  int64_t total = 0, pos = 0, end = 0, base = 0;  // tiles: all, this workgroup's, before sequence b
+  int64_t total = 0, pos = 0, end = 0, base = 0;  // places: all, this workgroup's, before sequence b
   int64_t b = 0;
   int wgs = 0;
   if (a.wgs) {
-    int64_t mine = 0;
-    for (int64_t i = tid; i < a.batch; i += kAtThreads) mine += at_tiles(at_length(a, i), a.window);
-    total = at_block_sum(mine, sums) * units;
-    wgs = at_dealt(total, a.wgs);
-    if ((int)blockIdx.x >= wgs) return;
-    pos = at_start(blockIdx.x, total, wgs);
-    end = at_start((int64_t)blockIdx.x + 1, total, wgs);
-    // the sequence that has tile pos
+    // all tiles; with more sequences than threads, by a pass of its own
+    if (a.batch > kAtThreads) {
+      int64_t mine = 0;
+      for (int64_t i = tid; i < a.batch; i += kAtThreads) mine += at_cost(at_tiles(at_length(a, i), a.window));
+      total = at_block_sum(mine, sums) * units;
+    }
     for (int64_t i0 = 0;; i0 += kAtThreads) {
       const int64_t i = i0 + tid;
-      const int64_t n = i < a.batch ? (int64_t)at_tiles(at_length(a, i), a.window) * units : 0;
+      const int64_t n = i < a.batch ? (int64_t)at_cost(at_tiles(at_length(a, i), a.window)) * units : 0;
       int64_t x = n;  // inclusive sum over the threads before
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
@@ -178,7 +176,14 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
         if (w < wave) x += sums[w];
         all += sums[w];
       }
-      if (pos >= base + x - n && pos < base + x) {
+      if (i0 == 0) {
+        if (a.batch <= kAtThreads) total = all;
+        wgs = at_dealt(total, a.wgs);
+        if ((int)blockIdx.x >= wgs) return;
+        pos = at_start(blockIdx.x, total, wgs);
+        end = at_start((int64_t)blockIdx.x + 1, total, wgs);
+      }
+      if (pos >= base + x - n && pos < base + x) {  // the sequence that has place pos
         found[0] = (int)i;
         found_base[0] = base + x - n;
       }
@@ -190,9 +195,9 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
     base = found_base[0];
   } else {
     b = blockIdx.x / (uint32_t)units;
-    const int tiles = at_tiles(at_length(a, b), a.window);
-    pos = (int64_t)(blockIdx.x - (uint32_t)b * (uint32_t)units) * tiles;
-    end = pos + tiles;
+    const int cost = at_cost(at_tiles(at_length(a, b), a.window));
+    pos = (int64_t)(blockIdx.x - (uint32_t)b * (uint32_t)units) * cost;
+    end = pos + cost;
     if (pos == end) {  // no key: the unit's rows get what an empty sum gives
       const int u = (int)(blockIdx.x - (uint32_t)b * (uint32_t)units);
       for (int r = tid / LPH; r < H; r += kAtThreads / LPH) {
@@ -208,17 +213,37 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
   const int n = at_length(a, b);
   const int first = a.window > 0 && n > a.window ? n - a.window : 0;
   const int s0 = at_skip(n, a.window), tiles = at_tiles(n, a.window);
-  if (pos >= base + (int64_t)tiles * units) {  // on to the next sequence (one without keys has no tiles)
-    base += (int64_t)tiles * units;
+  const int cost = at_cost(tiles);
+  if (pos >= base + (int64_t)cost * units) {  // on to the next sequence (one without keys has no place)
+    base += (int64_t)cost * units;
     ++b;
     continue;
   }
-  const int u = (int)((pos - base) / tiles);
-  const int64_t g0 = base + (int64_t)u * tiles;
-  const int tb = (int)(pos - g0), te = (int)(end - g0 < tiles ? end - g0 : tiles);
-  pos = g0 + te;
+  const int u = (int)((pos - base) / cost);
+  const int64_t g0 = base + (int64_t)u * cost + kAtLead;  // place of the unit's first tile
+  const int tb = pos > g0 ? (int)(pos - g0) : 0;
+  const int te = end - g0 < tiles ? (int)(end - g0) : tiles;
+  pos = g0 + tiles < end ? g0 + tiles : end;
+  if (te <= tb) continue;  // only of the unit's lead
   const int h = u / a.ht, h0 = (u - h * a.ht) * H;  // key-value head; first query head within its group
+  if (wgs && tb == 0 && tid == 0)  // who has the unit's parts, and the first one's slot, for the join
+    a.who[b * units + u] = make_int2((int)at_slot(blockIdx.x, g0, total, wgs),
+                                     te == tiles ? 0 : at_owner(g0 + tiles - 1, total, wgs) - (int)blockIdx.x);
 
+  const int64_t pbytes = a.pg.bytes();
+  const int32_t* row = a.table + b * a.ldt;
+  // the pages of 32 keys (16 of them share one); -1: no key there, or no page
+  int page[2];
+  auto look_up = [&](int k0) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int kk = k0 + 16 * t;
+      page[t] = kk < n ? row[kk >> a.lgP] : -1;
+    }
+  };
+  int k0 = s0 + tb * kAtTile + wave * kAtKeys;
+  const int kend = s0 + te * kAtTile < n ? s0 + te * kAtTile : n;
+  if (k0 < kend) look_up(k0);
   // queries: rotated, times the scale, in pieces
   const float sl = a.scale * 1.44269504088896341f;  // scores in units of log2
   for (int r = tid / LPH; r < H; r += kAtThreads / LPH) {
@@ -272,20 +297,6 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
 #pragma unroll
     for (int j = 0; j < R; ++j) o[t][j] = mxf4{0.f, 0.f, 0.f, 0.f};
   }
-  const int64_t pbytes = a.pg.bytes();
-  const int32_t* row = a.table + b * a.ldt;
-  // the pages of 32 keys (16 of them share one); -1: no key there, or no page
-  int page[2];
-  auto look_up = [&](int k0) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int kk = k0 + 16 * t;
-      page[t] = kk < n ? row[kk >> a.lgP] : -1;
-    }
-  };
-  int k0 = s0 + tb * kAtTile + wave * kAtKeys;
-  const int kend = s0 + te * kAtTile < n ? s0 + te * kAtTile : n;
-  if (k0 < kend) look_up(k0);
   for (; k0 < kend; k0 += kAtTile) {
     int pg[2];
     bool ok[2];
@@ -484,8 +495,8 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
   }
 }
 
-// Joins the parts of units that span workgroups, in order, and writes the rows
-// of sequences without keys.  ROWS query heads of one unit to a workgroup;
+// Joins the parts of units that span workgroups and writes the rows of
+// sequences without keys.  ROWS query heads of one unit to a workgroup;
 // each has G groups of D / 8 lanes, which take its parts in turn and are
 // joined in LDS.
 template <int D>
@@ -493,7 +504,6 @@ __global__ __launch_bounds__(kAtThreads) void at_join_kernel(AtArgs a, int rows)
   constexpr int LPH = D / kMxPerLane;
   constexpr int LD = D + 4;
   __shared__ float os[kAtThreads / LPH][LD];
-  __shared__ int64_t sums[kAtWaves];
   const int tid = threadIdx.x, lane = tid & 63;
   const int H = kAtCols * a.nt, units = a.heads * a.ht, per = H / rows;
   const int64_t ub = blockIdx.x / (uint32_t)per;
@@ -505,21 +515,15 @@ __global__ __launch_bounds__(kAtThreads) void at_join_kernel(AtArgs a, int rows)
   const int r = r0 + tid / LPH % rows, grp = tid / (LPH * rows), groups = kAtThreads / (LPH * rows);
   const int e0 = (tid % LPH) * kMxPerLane;
   const bool mine = h0 + r < a.group;
-  int64_t before = 0, all = 0;
-  for (int64_t i = tid; i < a.batch; i += kAtThreads) {
-    const int t = at_tiles(at_length(a, i), a.window);
-    all += t;
-    if (i < b) before += t;
-  }
-  const int64_t total = at_block_sum(all, sums) * units;
-  const int64_t g0 = at_block_sum(before, sums) * units + (int64_t)u * tiles;
   float M = -INFINITY, L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (tiles > 0) {
-    const int wgs = at_dealt(total, a.wgs);
-    const int w0 = at_owner(g0, total, wgs), w1 = at_owner(g0 + tiles - 1, total, wgs);
-    if (w0 == w1) return;  // finished by its workgroup
-    for (int w = w0 + grp; w <= w1; w += groups) {
-      const float* p = a.part + (at_slot(w, g0, total, wgs) * H + r) * (int64_t)LD;
+    const int2 who = a.who[ub];
+    if (who.y == 0) return;  // finished by its workgroup
+    // part s (of who.y + 1) is the first of workgroup who.x / 2 + s
+    const float* p0 = a.part + r * (int64_t)LD;
+#pragma unroll 2
+    for (int s = grp; s <= who.y; s += groups) {
+      const float* p = p0 + (s == 0 ? who.x : (who.x / 2 + s) * 2) * (int64_t)(H * LD);
       const float2 ml = *reinterpret_cast<const float2*>(p + D);
       float v[8];
       mx_load8<BRQ_F32>(p, e0, v);

@@ -163,18 +163,25 @@ constexpr int kAtMaxBatch = 4096;  // sequences whose tiles are dealt out evenly
 // A unit is the group of query heads of one workgroup over one sequence's
 // keys, in tiles of kAtTile keys.  Up to kAtMaxBatch sequences the tiles of
 // all units, in order, are dealt out evenly to a fixed number of workgroups
-// that the chip holds at once, whatever the lengths: workgroup w takes tiles
-// [at_start(w), at_start(w + 1)).  A unit within one workgroup is finished
-// there; the parts of the others go to the workspace, two slots a workgroup
-// (a part that begins its range, one that ends it), and are joined in order.
-// Workgroups that get tiles: no more than there are tiles, so each has one.
+// that the chip holds at once, whatever the lengths.  Ahead of its tiles a unit
+// has kAtLead empty places, since beginning one (its queries, its join) takes
+// as long as some tiles: without them a workgroup got fourteen short sequences
+// where another got fourteen tiles of a long one, and 96 sequences of 17 to
+// 16384 tokens took 109 us where they take 80.  Workgroup w has places
+// [at_start(w), at_start(w + 1)).  A unit whose tiles lie within one workgroup
+// is finished there; the parts of the others go to the workspace, two slots a
+// workgroup (a part from before its first place, one that it begins), and are
+// joined.
+constexpr int kAtLead = 2;
+__host__ __device__ inline int at_cost(int tiles) { return tiles > 0 ? tiles + kAtLead : 0; }
+// Workgroups that get places: no more than there are, so each has one.
 __host__ __device__ inline int at_dealt(int64_t total, int wgs) { return total < wgs ? (int)total : wgs; }
 __host__ __device__ inline int64_t at_start(int64_t w, int64_t total, int wgs) { return w * total / wgs; }
-// The workgroup that has tile g.
+// The workgroup that has place g.
 __host__ __device__ inline int at_owner(int64_t g, int64_t total, int wgs) {
   return (int)(((g + 1) * wgs - 1) / total);
 }
-// Slot of the part that workgroup w has of a unit beginning at tile g0.
+// Slot of the part that workgroup w has of a unit whose first tile is place g0.
 __host__ __device__ inline int64_t at_slot(int64_t w, int64_t g0, int64_t total, int wgs) {
   return 2 * w + (at_start(w, total, wgs) < g0 ? 1 : 0);
 }
@@ -218,7 +225,16 @@ struct AtArgs {
   float rnorm;
   int wgs;               // workgroups the tiles are dealt out to (0: one for each unit)
   float* part;           // [2 wgs][nt * kAtCols][D + 4]: o, then m and l
+  int2* who;             // [batch][heads][ht]: a unit's first slot, workgroups after its first
 };
+
+// Workspace bytes with and without the units' records.
+inline size_t at_part_bytes(int head_dim, int nt) {
+  return (size_t)2 * at_workgroups(head_dim, nt) * nt * kAtCols * (head_dim + 4) * sizeof(float);
+}
+inline size_t at_bytes(int head_dim, int nt, int64_t units) {
+  return at_part_bytes(head_dim, nt) + (size_t)units * sizeof(int2);
+}
 
 hipError_t launch_paged_attention(const AtArgs& a, hipStream_t s);
 

@@ -284,7 +284,7 @@ size_t brq_paged_attention_workspace_bytes(int64_t batch, int32_t q_heads, int32
   int nt, ht;
   at_shape(q_heads, heads, &nt, &ht);
   if (batch > kAtMaxBatch) return 0;
-  return (size_t)2 * at_workgroups(head_dim, nt) * nt * kAtCols * (head_dim + 4) * sizeof(float);
+  return at_bytes(head_dim, nt, batch * heads * ht);
 }
 
 brq_status brq_paged_attention(const brq_plan* plan, const void* q, int64_t ldq, int32_t qt, const uint8_t* cache,
@@ -343,6 +343,7 @@ brq_status brq_paged_attention(const brq_plan* plan, const void* q, int64_t ldq,
   a.lse = lse;
   a.wgs = batch <= kAtMaxBatch ? at_workgroups(head_dim, a.nt) : 0;
   a.part = static_cast<float*>(ws);
+  a.who = a.wgs ? reinterpret_cast<int2*>(static_cast<char*>(ws) + at_part_bytes(head_dim, a.nt)) : nullptr;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int tok = prof_begin("paged attention", s);
   const hipError_t e = launch_paged_attention(a, s);
