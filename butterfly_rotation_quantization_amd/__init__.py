@@ -296,9 +296,14 @@ def _h(plan: Optional[Plan]):
 
 # ---------------------------------------------------------------- torch marshalling
 
+_DTYPES: dict = {}
+
+
 def dtype_code(t) -> int:
-    import torch
-    return {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}[t.dtype]
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
+    return _DTYPES[t.dtype]
 
 
 def _torch_dtype(code: int):
@@ -544,19 +549,34 @@ def orp_geo_dequant(codes, signs, coef, m: int, n: int, bits: int, group: int, s
 
 # ---------------------------------------------------------------- microscaled 4-bit rows
 
+# These calls are short (a decode step makes hundreds), so the marshalling keeps
+# to few torch calls; every check stays, since a wrong pointer would be the
+# GPU's to find.
+
+def _stream_of(stream, t) -> int:
+    """The raw stream: the one given, or the current one of t's GPU."""
+    if stream is not None:
+        return _stream(stream)
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
 def _rows(t) -> tuple:
-    """(rows, n, leading dimension) of a 2-D tensor of contiguous rows."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("expected a 2-D tensor with unit column stride")
+    """(rows, n, leading dimension) of a 2-D GPU tensor of contiguous rows."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError("expected a 2-D tensor on the GPU")
     rows, n = t.shape
-    return rows, n, (t.stride(0) if rows > 1 else max(t.stride(0), n))
+    ld, one = t.stride()
+    if one != 1 and n > 1:
+        raise ValueError("expected a 2-D tensor with unit column stride")
+    return rows, n, (ld if rows > 1 and ld >= 0 else max(ld, n))
 
 
-def _packed(t, dtype, shape, what):
-    """Check a contiguous tensor of the library's own layout."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
+def _packed(t, dtype, shape, what) -> int:
+    """Address of a contiguous GPU tensor of the library's own layout."""
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on the GPU, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
@@ -565,30 +585,31 @@ def mx_quantize(right: Optional[Plan], x, codes=None, scales=None, stream=None):
     the microscaled 4-bit format, after the Hadamard plan `right` (d = 32..256)
     or none (brq_mx_quantize).  Returns (codes uint8 [rows, n/2], scales uint8
     [rows, n/32])."""
-    import torch
+    from torch import uint8
     rows, n, ld = _rows(x)
     if codes is None:
-        codes = torch.empty((rows, n // 2), dtype=torch.uint8, device=x.device)
+        codes = x.new_empty((rows, n // 2), dtype=uint8)
     if scales is None:
-        scales = torch.empty((rows, n // 32), dtype=torch.uint8, device=x.device)
-    check(lib().brq_mx_quantize(_h(right), x.data_ptr(), dtype_code(x), ld, rows, n,
-                                _packed(codes, torch.uint8, (rows, n // 2), "codes"),
-                                _packed(scales, torch.uint8, (rows, n // 32), "scales"), _stream(stream)))
+        scales = x.new_empty((rows, n // 32), dtype=uint8)
+    check(lib().brq_mx_quantize(None if right is None else right._h, x.data_ptr(), dtype_code(x), ld, rows, n,
+                                _packed(codes, uint8, (rows, n // 2), "codes"),
+                                _packed(scales, uint8, (rows, n // 32), "scales"), _stream_of(stream, x)))
     return codes, scales
 
 
 def mx_dequantize(right: Optional[Plan], codes, scales, out=None, out_dtype=None, stream=None):
     """The values of microscaled 4-bit rows, with the plan `right` undone
     (brq_mx_dequantize).  Returns out [rows, n] (float32 by default)."""
-    import torch
-    rows, n = codes.shape[0], codes.shape[1] * 2
+    from torch import float32, uint8
+    rows, n, _ = _rows(codes)
+    n *= 2
     if out is None:
-        out = torch.empty((rows, n), dtype=out_dtype or torch.float32, device=codes.device)
-    if tuple(out.shape) != (rows, n):
+        out = codes.new_empty((rows, n), dtype=out_dtype or float32)
+    elif out.shape != (rows, n):
         raise ValueError(f"out: expected shape {(rows, n)}, got {tuple(out.shape)}")
-    check(lib().brq_mx_dequantize(_h(right), _packed(codes, torch.uint8, (rows, n // 2), "codes"),
-                                  _packed(scales, torch.uint8, (rows, n // 32), "scales"), rows, n,
-                                  out.data_ptr(), dtype_code(out), _rows(out)[2], _stream(stream)))
+    check(lib().brq_mx_dequantize(None if right is None else right._h, _packed(codes, uint8, (rows, n // 2), "codes"),
+                                  _packed(scales, uint8, (rows, n // 32), "scales"), rows, n,
+                                  out.data_ptr(), dtype_code(out), _rows(out)[2], _stream_of(stream, out)))
     return out
 
 
@@ -603,21 +624,22 @@ def mx_matmul(a_codes, a_scales, b_codes, b_scales, y=None, out_dtype=None, ws=N
     """y[t, o] = sum_k a[t, k] b[o, k] of two microscaled 4-bit matrices
     (brq_mx_matmul): activations [T, n] times a weight [m, n] kept by output
     rows.  Returns y [T, m] (bfloat16 by default)."""
-    import torch
-    T, n, m = a_codes.shape[0], a_codes.shape[1] * 2, b_codes.shape[0]
+    from torch import bfloat16, uint8
+    T, n, _ = _rows(a_codes)
+    n *= 2
+    m = b_codes.shape[0]
     if y is None:
-        y = torch.empty((T, m), dtype=out_dtype or torch.bfloat16, device=a_codes.device)
-    if tuple(y.shape) != (T, m):
+        y = a_codes.new_empty((T, m), dtype=out_dtype or bfloat16)
+    elif y.shape != (T, m):
         raise ValueError(f"y: expected shape {(T, m)}, got {tuple(y.shape)}")
     if ws is None:
         ws = mx_matmul_workspace(T, m, n, a_codes.device)
-    wp, wb = _ws_args(ws)
-    u8 = torch.uint8
-    check(lib().brq_mx_matmul(_packed(a_codes, u8, (T, n // 2), "a_codes"),
-                              _packed(a_scales, u8, (T, n // 32), "a_scales"),
-                              _packed(b_codes, u8, (m, n // 2), "b_codes"),
-                              _packed(b_scales, u8, (m, n // 32), "b_scales"), T, m, n,
-                              y.data_ptr(), dtype_code(y), _rows(y)[2], wp, wb, _stream(stream)))
+    wp, wb = (None, 0) if ws is None else _ws_args(ws)
+    check(lib().brq_mx_matmul(_packed(a_codes, uint8, (T, n // 2), "a_codes"),
+                              _packed(a_scales, uint8, (T, n // 32), "a_scales"),
+                              _packed(b_codes, uint8, (m, n // 2), "b_codes"),
+                              _packed(b_scales, uint8, (m, n // 32), "b_scales"), T, m, n,
+                              y.data_ptr(), dtype_code(y), _rows(y)[2], wp, wb, _stream_of(stream, y)))
     return y
 
 
@@ -633,33 +655,34 @@ def kv_cache(pages: int, heads: int, head_dim: int, page: int, device="cuda"):
 
 
 def _heads(t, D, what) -> tuple:
-    """(tokens, heads, leading dimension) of a [tokens, heads, D] tensor whose
+    """(tokens, heads, leading dimension) of a [tokens, heads, D] GPU tensor whose
     heads follow one another."""
-    if t.dim() != 3 or t.shape[2] != D or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
-        raise ValueError(f"{what}: expected [tokens, heads, {D}] with the heads of a token contiguous, "
-                         f"got {tuple(t.shape)} with strides {tuple(t.stride())}")
-    n, h = t.shape[0], t.shape[1]
-    return n, h, (t.stride(0) if n > 1 else max(t.stride(0), h * D))
+    if t.dim() == 3 and t.is_cuda:
+        n, h, d = t.shape
+        ld, sh, one = t.stride()
+        if d == D and one == 1 and (h == 1 or sh == D):
+            return n, h, (ld if n > 1 and ld >= 0 else max(ld, h * D))
+    raise ValueError(f"{what}: expected [tokens, heads, {D}] on the GPU with the heads of a token contiguous, "
+                     f"got {tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
 
 
-def _cache_ptr(cache, heads, D, page):
-    import torch
-    return _packed(cache, torch.uint8, (cache.shape[0], heads, page * (D + D // 16)), "cache")
+def _cache_ptr(cache, heads, D, page) -> int:
+    from torch import uint8
+    return _packed(cache, uint8, (cache.shape[0], heads, page * (D + D // 16)), "cache")
 
 
 def kv_append(plan: Optional[Plan], k, v, slots, cache, page: int, stream=None):
     """Rotate, quantize and write the keys and values [tokens, heads, D] of new
     tokens to cache slots int64 [tokens] (brq_kv_append; a slot outside the
     cache is skipped).  Returns cache."""
-    import torch
+    from torch import int64
     D = k.shape[-1]
     n, h, ldk = _heads(k, D, "k")
     if v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError("k and v must have the same shape and dtype")
-    check(lib().brq_kv_append(_h(plan), k.data_ptr(), ldk, v.data_ptr(), _heads(v, D, "v")[2],
-                              dtype_code(k), _packed(slots, torch.int64, (n,), "slots"), n, h, D,
-                              int(page), cache.shape[0], _cache_ptr(cache, h, D, int(page)),
-                              _stream(stream)))
+    check(lib().brq_kv_append(None if plan is None else plan._h, k.data_ptr(), ldk, v.data_ptr(),
+                              _heads(v, D, "v")[2], dtype_code(k), _packed(slots, int64, (n,), "slots"), n, h, D,
+                              page, cache.shape[0], _cache_ptr(cache, h, D, page), _stream_of(stream, k)))
     return cache
 
 
@@ -668,18 +691,18 @@ def kv_read(plan: Optional[Plan], cache, slots, head_dim: int, page: int, k=None
     """Keys and values of the given slots, dequantized and unrotated
     (brq_kv_read).  Returns (k, v), each [tokens, heads, head_dim] (bfloat16 by
     default); a slot outside the cache reads as zeros."""
-    import torch
-    n, h, D = slots.shape[0], cache.shape[1], int(head_dim)
+    from torch import bfloat16, int64
+    n, h, D = slots.shape[0], cache.shape[1], head_dim
     if k is None:
-        k = torch.empty((n, h, D), dtype=out_dtype or torch.bfloat16, device=cache.device)
+        k = cache.new_empty((n, h, D), dtype=out_dtype or bfloat16)
     if v is None:
-        v = torch.empty_like(k)
-    if tuple(k.shape) != (n, h, D) or v.shape != k.shape or v.dtype != k.dtype:
+        v = k.new_empty((n, h, D))
+    if k.shape != (n, h, D) or v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError(f"k and v must have shape {(n, h, D)} and the same dtype")
-    check(lib().brq_kv_read(_h(plan), _cache_ptr(cache, h, D, int(page)),
-                            _packed(slots, torch.int64, (n,), "slots"), n, h, D, int(page),
+    check(lib().brq_kv_read(None if plan is None else plan._h, _cache_ptr(cache, h, D, page),
+                            _packed(slots, int64, (n,), "slots"), n, h, D, page,
                             cache.shape[0], k.data_ptr(), _heads(k, D, "k")[2], v.data_ptr(),
-                            _heads(v, D, "v")[2], dtype_code(k), _stream(stream)))
+                            _heads(v, D, "v")[2], dtype_code(k), _stream_of(stream, k)))
     return k, v
 
 
@@ -697,28 +720,23 @@ def paged_attention(plan: Optional[Plan], q, cache, table, lens, page: int, scal
     [batch, pages of a sequence], lens int32 [batch]; scale defaults to
     1/sqrt(D), window 0 sees every cached token; lse, if given, is a float32
     [batch, q_heads] output.  Returns out, like q."""
-    import torch
-    B, hq, D = q.shape
-    h = cache.shape[1]
+    from torch import float32, int32
+    D = q.shape[-1]
+    B, hq, ldq = _heads(q, D, "q")
+    h, pages = cache.shape[1], table.shape[-1]
     if out is None:
-        out = torch.empty((B, hq, D), dtype=q.dtype, device=q.device)
-    if out.shape != q.shape or out.dtype != q.dtype:
+        out = q.new_empty((B, hq, D))
+    elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and dtype")
     if ws is None:
         ws = paged_attention_workspace(B, hq, h, D, q.device)
-    wp, wb = _ws_args(ws)
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"table: expected int32 [{B}, pages] with unit column stride")
-    ldt = table.shape[1] if B == 1 else table.stride(0)
-    if ldt != table.shape[1]:
-        raise ValueError("table must be contiguous")
+    wp, wb = (None, 0) if ws is None else _ws_args(ws)
     check(lib().brq_paged_attention(
-        _h(plan), q.data_ptr(), _heads(q, D, "q")[2], dtype_code(q),
-        _cache_ptr(cache, h, D, int(page)), cache.shape[0], table.data_ptr(), ldt,
-        _packed(lens, torch.int32, (B,), "lens"), B, hq, h, D, int(page),
-        D ** -0.5 if scale is None else float(scale), int(window), out.data_ptr(),
-        _heads(out, D, "out")[2], None if lse is None else _packed(lse, torch.float32, (B, hq), "lse"),
-        wp, wb, _stream(stream)))
+        None if plan is None else plan._h, q.data_ptr(), ldq, dtype_code(q), _cache_ptr(cache, h, D, page),
+        cache.shape[0], _packed(table, int32, (B, pages), "table"), pages, _packed(lens, int32, (B,), "lens"),
+        B, hq, h, D, page, D ** -0.5 if scale is None else scale, window, out.data_ptr(),
+        _heads(out, D, "out")[2], None if lse is None else _packed(lse, float32, (B, hq), "lse"),
+        wp, wb, _stream_of(stream, q)))
     return out
 
 
