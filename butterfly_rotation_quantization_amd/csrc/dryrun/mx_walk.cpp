@@ -17,19 +17,19 @@ static hipError_t bad(const char* fmt, long long a, long long b) {
 
 static hipError_t walk_mx(const MxArgs& a, int64_t ld) {
   dry_launch();
-  const int64_t n = (int64_t)a.lpr * kMxPerLane;
-  if (n % kMxBlock || a.lanes != (uint64_t)a.rows * a.lpr || ld < n || (a.d && n % a.d))
+  const int64_t n = (int64_t)a.lpr * a.per;
+  if ((a.per != 8 && a.per != 16) || n % kMxBlock || a.lanes != (uint64_t)a.rows * a.lpr || ld < n || (a.d && n % a.d))
     return bad("mx geometry (row of %lld, d %lld)", n, a.d);
   if (a.lanes / kMxThreads >= ((uint64_t)1 << 31)) return bad("mx grid of %lld lanes", (long long)a.lanes, 0);
   if (a.lanes > (1 << 22)) return hipSuccess;  // walked in full at test sizes
   std::vector<uint8_t> cover((size_t)(a.rows * n), 0);
   for (uint64_t li = 0; li < a.lanes; ++li) {
     int64_t row, col;
-    mx_lane(a.lpr, li, &row, &col);
-    if (row < 0 || row >= a.rows || col < 0 || col + kMxPerLane > n) return bad("mx lane at (%lld, %lld)", row, col);
-    if ((row * n + col) / kMxPerLane != (int64_t)li) return bad("mx codes word %lld of lane %lld", row * n + col, li);
-    if ((li & 3) == 0 && col % kMxBlock) return bad("mx block at column %lld", col, 0);
-    for (int e = 0; e < kMxPerLane; ++e) cover[(size_t)(row * n + col + e)]++;
+    mx_lane(a.lpr, a.per, li, &row, &col);
+    if (row < 0 || row >= a.rows || col < 0 || col + a.per > n) return bad("mx lane at (%lld, %lld)", row, col);
+    if ((row * n + col) / a.per != (int64_t)li) return bad("mx codes word %lld of lane %lld", row * n + col, li);
+    if (li % (kMxBlock / a.per) == 0 && col % kMxBlock) return bad("mx block at column %lld", col, 0);
+    for (int e = 0; e < a.per; ++e) cover[(size_t)(row * n + col + e)]++;
   }
   for (size_t i = 0; i < cover.size(); ++i)
     if (cover[i] != 1) return bad("mx value %lld handled %lld times", (long long)i, cover[i]);
@@ -56,10 +56,11 @@ static hipError_t walk_page(const KvPage& pg) {
     return true;
   };
   for (int t = 0; t < P; ++t)
-    for (int c = 0; c < D; c += kMxPerLane) {
-      bool ok = put(pg.kcode(t) + c / 2, 4);
-      if (D == 64) ok = ok && put(pg.vcode(t, c / 4), 2) && put(pg.vcode(t, c / 4 + 1), 2);
-      else ok = ok && put(pg.vcode(t, c / (D / 16)) + (c % (D / 16)) / 2, 4);
+    for (int c = 0; c < D; c += kKvPerLane) {
+      const int run = D / 16, w = D / 32;  // a run's dimensions and bytes; runs are D / 8 bytes apart
+      bool ok = put(pg.kcode(t) + c / 2, 8);
+      for (int q = 0; q < kKvPerLane / run; ++q)
+        ok = ok && pg.vcode(t, c / run + q) == pg.vcode(t, c / run) + q * (D / 8) && put(pg.vcode(t, c / run + q), w);
       if (c % kMxBlock == 0) ok = ok && put(pg.kscale(t) + c / 32, 1) && put(pg.vscale(t, c / 32), 1);
       if (!ok) return bad("cache page access of token %lld, value %lld", t, c);
     }

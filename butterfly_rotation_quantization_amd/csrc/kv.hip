@@ -1,46 +1,52 @@
 // Append to and read from the paged 4-bit key-value cache (layout: KvPage in
-// mx.h).  A row is one head of one token, its D values on D / 8 lanes; keys
-// are rows [0, R), values rows [R, 2R), R = tokens * heads.
+// mx.h).  A row is one head of one token, its D values on D / 16 lanes (append)
+// or D / 8 (read); keys are the first half of the grid, values the second.
+// Memory-bound for prompts, latency for single tokens: 8190 tokens of 8 heads
+// of 128 are appended in APP us and read in 12; 33 tokens in 3 us each.
 #include "mx_dev.h"
 
 namespace brq {
 namespace {
 
-template <int T>
+template <int T, int D>
 __global__ __launch_bounds__(kMxThreads) void kv_append_kernel(KvArgs a) {
-  const int D = a.pg.D, lane = threadIdx.x & 63;
-  const uint32_t lpr = (uint32_t)D / kMxPerLane;
-  const uint64_t li = (uint64_t)blockIdx.x * kMxThreads + threadIdx.x;
-  const int64_t row = (int64_t)(li / lpr);
-  const int c = (int)(li % lpr) * kMxPerLane;
-  const int64_t rows = a.tokens * a.heads;
-  if (row >= rows) return;
+  constexpr int LPR = D / kKvPerLane, RUN = D / 16;  // lanes per row; dimensions of a run of the values' layout
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * (kMxThreads / LPR) + threadIdx.x / LPR;
+  const int c = (int)(threadIdx.x % LPR) * kKvPerLane;
+  if (row >= a.tokens * a.heads) return;
   const bool val = blockIdx.y != 0;
-  const int64_t tok = row / a.heads;
-  const int h = (int)(row - tok * a.heads);
+  const int64_t tok = (uint32_t)row / (uint32_t)a.heads;  // rows < 2^31
+  const int h = (int)((uint32_t)row - (uint32_t)tok * (uint32_t)a.heads);
   const int64_t slot = a.slots[tok];
+  float v[16];
+  const void* x = val ? a.v : a.k;
+  const int64_t at = tok * (val ? a.ldv : a.ldk) + (int64_t)h * D + c;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) mx_load8<T>(x, at + 8 * q, *reinterpret_cast<float (*)[8]>(&v[8 * q]));
   if (slot < 0 || (slot >> a.lgP) >= a.pages) return;  // uniform over the row's lanes
-  float v[8];
-  if (val) mx_load8<T>(a.v, tok * a.ldv + (int64_t)h * D + c, v);
-  else mx_load8<T>(a.k, tok * a.ldk + (int64_t)h * D + c, v);
-  if (a.d) mx_rotate(v, a.signs, a.d, a.rnorm, c, lane);
-  uint32_t byte;
-  const uint32_t w = mx_round8(v, &byte);
-  uint8_t* pb = a.cache + ((slot >> a.lgP) * a.heads + h) * a.pg.bytes();
+  if (a.d) mx_rotate(v, a.signs, D, a.rnorm, c, lane);
+  uint32_t byte, w[2];
+  mx_round(v, w, &byte);
+  const KvPage pg{D, a.pg.P};
+  uint8_t* pb = a.cache + ((slot >> a.lgP) * a.heads + h) * pg.bytes();
   const int t = (int)(slot & (a.pg.P - 1));
   if (!val) {
-    *reinterpret_cast<uint32_t*>(pb + a.pg.kcode(t) + c / 2) = w;
-    if ((c & 31) == 0) pb[a.pg.kscale(t) + c / 32] = (uint8_t)byte;
+    *reinterpret_cast<uint2*>(pb + pg.kcode(t) + c / 2) = make_uint2(w[0], w[1]);
+    if ((c & 31) == 0) pb[pg.kscale(t) + c / 32] = (uint8_t)byte;
     return;
   }
-  if (D == 64) {  // the lane holds two runs of four values
-    *reinterpret_cast<uint16_t*>(pb + a.pg.vcode(t, c / 4)) = (uint16_t)w;
-    *reinterpret_cast<uint16_t*>(pb + a.pg.vcode(t, c / 4 + 1)) = (uint16_t)(w >> 16);
-  } else {        // one run of eight, or half a run of sixteen
-    const int run = D / 16;
-    *reinterpret_cast<uint32_t*>(pb + a.pg.vcode(t, c / run) + (c % run) / 2) = w;
+  uint8_t* d = pb + pg.vcode(t, c / RUN);  // runs are D / 8 bytes apart
+  if constexpr (D == 64) {         // the lane holds four runs of four values
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint16_t*>(d + q * (D / 8)) = (uint16_t)(w[q / 2] >> (16 * (q & 1)));
+  } else if constexpr (D == 128) {  // two of eight
+    *reinterpret_cast<uint32_t*>(d) = w[0];
+    *reinterpret_cast<uint32_t*>(d + D / 8) = w[1];
+  } else {                          // one of sixteen
+    *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
   }
-  if ((c & 31) == 0) pb[a.pg.vscale(t, c / 32)] = (uint8_t)byte;
+  if ((c & 31) == 0) pb[pg.vscale(t, c / 32)] = (uint8_t)byte;
 }
 
 template <int T>
@@ -53,8 +59,8 @@ __global__ __launch_bounds__(kMxThreads) void kv_read_kernel(KvArgs a) {
   const int64_t rows = a.tokens * a.heads;
   if (row >= rows) return;
   const bool val = blockIdx.y != 0;
-  const int64_t tok = row / a.heads;
-  const int h = (int)(row - tok * a.heads);
+  const int64_t tok = (uint32_t)row / (uint32_t)a.heads;  // rows < 2^31
+  const int h = (int)((uint32_t)row - (uint32_t)tok * (uint32_t)a.heads);
   const int64_t slot = a.slots[tok];
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (slot >= 0 && (slot >> a.lgP) < a.pages) {  // uniform over the row's lanes
@@ -77,6 +83,15 @@ __global__ __launch_bounds__(kMxThreads) void kv_read_kernel(KvArgs a) {
   else mx_store8<T>(const_cast<void*>(a.k), tok * a.ldk + (int64_t)h * D + c, v);
 }
 
+template <int T>
+void kv_append(const KvArgs& a, hipStream_t s) {
+  const int64_t lanes = a.tokens * a.heads * (a.pg.D / kKvPerLane);
+  const dim3 grid((unsigned)((lanes + kMxThreads - 1) / kMxThreads), 2);
+  if (a.pg.D == 64) kv_append_kernel<T, 64><<<grid, kMxThreads, 0, s>>>(a);
+  else if (a.pg.D == 128) kv_append_kernel<T, 128><<<grid, kMxThreads, 0, s>>>(a);
+  else kv_append_kernel<T, 256><<<grid, kMxThreads, 0, s>>>(a);
+}
+
 dim3 kv_grid(const KvArgs& a) {
   const int64_t lanes = a.tokens * a.heads * (a.pg.D / kMxPerLane);
   return dim3((unsigned)((lanes + kMxThreads - 1) / kMxThreads), 2);
@@ -85,9 +100,9 @@ dim3 kv_grid(const KvArgs& a) {
 }  // namespace
 
 hipError_t launch_kv_append(const KvArgs& a, hipStream_t s) {
-  if (a.t == BRQ_F32) kv_append_kernel<BRQ_F32><<<kv_grid(a), kMxThreads, 0, s>>>(a);
-  else if (a.t == BRQ_BF16) kv_append_kernel<BRQ_BF16><<<kv_grid(a), kMxThreads, 0, s>>>(a);
-  else kv_append_kernel<BRQ_F16><<<kv_grid(a), kMxThreads, 0, s>>>(a);
+  if (a.t == BRQ_F32) kv_append<BRQ_F32>(a, s);
+  else if (a.t == BRQ_BF16) kv_append<BRQ_BF16>(a, s);
+  else kv_append<BRQ_F16>(a, s);
   return hipGetLastError();
 }
 

@@ -2,9 +2,10 @@
 // shared by the kernels (mx.hip, mx_matmul.hip, kv.hip, kv_attn.hip) and the
 // host dry-run checker.
 //
-// Element lanes: a lane holds kMxPerLane consecutive values of a row, so a
-// block of 32 spans 4 lanes and a transform of d values d / 8 lanes; both are
-// aligned, since rows are whole blocks (whole transforms).
+// Element lanes: a lane holds 8 consecutive values of a row (16 where it also
+// transforms them for the quantizer: half the exchanges between lanes), so a
+// block of 32 spans 4 (2) lanes and a transform of d values d / 8 (d / 16);
+// both are aligned, since rows are whole blocks (whole transforms).
 #pragma once
 
 #include "brq_internal.h"
@@ -25,7 +26,8 @@ struct MxArgs {
   int yt;
   int64_t ldy;
   int64_t rows;
-  uint32_t lpr;          // lanes per row: n / kMxPerLane
+  int per;               // values per lane: 8 or 16
+  uint32_t lpr;          // lanes per row: n / per
   uint64_t lanes;        // rows * lpr
   uint8_t* codes;        // [rows][n/2]
   uint8_t* scales;       // [rows][n/32]
@@ -35,10 +37,10 @@ struct MxArgs {
 };
 
 // Row and first column of lane li (li < a.lanes).
-__host__ __device__ inline void mx_lane(uint32_t lpr, uint64_t li, int64_t* row, int64_t* col) {
+__host__ __device__ inline void mx_lane(uint32_t lpr, int per, uint64_t li, int64_t* row, int64_t* col) {
   const uint64_t r = (li >> 32) ? li / lpr : (uint64_t)((uint32_t)li / lpr);
   *row = (int64_t)r;
-  *col = (int64_t)(li - r * lpr) * kMxPerLane;
+  *col = (int64_t)(li - r * lpr) * per;
 }
 
 hipError_t launch_mx_quant(const MxArgs& a, hipStream_t s);
@@ -146,6 +148,7 @@ struct KvArgs {
   float rnorm;
 };
 
+constexpr int kKvPerLane = 16;    // values per lane of an append
 hipError_t launch_kv_append(const KvArgs& a, hipStream_t s);
 hipError_t launch_kv_read(const KvArgs& a, hipStream_t s);
 

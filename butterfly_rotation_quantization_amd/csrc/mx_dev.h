@@ -75,7 +75,7 @@ __device__ __forceinline__ uint32_t mx_xor(uint32_t x) {
   static_assert(X == 1 || X == 2 || X == 4 || X == 8, "moves within 16 lanes");
   if constexpr (X == 1) return mx_dpp<0xb1>(x);       // swap neighbours
   else if constexpr (X == 2) return mx_dpp<0x4e>(x);  // swap pairs
-  else if constexpr (X == 4) return mx_dpp<0x1b>(mx_dpp<0x141>(x));  // mirror 8 lanes, then each 4
+  else if constexpr (X == 4) return (uint32_t)__builtin_amdgcn_ds_swizzle((int)x, 4 << 10 | 0x1f);  // no one move does
   else return mx_dpp<0x128>(x);                       // rotate 16 lanes by 8
 }
 template <int X>
@@ -85,11 +85,11 @@ __device__ __forceinline__ float mx_xorf(float x) {
 
 // One butterfly stage between lanes: the lower lane gets lo + hi, the upper
 // one lo - hi, each one addition (the product with +-1 is exact).
-template <int X>
-__device__ __forceinline__ void mx_stage(float (&v)[8], int lane) {
+template <int X, int N>
+__device__ __forceinline__ void mx_stage(float (&v)[N], int lane) {
   if constexpr (X == 16) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < N; ++e) {
       const uint32_t u = __float_as_uint(v[e]);
       const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
       const float lo = __uint_as_float(r[0]), hi = __uint_as_float(r[1]);
@@ -98,84 +98,90 @@ __device__ __forceinline__ void mx_stage(float (&v)[8], int lane) {
   } else {
     const float s = (lane & X) ? -1.0f : 1.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], s, mx_xorf<X>(v[e]));
+    for (int e = 0; e < N; ++e) v[e] = fmaf(v[e], s, mx_xorf<X>(v[e]));
   }
 }
 
-// H_d v for the d / 8 lanes of a transform (d = 32..256), unnormalised: the
-// additions in the order of strides 1, 2, 4, ..., d / 2.
-__device__ __forceinline__ void mx_hadamard(float (&v)[8], int d, int lane) {
+// H_d v for the d / N lanes of a transform (d = 32..256, N = 8 or 16 values a
+// lane), unnormalised: the additions in the order of strides 1, 2, 4, ..., d / 2.
+template <int N>
+__device__ __forceinline__ void mx_hadamard(float (&v)[N], int d, int lane) {
 #pragma unroll
-  for (int s = 1; s < 8; s *= 2)
+  for (int s = 1; s < N; s *= 2)
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < N; ++e)
       if (!(e & s)) {
         const float a = v[e], b = v[e + s];
         v[e] = a + b;
         v[e + s] = a - b;
       }
   mx_stage<1>(v, lane);
-  mx_stage<2>(v, lane);
-  if (d > 32) mx_stage<4>(v, lane);
-  if (d > 64) mx_stage<8>(v, lane);
-  if (d > 128) mx_stage<16>(v, lane);
+  if (d > 2 * N) mx_stage<2>(v, lane);
+  if (d > 4 * N) mx_stage<4>(v, lane);
+  if (d > 8 * N) mx_stage<8>(v, lane);
+  if constexpr (N == 8)
+    if (d > 128) mx_stage<16>(v, lane);
+}
+
+template <int N>
+__device__ __forceinline__ void mx_signs(float (&v)[N], const float* signs, int c) {
+#pragma unroll
+  for (int q = 0; q < N / 8; ++q) {
+    float s[8];
+    mx_load8<BRQ_F32>(signs, c + 8 * q, s);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[8 * q + e] *= s[e];
+  }
 }
 
 // The plan's transform of the lane's values, which start at position c of
 // their d values: signs, additions, one product.
-__device__ __forceinline__ void mx_rotate(float (&v)[8], const float* signs, int d, float rnorm, int c, int lane) {
-  if (signs) {
-    float s[8];
-    mx_load8<BRQ_F32>(signs, c, s);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= s[e];
-  }
+template <int N>
+__device__ __forceinline__ void mx_rotate(float (&v)[N], const float* signs, int d, float rnorm, int c, int lane) {
+  if (signs) mx_signs(v, signs, c);
   mx_hadamard(v, d, lane);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] *= rnorm;
+  for (int e = 0; e < N; ++e) v[e] *= rnorm;
 }
 // Its inverse (the transform is symmetric): additions, product, signs.
 __device__ __forceinline__ void mx_unrotate(float (&v)[8], const float* signs, int d, float rnorm, int c, int lane) {
   mx_hadamard(v, d, lane);
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] *= rnorm;
-  if (signs) {
-    float s[8];
-    mx_load8<BRQ_F32>(signs, c, s);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= s[e];
-  }
+  if (signs) mx_signs(v, signs, c);
 }
 
-// 2^(byte - 127); byte 0 is the subnormal 2^-127, byte 255 a NaN (its bits
-// are infinity's, which the conversions below read as the NaN scale).
+// 2^(byte - 127); byte 0 is the subnormal 2^-127.  Byte 255, which stands for
+// NaN, gives infinity's bits: of a scale the conversions read the exponent
+// only, and take that one for NaN.
 __device__ __forceinline__ float mx_scale(uint32_t byte) {
   return __uint_as_float(byte ? byte << 23 : 0x400000u);
 }
 
-// Round the lane's eight values: the eight codes as a word (value 0 in the
-// lowest half-byte) and the block's scale byte.  The block is the lane's
-// aligned group of four lanes; magnitudes are compared as integers, which
+// Round the lane's N values (8 or 16): the codes, eight to a word (the first in
+// the lowest half-byte), and the block's scale byte.  The block is the lane's
+// aligned group of 32 / N lanes; magnitudes are compared as integers, which
 // order NaN above infinity above every number.
-__device__ __forceinline__ uint32_t mx_round8(const float (&v)[8], uint32_t* byte) {
+template <int N>
+__device__ __forceinline__ void mx_round(const float (&v)[N], uint32_t (&w)[N / 8], uint32_t* byte) {
   uint32_t top = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+  for (int e = 0; e < N; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
   top = max(top, mx_xor<1>(top));
-  top = max(top, mx_xor<2>(top));
-  if (top >= 0x7f800000u) {
-    *byte = 255u;
-    return 0u;
-  }
+  if constexpr (N == 8) top = max(top, mx_xor<2>(top));
+  const bool bad = top >= 0x7f800000u;
   const int b = (int)(top >> 23) - 2;  // floor(log2 A) - 2 + 127
-  *byte = b > 0 ? (uint32_t)b : 0u;
+  *byte = bad ? 255u : b > 0 ? (uint32_t)b : 0u;
   const float s = mx_scale(*byte);
-  uint32_t w = 0;  // the conversion divides by the scale, rounds half to even and saturates
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], s, 0);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], s, 1);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], s, 2);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], s, 3);
-  return w;
+#pragma unroll
+  for (int q = 0; q < N / 8; ++q) {  // the conversion divides by the scale, rounds half to even and saturates
+    uint32_t x = 0;
+    x = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(x, v[8 * q], v[8 * q + 1], s, 0);
+    x = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(x, v[8 * q + 2], v[8 * q + 3], s, 1);
+    x = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(x, v[8 * q + 4], v[8 * q + 5], s, 2);
+    x = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(x, v[8 * q + 6], v[8 * q + 7], s, 3);
+    w[q] = bad ? 0u : x;
+  }
 }
 
 // Eight codes times a block's scale.

@@ -59,7 +59,7 @@ int log2_of(int64_t x) {
 // Shared checks of brq_mx_quantize and brq_mx_dequantize; *done set when
 // there is nothing to do.
 brq_status mx_setup(MxArgs& a, const brq_plan* right, int64_t rows, int64_t n, const void* x, int32_t t, int64_t ld,
-                    const uint8_t* codes, const uint8_t* scales, bool* done) {
+                    const uint8_t* codes, const uint8_t* scales, bool quantize, bool* done) {
   clear_error();
   *done = false;
   std::memset(&a, 0, sizeof a);
@@ -82,7 +82,8 @@ brq_status mx_setup(MxArgs& a, const brq_plan* right, int64_t rows, int64_t n, c
   if (misaligned(codes, 16) || misaligned(scales, 4))
     return refuse(BRQ_ERR_ALIGNMENT, "codes must be 16-byte and scales 4-byte aligned");
   a.rows = rows;
-  a.lpr = (uint32_t)(n / kMxPerLane);
+  a.per = quantize && a.d ? 16 : kMxPerLane;
+  a.lpr = (uint32_t)(n / a.per);
   a.lanes = (uint64_t)rows * a.lpr;
   a.codes = const_cast<uint8_t*>(codes);
   a.scales = const_cast<uint8_t*>(scales);
@@ -100,7 +101,7 @@ brq_status brq_mx_quantize(const brq_plan* right, const void* x, int32_t xt, int
                            uint8_t* codes, uint8_t* scales, void* stream) {
   MxArgs a;
   bool done;
-  const brq_status st = mx_setup(a, right, rows, n, x, xt, ldx, codes, scales, &done);
+  const brq_status st = mx_setup(a, right, rows, n, x, xt, ldx, codes, scales, true, &done);
   if (st != BRQ_OK || done) return st;
   a.x = x;
   a.xt = xt;
@@ -116,7 +117,7 @@ brq_status brq_mx_dequantize(const brq_plan* right, const uint8_t* codes, const 
                              int64_t n, void* out, int32_t ot, int64_t ldo, void* stream) {
   MxArgs a;
   bool done;
-  const brq_status st = mx_setup(a, right, rows, n, out, ot, ldo, codes, scales, &done);
+  const brq_status st = mx_setup(a, right, rows, n, out, ot, ldo, codes, scales, false, &done);
   if (st != BRQ_OK || done) return st;
   a.y = out;
   a.yt = ot;
