@@ -29,6 +29,7 @@ struct MxArgs {
   int per;               // values per lane: 8 or 16
   uint32_t lpr;          // lanes per row: n / per
   uint64_t lanes;        // rows * lpr
+  int gap;               // rows do not follow one another in x or y
   uint8_t* codes;        // [rows][n/2]
   uint8_t* scales;       // [rows][n/32]
   const float* signs;    // the transform's signs, or null

@@ -85,6 +85,7 @@ brq_status mx_setup(MxArgs& a, const brq_plan* right, int64_t rows, int64_t n, c
   a.per = quantize && a.d ? 16 : kMxPerLane;
   a.lpr = (uint32_t)(n / a.per);
   a.lanes = (uint64_t)rows * a.lpr;
+  a.gap = ld != n;
   a.codes = const_cast<uint8_t*>(codes);
   a.scales = const_cast<uint8_t*>(scales);
   return BRQ_OK;
@@ -152,6 +153,7 @@ brq_status brq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const 
   const int64_t most = ((int64_t)1 << 31) - 1;
   if (T > most || m > most || n > most) return refuse(BRQ_ERR_UNSUPPORTED, "a dimension above 2^31 - 1");
   if (T == 0 || m == 0) return BRQ_OK;
+  if (((T + 15) / 16) * ((m + 15) / 16) > most) return refuse(BRQ_ERR_UNSUPPORTED, "an output above 2^39 values");
   if (!y || (n > 0 && (!a_codes || !a_scales || !b_codes || !b_scales)))
     return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL data pointer");
   if (misaligned(a_codes, 16) || misaligned(b_codes, 16) || misaligned(a_scales, 4) || misaligned(b_scales, 4))

@@ -11,11 +11,13 @@ __device__ __forceinline__ void mm_store(void* y, int yt, int64_t off, float v) 
   else static_cast<uint16_t*>(y)[off] = (uint16_t)mx_f16(v);
 }
 
-// One wavefront per 16 x 16 outputs: lane l holds block l / 16 of a step of
+// For rows too short (or too long) for the kernels below.  One wavefront per
+// 16 x 16 outputs: lane l holds block l / 16 of a step of
 // 128 values of row l % 16, of both operands, with the block's scale.
 __global__ __launch_bounds__(64) void mm_simple_kernel(MmArgs a) {
   const int lane = threadIdx.x, lr = lane & 15, lg = lane >> 4;
-  const int64_t t0 = (int64_t)blockIdx.y * 16, o0 = (int64_t)blockIdx.x * 16;
+  const uint32_t go = (uint32_t)((a.m + 15) / 16);
+  const int64_t t0 = (int64_t)(blockIdx.x / go) * 16, o0 = (int64_t)(blockIdx.x % go) * 16;
   const int64_t ra = t0 + lr, rb = o0 + lr;
   const int64_t nb = a.n / kMxBlock;
   const bool va = ra < a.T, vb = rb < a.m;
@@ -175,11 +177,13 @@ hipError_t mm_rows(const MmArgs& a, hipStream_t s) {
 // accumulation registers.  Written out because with all 256 of them in use the
 // register allocator moved sums to and fro between the two files (90 moves in
 // a stage of 128 products of 16 x 16 x 128).  The hardware orders these among themselves and
-// after the loads of their operands; mm_settle comes before other reads of c.
+// after the loads of their operands; two wait states cover a move into an
+// operand just before (the matrix unit is busy longer than that with the
+// product before); mm_settle comes before other reads of c.
 template <int SA, int SB>
 __device__ __forceinline__ void mm_mfma(mxi4 a, mxi4 b, mxf16& c, int sa, int sb) {
   asm volatile(
-      "v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%6,0] op_sel_hi:[%7,%8,0] cbsz:4 blgp:4"
+      "s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%6,0] op_sel_hi:[%7,%8,0] cbsz:4 blgp:4"
       : "+a"(c)
       : "v"(a), "v"(b), "v"(sa), "v"(sb), "n"(SA & 1), "n"(SB & 1), "n"(SA >> 1), "n"(SB >> 1));
 }
@@ -632,8 +636,7 @@ hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t s) {
   if (a.T <= 16) return mm_rows<1>(a, s);
   if (a.T <= 32) return mm_rows<2>(a, s);
   if (a.T <= 64) return mm_rows<4>(a, s);
-  const dim3 grid((unsigned)((a.m + 15) / 16), (unsigned)((a.T + 15) / 16));
-  mm_simple_kernel<<<grid, 64, 0, s>>>(a);
+  mm_simple_kernel<<<dim3((unsigned)(((a.m + 15) / 16) * ((a.T + 15) / 16))), 64, 0, s>>>(a);
   return hipGetLastError();
 }
 

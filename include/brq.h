@@ -421,7 +421,8 @@ brq_status brq_mx_dequantize(const brq_plan* right, const uint8_t* codes, const 
  *     split among workgroups.  The split depends on the sizes only, and the
  *     parts are added in order: a call's result does not vary.
  * T, m >= 0, n a multiple of 32 (n == 0: y = 0).  Errors: INVALID_ARGUMENT
- * (dtype, shapes, NULLs), UNSUPPORTED (T, m or n above 2^31 - 1), ALIGNMENT,
+ * (dtype, shapes, NULLs), UNSUPPORTED (T, m or n above 2^31 - 1, or an output
+ * above 2^39 values), ALIGNMENT,
  * WORKSPACE, HIP. */
 size_t brq_mx_matmul_workspace_bytes(int64_t T, int64_t m, int64_t n);
 brq_status brq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
