@@ -39,9 +39,73 @@ static hipError_t walk_mx(const MxArgs& a, int64_t ld) {
 hipError_t launch_mx_quant(const MxArgs& a, hipStream_t) { return walk_mx(a, a.ldx); }
 hipError_t launch_mx_dequant(const MxArgs& a, hipStream_t) { return walk_mx(a, a.ldy); }
 
+// Tiles, parts, scale images and LDS places of the tile kernels of a matmul.
+static hipError_t walk_tiles(const MmArgs& a) {
+  MmArgs b = a;
+  const size_t bytes = mm_plan(b, a.ts);
+  const int R = a.tile;
+  const int64_t image = (int64_t)a.stages * 8 * R, images = (a.gt + a.go) * image;
+  if (b.os != a.os || b.part != a.part || b.splits != a.splits || (R != 128 && R != 256) || a.os != a.ts + a.gt * image ||
+      reinterpret_cast<uint8_t*>(a.part) != a.ts + images ||
+      (int64_t)bytes != images + (a.splits > 1 ? a.splits * a.T * a.m * 4 : 0))
+    return bad("mx matmul workspace (%lld bytes, tile %lld)", (long long)bytes, R);
+  if (a.gt * R < a.T || a.go * R < a.m || (int64_t)a.stages * kMmK < a.n || 8 * a.per_xcd >= (int64_t)1 << 31)
+    return bad("mx matmul tiles (%lld x %lld)", a.gt, a.go);
+  for (int p = 0; p < a.splits; ++p)
+    if (a.stages - p * a.per < 1 || (p + 1 == a.splits && a.stages > (p + 1) * a.per))
+      return bad("mx matmul part %lld of %lld", p, a.splits);
+  // addresses in the kernel are offsets in 32 bits from a tile's first row
+  if (R * (a.n / 2) >= (int64_t)1 << 31) return bad("mx matmul row of %lld", a.n, 0);
+  const int64_t places = a.gt * a.go * a.splits;
+  if (places <= 1 << 16) {
+    std::vector<uint8_t> cover((size_t)places, 0);
+    for (int64_t x = 0; x < 8 * a.per_xcd; ++x) {
+      MmWhere w;
+      if (!mm_where(a, (uint32_t)x, w)) continue;
+      if (w.tt < 0 || w.tt >= a.gt || w.to < 0 || w.to >= a.go || w.part < 0 || w.part >= a.splits)
+        return bad("mx matmul tile (%lld, %lld)", w.tt, w.to);
+      cover[(size_t)((w.part * a.gt + w.tt) * a.go + w.to)]++;
+    }
+    for (size_t i = 0; i < cover.size(); ++i)
+      if (cover[i] != 1) return bad("mx matmul tile %lld taken %lld times", (long long)i, cover[i]);
+  }
+  // a stage of an image: every byte one block's scale of one row, words of
+  // tiles of 32 rows whole
+  std::vector<uint8_t> cover((size_t)(8 * R), 0);
+  for (int c = 0; c < 8; ++c)
+    for (int r = 0; r < R; ++r) {
+      const int at = mm_scale_at(R, c, r);
+      if (at < 0 || at >= 8 * R || cover[(size_t)at]++ || at != mm_scale_at(R, c, r % 32) + r / 32)
+        return bad("mx matmul scale of block %lld, row %lld", c, r);
+    }
+  // codes in LDS: thread tid brings piece (tid & 7) ^ (row & 7) of row tid / 8
+  // + 32 j to its own 16 bytes; eight rows' pieces c are in different places
+  const int threads = 256;
+  for (int j = 0; j < 2 * R * 8 / threads; ++j)
+    for (int tid = 0; tid < threads; ++tid) {
+      const int row = tid / 8 + j * (threads / 8), c = (tid & 7) ^ (tid / 8 & 7);
+      if (mm_piece(row, c) != j * threads + tid) return bad("mx matmul piece of row %lld, thread %lld", row, tid);
+    }
+  for (int c = 0; c < 8; ++c)
+    for (int r = 0; r < 2 * R; r += 8) {
+      unsigned seen = 0;
+      for (int i = 0; i < 8; ++i) seen |= 1u << (mm_piece(r + i, c) & 7);
+      if (seen != 0xff) return bad("mx matmul piece %lld of rows from %lld", c, r);
+    }
+  return hipSuccess;
+}
+
 hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t) {
   dry_launch();
   if (a.T < 1 || a.m < 1 || a.n % kMxBlock || a.ldy < a.m) return bad("mx matmul geometry (%lld x %lld)", a.T, a.m);
+  if (a.tile) return walk_tiles(a);
+  if (a.T <= 64) {
+    const int rows = mm_stream_rows(a);
+    if ((rows != 16 && rows != 32) || (a.m + rows - 1) / rows >= (int64_t)1 << 31)
+      return bad("mx matmul stream of %lld rows", a.m, 0);
+  } else if (((a.T + 15) / 16) * ((a.m + 15) / 16) >= (int64_t)1 << 31) {
+    return bad("mx matmul grid (%lld x %lld)", a.T, a.m);
+  }
   return hipSuccess;
 }
 

@@ -1,19 +1,29 @@
 // Attention of one new token per sequence over the paged 4-bit cache
 // (layout: KvPage in mx.h).
 //
-// Per key-value head the scores and the output are products on the bfloat16
-// matrix instructions, S^T = K Q^T and O^T = V^T P^T, with the query heads of
-// the group as columns.  Codes times their scale are exact in bfloat16; each
-// query and each probability enters as a pair of bfloat16 (its rounding and
-// the rest), the pair in columns c and c + 8, so products keep 16 bits and
-// more of them; sums, maxima and normalisers are float32.
+// Per key-value head the scores are products S^T = K Q^T on the scaled matrix
+// instructions: the keys' codes and scale bytes as they lie in the cache, the
+// queries of the group as columns, each in four 8-bit floating-point pieces
+// (at_pieces) of which columns c and c + 8 of two products hold one each.  The
+// output is O^T = V^T P^T on the bfloat16 ones: a value's code times its scale
+// is exact in bfloat16, and a probability is a pair of bfloat16 (its upper 16
+// bits and the rest), in columns c and c + 8 again.  Sums, maxima and
+// normalisers are float32.
 //
-// Lane l = 16 g + c of a wavefront: of 16 keys x D it holds key c, dimensions
-// [g D/4, (g + 1) D/4) as the A operand of the scores; the scores come out as
-// column c, keys 4 g + i, which is where the B operand of O^T wants the
-// probabilities when the values' A operand takes keys 4 g + i as well: nothing
-// moves between lanes in between.  The values of four keys lie together in the
-// cache for that reason.
+// Lane l = 16 g + c of a wavefront holds block g of key c as the A operand of
+// the scores; these come out as column c, keys 4 g + i, which is where the B
+// operand of O^T wants the probabilities when the values' A operand takes keys
+// 4 g + i as well: nothing moves between lanes in between.  The values of four
+// keys lie together in the cache for that reason.
+//
+// A tile is 128 keys of one unit (workgroup: four wavefronts, 32 keys each);
+// which workgroup takes which tiles: kAtLead in mx.h.  64 query heads over 8
+// of 128: 4 sequences of 131072 tokens take 120 us, 4.7 TB/s of the cache,
+// bound by memory; 96 of 17 to 16384 tokens 72 us, 3.5 TB/s, the rest being
+// what beginning and joining 768 units takes.  With the keys converted and the
+// queries in pairs of bfloat16 the two took 139 and 84 us; fetching a tile
+// ahead takes more registers than four workgroups a compute unit leave (135 us
+// where the kernel took 111 without).
 #include "mx_dev.h"
 
 namespace brq {

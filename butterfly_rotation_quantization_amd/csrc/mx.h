@@ -15,6 +15,7 @@ namespace brq {
 constexpr int kMxBlock = 32;      // values that share a scale
 constexpr int kMxPerLane = 8;
 constexpr int kMxThreads = 256;   // four wavefronts per workgroup
+constexpr int64_t kMxMost = (int64_t)1 << 34;  // values of a call: within 2^32 threads a launch
 
 // ---- quantize / dequantize (mx.hip)
 
@@ -72,6 +73,12 @@ struct MmArgs {
 
 constexpr int kMmK = 256;  // values of a row per stage
 
+// Launches within 2^32 threads (at most 64 per 16 x 16 outputs, 32 per row).
+inline bool mm_supported(int64_t T, int64_t m, int64_t n) {
+  const int64_t most = (int64_t)1 << 28;
+  return T <= most && m <= most && n <= most && (m == 0 || T <= kMxMost / 2 / m);
+}
+
 // Kernel and workspace of a product (a.T, a.m, a.n set): returns the
 // workspace bytes.
 inline size_t mm_plan(MmArgs& a, uint8_t* ws) {
@@ -90,11 +97,16 @@ inline size_t mm_plan(MmArgs& a, uint8_t* ws) {
   a.stages = (int)((a.n + kMmK - 1) / kMmK);
   a.gt = (a.T + a.tile - 1) / a.tile;
   a.go = (a.m + a.tile - 1) / a.tile;
-  // Too few tiles for the chip: the long axis in parts of eight stages or more.
+  // Too few tiles for the chip: the long axis in parts, of eight stages or more
+  // up to a workgroup for each compute unit, of 28 or more up to two (their
+  // sums written and read cost what shorter parts save: 384x4096 by 8192, 2
+  // parts 24 us, 4 parts 27; by 65536, 2 parts 120 us, 5 parts 97;
+  // 128x8192x28672, 2, 4 and 8 parts 62, 50 and 53 us).
   a.per = a.stages;
   if (a.tile == 128 && tiles(128) <= 256) {
-    const int64_t want = 512 / tiles(128), most = a.stages / 8;
-    const int64_t parts = want < most ? want : most;
+    auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
+    const int64_t one = least(256 / tiles(128), a.stages / 8), two = least(512 / tiles(128), a.stages / 28);
+    const int64_t parts = one > two ? one : two;
     if (parts > 1) a.per = (int)((a.stages + parts - 1) / parts);
   }
   a.splits = (a.stages + a.per - 1) / a.per;
@@ -106,6 +118,40 @@ inline size_t mm_plan(MmArgs& a, uint8_t* ws) {
   a.part = reinterpret_cast<float*>(a.os + a.go * image);
   return (size_t)((a.gt + a.go) * image) + (a.splits > 1 ? (size_t)a.splits * a.T * a.m * sizeof(float) : 0);
 }
+
+// Index arithmetic of the tile kernels.
+
+// A workgroup's tile and part.  Blocks go to the XCDs in turn, so those with
+// one remainder by 8 take consecutive places, whose tiles share operands; a
+// place is a part, in it a band of rows of tiles, in it the rows fastest.
+// False: no tile for this workgroup.
+struct MmWhere {
+  int64_t tt, to;  // the tile, along tokens and outputs
+  int part;
+};
+__host__ __device__ inline bool mm_where(const MmArgs& a, uint32_t block, MmWhere& w) {
+  int64_t p = (int64_t)(block & 7) * a.per_xcd + (block >> 3);
+  if (p >= a.gt * a.go * a.splits) return false;
+  w.part = (int)(p / (a.gt * a.go));
+  p -= w.part * (a.gt * a.go);
+  const int64_t band = p / ((int64_t)a.band * a.go);
+  const int64_t q = p - band * a.band * a.go;
+  const int64_t h = a.gt - band * a.band < a.band ? a.gt - band * a.band : a.band;  // rows of tiles in this band
+  w.tt = band * a.band + q % h;
+  w.to = q / h;
+  return true;
+}
+// Place in LDS of 16-byte piece c of row r, in pieces: eight consecutive rows'
+// pieces c lie in eight different places, so that a read of piece c by 32
+// rows meets each bank equally often.  XOR: piece of place, too.
+__host__ __device__ constexpr int mm_piece(int r, int c) { return r * 8 + (c ^ (r & 7)); }
+// Place of the scale of block c of row r in a stage of a tile of R rows.
+__host__ __device__ constexpr int mm_scale_at(int R, int c, int r) { return (c * 32 + r % 32) * (R / 32) + r / 32; }
+
+// Rows of the weight per workgroup of the stream.  32 where that still gives
+// every compute unit one: the activations are read half as often (8192x28672:
+// 16 tokens 37 -> 30 us, 64 tokens 83 -> 53 us).
+inline int mm_stream_rows(const MmArgs& a) { return a.m >= 32 * 256 ? 32 : 16; }
 
 hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t s);
 
@@ -171,7 +217,7 @@ constexpr int kAtMaxBatch = 4096;  // sequences whose tiles are dealt out evenly
 // has kAtLead empty places, since beginning one (its queries, its join) takes
 // as long as some tiles: without them a workgroup got fourteen short sequences
 // where another got fourteen tiles of a long one, and 96 sequences of 17 to
-// 16384 tokens took 109 us where they take 80.  Workgroup w has places
+// 16384 tokens took 109 us where they take 71.  Workgroup w has places
 // [at_start(w), at_start(w + 1)).  A unit whose tiles lie within one workgroup
 // is finished there; the parts of the others go to the workspace, two slots a
 // workgroup (a part from before its first place, one that it begins), and are

@@ -75,8 +75,7 @@ brq_status mx_setup(MxArgs& a, const brq_plan* right, int64_t rows, int64_t n, c
     *done = true;
     return BRQ_OK;
   }
-  if (n > ((int64_t)1 << 36) || rows > ((int64_t)1 << 36) / n)
-    return refuse(BRQ_ERR_UNSUPPORTED, "more than 2^36 values");
+  if (n > kMxMost || rows > kMxMost / n) return refuse(BRQ_ERR_UNSUPPORTED, "more than 2^34 values");
   if (!x || !codes || !scales) return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL data pointer");
   if (rows_misaligned(x, ld, t)) return refuse(BRQ_ERR_ALIGNMENT, "rows must be 16-byte aligned");
   if (misaligned(codes, 16) || misaligned(scales, 4))
@@ -131,8 +130,7 @@ brq_status brq_mx_dequantize(const brq_plan* right, const uint8_t* codes, const 
 }
 
 size_t brq_mx_matmul_workspace_bytes(int64_t T, int64_t m, int64_t n) {
-  const int64_t most = ((int64_t)1 << 31) - 1;
-  if (T <= 0 || m <= 0 || n <= 0 || T > most || m > most || n > most || n % kMxBlock) return 0;
+  if (T <= 0 || m <= 0 || n <= 0 || n % kMxBlock || !mm_supported(T, m, n)) return 0;
   MmArgs a;
   std::memset(&a, 0, sizeof a);
   a.T = T;
@@ -150,10 +148,8 @@ brq_status brq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const 
     return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad shape or leading dimension");
   if (n % kMxBlock)
     return refuse(BRQ_ERR_INVALID_ARGUMENT, "n = %lld must be a multiple of %d", (long long)n, kMxBlock);
-  const int64_t most = ((int64_t)1 << 31) - 1;
-  if (T > most || m > most || n > most) return refuse(BRQ_ERR_UNSUPPORTED, "a dimension above 2^31 - 1");
+  if (!mm_supported(T, m, n)) return refuse(BRQ_ERR_UNSUPPORTED, "T, m or n above 2^28, or more than 2^33 outputs");
   if (T == 0 || m == 0) return BRQ_OK;
-  if (((T + 15) / 16) * ((m + 15) / 16) > most) return refuse(BRQ_ERR_UNSUPPORTED, "an output above 2^39 values");
   if (!y || (n > 0 && (!a_codes || !a_scales || !b_codes || !b_scales)))
     return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL data pointer");
   if (misaligned(a_codes, 16) || misaligned(b_codes, 16) || misaligned(a_scales, 4) || misaligned(b_scales, 4))
@@ -214,7 +210,7 @@ brq_status kv_setup(KvArgs& a, const brq_plan* plan, const void* k, int64_t ldk,
     *done = true;
     return BRQ_OK;
   }
-  if (tokens > (((int64_t)1 << 31) - 1) / heads) return refuse(BRQ_ERR_UNSUPPORTED, "more than 2^31 - 1 rows");
+  if (tokens > kMxMost / row) return refuse(BRQ_ERR_UNSUPPORTED, "more than 2^34 values");
   if (!k || !v || !slots || (!cache && pages > 0)) return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL data pointer");
   if (rows_misaligned(k, ldk, t) || rows_misaligned(v, ldv, t))
     return refuse(BRQ_ERR_ALIGNMENT, "rows must be 16-byte aligned");

@@ -161,12 +161,9 @@ __global__ __launch_bounds__(64 * kMmWaves) void mm_rows_kernel(MmArgs a) {
 
 template <int TT>
 hipError_t mm_rows(const MmArgs& a, hipStream_t s) {
-  // 32 rows to a workgroup where that still gives every compute unit one: the
-  // activations are read half as often (8192x28672: 16 tokens 37 -> 30 us, 64
-  // tokens 83 -> 53 us).
-  const bool two = a.m >= 32 * 256;
-  const dim3 grid((unsigned)((a.m + (two ? 31 : 15)) / (two ? 32 : 16)));
-  if (two) mm_rows_kernel<TT, 2><<<grid, 64 * kMmWaves, 0, s>>>(a);
+  const int rows = mm_stream_rows(a);
+  const dim3 grid((unsigned)((a.m + rows - 1) / rows));
+  if (rows == 32) mm_rows_kernel<TT, 2><<<grid, 64 * kMmWaves, 0, s>>>(a);
   else mm_rows_kernel<TT, 1><<<grid, 64 * kMmWaves, 0, s>>>(a);
   return hipGetLastError();
 }
@@ -250,9 +247,9 @@ __device__ __forceinline__ void mm_to_lds(const void* base, uint32_t& off, uint3
 }
 
 // Scales of one operand in the order the tiles take them: for each tile of R
-// rows and each stage, [block][row % 32][row / 32], so that a stage's are one
-// run of 8 R bytes, fetched straight to LDS, in which a lane finds those of
-// its tiles in one word.  Read from the rows they are 8 bytes out of a line
+// rows and each stage, as mm_scale_at says, so that a stage's are one run of
+// 8 R bytes, fetched straight to LDS, in which a lane finds those of its tiles
+// in one word.  Read from the rows they are 8 bytes out of a line
 // for each row and stage (measured at 4096x8192x28672, rows read by the tile
 // kernel: 15% of its time; this pass: 1.5%).  Rows and blocks past the end
 // get zeros (2^-127, times codes of zero).  One workgroup: a tile, kMmRun
@@ -283,7 +280,7 @@ __device__ __forceinline__ void mm_scale_tile(const uint8_t* src, int64_t rows, 
   for (int e = tid; e < kMmRun * kMmKS * 32; e += kMxThreads) {
     const int r = e & 31, c = e >> 5, s = s0 + c / kMmKS;  // block c of the run
     if (s >= stages) break;
-    uint8_t* d = out + (tile * stages + s) * (8 * R) + (c % kMmKS * 32 + r) * (R / 32);
+    uint8_t* d = out + (tile * stages + s) * (8 * R) + mm_scale_at(R, c % kMmKS, r);
 #pragma unroll
     for (int q = 0; q < R / 128; ++q) {
       uint32_t w = 0;
@@ -324,8 +321,8 @@ struct MmTile {
   using Frag = MmFrag<TT, TO>;
 
   struct Lds {
-    uint4 codes[2][ROWS * 8];     // piece c of row r at r * 8 + (c ^ (r & 7))
-    uint8_t scales[2][ROWS * 8];  // [block][row % 32][tile], tokens first
+    uint4 codes[2][ROWS * 8];     // piece c of row r at mm_piece
+    uint8_t scales[2][ROWS * 8];  // mm_scale_at, tokens first
   };
 
   const MmArgs& a;
@@ -417,9 +414,9 @@ struct MmTile {
   template <int E>  // operand E of step k2: the first 64 values, tokens first, then the second
   __device__ __forceinline__ void read(Frag& f, int buf, int k2) const {
     constexpr int u = E / (TT + TO), e = E % (TT + TO);
-    const int c = (4 * k2 + 2 * u + lg) ^ (lr & 7);
-    if constexpr (e < TT) f.x[u][e] = *reinterpret_cast<const mxi4*>(&lds.codes[buf][(32 * (TT * wt + e) + lr) * 8 + c]);
-    else f.w[u][e - TT] = *reinterpret_cast<const mxi4*>(&lds.codes[buf][(BT + 32 * (TO * wo + e - TT) + lr) * 8 + c]);
+    const int c = 4 * k2 + 2 * u + lg;
+    if constexpr (e < TT) f.x[u][e] = *reinterpret_cast<const mxi4*>(&lds.codes[buf][mm_piece(32 * (TT * wt + e) + lr, c)]);
+    else f.w[u][e - TT] = *reinterpret_cast<const mxi4*>(&lds.codes[buf][mm_piece(BT + 32 * (TO * wo + e - TT) + lr, c)]);
   }
   __device__ __forceinline__ void read_scales(Frag& f, int buf, int k2) const {
 #pragma unroll
@@ -576,17 +573,11 @@ __global__ __launch_bounds__(64 * WT * WO, 1) void mm_tile_kernel(MmArgs a) {
   using Full = MmTile<WT, WO, TT, TO, true>;
   using Any = MmTile<WT, WO, TT, TO, false>;
   __shared__ typename Full::Lds lds;
-  // the workgroup's tile: consecutive ones, which share operands, on one XCD
-  int64_t p = (int64_t)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
-  if (p >= a.gt * a.go * a.splits) return;
-  const int part = (int)(p / (a.gt * a.go));
-  p -= part * (a.gt * a.go);
-  const int64_t band = p / ((int64_t)a.band * a.go);
-  const int64_t q = p - band * a.band * a.go;
-  const int64_t h = a.gt - band * a.band < a.band ? a.gt - band * a.band : a.band;  // rows of tiles in this band
-  const int64_t t0 = (band * a.band + q % h) * Full::BT, o0 = q / h * Full::BO;
-  if (t0 + Full::BT <= a.T && o0 + Full::BO <= a.m && a.n % kMmK == 0) Full(a, lds, t0, o0, part).run();
-  else Any(a, reinterpret_cast<typename Any::Lds&>(lds), t0, o0, part).run();
+  MmWhere w;
+  if (!mm_where(a, blockIdx.x, w)) return;
+  const int64_t t0 = w.tt * Full::BT, o0 = w.to * Full::BO;
+  if (t0 + Full::BT <= a.T && o0 + Full::BO <= a.m && a.n % kMmK == 0) Full(a, lds, t0, o0, w.part).run();
+  else Any(a, reinterpret_cast<typename Any::Lds&>(lds), t0, o0, w.part).run();
 }
 
 // Parts of the long axis, added in order.  W: outputs per thread.

@@ -401,7 +401,7 @@ brq_status brq_orp_geo_dequant(const uint8_t* codes, const uint8_t* signs, const
  *   out: device [rows][ldo], 16-byte aligned rows.
  * Errors of both: INVALID_ARGUMENT (dtype, shapes, n not a multiple of 32 or
  * of d, NULLs, plan of another device), UNSUPPORTED (the plan; rows * n above
- * 2^36), ALIGNMENT, HIP.  rows == 0 or n == 0 is a no-op. */
+ * 2^34), ALIGNMENT, HIP.  rows == 0 or n == 0 is a no-op. */
 brq_status brq_mx_quantize(const brq_plan* right, const void* x, int32_t xt, int64_t ldx,
                            int64_t rows, int64_t n, uint8_t* codes, uint8_t* scales,
                            void* stream);
@@ -417,13 +417,12 @@ brq_status brq_mx_dequantize(const brq_plan* right, const uint8_t* codes, const 
  *   a_codes [T][n/2], a_scales [T][n/32], b_codes [m][n/2], b_scales [m][n/32]
  *     (codes 16-byte, scales 4-byte aligned); y: device [T][ldy].
  *   ws: device workspace of brq_mx_matmul_workspace_bytes(T, m, n) bytes (16-byte
- *     aligned; may be NULL if that is 0): partial sums when the long axis n is
- *     split among workgroups.  The split depends on the sizes only, and the
+ *     aligned; may be NULL if that is 0): the scales in the order the kernel takes
+ *     them, and partial sums when the long axis n is split among workgroups.  The split depends on the sizes only, and the
  *     parts are added in order: a call's result does not vary.
  * T, m >= 0, n a multiple of 32 (n == 0: y = 0).  Errors: INVALID_ARGUMENT
- * (dtype, shapes, NULLs), UNSUPPORTED (T, m or n above 2^31 - 1, or an output
- * above 2^39 values), ALIGNMENT,
- * WORKSPACE, HIP. */
+ * (dtype, shapes, NULLs), UNSUPPORTED (T, m or n above 2^28, or more than
+ * 2^33 outputs), ALIGNMENT, WORKSPACE, HIP. */
 size_t brq_mx_matmul_workspace_bytes(int64_t T, int64_t m, int64_t n);
 brq_status brq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
                          const uint8_t* b_scales, int64_t T, int64_t m, int64_t n, void* y,
@@ -454,7 +453,7 @@ brq_status brq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const 
  * brq_kv_read is the inverse for any list of slots: dequantized, the plan
  * undone, rounded once to ot; a slot outside the cache reads as zeros.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED (head_dim, page, the plan; more than
- * 2^31 - 1 rows tokens * heads), ALIGNMENT (rows, cache 16 bytes), HIP.
+ * 2^34 values a tensor), ALIGNMENT (rows, cache 16 bytes), HIP.
  * tokens == 0 is a no-op. */
 size_t brq_kv_page_bytes(int32_t head_dim, int32_t page);
 brq_status brq_kv_append(const brq_plan* plan, const void* k, int64_t ldk, const void* v,
@@ -484,8 +483,10 @@ brq_status brq_kv_read(const brq_plan* plan, const uint8_t* cache, const int64_t
  *   ws: device workspace of brq_paged_attention_workspace_bytes(...) bytes
  *       (16-byte aligned): partial results where a sequence's length is split.
  * Lengths and tables are read on the device at each call, so a captured call
- * can be replayed while sequences grow.  Queries, probabilities and sums are
- * held in float32 (in pairs of bfloat16 where they enter the matrix units).
+ * can be replayed while sequences grow.  Maxima, normalisers and sums are held
+ * in float32.  Where they enter the matrix units a query has 16 bits (four
+ * 8-bit pieces, within 2^-17 of the largest magnitude of its block of 32) and a
+ * probability too (a pair of bfloat16).
  * Errors: INVALID_ARGUMENT (q_heads not a multiple of heads, NULLs, scale not
  * finite, window < 0), UNSUPPORTED (head_dim, page, the plan; more than 2^24
  * sequences times query heads), ALIGNMENT, WORKSPACE, HIP.  batch == 0 is a no-op. */

@@ -2,9 +2,11 @@
 reads it, against the oracle (oracle/mx.py).
 
 The cache's bytes are compared bit for bit.  Attention's bound: a query enters
-as a pair of bfloat16 (2^-17 of it lost at most) after a float32 transform
-((log2 D + 2) 2^-24 sqrt(D) of its largest entry, which the terms below cover
-with sqrt(D) to spare); a score's D terms are summed in float32 (2^-23 each at
+with 16 bits (as four 8-bit pieces, 2^-17 of its block's largest entry lost at
+most; the losses of a block's entries have either sign, and their sum stays
+under 2^-16 of the sum of magnitudes) after a float32 transform ((log2 D + 2)
+2^-24 sqrt(D) of its largest entry, which the terms below cover with sqrt(D) to
+spare); a score's D terms are summed in float32 (2^-23 each at
 most); so a score is off by e = (2^-16 + 2 D 2^-23) times its sum of |q_i k_i|.
 A probability then is off by a factor of exp(2 e), by 2^-17 of its pair and by
 a few 2^-22 of its exponential; sums run over at most n / 32 + 96 additions of
@@ -168,6 +170,14 @@ def test_single_long_sequence_is_split():
 def test_many_sequences():
     rng = np.random.default_rng(0)
     attend(rng.integers(0, 120, 300), 8, 4, 64, 16, True, "f16")
+
+
+def test_more_sequences_than_are_dealt_out():
+    """Above 4096 sequences each group of heads has a workgroup of its own."""
+    rng = np.random.default_rng(1)
+    lens = rng.integers(0, 40, 4100)
+    lens[77] = 700
+    attend(lens, 2, 1, 64, 16, True, "f32")
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])

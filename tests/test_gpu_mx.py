@@ -152,7 +152,10 @@ def check_product(got, a, b, n, dtype):
 
 SHAPES = [(1, 1, 32), (1, 4096, 4096), (1, 300, 28672), (2, 129, 96), (7, 256, 160), (16, 11008, 4000), (17, 64, 1024),
           (31, 1000, 352), (33, 48, 8192), (64, 512, 512), (65, 513, 544), (128, 256, 1376), (200, 384, 2048),
-          (256, 256, 256), (257, 770, 288), (333, 4096, 11008), (512, 1024, 768), (1030, 520, 640)]
+          (256, 256, 256), (257, 770, 288), (333, 4096, 11008), (512, 1024, 768), (1030, 520, 640),
+          # large tiles, ragged and whole; 32 weight rows a workgroup; rows too short for tiles
+          (2100, 4200, 544), (2101, 4197, 768), (9, 8200, 1056), (20, 8200, 352), (50, 8193, 544), (100, 70, 160),
+          (65, 17, 32)]
 
 
 @pytest.mark.parametrize("T,m,n", SHAPES)

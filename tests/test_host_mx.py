@@ -49,7 +49,8 @@ def test_quantize_refusals(dl):
 
 
 MM = [(1, 8192, 28672), (16, 11008, 4000), (17, 130, 96), (333, 4096, 11008), (1, 1, 32), (5, 3, 0), (2049, 513, 160),
-      (4096, 8192, 28672), (300, 16384, 256), (64, 128, 65536)]
+      (4096, 8192, 28672), (300, 16384, 256), (64, 128, 65536), (2101, 4197, 768), (50, 8193, 544), (100, 70, 160),
+      (1 << 16, 1 << 17, 4096), (70, 1 << 26, 256), (1, 1 << 28, 64), (1 << 17, 1 << 16, 128), (1 << 28, 32, 32), (100, 300, 1 << 23), (65, 128, (1 << 23) + 32)]
 
 
 @pytest.mark.parametrize("T,m,n", MM)
@@ -78,6 +79,10 @@ def test_matmul_refusals(dl):
     assert f(a=CODES + 4) == ALIGNMENT and f(b=B2 + 8) == ALIGNMENT
     assert f(sa=SCALES + 1) == ALIGNMENT and f(sb=S2 + 2) == ALIGNMENT and f(y=Y + 1) == ALIGNMENT
     assert f(m=1 << 31, ldy=1 << 31) == UNSUPPORTED
+    # more threads than a launch can have
+    assert f(T=(1 << 28) + 1) == UNSUPPORTED and f(m=(1 << 28) + 1, ldy=1 << 29) == UNSUPPORTED
+    assert f(T=1 << 17, m=(1 << 16) + 1, ldy=1 << 17) == UNSUPPORTED and f(n=(1 << 28) + 32) == UNSUPPORTED
+    assert dl.brq_mx_matmul_workspace_bytes(1 << 17, (1 << 16) + 1, 128) == 0
 
 
 def test_page_bytes(dl):
