@@ -554,11 +554,23 @@ def orp_geo_dequant(codes, signs, coef, m: int, n: int, bits: int, group: int, s
 # GPU's to find.
 
 def _stream_of(stream, t) -> int:
-    """The raw stream: the one given, or the current one of t's GPU."""
-    if stream is not None:
-        return _stream(stream)
+    """The raw stream: the one given, or the current one of t's GPU, which has to
+    be the current GPU (a kernel launched on another one's stream 0 would run here)."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    dev = t.get_device()
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on GPU {dev}, which is not the current one")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _scratch(stream, ws):
+    """A workspace made for one call, marked as used by the call's stream: on
+    another stream than the current one its memory is not handed out again
+    before that stream is done with it."""
+    if ws is not None and stream is not None:
+        import torch
+        ws.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    return ws
 
 
 def _rows(t) -> tuple:
@@ -633,8 +645,8 @@ def mx_matmul(a_codes, a_scales, b_codes, b_scales, y=None, out_dtype=None, ws=N
     elif y.shape != (T, m):
         raise ValueError(f"y: expected shape {(T, m)}, got {tuple(y.shape)}")
     if ws is None:
-        ws = mx_matmul_workspace(T, m, n, a_codes.device)
-    wp, wb = (None, 0) if ws is None else _ws_args(ws)
+        ws = _scratch(stream, mx_matmul_workspace(T, m, n, a_codes.device))
+    wp, wb = _ws_args(ws)
     check(lib().brq_mx_matmul(_packed(a_codes, uint8, (T, n // 2), "a_codes"),
                               _packed(a_scales, uint8, (T, n // 32), "a_scales"),
                               _packed(b_codes, uint8, (m, n // 2), "b_codes"),
@@ -729,8 +741,8 @@ def paged_attention(plan: Optional[Plan], q, cache, table, lens, page: int, scal
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and dtype")
     if ws is None:
-        ws = paged_attention_workspace(B, hq, h, D, q.device)
-    wp, wb = (None, 0) if ws is None else _ws_args(ws)
+        ws = _scratch(stream, paged_attention_workspace(B, hq, h, D, q.device))
+    wp, wb = _ws_args(ws)
     check(lib().brq_paged_attention(
         None if plan is None else plan._h, q.data_ptr(), ldq, dtype_code(q), _cache_ptr(cache, h, D, page),
         cache.shape[0], _packed(table, int32, (B, pages), "table"), pages, _packed(lens, int32, (B,), "lens"),

@@ -267,6 +267,44 @@ def test_another_stream_and_a_graph():
             assert torch.equal(y, eager), f"replay {r} differs"
 
 
+def test_a_workspace_made_for_another_stream_outlives_the_call(monkeypatch):
+    """The memory of a workspace that the binding made is not handed out again
+    while the stream it was made for still has the call ahead of it."""
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce("mx workspaces on another stream")
+    made = []
+
+    def note(f):
+        def g(*args):
+            made.append(f(*args))
+            return made[-1]
+        return g
+    monkeypatch.setattr(brq, "mx_matmul_workspace", note(brq.mx_matmul_workspace))
+    monkeypatch.setattr(brq, "paged_attention_workspace", note(brq.paged_attention_workspace))
+    a, b = [brq.mx_quantize(None, torch.randn((300, 4096), device="cuda")) for _ in range(2)]
+    cache, table = brq.kv_cache(4, 2, 128, 64), torch.zeros((3, 1), dtype=torch.int32, device="cuda")
+    lens, q = torch.full((3,), 50, dtype=torch.int32, device="cuda"), torch.randn((3, 4, 128), device="cuda")
+    want = brq.mx_matmul(*a, *b), brq.paged_attention(None, q, cache, table, lens, 64)
+    out = torch.empty_like(want[0]), torch.empty_like(want[1])
+    made.clear()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(200_000_000)
+        brq.mx_matmul(*a, *b, y=out[0], stream=stream)
+        brq.paged_attention(None, q, cache, table, lens, 64, out=out[1], stream=stream)
+        spans = [(w.data_ptr(), w.numel()) for w in made]
+        made.clear()
+        others = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in spans]
+        assert not s.query(), "the stream was to be busy still"
+        for p, n in spans:
+            assert all(o.data_ptr() + o.numel() <= p or p + n <= o.data_ptr() for o in others)
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
 def test_binding_refuses_other_layouts():
     import butterfly_rotation_quantization_amd as brq
     import torch
