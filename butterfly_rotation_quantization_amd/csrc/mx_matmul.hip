@@ -47,7 +47,6 @@ __global__ __launch_bounds__(64) void mm_simple_kernel(MmArgs a) {
 
 // ---- few tokens: a stream over the weight
 
-constexpr int kMmWaves = 8;      // wavefronts of a workgroup, which share its rows
 constexpr int kMmChunk = 512;    // values of a row a wavefront takes at a time
 
 // 512 values of 16 rows: lane l holds blocks 4 s + l / 16 of row l % 16.
@@ -83,13 +82,13 @@ __device__ __forceinline__ int mm_scale_of(const uint4& v, int s, int sh) {
   return (int)(w >> sh);
 }
 
-// 16 RT outputs, up to 16 TT tokens.  The workgroup's wavefronts take chunks
+// 16 RT outputs, up to 16 TT tokens.  The workgroup's W wavefronts take chunks
 // of its weight rows in turn, 2 KB of each row in flight at a time, and join
 // their sums in LDS: the weight is read once, in one launch.  Bound by memory:
-// one token at 8192x28672 24 us, 5.2 TB/s of the weight.
-template <int TT, int RT>
-__global__ __launch_bounds__(64 * kMmWaves) void mm_rows_kernel(MmArgs a) {
-  __shared__ float sums[kMmWaves][RT][TT][16][17];
+// one token at 8192x28672 23 us, 5.4 TB/s of the weight.
+template <int TT, int RT, int W>
+__global__ __launch_bounds__(64 * W) void mm_rows_kernel(MmArgs a) {
+  __shared__ float sums[W][RT][TT][16][17];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lg = lane >> 4, sh = 8 * lg;
   const int64_t o0 = (int64_t)blockIdx.x * (16 * RT), nb = a.n / kMxBlock;
@@ -118,7 +117,7 @@ __global__ __launch_bounds__(64 * kMmWaves) void mm_rows_kernel(MmArgs a) {
 #pragma unroll
     for (int i = 0; i < RT; ++i) mm_chunk(w[i], wrow[i], wsrow[i], k, nb, lg);
   while (k < nb) {
-    const int64_t next = k + kMmWaves * B;
+    const int64_t next = k + W * B;
     MmChunk wn[RT];
 #pragma unroll
     for (int j = 0; j < TT; ++j) mm_chunk(x[j], xrow[j], xsrow[j], k, nb, lg);
@@ -129,12 +128,12 @@ __global__ __launch_bounds__(64 * kMmWaves) void mm_rows_kernel(MmArgs a) {
     for (int s = 0; s < 4; ++s)
 #pragma unroll
       for (int j = 0; j < TT; ++j) {
-        const mxi8 X = {x[j].c[s][0], x[j].c[s][1], x[j].c[s][2], x[j].c[s][3], 0, 0, 0, 0};
+        const mxi8 A8 = {x[j].c[s][0], x[j].c[s][1], x[j].c[s][2], x[j].c[s][3], 0, 0, 0, 0};
         const int sx = mm_scale_of(x[j].s, s, sh);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-          const mxi8 W = {w[i].c[s][0], w[i].c[s][1], w[i].c[s][2], w[i].c[s][3], 0, 0, 0, 0};
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(W, X, acc[i][j], 4, 4, 0,
+          const mxi8 B8 = {w[i].c[s][0], w[i].c[s][1], w[i].c[s][2], w[i].c[s][3], 0, 0, 0, 0};
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(B8, A8, acc[i][j], 4, 4, 0,
                                                                        mm_scale_of(w[i].s, s, sh), 0, sx);
         }
       }
@@ -149,22 +148,26 @@ __global__ __launch_bounds__(64 * kMmWaves) void mm_rows_kernel(MmArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) sums[wave][i][j][lr][4 * lg + e] = acc[i][j][e];  // token lr, output 4 lg + e
   __syncthreads();
-  for (int e = tid; e < 256 * TT * RT; e += 64 * kMmWaves) {
+  for (int e = tid; e < 256 * TT * RT; e += 64 * W) {
     const int c = e & 15, i = (e >> 4) % RT, t = (e >> 4) / RT, j = t >> 4;  // a token's outputs on consecutive lanes
     float v = sums[0][i][j][t & 15][c];
 #pragma unroll
-    for (int u = 1; u < kMmWaves; ++u) v += sums[u][i][j][t & 15][c];
+    for (int u = 1; u < W; ++u) v += sums[u][i][j][t & 15][c];
     const int64_t o = o0 + 16 * i + c;
     if (t < a.T && o < a.m) mm_store(a.y, a.yt, t * a.ldy + o, v);
   }
 }
 
+template <int TT, int RT>
+void mm_rows(const MmArgs& a, hipStream_t s) {
+  const int64_t wgs = (a.m + 16 * RT - 1) / (16 * RT);
+  if (mm_stream_waves(wgs) == 8) mm_rows_kernel<TT, RT, 8><<<dim3((unsigned)wgs), 512, 0, s>>>(a);
+  else mm_rows_kernel<TT, RT, 4><<<dim3((unsigned)wgs), 256, 0, s>>>(a);
+}
 template <int TT>
 hipError_t mm_rows(const MmArgs& a, hipStream_t s) {
-  const int rows = mm_stream_rows(a);
-  const dim3 grid((unsigned)((a.m + rows - 1) / rows));
-  if (rows == 32) mm_rows_kernel<TT, 2><<<grid, 64 * kMmWaves, 0, s>>>(a);
-  else mm_rows_kernel<TT, 1><<<grid, 64 * kMmWaves, 0, s>>>(a);
+  if (mm_stream_rows(a) == 32) mm_rows<TT, 2>(a, s);
+  else mm_rows<TT, 1>(a, s);
   return hipGetLastError();
 }
 
