@@ -309,9 +309,9 @@ struct MmFrag {
 };
 
 // One workgroup's tile, WT x WO wavefronts of TT x TO tiles of 32 tokens x 32
-// outputs.  FULL: no row of the tile is past the end and rows are whole
+// outputs; NB stages in LDS.  FULL: no row of the tile is past the end and rows are whole
 // stages, so that a piece takes three instructions to fetch.
-template <int WT, int WO, int TT, int TO, bool FULL>
+template <int WT, int WO, int TT, int TO, int NB, bool FULL>
 struct MmTile {
   static constexpr int NTH = 64 * WT * WO;
   static constexpr int BT = 32 * TT * WT, BO = 32 * TO * WO, ROWS = BT + BO;
@@ -324,8 +324,8 @@ struct MmTile {
   using Frag = MmFrag<TT, TO>;
 
   struct Lds {
-    uint4 codes[2][ROWS * 8];     // piece c of row r at mm_piece
-    uint8_t scales[2][ROWS * 8];  // mm_scale_at, tokens first
+    uint4 codes[NB][ROWS * 8];     // piece c of row r at mm_piece
+    uint8_t scales[NB][ROWS * 8];  // mm_scale_at, tokens first
   };
 
   const MmArgs& a;
@@ -447,8 +447,8 @@ struct MmTile {
       first_step<BUF, X + 1>(f, g);
     }
   }
-  // Its second step: the products of g; between them, the pieces of the stage
-  // after next into buffer BUF; half way, once the next stage has arrived (all
+  // Its second step: the products of g; between them, the pieces of stage
+  // s + NB into buffer BUF; half way, once the next stage has arrived (all
   // but this step's fetches so far), the reads of f, the operands of its first
   // step.  Waiting this late leaves a fetch 3/4 of a stage at least (half
   // way through the stage, with the reads spread over the step: 488 us where
@@ -459,14 +459,15 @@ struct MmTile {
       constexpr int H = NM / 2, Y = X < H ? 0 : X - H;
       constexpr int e0 = Y * NG / H, e1 = X < H ? 0 : (Y + 1) * NG / H;
       constexpr int j0 = X * NL / NM, j1 = (X + 1) * NL / NM;
+      constexpr int next = (BUF + 1) % NB;
       if constexpr (X == H) {
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(1 + NL / 2) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NB - 2) * (1 + NL) + 1 + NL / 2) : "memory");
         __syncthreads();
-        read_scales(f, BUF ^ 1, 0);
+        read_scales(f, next, 0);
       }
       multiply<X>(g);
-      if constexpr (e1 > e0) read<e0>(f, BUF ^ 1, 0);
-      if constexpr (e1 > e0 + 1) read<e0 + 1>(f, BUF ^ 1, 0);
+      if constexpr (e1 > e0) read<e0>(f, next, 0);
+      if constexpr (e1 > e0 + 1) read<e0 + 1>(f, next, 0);
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (j1 > j0) fetch<BUF, j0>(src);
       if constexpr (j1 > j0 + 1) fetch<BUF, j0 + 1>(src);
@@ -487,6 +488,16 @@ struct MmTile {
       fetch_all<BUF, J + 1>(f);
     }
   }
+  // The first NB stages, into their buffers.
+  template <int BUF>
+  __device__ __forceinline__ void begin(Source& src) const {
+    if constexpr (BUF < NB) {
+      src = source(BUF);
+      fetch_scales<BUF>(BUF);
+      fetch_all<BUF, 0>(src);
+      begin<BUF + 1>(src);
+    }
+  }
   template <int E>
   __device__ __forceinline__ void read_all(Frag& f, int buf, int k2) const {
     if constexpr (E < NG) {
@@ -495,7 +506,7 @@ struct MmTile {
     }
   }
 
-  // Stage s, in buffer BUF, which is free for stage s + 2 once every wavefront
+  // Stage s, in buffer BUF, which is free for stage s + NB once every wavefront
   // has its second step's operands.
   template <int BUF>
   __device__ __forceinline__ void stage(int s, Frag& f0, Frag& f1, Source& src) {
@@ -503,8 +514,8 @@ struct MmTile {
     __builtin_amdgcn_sched_barrier(0);
     first_step<BUF, 0>(f0, f1);
     __syncthreads();
-    src = source(s + 2);
-    fetch_scales<BUF>(s + 2);
+    src = source(s + NB);
+    fetch_scales<BUF>(s + NB);
     __builtin_amdgcn_sched_barrier(0);
     second_step<BUF, 0>(f1, f0, src);
   }
@@ -516,23 +527,24 @@ struct MmTile {
       for (int j = 0; j < TT; ++j)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-    Source src = source(0);
-    fetch_all<0, 0>(src);
-    fetch_scales<0>(0);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    Source src;
+    begin<0>(src);
+    // all but the first stage may be on their way still
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NB - 1) * (1 + NL)) : "memory");
     __syncthreads();
     Frag f0, f1;
     read_scales(f0, 0, 0);
     read_all<0>(f0, 0, 0);
-    src = source(1);
-    fetch_scales<1>(1);
-    fetch_all<1, 0>(src);
     int s = 0;
-    for (; s + 1 < stages; s += 2) {
+    for (; s + NB <= stages; s += NB) {
       stage<0>(s, f0, f1, src);
       stage<1>(s + 1, f0, f1, src);
+      if constexpr (NB > 2) stage<2>(s + 2, f0, f1, src);
     }
     if (s < stages) stage<0>(s, f0, f1, src);
+    if constexpr (NB > 2) {
+      if (s + 1 < stages) stage<1>(s + 1, f0, f1, src);
+    }
     mm_settle();
     // LDS is about to hold the sums: the last pieces, fetched for no stage,
     // have to be in it before, and every wavefront's reads done
@@ -571,10 +583,10 @@ struct MmTile {
   }
 };
 
-template <int WT, int WO, int TT, int TO>
+template <int WT, int WO, int TT, int TO, int NB>
 __global__ __launch_bounds__(64 * WT * WO, 1) void mm_tile_kernel(MmArgs a) {
-  using Full = MmTile<WT, WO, TT, TO, true>;
-  using Any = MmTile<WT, WO, TT, TO, false>;
+  using Full = MmTile<WT, WO, TT, TO, NB, true>;
+  using Any = MmTile<WT, WO, TT, TO, NB, false>;
   __shared__ typename Full::Lds lds;
   MmWhere w;
   if (!mm_where(a, blockIdx.x, w)) return;
@@ -609,7 +621,7 @@ hipError_t mm_join(const MmArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int WT, int WO, int TT, int TO>
+template <int WT, int WO, int TT, int TO, int NB>
 hipError_t mm_tiles(const MmArgs& a, hipStream_t s) {
   constexpr int BT = 32 * TT * WT, BO = 32 * TO * WO;
   static_assert(BT == BO && (BT == 128 || BT == 256), "mm_plan's tiles");
@@ -617,7 +629,7 @@ hipError_t mm_tiles(const MmArgs& a, hipStream_t s) {
   mm_scales_kernel<BT, BO><<<dim3((unsigned)(a.gt + a.go), (unsigned)runs), kMxThreads, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  mm_tile_kernel<WT, WO, TT, TO><<<dim3((unsigned)(8 * a.per_xcd)), 64 * WT * WO, 0, s>>>(a);
+  mm_tile_kernel<WT, WO, TT, TO, NB><<<dim3((unsigned)(8 * a.per_xcd)), 64 * WT * WO, 0, s>>>(a);
   e = hipGetLastError();
   return e != hipSuccess || a.splits == 1 ? e : mm_join(a, s);
 }
@@ -625,8 +637,11 @@ hipError_t mm_tiles(const MmArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t s) {
-  if (a.tile == 256) return mm_tiles<2, 2, 4, 4>(a, s);
-  if (a.tile == 128) return mm_tiles<2, 2, 2, 2>(a, s);
+  if (a.tile == 256) return mm_tiles<2, 2, 4, 4, 2>(a, s);
+  // a compute unit that has one workgroup has LDS for a third stage
+  // (65x8192x28672: 48 -> 44 us, 128: 50 -> 48.5)
+  if (a.tile == 128 && a.gt * a.go * a.splits <= 256) return mm_tiles<2, 2, 2, 2, 3>(a, s);
+  if (a.tile == 128) return mm_tiles<2, 2, 2, 2, 2>(a, s);
   if (a.T <= 16) return mm_rows<1>(a, s);
   if (a.T <= 32) return mm_rows<2>(a, s);
   if (a.T <= 64) return mm_rows<4>(a, s);
