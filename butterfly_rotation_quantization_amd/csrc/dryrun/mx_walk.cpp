@@ -78,19 +78,20 @@ static hipError_t walk_tiles(const MmArgs& a) {
       if (at < 0 || at >= 8 * R || cover[(size_t)at]++ || at != mm_scale_at(R, c, r % 32) + r / 32)
         return bad("mx matmul scale of block %lld, row %lld", c, r);
     }
-  // codes in LDS: thread tid brings piece (tid & 7) ^ (row & 7) of row tid / 8
-  // + 32 j to its own 16 bytes; eight rows' pieces c are in different places
+  // codes in LDS: thread tid brings piece (tid & 7) ^ (row / 2 & 7) of row tid / 8
+  // + 32 j to its own 16 bytes; sixteen rows' pieces c are in different places
+  // of 256 bytes
   const int threads = 256;
   for (int j = 0; j < 2 * R * 8 / threads; ++j)
     for (int tid = 0; tid < threads; ++tid) {
-      const int row = tid / 8 + j * (threads / 8), c = (tid & 7) ^ (tid / 8 & 7);
+      const int row = tid / 8 + j * (threads / 8), c = (tid & 7) ^ (tid / 16 & 7);
       if (mm_piece(row, c) != j * threads + tid) return bad("mx matmul piece of row %lld, thread %lld", row, tid);
     }
   for (int c = 0; c < 8; ++c)
-    for (int r = 0; r < 2 * R; r += 8) {
+    for (int r = 0; r < 2 * R; r += 16) {
       unsigned seen = 0;
-      for (int i = 0; i < 8; ++i) seen |= 1u << (mm_piece(r + i, c) & 7);
-      if (seen != 0xff) return bad("mx matmul piece %lld of rows from %lld", c, r);
+      for (int i = 0; i < 16; ++i) seen |= 1u << (mm_piece(r + i, c) & 15);
+      if (seen != 0xffff) return bad("mx matmul piece %lld of rows from %lld", c, r);
     }
   return hipSuccess;
 }

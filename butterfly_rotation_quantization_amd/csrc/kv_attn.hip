@@ -549,15 +549,21 @@ __global__ __launch_bounds__(kAtThreads) void at_join_kernel(AtArgs a, int rows)
   if (e0 == 0) *reinterpret_cast<float2*>(&os[tid / LPH][D]) = make_float2(M, L);
   __syncthreads();
   if (grp != 0 || !mine) return;
+  // the maximum first, so that the parts' factors do not wait for one another
+  const float own = M;
+#pragma unroll 4
+  for (int s = 1; s < groups; ++s) M = fmaxf(M, os[tid / LPH + s * rows][D]);
+  const float base = M == -INFINITY ? 0.f : M, f = __builtin_amdgcn_exp2f(own - base);
+  L *= f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] *= f;
+#pragma unroll 4
   for (int s = 1; s < groups; ++s) {
     const float* p = os[tid / LPH + s * rows];
-    const float2 ml = *reinterpret_cast<const float2*>(p + D);
-    const float m = fmaxf(M, ml.x), base = m == -INFINITY ? 0.f : m;
-    const float f = __builtin_amdgcn_exp2f(M - base), q = __builtin_amdgcn_exp2f(ml.x - base);
-    M = m;
-    L = L * f + ml.y * q;
+    const float q = __builtin_amdgcn_exp2f(p[D] - base);
+    L += p[D + 1] * q;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = o[e] * f + p[e0 + e] * q;
+    for (int e = 0; e < 8; ++e) o[e] += p[e0 + e] * q;
   }
   at_finish(a, b, h * a.group + h0 + r, e0, lane, o, M, L);
 }

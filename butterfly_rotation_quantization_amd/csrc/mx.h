@@ -141,10 +141,11 @@ __host__ __device__ inline bool mm_where(const MmArgs& a, uint32_t block, MmWher
   w.to = q / h;
   return true;
 }
-// Place in LDS of 16-byte piece c of row r, in pieces: eight consecutive rows'
-// pieces c lie in eight different places, so that a read of piece c by 32
-// rows meets each bank equally often.  XOR: piece of place, too.
-__host__ __device__ constexpr int mm_piece(int r, int c) { return r * 8 + (c ^ (r & 7)); }
+// Place in LDS of 16-byte piece c of row r, in pieces: the pieces c of sixteen
+// consecutive rows lie in sixteen different places of 256 bytes, the width of
+// the banks (by r & 7, eight of 128 bytes, half of the reads' cycles were
+// conflicts; 384x4096x65536 100 -> 99 us).  XOR: piece of place, too.
+__host__ __device__ constexpr int mm_piece(int r, int c) { return r * 8 + (c ^ (r >> 1 & 7)); }
 // Place of the scale of block c of row r in a stage of a tile of R rows.
 __host__ __device__ constexpr int mm_scale_at(int R, int c, int r) { return (c * 32 + r % 32) * (R / 32) + r / 32; }
 

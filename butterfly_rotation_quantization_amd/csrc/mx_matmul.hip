@@ -349,7 +349,7 @@ struct MmTile {
   __device__ __forceinline__ MmTile(const MmArgs& a_, Lds& l, int64_t t0_, int64_t o0_, int part)
       : a(a_), lds(l), tid(threadIdx.x), lane(tid & 63), wave(tid >> 6), lr(lane & 31), lg(lane >> 5), wt(wave % WT),
         wo(wave / WT), t0(t0_), o0(o0_), nb(a_.n / kMxBlock), ld(a_.n / 2),
-        first(part * a_.per), stages(a_.stages - first < a_.per ? a_.stages - first : a_.per), pr(tid >> 3), pc((tid & 7) ^ (pr & 7)),
+        first(part * a_.per), stages(a_.stages - first < a_.per ? a_.stages - first : a_.per), pr(tid >> 3), pc((tid & 7) ^ (pr >> 1 & 7)),
         lt((int)(a_.T - t0_ < BT ? a_.T - t0_ : BT) - 1), lo((int)(a_.m - o0_ < BO ? a_.m - o0_ : BO) - 1),
         base((uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)&l)),
         at(__builtin_amdgcn_readfirstlane(base + 16 * (tid & ~63))) {
