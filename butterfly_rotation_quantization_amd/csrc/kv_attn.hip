@@ -18,12 +18,15 @@
 //
 // A tile is 128 keys of one unit (workgroup: four wavefronts, 32 keys each);
 // which workgroup takes which tiles: kAtLead in mx.h.  64 query heads over 8
-// of 128: 4 sequences of 131072 tokens take 120 us, 4.7 TB/s of the cache,
-// bound by memory; 96 of 17 to 16384 tokens 72 us, 3.5 TB/s, the rest being
-// what beginning and joining 768 units takes.  With the keys converted and the
-// queries in pairs of bfloat16 the two took 139 and 84 us; fetching a tile
-// ahead takes more registers than four workgroups a compute unit leave (135 us
-// where the kernel took 111 without).
+// of 128: 4 sequences of 131072 tokens take 114 us, 5.0 TB/s of the cache,
+// bound by memory; 96 of 17 to 16384 tokens 67 us, 3.9 TB/s, the rest being
+// what beginning and joining 768 units takes.  The loads of the next 32 keys
+// are under way while these are worked on; that needs the queries in LDS
+// rather than in registers (in registers, with four workgroups a compute unit:
+// spilled, 132 and 88 us; without loads ahead 122 and 72).  With the keys
+// converted and the queries in pairs of bfloat16 the two took 139 and 84 us.
+#include <type_traits>
+
 #include "mx_dev.h"
 
 namespace brq {
@@ -149,8 +152,9 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
   __shared__ int found[1];
   __shared__ int64_t found_base[1];
   __shared__ uint8_t qb[H][4][D / 32];
-  uint8_t (*qs)[4][D] = reinterpret_cast<uint8_t (*)[4][D]>(&os[0]);
-  static_assert(sizeof(uint8_t[H][4][D]) <= sizeof(os), "the pieces lie where the sums will");
+  constexpr int QD = D + 16;  // a piece's row; the gap keeps a column's lanes on banks of their own
+  uint8_t (*qs)[4][QD] = reinterpret_cast<uint8_t (*)[4][QD]>(&os[0]);
+  static_assert(sizeof(uint8_t[H][4][QD]) <= sizeof(os), "the pieces lie where the sums will");
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
@@ -242,18 +246,63 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
 
   const int64_t pbytes = a.pg.bytes();
   const int32_t* row = a.table + b * a.ldt;
-  // the pages of 32 keys (16 of them share one); -1: no key there, or no page
-  int page[2];
-  auto look_up = [&](int k0) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int kk = k0 + 16 * t;
-      page[t] = kk < n ? row[kk >> a.lgP] : -1;
-    }
-  };
   int k0 = s0 + tb * kAtTile + wave * kAtKeys;
   const int kend = s0 + te * kAtTile < n ? s0 + te * kAtTile : n;
-  if (k0 < kend) look_up(k0);
+  // Operands of 32 keys, 16 of them from one page.  The next keys are fetched
+  // once the scores have used these, the next values once the output has, so
+  // each travels during the other's arithmetic without registers of its own.
+  // Where there is no key, or no page, page 0 is read and masked below: loads
+  // under no condition, or the wait for one would be a wait for all.
+  int page[2], pg[2];
+  bool ok[2];
+  mxi4 kw[2][NQ];
+  uint32_t vw[2][KW], vs[2];
+  int ks[2][NQ];
+  auto look_up = [&](int k) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) page[t] = row[(k + 16 * t < n ? k + 16 * t : n - 1) >> a.lgP];
+  };
+  auto fetch_keys = [&](int k) {  // looked up before; looks up the next
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      pg[t] = __builtin_amdgcn_readfirstlane(page[t]);
+      ok[t] = pg[t] >= 0 && pg[t] < a.pages && k + 16 * t < n;
+      pg[t] = ok[t] ? pg[t] : 0;
+      const uint8_t* pb = a.cache + ((int64_t)pg[t] * a.heads + h) * pbytes;
+      const int p = (k + 16 * t) & (a.pg.P - 1);
+#pragma unroll
+      for (int e = 0; e < NQ; ++e) {
+        const int blk = D == 64 ? (g & 1) : 4 * e + g;  // D = 64: both halves of the lanes hold the 64 values
+        kw[t][e] = *reinterpret_cast<const mxi4*>(pb + a.pg.kcode(p) + (uint32_t)(c * (D / 2) + 16 * blk));
+        ks[t][e] = pb[a.pg.kscale(p) + (uint32_t)(c * (D / 32) + blk)];
+      }
+    }
+    look_up(k + kAtTile);
+  };
+  auto fetch_values = [&](int k) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint8_t* pb = a.cache + ((int64_t)pg[t] * a.heads + h) * pbytes;
+      const int p = (k + 16 * t) & (a.pg.P - 1);
+      const uint8_t* vp = pb + a.pg.vcode(p, 0) + (uint32_t)(g * (2 * D) + c * (D / 8));
+      if constexpr (D == 64) {
+        const uint2 y = *reinterpret_cast<const uint2*>(vp);
+        vw[t][0] = y.x; vw[t][1] = y.y;
+      } else {
+#pragma unroll
+        for (int q = 0; q < KW / 4; ++q) {
+          const uint4 y = reinterpret_cast<const uint4*>(vp)[q];
+          vw[t][4 * q] = y.x; vw[t][4 * q + 1] = y.y; vw[t][4 * q + 2] = y.z; vw[t][4 * q + 3] = y.w;
+        }
+      }
+      vs[t] = *reinterpret_cast<const uint32_t*>(pb + a.pg.vscale(p, 0) + (uint32_t)(g * (D / 8) + (c * D / 512) * 4));
+    }
+  };
+  if (k0 < kend) {
+    look_up(k0);
+    fetch_keys(k0);
+    fetch_values(k0);
+  }
   // queries: rotated, times the scale, in pieces
   const float sl = a.scale * 1.44269504088896341f;  // scores in units of log2
   for (int r = tid / LPH; r < H; r += kAtThreads / LPH) {
@@ -281,7 +330,6 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
   // and its scale is that of block g.  With D = 64 one product takes all: the
   // second half of the words repeats dimensions 16 g .. with pieces 3 and 4,
   // as the keys' lanes repeat theirs.
-  mxi8 qf[NT][NQ][NP];
   int qsc[NT][NQ][NP];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -290,13 +338,15 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
 #pragma unroll
       for (int w = 0; w < NP; ++w) {
         const int r = 8 * t + (c & 7), k = (c >> 3) + 2 * w;
-        const mxi4 x = *reinterpret_cast<const mxi4*>(&qs[r][k][128 * e + 16 * g]);
-        const mxi4 y = D == 64 ? *reinterpret_cast<const mxi4*>(&qs[r][k + 2][16 * g])
-                               : *reinterpret_cast<const mxi4*>(&qs[r][k][128 * e + 64 + 16 * g]);
-        qf[t][e][w] = mxi8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
         qsc[t][e][w] = D == 64 ? qb[r][k + 2 * (g >> 1)][g & 1] : qb[r][k][4 * e + g];
       }
-  __syncthreads();
+  auto query = [&](int t, int e, int w) {
+    const int r = 8 * t + (c & 7), k = (c >> 3) + 2 * w;
+    const mxi4 x = *reinterpret_cast<const mxi4*>(&qs[r][k][128 * e + 16 * g]);
+    const mxi4 y = D == 64 ? *reinterpret_cast<const mxi4*>(&qs[r][k + 2][16 * g])
+                           : *reinterpret_cast<const mxi4*>(&qs[r][k][128 * e + 64 + 16 * g]);
+    return mxi8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+  };
 
   mxf4 o[NT][R], l[NT];
   float m[NT];
@@ -307,75 +357,31 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
 #pragma unroll
     for (int j = 0; j < R; ++j) o[t][j] = mxf4{0.f, 0.f, 0.f, 0.f};
   }
-  for (; k0 < kend; k0 += kAtTile) {
-    int pg[2];
-    bool ok[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      pg[t] = __builtin_amdgcn_readfirstlane(page[t]);
-      ok[t] = pg[t] >= 0 && pg[t] < a.pages;
-    }
-    mxi4 kw[2][NQ];
-    uint32_t vw[2][KW], vs[2];
-    int ks[2][NQ];
-    auto load = [&](int t) {
-      const uint8_t* pb = a.cache + ((int64_t)pg[t] * a.heads + h) * pbytes;
-      const int p = (k0 + 16 * t) & (a.pg.P - 1);
-#pragma unroll
-      for (int e = 0; e < NQ; ++e) {
-        const int blk = D == 64 ? (g & 1) : 4 * e + g;  // D = 64: both halves of the lanes hold the 64 values
-        kw[t][e] = *reinterpret_cast<const mxi4*>(pb + a.pg.kcode(p) + (uint32_t)(c * (D / 2) + 16 * blk));
-        ks[t][e] = pb[a.pg.kscale(p) + (uint32_t)(c * (D / 32) + blk)];
-      }
-      const uint8_t* vp = pb + a.pg.vcode(p, 0) + (uint32_t)(g * (2 * D) + c * (D / 8));
-      if constexpr (D == 64) {
-        const uint2 y = *reinterpret_cast<const uint2*>(vp);
-        vw[t][0] = y.x; vw[t][1] = y.y;
-      } else {
-#pragma unroll
-        for (int q = 0; q < KW / 4; ++q) {
-          const uint4 y = reinterpret_cast<const uint4*>(vp)[q];
-          vw[t][4 * q] = y.x; vw[t][4 * q + 1] = y.y; vw[t][4 * q + 2] = y.z; vw[t][4 * q + 3] = y.w;
-        }
-      }
-      vs[t] = *reinterpret_cast<const uint32_t*>(pb + a.pg.vscale(p, 0) + (uint32_t)(g * (D / 8) + (c * D / 512) * 4));
-    };
-    if (ok[0] && ok[1]) {
-      load(0);
-      load(1);
-    } else {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-#pragma unroll
-        for (int e = 0; e < NQ; ++e) {
-          kw[t][e] = mxi4{0, 0, 0, 0};
-          ks[t][e] = 127;
-        }
-#pragma unroll
-        for (int i = 0; i < KW; ++i) vw[t][i] = 0u;
-        vs[t] = 0x7f7f7f7fu;
-        if (ok[t]) load(t);
-      }
-    }
-    if (k0 + kAtTile < kend) look_up(k0 + kAtTile);  // the next keys' pages, ahead of their use
+  // One step of 32 keys.  The last one fetches nothing (and is code of its own:
+  // under a condition in the loop, the fetches would be waited for at once).
+  auto step = [&](auto last) {
+    constexpr bool more = !decltype(last)::value;
+    asm volatile("" ::: "memory");  // the queries stay in LDS
     // scores: column c, keys 16 t + 4 g + i
     float s[NT][2][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int u = 0; u < NT; ++u) {
+      mxf4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-      for (int u = 0; u < NT; ++u) {
-        mxf4 acc = {0.f, 0.f, 0.f, 0.f};
+      for (int e = 0; e < NQ; ++e)
 #pragma unroll
-        for (int e = 0; e < NQ; ++e) {
-          const mxi8 K = {kw[t][e][0], kw[t][e][1], kw[t][e][2], kw[t][e][3], 0, 0, 0, 0};
+        for (int w = 0; w < NP; ++w) {
+          const mxi8 Q = query(u, e, w);
 #pragma unroll
-          for (int w = 0; w < NP; ++w)
-            acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(K, qf[u][e][w], acc, 4, 0, 0, ks[t][e], 0,
-                                                                   qsc[u][e][w]);
+          for (int t = 0; t < 2; ++t) {
+            const mxi8 K = {kw[t][e][0], kw[t][e][1], kw[t][e][2], kw[t][e][3], 0, 0, 0, 0};
+            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(K, Q, acc[t], 4, 0, 0, ks[t][e], 0, qsc[u][e][w]);
+          }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[u][t][i] = acc[i] + at_ror8(acc[i]);
-      }
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[u][t][i] = acc[t][i] + at_ror8(acc[t][i]);
     }
     // masked keys: scores to -infinity, values to zero
     if (k0 < first || k0 + kAtKeys > n || !ok[0] || !ok[1]) {
@@ -397,6 +403,7 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
           }
         }
     }
+    if constexpr (more) fetch_keys(k0 + kAtTile);
     mxb8 pf[NT];
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
@@ -459,9 +466,13 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
         o[u][2 * q + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, pf[u], o[u][2 * q + 1], 0, 0, 0);
       }
     }
-  }
+    if constexpr (more) fetch_values(k0 + kAtTile);
+  };
+  for (; k0 + kAtTile < kend; k0 += kAtTile) step(std::false_type{});
+  if (k0 < kend) step(std::true_type{});
 
   // join the wavefronts: all parts to the common maximum, summed in order
+  __syncthreads();  // the sums go where the queries were
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const float sum = l[t][0] + at_ror8(l[t][0]);  // every row of the product is the column's sum

@@ -212,7 +212,6 @@ constexpr int kAtTile = kAtWaves * kAtKeys;
 constexpr int kAtCols = 8;        // query heads per 16 matrix columns (each as a high and a low part)
 
 constexpr int kAtMaxKeys = 1 << 30;
-constexpr int kAtMaxSplits = 64;
 
 constexpr int kAtMaxBatch = 4096;  // sequences whose tiles are dealt out evenly
 
@@ -223,12 +222,13 @@ constexpr int kAtMaxBatch = 4096;  // sequences whose tiles are dealt out evenly
 // has kAtLead empty places, since beginning one (its queries, its join) takes
 // as long as some tiles: without them a workgroup got fourteen short sequences
 // where another got fourteen tiles of a long one, and 96 sequences of 17 to
-// 16384 tokens took 109 us where they take 71.  Workgroup w has places
+// 16384 tokens took 109 us (with 1, 2, 3 and 4 places 85, 72, 67 and 66.5; 64
+// sequences of 1000 tokens 26, 26, 27 and 28).  Workgroup w has places
 // [at_start(w), at_start(w + 1)).  A unit whose tiles lie within one workgroup
 // is finished there; the parts of the others go to the workspace, two slots a
 // workgroup (a part from before its first place, one that it begins), and are
 // joined.
-constexpr int kAtLead = 2;
+constexpr int kAtLead = 4;
 __host__ __device__ inline int at_cost(int tiles) { return tiles > 0 ? tiles + kAtLead : 0; }
 // Workgroups that get places: no more than there are, so each has one.
 __host__ __device__ inline int at_dealt(int64_t total, int wgs) { return total < wgs ? (int)total : wgs; }

@@ -331,7 +331,8 @@ brq_status brq_paged_attention(const brq_plan* plan, const void* q, int64_t ldq,
   a.table = table;
   a.ldt = ldt;
   a.lens = lens;
-  a.cap = (int)(ldt < (kAtMaxKeys >> a.lgP) ? ldt << a.lgP : kAtMaxKeys);
+  // without a page there is no visible token (and none to read where there is no other)
+  a.cap = pages == 0 ? 0 : (int)(ldt < (kAtMaxKeys >> a.lgP) ? ldt << a.lgP : kAtMaxKeys);
   a.batch = batch;
   a.q_heads = q_heads;
   a.heads = heads;

@@ -196,6 +196,17 @@ def test_pages_outside_the_cache_are_invisible():
     assert not out[2].any()
 
 
+def test_a_cache_without_pages():
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce("attention over no pages")
+    cache = brq.kv_cache(0, 2, 128, 32)
+    table, lens = torch.zeros((3, 2), dtype=torch.int32, device="cuda"), torch.tensor([40, 0, 1], dtype=torch.int32).cuda()
+    lse = torch.zeros((3, 4), device="cuda")
+    out = brq.paged_attention(None, torch.randn((3, 4, 128), device="cuda"), cache, table, lens, 32, lse=lse)
+    assert not out.any() and torch.isneginf(lse).all()
+
+
 def test_a_nan_key_or_value_reaches_only_who_sees_it():
     import butterfly_rotation_quantization_amd as brq
     import torch
