@@ -139,6 +139,20 @@ static hipError_t walk_kv(const KvArgs& a) {
   if ((1 << a.lgP) != a.pg.P || a.ldk < (int64_t)a.heads * a.pg.D || a.ldv < (int64_t)a.heads * a.pg.D ||
       (a.d && a.d != a.pg.D))
     return bad("cache geometry (page %lld, D %lld)", a.pg.P, a.pg.D);
+  const int64_t rows = kv_rows(a.tokens, a.heads);
+  if (rows >= (int64_t)1 << 31) return bad("cache rows of %lld tokens", a.tokens, 0);
+  if (rows <= 1 << 22) {  // every head of every token once
+    std::vector<uint8_t> cover((size_t)(a.tokens * a.heads), 0);
+    for (int64_t r = 0; r < rows; ++r) {
+      int64_t tok;
+      int h;
+      kv_row((uint32_t)r, a.heads, &tok, &h);
+      if (tok < 0 || h < 0 || h >= a.heads) return bad("cache row %lld of head %lld", r, h);
+      if (tok < a.tokens) cover[(size_t)(tok * a.heads + h)]++;
+    }
+    for (size_t i = 0; i < cover.size(); ++i)
+      if (cover[i] != 1) return bad("cache row %lld handled %lld times", (long long)i, cover[i]);
+  }
   return walk_page(a.pg);
 }
 

@@ -70,13 +70,18 @@ __device__ __forceinline__ void at_store8(int t, void* p, int64_t off, const flo
 
 // Eight values of a head's finished output: normalise, undo the transform,
 // store (m in units of log2).
+template <int D>
 __device__ __forceinline__ void at_finish(const AtArgs& a, int64_t b, int head, int c, int lane, float (&o)[8],
                                           float m, float l) {
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // a NaN sum stays one
 #pragma unroll
   for (int e = 0; e < 8; ++e) o[e] = l != 0.0f ? o[e] * inv : 0.0f;
-  if (a.d) mx_unrotate(o, a.signs, a.d, a.rnorm, c, lane);
-  at_store8(a.qt, a.out, b * a.ldo + (int64_t)head * a.pg.D + c, o);
+  if (a.d) {
+    float sign[8];
+    mx_signs(a.signs, c, sign);
+    mx_unrotate<D>(o, sign, a.rnorm, lane);
+  }
+  at_store8(a.qt, a.out, b * a.ldo + (int64_t)head * D + c, o);
   if (a.lse && c == 0)
     a.lse[b * a.q_heads + head] = l != 0.0f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
@@ -217,7 +222,7 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
       for (int r = tid / LPH; r < H; r += kAtThreads / LPH) {
         const int in = u % a.ht * H + r;
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (in < a.group) at_finish(a, b, u / a.ht * a.group + in, (tid % LPH) * kMxPerLane, lane, v, 0.f, 0.f);
+        if (in < a.group) at_finish<D>(a, b, u / a.ht * a.group + in, (tid % LPH) * kMxPerLane, lane, v, 0.f, 0.f);
       }
       return;
     }
@@ -310,7 +315,14 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (h0 + r < a.group) {
       at_load8(a.qt, a.q, b * a.ldq + (int64_t)(h * a.group + h0 + r) * D + e0, v);
-      if (a.d) mx_rotate(v, a.signs, a.d, a.rnorm, e0, lane);
+      if (a.d) {
+        if (a.signs)  // after the query: registers are short here
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] *= a.signs[e0 + e];
+        mx_hadamard<D>(v, lane);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= a.rnorm;
+      }
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= sl;
@@ -505,7 +517,7 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
       for (int e = 0; e < 8; ++e) v[e] += os[w][r][e0 + e] * f;
     }
     if (tb == 0 && te == tiles) {
-      at_finish(a, b, h * a.group + h0 + r, e0, lane, v, M, L);
+      at_finish<D>(a, b, h * a.group + h0 + r, e0, lane, v, M, L);
     } else {
       float* p = a.part + (at_slot(blockIdx.x, g0, total, wgs) * H + r) * (D + 4);
       mx_store8<BRQ_F32>(p, e0, v);
@@ -576,7 +588,7 @@ __global__ __launch_bounds__(kAtThreads) void at_join_kernel(AtArgs a, int rows)
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] += p[e0 + e] * q;
   }
-  at_finish(a, b, h * a.group + h0 + r, e0, lane, o, M, L);
+  at_finish<D>(a, b, h * a.group + h0 + r, e0, lane, o, M, L);
 }
 
 template <int D>

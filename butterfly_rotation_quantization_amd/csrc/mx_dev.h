@@ -104,8 +104,8 @@ __device__ __forceinline__ void mx_stage(float (&v)[N], int lane) {
 
 // H_d v for the d / N lanes of a transform (d = 32..256, N = 8 or 16 values a
 // lane), unnormalised: the additions in the order of strides 1, 2, 4, ..., d / 2.
-template <int N>
-__device__ __forceinline__ void mx_hadamard(float (&v)[N], int d, int lane) {
+template <int d, int N>
+__device__ __forceinline__ void mx_hadamard(float (&v)[N], int lane) {
 #pragma unroll
   for (int s = 1; s < N; s *= 2)
 #pragma unroll
@@ -116,39 +116,40 @@ __device__ __forceinline__ void mx_hadamard(float (&v)[N], int d, int lane) {
         v[e + s] = a - b;
       }
   mx_stage<1>(v, lane);
-  if (d > 2 * N) mx_stage<2>(v, lane);
-  if (d > 4 * N) mx_stage<4>(v, lane);
-  if (d > 8 * N) mx_stage<8>(v, lane);
-  if constexpr (N == 8)
-    if (d > 128) mx_stage<16>(v, lane);
+  if constexpr (d > 2 * N) mx_stage<2>(v, lane);
+  if constexpr (d > 4 * N) mx_stage<4>(v, lane);
+  if constexpr (d > 8 * N) mx_stage<8>(v, lane);
+  if constexpr (d > 16 * N) mx_stage<16>(v, lane);
 }
 
+// The plan's signs at positions c .. of its d values (none: all 1).  Asked for
+// before the values they go with, so that both loads travel together.
 template <int N>
-__device__ __forceinline__ void mx_signs(float (&v)[N], const float* signs, int c) {
+__device__ __forceinline__ void mx_signs(const float* signs, int c, float (&s)[N]) {
 #pragma unroll
-  for (int q = 0; q < N / 8; ++q) {
-    float s[8];
-    mx_load8<BRQ_F32>(signs, c + 8 * q, s);
+  for (int e = 0; e < N; ++e) s[e] = 1.0f;
+  if (signs)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[8 * q + e] *= s[e];
-  }
+    for (int q = 0; q < N / 8; ++q) mx_load8<BRQ_F32>(signs, c + 8 * q, *reinterpret_cast<float (*)[8]>(&s[8 * q]));
 }
 
-// The plan's transform of the lane's values, which start at position c of
-// their d values: signs, additions, one product.
-template <int N>
-__device__ __forceinline__ void mx_rotate(float (&v)[N], const float* signs, int d, float rnorm, int c, int lane) {
-  if (signs) mx_signs(v, signs, c);
-  mx_hadamard(v, d, lane);
+// The plan's transform of the lane's values: signs, additions, one product.
+template <int d, int N>
+__device__ __forceinline__ void mx_rotate(float (&v)[N], const float (&signs)[N], float rnorm, int lane) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) v[e] *= signs[e];
+  mx_hadamard<d>(v, lane);
 #pragma unroll
   for (int e = 0; e < N; ++e) v[e] *= rnorm;
 }
 // Its inverse (the transform is symmetric): additions, product, signs.
-__device__ __forceinline__ void mx_unrotate(float (&v)[8], const float* signs, int d, float rnorm, int c, int lane) {
-  mx_hadamard(v, d, lane);
+template <int d>
+__device__ __forceinline__ void mx_unrotate(float (&v)[8], const float (&signs)[8], float rnorm, int lane) {
+  mx_hadamard<d>(v, lane);
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] *= rnorm;
-  if (signs) mx_signs(v, signs, c);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= signs[e];
 }
 
 // 2^(byte - 127); byte 0 is the subnormal 2^-127.  Byte 255, which stands for

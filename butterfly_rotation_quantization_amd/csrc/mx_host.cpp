@@ -210,7 +210,7 @@ brq_status kv_setup(KvArgs& a, const brq_plan* plan, const void* k, int64_t ldk,
     *done = true;
     return BRQ_OK;
   }
-  if (tokens > kMxMost / row) return refuse(BRQ_ERR_UNSUPPORTED, "more than 2^34 values");
+  if (tokens + (kKvQuad - 1) > kMxMost / row) return refuse(BRQ_ERR_UNSUPPORTED, "more than 2^34 values");
   if (!k || !v || !slots || (!cache && pages > 0)) return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL data pointer");
   if (rows_misaligned(k, ldk, t) || rows_misaligned(v, ldv, t))
     return refuse(BRQ_ERR_ALIGNMENT, "rows must be 16-byte aligned");
