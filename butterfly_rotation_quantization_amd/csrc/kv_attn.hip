@@ -8,7 +8,8 @@
 // output is O^T = V^T P^T on the bfloat16 ones: a value's code times its scale
 // is exact in bfloat16, and a probability is a pair of bfloat16 (its upper 16
 // bits and the rest), in columns c and c + 8 again.  Sums, maxima and
-// normalisers are float32.
+// normalisers are float32.  With float32 queries the scores are bfloat16
+// products too, and queries and probabilities three pieces.
 //
 // Lane l = 16 g + c of a wavefront holds block g of key c as the A operand of
 // the scores; these come out as column c, keys 4 g + i, which is where the B
@@ -107,16 +108,47 @@ __device__ __forceinline__ void at_pieces(float (&v)[8], uint2 (&piece)[4], int 
     const float inv = __uint_as_float((uint32_t)(254 - (x > 0 ? x : 0)) << 23);
     const float back = __uint_as_float(x > 0 ? (uint32_t)x << 23 : 0x400000u);
     int w[2] = {0, 0};
+    // Beside 2^7 the matrix unit drops bits below 2^-6 (measured: 2^-7 counted
+    // as zero, 1.5 2^-6 as 2^-6), so a value that would have such bits is left
+    // to the next piece.
+    float t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      t[e] = v[e] * inv;
+      t[e] = fabsf(t[e]) < 0.125f ? 0.0f : t[e];
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      w[e] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * e] * inv, v[4 * e + 1] * inv, w[e], false);
-      w[e] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * e + 2] * inv, v[4 * e + 3] * inv, w[e], true);
+      w[e] = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * e], t[4 * e + 1], w[e], false);
+      w[e] = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * e + 2], t[4 * e + 3], w[e], true);
       v[4 * e] -= __builtin_amdgcn_cvt_f32_fp8(w[e], 0) * back;
       v[4 * e + 1] -= __builtin_amdgcn_cvt_f32_fp8(w[e], 1) * back;
       v[4 * e + 2] -= __builtin_amdgcn_cvt_f32_fp8(w[e], 2) * back;
       v[4 * e + 3] -= __builtin_amdgcn_cvt_f32_fp8(w[e], 3) * back;
     }
     piece[k] = make_uint2((uint32_t)w[0], (uint32_t)w[1]);
+  }
+}
+
+// For float32 a query, like a probability, is three bfloat16 pieces (24 bits):
+// the upper 16 bits, those of what they leave, and the rest.
+__device__ __forceinline__ void at_pieces(const float (&v)[8], uint4 (&piece)[3]) {
+  uint32_t x[3][8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float r = v[e];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      x[k][e] = __float_as_uint(r);
+      r -= __uint_as_float(x[k][e] & 0xffff0000u);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = __builtin_amdgcn_perm(x[k][2 * e + 1], x[k][2 * e], 0x07060302u);
+    piece[k] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -142,11 +174,15 @@ __device__ __forceinline__ int64_t at_block_sum(int64_t x, int64_t* scratch) {
 
 // One workgroup: its share of the tiles of all units (or, without a deal, the
 // unit of its number); its wavefronts take 32 keys at a time in turn.
-template <int D, int NT>
+// F32: queries and outputs are float32, and the scores and the output keep 24
+// bits.  The scaled instructions, which drop low bits of the smaller products
+// (scores within some 2^-18), do not: the keys are converted like the values.
+template <int D, int NT, bool F32>
 __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_kernel(AtArgs a) {
   constexpr int KW = D / 32;          // words of codes a lane holds per key (of the scores) or four keys (values)
   constexpr int NQ = D == 256 ? 2 : 1;  // matrix steps of 128 values of a score
   constexpr int NP = D == 64 ? 1 : 2;   // products of a step: two of a query's four pieces each (D = 64: all four)
+  constexpr int NJ = D == 64 ? 2 : 4;   // F32: products of 32 values in a step
   constexpr int R = D / 16;           // dimensions of a run = output tiles
   constexpr int H = kAtCols * NT;     // query heads
   constexpr int LD = D + 4;
@@ -156,10 +192,14 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
   __shared__ int64_t sums[kAtWaves];
   __shared__ int found[1];
   __shared__ int64_t found_base[1];
+  // the queries' pieces, with scales or (F32) of bfloat16; the gap in a row
+  // keeps a column's lanes on banks of their own
   __shared__ uint8_t qb[H][4][D / 32];
-  constexpr int QD = D + 16;  // a piece's row; the gap keeps a column's lanes on banks of their own
+  constexpr int QD = D + 16, FD = D + 8;
   uint8_t (*qs)[4][QD] = reinterpret_cast<uint8_t (*)[4][QD]>(&os[0]);
-  static_assert(sizeof(uint8_t[H][4][QD]) <= sizeof(os), "the pieces lie where the sums will");
+  uint16_t (*qh)[3][FD] = reinterpret_cast<uint16_t (*)[3][FD]>(&os[0]);
+  static_assert(sizeof(uint8_t[H][4][QD]) <= sizeof(os) && sizeof(uint16_t[H][3][FD]) <= sizeof(os),
+                "the pieces lie where the sums will");
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
@@ -326,13 +366,20 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= sl;
-    uint2 piece[4];
-    int byte[4];
-    at_pieces(v, piece, byte);
+    if constexpr (F32) {
+      uint4 piece[3];
+      at_pieces(v, piece);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      *reinterpret_cast<uint2*>(&qs[r][k][e0]) = piece[k];
-      if ((e0 & 31) == 0) qb[r][k][e0 / 32] = (uint8_t)byte[k];
+      for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(&qh[r][k][e0]) = piece[k];
+    } else {
+      uint2 piece[4];
+      int byte[4];
+      at_pieces(v, piece, byte);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        *reinterpret_cast<uint2*>(&qs[r][k][e0]) = piece[k];
+        if ((e0 & 31) == 0) qb[r][k][e0 / 32] = (uint8_t)byte[k];
+      }
     }
   }
   __syncthreads();
@@ -343,21 +390,30 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
   // second half of the words repeats dimensions 16 g .. with pieces 3 and 4,
   // as the keys' lanes repeat theirs.
   int qsc[NT][NQ][NP];
+  if constexpr (!F32) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int e = 0; e < NQ; ++e)
+      for (int e = 0; e < NQ; ++e)
 #pragma unroll
-      for (int w = 0; w < NP; ++w) {
-        const int r = 8 * t + (c & 7), k = (c >> 3) + 2 * w;
-        qsc[t][e][w] = D == 64 ? qb[r][k + 2 * (g >> 1)][g & 1] : qb[r][k][4 * e + g];
-      }
+        for (int w = 0; w < NP; ++w) {
+          const int r = 8 * t + (c & 7), k = (c >> 3) + 2 * w;
+          qsc[t][e][w] = D == 64 ? qb[r][k + 2 * (g >> 1)][g & 1] : qb[r][k][4 * e + g];
+        }
+  }
   auto query = [&](int t, int e, int w) {
     const int r = 8 * t + (c & 7), k = (c >> 3) + 2 * w;
     const mxi4 x = *reinterpret_cast<const mxi4*>(&qs[r][k][128 * e + 16 * g]);
     const mxi4 y = D == 64 ? *reinterpret_cast<const mxi4*>(&qs[r][k + 2][16 * g])
                            : *reinterpret_cast<const mxi4*>(&qs[r][k][128 * e + 64 + 16 * g]);
     return mxi8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+  };
+  // F32: word j of a lane's keys is 8 j .. + 7 of its block (with D = 64, where
+  // two lanes have the same block, word j + 2 for the second); piece k of the
+  // query's values there
+  auto query_f32 = [&](int t, int e, int j, int k) {
+    const int at = D == 64 ? 32 * (g & 1) + 8 * (j + 2 * (g >> 1)) : 128 * e + 32 * g + 8 * j;
+    return *reinterpret_cast<const uint4*>(&qh[8 * t + (c & 7)][k][at]);
   };
 
   mxf4 o[NT][R], l[NT];
@@ -379,17 +435,38 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       mxf4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      if constexpr (F32) {  // columns c < 8: the first and third pieces, c + 8: the second
 #pragma unroll
-      for (int e = 0; e < NQ; ++e)
+        for (int e = 0; e < NQ; ++e)
 #pragma unroll
-        for (int w = 0; w < NP; ++w) {
-          const mxi8 Q = query(u, e, w);
+          for (int j = 0; j < NJ; ++j) {
+            const mxb8 q1 = __builtin_bit_cast(mxb8, query_f32(u, e, j, c >> 3));
+            uint4 third = query_f32(u, e, j, 2);
+            if (low) third = make_uint4(0u, 0u, 0u, 0u);
+            const mxb8 q2 = __builtin_bit_cast(mxb8, third);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const mxi8 K = {kw[t][e][0], kw[t][e][1], kw[t][e][2], kw[t][e][3], 0, 0, 0, 0};
-            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(K, Q, acc[t], 4, 0, 0, ks[t][e], 0, qsc[u][e][w]);
+            for (int t = 0; t < 2; ++t) {
+              const uint32_t x = D == 64 && g >= 2 ? kw[t][e][(j + 2) & 3] : kw[t][e][j];
+              const float sc = __uint_as_float((uint32_t)ks[t][e] << 23);
+              const mxb8 K = __builtin_bit_cast(mxb8, make_uint4(at_bits(at_pair(x, sc, 0)), at_bits(at_pair(x, sc, 1)),
+                                                                 at_bits(at_pair(x, sc, 2)), at_bits(at_pair(x, sc, 3))));
+              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(K, q1, acc[t], 0, 0, 0);
+              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(K, q2, acc[t], 0, 0, 0);
+            }
           }
-        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < NQ; ++e)
+#pragma unroll
+          for (int w = 0; w < NP; ++w) {
+            const mxi8 Q = query(u, e, w);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const mxi8 K = {kw[t][e][0], kw[t][e][1], kw[t][e][2], kw[t][e][3], 0, 0, 0, 0};
+              acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(K, Q, acc[t], 4, 0, 0, ks[t][e], 0, qsc[u][e][w]);
+            }
+          }
+      }
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -416,7 +493,7 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
         }
     }
     if constexpr (more) fetch_keys(k0 + kAtTile);
-    mxb8 pf[NT];
+    mxb8 pf[NT], pl[NT];
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       float mx = fmaxf(fmaxf(s[u][0][0], s[u][0][1]), fmaxf(s[u][0][2], s[u][0][3]));
@@ -434,21 +511,32 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
           for (int i = 0; i < 4; ++i) o[u][j][i] *= f;
       }
       // columns 0..7 take a probability's upper 16 bits, columns 8..15 the
-      // rest, rounded toward zero to 8 bits (2^-16 of the probability); the sum
-      // below is of what the products use
-      uint32_t w[4];
+      // rest, rounded toward zero to 8 bits (2^-16 of the probability); for
+      // float32 a second product's columns 0..7 take what is left then.  The
+      // sum below is of what the products use.
+      uint32_t w[4], y[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        float x[2];
+        float x[2], z[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float p = __builtin_amdgcn_exp2f(s[u][q / 2][2 * (q & 1) + e] - base);
           x[e] = p - __uint_as_float(__float_as_uint(p) & low);
+          if constexpr (F32) {
+            const float r = p - __uint_as_float(__float_as_uint(p) & 0xffff0000u);
+            z[e] = r - __uint_as_float(__float_as_uint(r) & 0xffff0000u);
+          }
         }
         w[q] = __builtin_amdgcn_perm(__float_as_uint(x[1]), __float_as_uint(x[0]), 0x07060302u);
+        if constexpr (F32)
+          y[q] = low ? 0u : __builtin_amdgcn_perm(__float_as_uint(z[1]), __float_as_uint(z[0]), 0x07060302u);
       }
       pf[u] = __builtin_bit_cast(mxb8, make_uint4(w[0], w[1], w[2], w[3]));
       l[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pf[u], l[u], 0, 0, 0);
+      if constexpr (F32) {
+        pl[u] = __builtin_bit_cast(mxb8, make_uint4(y[0], y[1], y[2], y[3]));
+        l[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pl[u], l[u], 0, 0, 0);
+      }
     }
     // values: keys in pairs, one run of dimensions per lane (of a scale the
     // conversion reads the exponent, so byte 0 is 2^-127 and 255 NaN)
@@ -476,6 +564,10 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
       for (int u = 0; u < NT; ++u) {
         o[u][2 * q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, pf[u], o[u][2 * q], 0, 0, 0);
         o[u][2 * q + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, pf[u], o[u][2 * q + 1], 0, 0, 0);
+        if constexpr (F32) {
+          o[u][2 * q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, pl[u], o[u][2 * q], 0, 0, 0);
+          o[u][2 * q + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, pl[u], o[u][2 * q + 1], 0, 0, 0);
+        }
       }
     }
     if constexpr (more) fetch_values(k0 + kAtTile);
@@ -595,8 +687,11 @@ template <int D>
 hipError_t at_launch(const AtArgs& a, hipStream_t s) {
   const int64_t units = a.batch * a.heads * a.ht;
   const dim3 grid((unsigned)(a.wgs ? a.wgs : units));
-  if (a.nt == 1) at_kernel<D, 1><<<grid, kAtThreads, 0, s>>>(a);
-  else at_kernel<D, 2><<<grid, kAtThreads, 0, s>>>(a);
+  const bool f32 = a.qt == BRQ_F32;
+  if (a.nt == 1 && f32) at_kernel<D, 1, true><<<grid, kAtThreads, 0, s>>>(a);
+  else if (a.nt == 1) at_kernel<D, 1, false><<<grid, kAtThreads, 0, s>>>(a);
+  else if (f32) at_kernel<D, 2, true><<<grid, kAtThreads, 0, s>>>(a);
+  else at_kernel<D, 2, false><<<grid, kAtThreads, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.wgs) return e;
   // few units: each has many parts, and a workgroup for every row; many: most

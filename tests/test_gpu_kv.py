@@ -2,7 +2,7 @@
 reads it, against the oracle (oracle/mx.py).
 
 The cache's bytes are compared bit for bit.  Attention's bound: a query enters
-with 16 bits (as four 8-bit pieces, 2^-17 of its block's largest entry lost at
+with 16 bits or more (as four 8-bit pieces, 2^-17 of its block's largest entry lost at
 most; the losses of a block's entries have either sign, and their sum stays
 under 2^-16 of the sum of magnitudes) after a float32 transform ((log2 D + 2)
 2^-24 sqrt(D) of its largest entry, which the terms below cover with sqrt(D) to
@@ -157,6 +157,49 @@ def test_wide_groups(D):
 @pytest.mark.parametrize("window", [1, 5, 16, 31, 32, 100, 1000])
 def test_windows(window):
     attend(EDGES, 6, 2, 128, 16, False, "f32", window=window)
+
+
+@pytest.mark.parametrize("D,hq,rot", [(64, 8, True), (128, 8, True), (128, 40, False), (256, 3, True)])
+def test_float32_keeps_float32(D, hq, rot):
+    """Scores of a few units are off by some 2^-21 in float32 (products of 24
+    bits, sums of D terms of either sign, one exponential), and the output, a
+    mean of values around 0.5, by no more than twice that in the mean: 2^-18 of
+    its norm leaves a factor of four.  Probabilities or queries of 16 bits
+    would be at 2^-17."""
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce(f"attention float32 D={D} hq={hq} rot={rot}")
+    rng = np.random.default_rng(D + hq)
+    lens = [150, 700]
+    cache, ref, table, plan, M, _ = build(rng, lens, 1, D, 64, rot)
+    q = torch.from_numpy(rng.standard_normal((2, hq, D)).astype(np.float32)).cuda()
+    out = brq.paged_attention(plan, q, cache, to_dev(table, "i32"), torch.tensor(lens, dtype=torch.int32).cuda(), 64)
+    want, _, _ = X.attention(q.cpu().numpy().astype(np.float64), ref, table, lens, D ** -0.5, 0, M)
+    assert np.linalg.norm(from_dev(out) - want) < 2.0 ** -18 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_small_entries_of_a_query_count(D, dtype):
+    """One key of ones, so that lse is the sum of the query: every entry counts,
+    however far below the largest of its block it lies, to 2^-17 of that one
+    (float32: 2^-22), which the additions' 2^-22 of the sum, log and exponential
+    stay within too."""
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce(f"attention of small query entries D={D} {dtype}")
+    cache = brq.kv_cache(1, 1, D, 16)
+    ones = torch.ones((1, 1, D), device="cuda")
+    brq.kv_append(None, ones, ones, torch.zeros(1, dtype=torch.int64, device="cuda"), cache, 16)
+    q = torch.zeros((1, 24, D), device="cuda")
+    q[0, :, 3] = 1.0
+    q[0, :, 5] = -(2.0 ** -torch.arange(24, device="cuda"))
+    q = q.to(torch_dtype(dtype))
+    lse = torch.empty((1, 24), device="cuda")
+    brq.paged_attention(None, q, cache, torch.zeros((1, 1), dtype=torch.int32, device="cuda"),
+                        torch.ones(1, dtype=torch.int32, device="cuda"), 16, scale=1.0, lse=lse)
+    off = (lse.double() - q.double().sum(-1)).abs().max().item()
+    assert off <= (2.0 ** -21 if dtype == "f32" else 2.0 ** -17 + 2.0 ** -21), off
 
 
 def test_long_and_ragged():
