@@ -254,7 +254,7 @@ __device__ __forceinline__ void mm_to_lds(const void* base, uint32_t& off, uint3
 // 8 R bytes, fetched straight to LDS, in which a lane finds those of its tiles
 // in one word.  Read from the rows they are 8 bytes out of a line
 // for each row and stage (measured at 4096x8192x28672, rows read by the tile
-// kernel: 15% of its time; this pass: 1.5%).  Rows and blocks past the end
+// kernel: 15% of its time; this pass: 2%).  Rows and blocks past the end
 // get zeros (2^-127, times codes of zero).  One workgroup: a tile, kMmRun
 // stages.
 constexpr int kMmRun = 4;
