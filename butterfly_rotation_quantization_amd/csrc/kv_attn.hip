@@ -3,13 +3,12 @@
 //
 // Per key-value head the scores are products S^T = K Q^T on the scaled matrix
 // instructions: the keys' codes and scale bytes as they lie in the cache, the
-// queries of the group as columns, each in four 8-bit floating-point pieces
-// (at_pieces) of which columns c and c + 8 of two products hold one each.  The
+// queries of the group as columns, each in eight 4-bit floating-point pieces
+// (at_pieces) of which columns c and c + 8 of four products hold one each.  The
 // output is O^T = V^T P^T on the bfloat16 ones: a value's code times its scale
-// is exact in bfloat16, and a probability is a pair of bfloat16 (its upper 16
-// bits and the rest), in columns c and c + 8 again.  Sums, maxima and
-// normalisers are float32.  With float32 queries the scores are bfloat16
-// products too, and queries and probabilities three pieces.
+// is exact in bfloat16, and a probability is three pieces of 8 bits, in columns c
+// and c + 8 of one product and c of another.  Nothing is held in fewer than 24
+// bits, so a result is as near to the formula as one in plain float32.
 //
 // Lane l = 16 g + c of a wavefront holds block g of key c as the A operand of
 // the scores; these come out as column c, keys 4 g + i, which is where the B
@@ -87,12 +86,18 @@ __device__ __forceinline__ void at_finish(const AtArgs& a, int64_t b, int head, 
     a.lse[b * a.q_heads + head] = l != 0.0f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// A query enters the scores as four 8-bit floating-point pieces, each the
-// rounding of what the ones before it left (4 bits each: together within
-// 2^-17 of its block's largest magnitude), with a scale for each block of 32.
-// The eight values of a lane (its block is four lanes): the pieces' words and
+// A query enters the scores as eight 4-bit floating-point pieces, each the
+// rounding of what the ones before it left.  The first has half the scale of
+// the largest exponent of its block of 32, so that it lies below 4, where the
+// format's steps are 1/2 and less, or 1: half of that is left, 4 of the next
+// piece, whose scale is an eighth.  Together the pieces are within 2^-23 of the
+// block's largest magnitude.  Products of 4-bit values lose nothing that a
+// float32 sum would keep; those of 8-bit ones, which would need four pieces for
+// 16 bits, drop what lies 14 bits below the largest of a block (a key's code of
+// 6 beside one of 1/2: scores 2^-14 of the sum of magnitudes off).
+// The eight values of a lane (its block is four lanes): the pieces' codes and
 // scale bytes.
-__device__ __forceinline__ void at_pieces(float (&v)[8], uint2 (&piece)[4], int (&byte)[4]) {
+__device__ __forceinline__ void at_pieces(float (&v)[8], uint32_t (&piece)[8], uint32_t (&byte)[8]) {
   uint32_t top = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
@@ -100,55 +105,32 @@ __device__ __forceinline__ void at_pieces(float (&v)[8], uint2 (&piece)[4], int 
   top = max(top, mx_xor<2>(top));
   const int ex = (int)(top >> 23);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    // times 2^(7 - 4 k) of the largest exponent: the first piece lies below
-    // 256, what is left of it below 128; an infinity or a NaN: a NaN scale
-    const int x = ex - 7 - 4 * k;
-    byte[k] = ex == 255 ? 255 : x > 0 ? x : 0;
-    const float inv = __uint_as_float((uint32_t)(254 - (x > 0 ? x : 0)) << 23);
-    const float back = __uint_as_float(x > 0 ? (uint32_t)x << 23 : 0x400000u);
-    int w[2] = {0, 0};
-    // Beside 2^7 the matrix unit drops bits below 2^-6 (measured: 2^-7 counted
-    // as zero, 1.5 2^-6 as 2^-6), so a value that would have such bits is left
-    // to the next piece.
-    float t[8];
+  for (int k = 0; k < 8; ++k) {
+    const int x = ex - 1 - 3 * k;
+    byte[k] = ex == 255 ? 255u : x > 0 ? (uint32_t)x : 0u;  // an infinity or a NaN: a NaN scale
+    const float sc = mx_scale(byte[k]);
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], sc, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], sc, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], sc, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], sc, 3);
+    piece[k] = w;
+    if (k < 7) {
+      float back[8];
+      mx_values8(w, byte[k], back);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      t[e] = v[e] * inv;
-      t[e] = fabsf(t[e]) < 0.125f ? 0.0f : t[e];
+      for (int e = 0; e < 8; ++e) v[e] -= back[e];  // exact
     }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      w[e] = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * e], t[4 * e + 1], w[e], false);
-      w[e] = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * e + 2], t[4 * e + 3], w[e], true);
-      v[4 * e] -= __builtin_amdgcn_cvt_f32_fp8(w[e], 0) * back;
-      v[4 * e + 1] -= __builtin_amdgcn_cvt_f32_fp8(w[e], 1) * back;
-      v[4 * e + 2] -= __builtin_amdgcn_cvt_f32_fp8(w[e], 2) * back;
-      v[4 * e + 3] -= __builtin_amdgcn_cvt_f32_fp8(w[e], 3) * back;
-    }
-    piece[k] = make_uint2((uint32_t)w[0], (uint32_t)w[1]);
   }
 }
 
-// For float32 a query, like a probability, is three bfloat16 pieces (24 bits):
-// the upper 16 bits, those of what they leave, and the rest.
-__device__ __forceinline__ void at_pieces(const float (&v)[8], uint4 (&piece)[3]) {
-  uint32_t x[3][8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float r = v[e];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      x[k][e] = __float_as_uint(r);
-      r -= __uint_as_float(x[k][e] & 0xffff0000u);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = __builtin_amdgcn_perm(x[k][2 * e + 1], x[k][2 * e], 0x07060302u);
-    piece[k] = make_uint4(w[0], w[1], w[2], w[3]);
+// c += K Q, both 4-bit; the queries' scale is byte w of qs.
+__device__ __forceinline__ mxf4 at_score(mxi8 K, mxi8 Q, mxf4 c, int ks, int qs, int w) {
+  switch (w & 3) {
+    case 0: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(K, Q, c, 4, 4, 0, ks, 0, qs);
+    case 1: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(K, Q, c, 4, 4, 0, ks, 1, qs);
+    case 2: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(K, Q, c, 4, 4, 0, ks, 2, qs);
+    default: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(K, Q, c, 4, 4, 0, ks, 3, qs);
   }
 }
 
@@ -174,15 +156,11 @@ __device__ __forceinline__ int64_t at_block_sum(int64_t x, int64_t* scratch) {
 
 // One workgroup: its share of the tiles of all units (or, without a deal, the
 // unit of its number); its wavefronts take 32 keys at a time in turn.
-// F32: queries and outputs are float32, and the scores and the output keep 24
-// bits.  The scaled instructions, which drop low bits of the smaller products
-// (scores within some 2^-18), do not: the keys are converted like the values.
-template <int D, int NT, bool F32>
+template <int D, int NT>
 __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_kernel(AtArgs a) {
   constexpr int KW = D / 32;          // words of codes a lane holds per key (of the scores) or four keys (values)
   constexpr int NQ = D == 256 ? 2 : 1;  // matrix steps of 128 values of a score
-  constexpr int NP = D == 64 ? 1 : 2;   // products of a step: two of a query's four pieces each (D = 64: all four)
-  constexpr int NJ = D == 64 ? 2 : 4;   // F32: products of 32 values in a step
+  constexpr int NP = D == 64 ? 2 : 4;   // products of a step: two of a query's eight pieces each (D = 64: four)
   constexpr int R = D / 16;           // dimensions of a run = output tiles
   constexpr int H = kAtCols * NT;     // query heads
   constexpr int LD = D + 4;
@@ -192,20 +170,18 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
   __shared__ int64_t sums[kAtWaves];
   __shared__ int found[1];
   __shared__ int64_t found_base[1];
-  // the queries' pieces, with scales or (F32) of bfloat16; the gap in a row
-  // keeps a column's lanes on banks of their own
-  __shared__ uint8_t qb[H][4][D / 32];
-  constexpr int QD = D + 16, FD = D + 8;
-  uint8_t (*qs)[4][QD] = reinterpret_cast<uint8_t (*)[4][QD]>(&os[0]);
-  uint16_t (*qh)[3][FD] = reinterpret_cast<uint16_t (*)[3][FD]>(&os[0]);
-  static_assert(sizeof(uint8_t[H][4][QD]) <= sizeof(os) && sizeof(uint16_t[H][3][FD]) <= sizeof(os),
-                "the pieces lie where the sums will");
+  // The queries' pieces, and their scales.  Pieces are an odd number of 16-byte
+  // places apart and heads twice an odd number, so that the 16 columns of a
+  // block lie in 16 different places of the banks' 256 bytes.
+  constexpr int QP = D / 2 + 16, QH = 8 * QP + 32;
+  __shared__ __align__(4) uint8_t qb[H][2][D / 32][4];  // of head, column half, block: the products' scales
+  uint8_t* qs = reinterpret_cast<uint8_t*>(&os[0]);
+  static_assert(H * QH <= (int)sizeof(os) && QP % 32 == 16 && QH % 64 == 32, "the pieces lie where the sums will");
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const uint32_t low = c < 8 ? 0u : 0xffff0000u;
-  const uint32_t one2 = 0x3f803f80u;
-  const mxb8 ones = __builtin_bit_cast(mxb8, make_uint4(one2, one2, one2, one2));
+  const bool first8 = c < 8;
+  const uint32_t third = first8 ? 0x07060302u : 0x0c0c0c0cu;  // columns 8..15 of the second product are zero
   const int units = a.heads * a.ht;   // of a sequence
   int64_t total = 0, pos = 0, end = 0, base = 0;  // places: all, this workgroup's, before sequence b
   int64_t b = 0;
@@ -366,62 +342,40 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= sl;
-    if constexpr (F32) {
-      uint4 piece[3];
-      at_pieces(v, piece);
+    uint32_t piece[8], byte[8];
+    at_pieces(v, piece, byte);
 #pragma unroll
-      for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(&qh[r][k][e0]) = piece[k];
-    } else {
-      uint2 piece[4];
-      int byte[4];
-      at_pieces(v, piece, byte);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        *reinterpret_cast<uint2*>(&qs[r][k][e0]) = piece[k];
-        if ((e0 & 31) == 0) qb[r][k][e0 / 32] = (uint8_t)byte[k];
-      }
+    for (int k = 0; k < 8; ++k) {
+      *reinterpret_cast<uint32_t*>(qs + r * QH + k * QP + e0 / 2) = piece[k];
+      if ((e0 & 31) == 0) qb[r][k & 1][e0 / 32][D == 64 ? (k >> 1 & 1) * 2 + (k >> 2) : k >> 1] = (uint8_t)byte[k];
     }
   }
   __syncthreads();
-  // The B operand: column c < 8 holds pieces 1 and 3 of query head c, column
-  // c + 8 its pieces 2 and 4; product w takes the first or the second.  A
-  // lane's words hold dimensions 16 g .. + 15 and 64 + 16 g .. + 15 of a step,
-  // and its scale is that of block g.  With D = 64 one product takes all: the
-  // second half of the words repeats dimensions 16 g .. with pieces 3 and 4,
-  // as the keys' lanes repeat theirs.
-  int qsc[NT][NQ][NP];
-  if constexpr (!F32) {
+  // The B operand: in product w column c < 8 holds piece 2 w of query head c,
+  // column c + 8 its piece 2 w + 1; a lane's words are block g of a step.  With
+  // D = 64 blocks 2 and 3 repeat the two, as the keys' lanes repeat theirs, with
+  // the pieces after next: piece 4 w + 2 (g / 2) and the one after it.
+  int qsc[NT][NQ];  // the products' scales, a byte each
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < NQ; ++e)
-#pragma unroll
-        for (int w = 0; w < NP; ++w) {
-          const int r = 8 * t + (c & 7), k = (c >> 3) + 2 * w;
-          qsc[t][e][w] = D == 64 ? qb[r][k + 2 * (g >> 1)][g & 1] : qb[r][k][4 * e + g];
-        }
-  }
+    for (int e = 0; e < NQ; ++e) {
+      const int r = 8 * t + (c & 7);
+      qsc[t][e] = D == 64 ? *reinterpret_cast<const uint16_t*>(&qb[r][c >> 3][g & 1][2 * (g >> 1)])
+                          : *reinterpret_cast<const int*>(&qb[r][c >> 3][4 * e + g][0]);
+    }
+  const uint8_t* ql = qs + (c & 7) * QH + (c >> 3) * QP + (D == 64 ? 16 * (g & 1) + (g >> 1) * (2 * QP) : 16 * g);
   auto query = [&](int t, int e, int w) {
-    const int r = 8 * t + (c & 7), k = (c >> 3) + 2 * w;
-    const mxi4 x = *reinterpret_cast<const mxi4*>(&qs[r][k][128 * e + 16 * g]);
-    const mxi4 y = D == 64 ? *reinterpret_cast<const mxi4*>(&qs[r][k + 2][16 * g])
-                           : *reinterpret_cast<const mxi4*>(&qs[r][k][128 * e + 64 + 16 * g]);
-    return mxi8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-  };
-  // F32: word j of a lane's keys is 8 j .. + 7 of its block (with D = 64, where
-  // two lanes have the same block, word j + 2 for the second); piece k of the
-  // query's values there
-  auto query_f32 = [&](int t, int e, int j, int k) {
-    const int at = D == 64 ? 32 * (g & 1) + 8 * (j + 2 * (g >> 1)) : 128 * e + 32 * g + 8 * j;
-    return *reinterpret_cast<const uint4*>(&qh[8 * t + (c & 7)][k][at]);
+    const mxi4 x = *reinterpret_cast<const mxi4*>(ql + t * (8 * QH) + e * 64 + w * (D == 64 ? 4 * QP : 2 * QP));
+    return mxi8{x[0], x[1], x[2], x[3], 0, 0, 0, 0};
   };
 
-  mxf4 o[NT][R], l[NT];
-  float m[NT];
+  mxf4 o[NT][R];
+  float m[NT], l[NT];  // l: of the lane's keys
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     m[t] = -INFINITY;
-    l[t] = mxf4{0.f, 0.f, 0.f, 0.f};
+    l[t] = 0.f;
 #pragma unroll
     for (int j = 0; j < R; ++j) o[t][j] = mxf4{0.f, 0.f, 0.f, 0.f};
   }
@@ -435,38 +389,17 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       mxf4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      if constexpr (F32) {  // columns c < 8: the first and third pieces, c + 8: the second
 #pragma unroll
-        for (int e = 0; e < NQ; ++e)
+      for (int e = 0; e < NQ; ++e)
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            const mxb8 q1 = __builtin_bit_cast(mxb8, query_f32(u, e, j, c >> 3));
-            uint4 third = query_f32(u, e, j, 2);
-            if (low) third = make_uint4(0u, 0u, 0u, 0u);
-            const mxb8 q2 = __builtin_bit_cast(mxb8, third);
+        for (int w = 0; w < NP; ++w) {
+          const mxi8 Q = query(u, e, w);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const uint32_t x = D == 64 && g >= 2 ? kw[t][e][(j + 2) & 3] : kw[t][e][j];
-              const float sc = __uint_as_float((uint32_t)ks[t][e] << 23);
-              const mxb8 K = __builtin_bit_cast(mxb8, make_uint4(at_bits(at_pair(x, sc, 0)), at_bits(at_pair(x, sc, 1)),
-                                                                 at_bits(at_pair(x, sc, 2)), at_bits(at_pair(x, sc, 3))));
-              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(K, q1, acc[t], 0, 0, 0);
-              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(K, q2, acc[t], 0, 0, 0);
-            }
+          for (int t = 0; t < 2; ++t) {
+            const mxi8 K = {kw[t][e][0], kw[t][e][1], kw[t][e][2], kw[t][e][3], 0, 0, 0, 0};
+            acc[t] = at_score(K, Q, acc[t], ks[t][e], qsc[u][e], w);
           }
-      } else {
-#pragma unroll
-        for (int e = 0; e < NQ; ++e)
-#pragma unroll
-          for (int w = 0; w < NP; ++w) {
-            const mxi8 Q = query(u, e, w);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const mxi8 K = {kw[t][e][0], kw[t][e][1], kw[t][e][2], kw[t][e][3], 0, 0, 0, 0};
-              acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(K, Q, acc[t], 4, 0, 0, ks[t][e], 0, qsc[u][e][w]);
-            }
-          }
-      }
+        }
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -503,40 +436,36 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
       if (__builtin_amdgcn_ballot_w64(mx != m[u])) {  // seldom after the first tiles
         const float f = __builtin_amdgcn_exp2f(m[u] - base);
         m[u] = mx;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) l[u][i] *= f;
+        l[u] *= f;
 #pragma unroll
         for (int j = 0; j < R; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[u][j][i] *= f;
       }
-      // columns 0..7 take a probability's upper 16 bits, columns 8..15 the
-      // rest, rounded toward zero to 8 bits (2^-16 of the probability); for
-      // float32 a second product's columns 0..7 take what is left then.  The
-      // sum below is of what the products use.
+      // A probability's first 8 bits go to columns 0..7 of a product, the next
+      // 8 to columns 8..15, the last 8 to columns 0..7 of a second one (with
+      // pairs, of 17 bits, the outputs of 96 sequences in bfloat16 were 7e-5 of
+      // their norm away from the formula's rounding, where float32 sums are 3e-5;
+      // the second product takes 4% of their time, of four long ones' 2%).  The normaliser is the sum of the probabilities as they are.
       uint32_t w[4], y[4];
+      float sum = 0.f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float x[2], z[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float p = __builtin_amdgcn_exp2f(s[u][q / 2][2 * (q & 1) + e] - base);
-          x[e] = p - __uint_as_float(__float_as_uint(p) & low);
-          if constexpr (F32) {
-            const float r = p - __uint_as_float(__float_as_uint(p) & 0xffff0000u);
-            z[e] = r - __uint_as_float(__float_as_uint(r) & 0xffff0000u);
-          }
+          sum += p;
+          const float r = p - __uint_as_float(__float_as_uint(p) & 0xffff0000u);
+          x[e] = first8 ? p : r;
+          z[e] = r - __uint_as_float(__float_as_uint(r) & 0xffff0000u);
         }
         w[q] = __builtin_amdgcn_perm(__float_as_uint(x[1]), __float_as_uint(x[0]), 0x07060302u);
-        if constexpr (F32)
-          y[q] = low ? 0u : __builtin_amdgcn_perm(__float_as_uint(z[1]), __float_as_uint(z[0]), 0x07060302u);
+        y[q] = __builtin_amdgcn_perm(__float_as_uint(z[1]), __float_as_uint(z[0]), third);
       }
+      l[u] += sum;
       pf[u] = __builtin_bit_cast(mxb8, make_uint4(w[0], w[1], w[2], w[3]));
-      l[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pf[u], l[u], 0, 0, 0);
-      if constexpr (F32) {
-        pl[u] = __builtin_bit_cast(mxb8, make_uint4(y[0], y[1], y[2], y[3]));
-        l[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pl[u], l[u], 0, 0, 0);
-      }
+      pl[u] = __builtin_bit_cast(mxb8, make_uint4(y[0], y[1], y[2], y[3]));
     }
     // values: keys in pairs, one run of dimensions per lane (of a scale the
     // conversion reads the exponent, so byte 0 is 2^-127 and 255 NaN)
@@ -564,10 +493,8 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
       for (int u = 0; u < NT; ++u) {
         o[u][2 * q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, pf[u], o[u][2 * q], 0, 0, 0);
         o[u][2 * q + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, pf[u], o[u][2 * q + 1], 0, 0, 0);
-        if constexpr (F32) {
-          o[u][2 * q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, pl[u], o[u][2 * q], 0, 0, 0);
-          o[u][2 * q + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, pl[u], o[u][2 * q + 1], 0, 0, 0);
-        }
+        o[u][2 * q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, pl[u], o[u][2 * q], 0, 0, 0);
+        o[u][2 * q + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, pl[u], o[u][2 * q + 1], 0, 0, 0);
       }
     }
     if constexpr (more) fetch_values(k0 + kAtTile);
@@ -579,7 +506,7 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
   __syncthreads();  // the sums go where the queries were
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const float sum = l[t][0] + at_ror8(l[t][0]);  // every row of the product is the column's sum
+    const float sum = at_colsum(l[t]);
     if (lane < 8) {
       ms[wave][8 * t + lane] = m[t];
       ls[wave][8 * t + lane] = sum;
@@ -687,11 +614,8 @@ template <int D>
 hipError_t at_launch(const AtArgs& a, hipStream_t s) {
   const int64_t units = a.batch * a.heads * a.ht;
   const dim3 grid((unsigned)(a.wgs ? a.wgs : units));
-  const bool f32 = a.qt == BRQ_F32;
-  if (a.nt == 1 && f32) at_kernel<D, 1, true><<<grid, kAtThreads, 0, s>>>(a);
-  else if (a.nt == 1) at_kernel<D, 1, false><<<grid, kAtThreads, 0, s>>>(a);
-  else if (f32) at_kernel<D, 2, true><<<grid, kAtThreads, 0, s>>>(a);
-  else at_kernel<D, 2, false><<<grid, kAtThreads, 0, s>>>(a);
+  if (a.nt == 1) at_kernel<D, 1><<<grid, kAtThreads, 0, s>>>(a);
+  else at_kernel<D, 2><<<grid, kAtThreads, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.wgs) return e;
   // few units: each has many parts, and a workgroup for every row; many: most

@@ -484,10 +484,9 @@ brq_status brq_kv_read(const brq_plan* plan, const uint8_t* cache, const int64_t
  *       (16-byte aligned): partial results where a sequence's length is split.
  * Lengths and tables are read on the device at each call, so a captured call
  * can be replayed while sequences grow.  Maxima, normalisers and sums are held
- * in float32.  Where they enter the matrix units, queries and probabilities
- * have 24 bits with float32 queries; with 16-bit ones a query has 16 bits
- * (four 8-bit pieces, within 2^-17 of the largest magnitude of its block of 32)
- * and a probability too (a pair of bfloat16).
+ * in float32.  Where they enter the matrix units, for every qt, a query is eight
+ * 4-bit pieces, together within 2^-23 of the largest magnitude of its block of
+ * 32 after the transform and the scale, and a probability has its 24 bits.
  * Errors: INVALID_ARGUMENT (q_heads not a multiple of heads, NULLs, scale not
  * finite, window < 0), UNSUPPORTED (head_dim, page, the plan; more than 2^24
  * sequences times query heads), ALIGNMENT, WORKSPACE, HIP.  batch == 0 is a no-op. */
