@@ -551,7 +551,9 @@ def orp_geo_dequant(codes, signs, coef, m: int, n: int, bits: int, group: int, s
 
 # These calls are short (a decode step makes hundreds), so the marshalling keeps
 # to few torch calls; every check stays, since a wrong pointer would be the
-# GPU's to find.
+# GPU's to find.  With `stream`, the call runs on that stream and what it makes
+# (outputs not given, workspaces) belongs to it; the inputs have to be ready
+# there, and whoever uses the outputs elsewhere waits for that stream.
 
 def _stream_of(stream, t) -> int:
     """The raw stream: the one given, or the current one of t's GPU, which has to
@@ -563,14 +565,22 @@ def _stream_of(stream, t) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _scratch(stream, ws):
-    """A workspace made for one call, marked as used by the call's stream: on
-    another stream than the current one its memory is not handed out again
-    before that stream is done with it."""
-    if ws is not None and stream is not None:
-        import torch
-        ws.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
-    return ws
+def _made(stream, make):
+    """make(), a tensor the binding makes for a call, from the memory of the
+    call's stream.  Memory of the current stream's may still be in use by work
+    ahead on it, and once freed would be handed out there again with the call
+    ahead on the other stream.  The current stream, where the caller goes on
+    (once it waits for the call), may use the tensor too."""
+    if stream is None:
+        return make()
+    import torch
+    at = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(at):
+        t = make()
+    if t is not None and here.cuda_stream != at.cuda_stream:
+        t.record_stream(here)
+    return t
 
 
 def _rows(t) -> tuple:
@@ -600,9 +610,9 @@ def mx_quantize(right: Optional[Plan], x, codes=None, scales=None, stream=None):
     from torch import uint8
     rows, n, ld = _rows(x)
     if codes is None:
-        codes = x.new_empty((rows, n // 2), dtype=uint8)
+        codes = _made(stream, lambda: x.new_empty((rows, n // 2), dtype=uint8))
     if scales is None:
-        scales = x.new_empty((rows, n // 32), dtype=uint8)
+        scales = _made(stream, lambda: x.new_empty((rows, n // 32), dtype=uint8))
     check(lib().brq_mx_quantize(None if right is None else right._h, x.data_ptr(), dtype_code(x), ld, rows, n,
                                 _packed(codes, uint8, (rows, n // 2), "codes"),
                                 _packed(scales, uint8, (rows, n // 32), "scales"), _stream_of(stream, x)))
@@ -616,7 +626,7 @@ def mx_dequantize(right: Optional[Plan], codes, scales, out=None, out_dtype=None
     rows, n, _ = _rows(codes)
     n *= 2
     if out is None:
-        out = codes.new_empty((rows, n), dtype=out_dtype or float32)
+        out = _made(stream, lambda: codes.new_empty((rows, n), dtype=out_dtype or float32))
     elif out.shape != (rows, n):
         raise ValueError(f"out: expected shape {(rows, n)}, got {tuple(out.shape)}")
     check(lib().brq_mx_dequantize(None if right is None else right._h, _packed(codes, uint8, (rows, n // 2), "codes"),
@@ -641,11 +651,11 @@ def mx_matmul(a_codes, a_scales, b_codes, b_scales, y=None, out_dtype=None, ws=N
     n *= 2
     m = b_codes.shape[0]
     if y is None:
-        y = a_codes.new_empty((T, m), dtype=out_dtype or bfloat16)
+        y = _made(stream, lambda: a_codes.new_empty((T, m), dtype=out_dtype or bfloat16))
     elif y.shape != (T, m):
         raise ValueError(f"y: expected shape {(T, m)}, got {tuple(y.shape)}")
     if ws is None:
-        ws = _scratch(stream, mx_matmul_workspace(T, m, n, a_codes.device))
+        ws = _made(stream, lambda: mx_matmul_workspace(T, m, n, a_codes.device))
     wp, wb = _ws_args(ws)
     check(lib().brq_mx_matmul(_packed(a_codes, uint8, (T, n // 2), "a_codes"),
                               _packed(a_scales, uint8, (T, n // 32), "a_scales"),
@@ -706,9 +716,9 @@ def kv_read(plan: Optional[Plan], cache, slots, head_dim: int, page: int, k=None
     from torch import bfloat16, int64
     n, h, D = slots.shape[0], cache.shape[1], head_dim
     if k is None:
-        k = cache.new_empty((n, h, D), dtype=out_dtype or bfloat16)
+        k = _made(stream, lambda: cache.new_empty((n, h, D), dtype=out_dtype or bfloat16))
     if v is None:
-        v = k.new_empty((n, h, D))
+        v = _made(stream, lambda: k.new_empty((n, h, D)))
     if k.shape != (n, h, D) or v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError(f"k and v must have shape {(n, h, D)} and the same dtype")
     check(lib().brq_kv_read(None if plan is None else plan._h, _cache_ptr(cache, h, D, page),
@@ -737,11 +747,11 @@ def paged_attention(plan: Optional[Plan], q, cache, table, lens, page: int, scal
     B, hq, ldq = _heads(q, D, "q")
     h, pages = cache.shape[1], table.shape[-1]
     if out is None:
-        out = q.new_empty((B, hq, D))
+        out = _made(stream, lambda: q.new_empty((B, hq, D)))
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and dtype")
     if ws is None:
-        ws = _scratch(stream, paged_attention_workspace(B, hq, h, D, q.device))
+        ws = _made(stream, lambda: paged_attention_workspace(B, hq, h, D, q.device))
     wp, wb = _ws_args(ws)
     check(lib().brq_paged_attention(
         None if plan is None else plan._h, q.data_ptr(), ldq, dtype_code(q), _cache_ptr(cache, h, D, page),
