@@ -291,6 +291,10 @@ class Plan:
 
 
 def _h(plan: Optional[Plan]):
+    """The handle of a plan, NULL (no transform) for None.  A closed plan's is
+    NULL too, and would pass for none."""
+    if plan is not None and not plan.handle:
+        raise ValueError("the plan is closed")
     return None if plan is None else plan.handle
 
 
@@ -613,7 +617,7 @@ def mx_quantize(right: Optional[Plan], x, codes=None, scales=None, stream=None):
         codes = _made(stream, lambda: x.new_empty((rows, n // 2), dtype=uint8))
     if scales is None:
         scales = _made(stream, lambda: x.new_empty((rows, n // 32), dtype=uint8))
-    check(lib().brq_mx_quantize(None if right is None else right._h, x.data_ptr(), dtype_code(x), ld, rows, n,
+    check(lib().brq_mx_quantize(_h(right), x.data_ptr(), dtype_code(x), ld, rows, n,
                                 _packed(codes, uint8, (rows, n // 2), "codes"),
                                 _packed(scales, uint8, (rows, n // 32), "scales"), _stream_of(stream, x)))
     return codes, scales
@@ -629,7 +633,7 @@ def mx_dequantize(right: Optional[Plan], codes, scales, out=None, out_dtype=None
         out = _made(stream, lambda: codes.new_empty((rows, n), dtype=out_dtype or float32))
     elif out.shape != (rows, n):
         raise ValueError(f"out: expected shape {(rows, n)}, got {tuple(out.shape)}")
-    check(lib().brq_mx_dequantize(None if right is None else right._h, _packed(codes, uint8, (rows, n // 2), "codes"),
+    check(lib().brq_mx_dequantize(_h(right), _packed(codes, uint8, (rows, n // 2), "codes"),
                                   _packed(scales, uint8, (rows, n // 32), "scales"), rows, n,
                                   out.data_ptr(), dtype_code(out), _rows(out)[2], _stream_of(stream, out)))
     return out
@@ -702,7 +706,7 @@ def kv_append(plan: Optional[Plan], k, v, slots, cache, page: int, stream=None):
     n, h, ldk = _heads(k, D, "k")
     if v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError("k and v must have the same shape and dtype")
-    check(lib().brq_kv_append(None if plan is None else plan._h, k.data_ptr(), ldk, v.data_ptr(),
+    check(lib().brq_kv_append(_h(plan), k.data_ptr(), ldk, v.data_ptr(),
                               _heads(v, D, "v")[2], dtype_code(k), _packed(slots, int64, (n,), "slots"), n, h, D,
                               page, cache.shape[0], _cache_ptr(cache, h, D, page), _stream_of(stream, k)))
     return cache
@@ -721,7 +725,7 @@ def kv_read(plan: Optional[Plan], cache, slots, head_dim: int, page: int, k=None
         v = _made(stream, lambda: k.new_empty((n, h, D)))
     if k.shape != (n, h, D) or v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError(f"k and v must have shape {(n, h, D)} and the same dtype")
-    check(lib().brq_kv_read(None if plan is None else plan._h, _cache_ptr(cache, h, D, page),
+    check(lib().brq_kv_read(_h(plan), _cache_ptr(cache, h, D, page),
                             _packed(slots, int64, (n,), "slots"), n, h, D, page,
                             cache.shape[0], k.data_ptr(), _heads(k, D, "k")[2], v.data_ptr(),
                             _heads(v, D, "v")[2], dtype_code(k), _stream_of(stream, k)))
@@ -754,7 +758,7 @@ def paged_attention(plan: Optional[Plan], q, cache, table, lens, page: int, scal
         ws = _made(stream, lambda: paged_attention_workspace(B, hq, h, D, q.device))
     wp, wb = _ws_args(ws)
     check(lib().brq_paged_attention(
-        None if plan is None else plan._h, q.data_ptr(), ldq, dtype_code(q), _cache_ptr(cache, h, D, page),
+        _h(plan), q.data_ptr(), ldq, dtype_code(q), _cache_ptr(cache, h, D, page),
         cache.shape[0], _packed(table, int32, (B, pages), "table"), pages, _packed(lens, int32, (B,), "lens"),
         B, hq, h, D, page, D ** -0.5 if scale is None else scale, window, out.data_ptr(),
         _heads(out, D, "out")[2], None if lse is None else _packed(lse, float32, (B, hq), "lse"),
