@@ -555,15 +555,15 @@ def orp_geo_dequant(codes, signs, coef, m: int, n: int, bits: int, group: int, s
 
 # These calls are short (a decode step makes hundreds), so the marshalling keeps
 # to few torch calls; every check stays, since a wrong pointer would be the
-# GPU's to find.  With `stream`, the call runs on that stream and what it makes
-# (outputs not given, workspaces) belongs to it; the inputs have to be ready
-# there, and whoever uses the outputs elsewhere waits for that stream.
+# GPU's to find.  All tensors are on one GPU (`dev`), the current one.  With
+# `stream`, the call runs on that stream and what it makes (outputs not given,
+# workspaces) belongs to it; the inputs have to be ready there, and whoever uses
+# the outputs elsewhere waits for that stream.
 
-def _stream_of(stream, t) -> int:
-    """The raw stream: the one given, or the current one of t's GPU, which has to
+def _stream_of(stream, dev) -> int:
+    """The raw stream: the one given, or the current one of GPU dev, which has to
     be the current GPU (a kernel launched on another one's stream 0 would run here)."""
     import torch
-    dev = t.get_device()
     if dev != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on GPU {dev}, which is not the current one")
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
@@ -587,10 +587,10 @@ def _made(stream, make):
     return t
 
 
-def _rows(t) -> tuple:
-    """(rows, n, leading dimension) of a 2-D GPU tensor of contiguous rows."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError("expected a 2-D tensor on the GPU")
+def _rows(t, dev) -> tuple:
+    """(rows, n, leading dimension) of a 2-D tensor of contiguous rows on GPU dev."""
+    if t.dim() != 2 or t.get_device() != dev or dev < 0:
+        raise ValueError(f"expected a 2-D tensor on the call's GPU, got {tuple(t.shape)} on {t.device}")
     rows, n = t.shape
     ld, one = t.stride()
     if one != 1 and n > 1:
@@ -598,12 +598,19 @@ def _rows(t) -> tuple:
     return rows, n, (ld if rows > 1 and ld >= 0 else max(ld, n))
 
 
-def _packed(t, dtype, shape, what) -> int:
-    """Address of a contiguous GPU tensor of the library's own layout."""
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on the GPU, "
+def _packed(t, dtype, shape, what, dev) -> int:
+    """Address of a contiguous tensor of the library's own layout on GPU dev."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on the call's GPU, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
+
+
+def _ws_on(ws, dev) -> tuple:
+    """Address and bytes of a workspace on GPU dev."""
+    if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
+        raise ValueError(f"the workspace: expected a contiguous tensor on the call's GPU, got one on {ws.device}")
+    return _ws_args(ws)
 
 
 def mx_quantize(right: Optional[Plan], x, codes=None, scales=None, stream=None):
@@ -612,14 +619,15 @@ def mx_quantize(right: Optional[Plan], x, codes=None, scales=None, stream=None):
     or none (brq_mx_quantize).  Returns (codes uint8 [rows, n/2], scales uint8
     [rows, n/32])."""
     from torch import uint8
-    rows, n, ld = _rows(x)
+    dev = x.get_device()
+    rows, n, ld = _rows(x, dev)
     if codes is None:
         codes = _made(stream, lambda: x.new_empty((rows, n // 2), dtype=uint8))
     if scales is None:
         scales = _made(stream, lambda: x.new_empty((rows, n // 32), dtype=uint8))
     check(lib().brq_mx_quantize(_h(right), x.data_ptr(), dtype_code(x), ld, rows, n,
-                                _packed(codes, uint8, (rows, n // 2), "codes"),
-                                _packed(scales, uint8, (rows, n // 32), "scales"), _stream_of(stream, x)))
+                                _packed(codes, uint8, (rows, n // 2), "codes", dev),
+                                _packed(scales, uint8, (rows, n // 32), "scales", dev), _stream_of(stream, dev)))
     return codes, scales
 
 
@@ -627,15 +635,16 @@ def mx_dequantize(right: Optional[Plan], codes, scales, out=None, out_dtype=None
     """The values of microscaled 4-bit rows, with the plan `right` undone
     (brq_mx_dequantize).  Returns out [rows, n] (float32 by default)."""
     from torch import float32, uint8
-    rows, n, _ = _rows(codes)
+    dev = codes.get_device()
+    rows, n, _ = _rows(codes, dev)
     n *= 2
     if out is None:
         out = _made(stream, lambda: codes.new_empty((rows, n), dtype=out_dtype or float32))
     elif out.shape != (rows, n):
         raise ValueError(f"out: expected shape {(rows, n)}, got {tuple(out.shape)}")
-    check(lib().brq_mx_dequantize(_h(right), _packed(codes, uint8, (rows, n // 2), "codes"),
-                                  _packed(scales, uint8, (rows, n // 32), "scales"), rows, n,
-                                  out.data_ptr(), dtype_code(out), _rows(out)[2], _stream_of(stream, out)))
+    check(lib().brq_mx_dequantize(_h(right), _packed(codes, uint8, (rows, n // 2), "codes", dev),
+                                  _packed(scales, uint8, (rows, n // 32), "scales", dev), rows, n,
+                                  out.data_ptr(), dtype_code(out), _rows(out, dev)[2], _stream_of(stream, dev)))
     return out
 
 
@@ -651,7 +660,8 @@ def mx_matmul(a_codes, a_scales, b_codes, b_scales, y=None, out_dtype=None, ws=N
     (brq_mx_matmul): activations [T, n] times a weight [m, n] kept by output
     rows.  Returns y [T, m] (bfloat16 by default)."""
     from torch import bfloat16, uint8
-    T, n, _ = _rows(a_codes)
+    dev = a_codes.get_device()
+    T, n, _ = _rows(a_codes, dev)
     n *= 2
     m = b_codes.shape[0]
     if y is None:
@@ -660,12 +670,12 @@ def mx_matmul(a_codes, a_scales, b_codes, b_scales, y=None, out_dtype=None, ws=N
         raise ValueError(f"y: expected shape {(T, m)}, got {tuple(y.shape)}")
     if ws is None:
         ws = _made(stream, lambda: mx_matmul_workspace(T, m, n, a_codes.device))
-    wp, wb = _ws_args(ws)
-    check(lib().brq_mx_matmul(_packed(a_codes, uint8, (T, n // 2), "a_codes"),
-                              _packed(a_scales, uint8, (T, n // 32), "a_scales"),
-                              _packed(b_codes, uint8, (m, n // 2), "b_codes"),
-                              _packed(b_scales, uint8, (m, n // 32), "b_scales"), T, m, n,
-                              y.data_ptr(), dtype_code(y), _rows(y)[2], wp, wb, _stream_of(stream, y)))
+    wp, wb = _ws_on(ws, dev)
+    check(lib().brq_mx_matmul(_packed(a_codes, uint8, (T, n // 2), "a_codes", dev),
+                              _packed(a_scales, uint8, (T, n // 32), "a_scales", dev),
+                              _packed(b_codes, uint8, (m, n // 2), "b_codes", dev),
+                              _packed(b_scales, uint8, (m, n // 32), "b_scales", dev), T, m, n,
+                              y.data_ptr(), dtype_code(y), _rows(y, dev)[2], wp, wb, _stream_of(stream, dev)))
     return y
 
 
@@ -680,21 +690,21 @@ def kv_cache(pages: int, heads: int, head_dim: int, page: int, device="cuda"):
     return torch.zeros((pages, heads, nb), dtype=torch.uint8, device=device)
 
 
-def _heads(t, D, what) -> tuple:
-    """(tokens, heads, leading dimension) of a [tokens, heads, D] GPU tensor whose
-    heads follow one another."""
-    if t.dim() == 3 and t.is_cuda:
+def _heads(t, D, what, dev) -> tuple:
+    """(tokens, heads, leading dimension) of a [tokens, heads, D] tensor on GPU dev
+    whose heads follow one another."""
+    if t.dim() == 3 and t.get_device() == dev and dev >= 0:
         n, h, d = t.shape
         ld, sh, one = t.stride()
         if d == D and one == 1 and (h == 1 or sh == D):
             return n, h, (ld if n > 1 and ld >= 0 else max(ld, h * D))
-    raise ValueError(f"{what}: expected [tokens, heads, {D}] on the GPU with the heads of a token contiguous, "
+    raise ValueError(f"{what}: expected [tokens, heads, {D}] on the call's GPU with the heads of a token contiguous, "
                      f"got {tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
 
 
-def _cache_ptr(cache, heads, D, page) -> int:
+def _cache_ptr(cache, heads, D, page, dev) -> int:
     from torch import uint8
-    return _packed(cache, uint8, (cache.shape[0], heads, page * (D + D // 16)), "cache")
+    return _packed(cache, uint8, (cache.shape[0], heads, page * (D + D // 16)), "cache", dev)
 
 
 def kv_append(plan: Optional[Plan], k, v, slots, cache, page: int, stream=None):
@@ -702,13 +712,14 @@ def kv_append(plan: Optional[Plan], k, v, slots, cache, page: int, stream=None):
     tokens to cache slots int64 [tokens] (brq_kv_append; a slot outside the
     cache is skipped).  Returns cache."""
     from torch import int64
-    D = k.shape[-1]
-    n, h, ldk = _heads(k, D, "k")
+    D, dev = k.shape[-1], k.get_device()
+    n, h, ldk = _heads(k, D, "k", dev)
     if v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError("k and v must have the same shape and dtype")
     check(lib().brq_kv_append(_h(plan), k.data_ptr(), ldk, v.data_ptr(),
-                              _heads(v, D, "v")[2], dtype_code(k), _packed(slots, int64, (n,), "slots"), n, h, D,
-                              page, cache.shape[0], _cache_ptr(cache, h, D, page), _stream_of(stream, k)))
+                              _heads(v, D, "v", dev)[2], dtype_code(k), _packed(slots, int64, (n,), "slots", dev),
+                              n, h, D, page, cache.shape[0], _cache_ptr(cache, h, D, page, dev),
+                              _stream_of(stream, dev)))
     return cache
 
 
@@ -718,17 +729,17 @@ def kv_read(plan: Optional[Plan], cache, slots, head_dim: int, page: int, k=None
     (brq_kv_read).  Returns (k, v), each [tokens, heads, head_dim] (bfloat16 by
     default); a slot outside the cache reads as zeros."""
     from torch import bfloat16, int64
-    n, h, D = slots.shape[0], cache.shape[1], head_dim
+    n, h, D, dev = slots.shape[0], cache.shape[1], head_dim, cache.get_device()
     if k is None:
         k = _made(stream, lambda: cache.new_empty((n, h, D), dtype=out_dtype or bfloat16))
     if v is None:
         v = _made(stream, lambda: k.new_empty((n, h, D)))
     if k.shape != (n, h, D) or v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError(f"k and v must have shape {(n, h, D)} and the same dtype")
-    check(lib().brq_kv_read(_h(plan), _cache_ptr(cache, h, D, page),
-                            _packed(slots, int64, (n,), "slots"), n, h, D, page,
-                            cache.shape[0], k.data_ptr(), _heads(k, D, "k")[2], v.data_ptr(),
-                            _heads(v, D, "v")[2], dtype_code(k), _stream_of(stream, k)))
+    check(lib().brq_kv_read(_h(plan), _cache_ptr(cache, h, D, page, dev),
+                            _packed(slots, int64, (n,), "slots", dev), n, h, D, page,
+                            cache.shape[0], k.data_ptr(), _heads(k, D, "k", dev)[2], v.data_ptr(),
+                            _heads(v, D, "v", dev)[2], dtype_code(k), _stream_of(stream, dev)))
     return k, v
 
 
@@ -747,8 +758,8 @@ def paged_attention(plan: Optional[Plan], q, cache, table, lens, page: int, scal
     1/sqrt(D), window 0 sees every cached token; lse, if given, is a float32
     [batch, q_heads] output.  Returns out, like q."""
     from torch import float32, int32
-    D = q.shape[-1]
-    B, hq, ldq = _heads(q, D, "q")
+    D, dev = q.shape[-1], q.get_device()
+    B, hq, ldq = _heads(q, D, "q", dev)
     h, pages = cache.shape[1], table.shape[-1]
     if out is None:
         out = _made(stream, lambda: q.new_empty((B, hq, D)))
@@ -756,13 +767,13 @@ def paged_attention(plan: Optional[Plan], q, cache, table, lens, page: int, scal
         raise ValueError("out must have q's shape and dtype")
     if ws is None:
         ws = _made(stream, lambda: paged_attention_workspace(B, hq, h, D, q.device))
-    wp, wb = _ws_args(ws)
+    wp, wb = _ws_on(ws, dev)
     check(lib().brq_paged_attention(
-        _h(plan), q.data_ptr(), ldq, dtype_code(q), _cache_ptr(cache, h, D, page),
-        cache.shape[0], _packed(table, int32, (B, pages), "table"), pages, _packed(lens, int32, (B,), "lens"),
+        _h(plan), q.data_ptr(), ldq, dtype_code(q), _cache_ptr(cache, h, D, page, dev),
+        cache.shape[0], _packed(table, int32, (B, pages), "table", dev), pages, _packed(lens, int32, (B,), "lens", dev),
         B, hq, h, D, page, D ** -0.5 if scale is None else scale, window, out.data_ptr(),
-        _heads(out, D, "out")[2], None if lse is None else _packed(lse, float32, (B, hq), "lse"),
-        wp, wb, _stream_of(stream, q)))
+        _heads(out, D, "out", dev)[2], None if lse is None else _packed(lse, float32, (B, hq), "lse", dev),
+        wp, wb, _stream_of(stream, dev)))
     return out
 
 

@@ -1,0 +1,102 @@
+"""CPU checks of the microscaled operators' binding: every tensor of a call has
+to be on one GPU, a workspace too.  The tensors are stand-ins that say where
+they are, and the library is one that only notes that it was called."""
+
+import pytest
+import torch
+
+import butterfly_rotation_quantization_amd as brq
+
+
+class At:
+    """A tensor said to be on GPU `gpu` (-1: in host memory)."""
+
+    def __init__(self, t, gpu):
+        self._t, self._gpu = t, gpu
+
+    def get_device(self):
+        return self._gpu
+
+    @property
+    def is_cuda(self):
+        return self._gpu >= 0
+
+    @property
+    def device(self):
+        return f"cuda:{self._gpu}" if self._gpu >= 0 else "cpu"
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+
+class Library:
+    def __init__(self):
+        self.called = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.called.append(name)
+            return 0
+        return call
+
+
+@pytest.fixture
+def library(monkeypatch):
+    lib = Library()
+    monkeypatch.setattr(brq, "lib", lambda: lib)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    return lib
+
+
+def u8(*shape):
+    return torch.zeros(shape, dtype=torch.uint8)
+
+
+KV = lambda: torch.zeros((5, 2, 64))  # noqa: E731
+CACHE = lambda: u8(3, 2, 16 * 68)  # noqa: E731
+CALLS = {
+    "quantize": (lambda a: brq.mx_quantize(None, a["x"], a["codes"], a["scales"]),
+                 dict(x=torch.zeros((4, 64)), codes=u8(4, 32), scales=u8(4, 2))),
+    "dequantize": (lambda a: brq.mx_dequantize(None, a["codes"], a["scales"], out=a["out"]),
+                   dict(out=torch.zeros((4, 64)), codes=u8(4, 32), scales=u8(4, 2))),
+    "matmul": (lambda a: brq.mx_matmul(a["a"], a["sa"], a["b"], a["sb"], y=a["y"], ws=a["ws"]),
+               dict(a=u8(4, 32), sa=u8(4, 2), b=u8(7, 32), sb=u8(7, 2), y=torch.zeros((4, 7)), ws=u8(64))),
+    "append": (lambda a: brq.kv_append(None, a["k"], a["v"], a["slots"], a["cache"], 16),
+               dict(k=KV(), v=KV(), slots=torch.arange(5), cache=CACHE())),
+    "read": (lambda a: brq.kv_read(None, a["cache"], a["slots"], 64, 16, k=a["k"], v=a["v"]),
+             dict(k=KV(), v=KV(), slots=torch.arange(5), cache=CACHE())),
+    "attention": (lambda a: brq.paged_attention(None, a["q"], a["cache"], a["table"], a["lens"], 16, out=a["out"],
+                                                lse=a["lse"], ws=a["ws"]),
+                  dict(q=torch.zeros((3, 4, 64)), cache=CACHE(), table=torch.zeros((3, 2), dtype=torch.int32),
+                       lens=torch.zeros(3, dtype=torch.int32), out=torch.zeros((3, 4, 64)), lse=torch.zeros((3, 4)),
+                       ws=u8(64))),
+}
+
+
+@pytest.mark.parametrize("call,name,gpu", [(c, n, g) for c, (_, a) in CALLS.items() for n in a for g in (1, -1)])
+def test_one_tensor_elsewhere(library, call, name, gpu):
+    f, tensors = CALLS[call]
+    f({n: At(t, 0) for n, t in tensors.items()})
+    assert library.called
+    library.called.clear()
+    with pytest.raises(ValueError):
+        f({n: At(t, gpu if n == name else 0) for n, t in tensors.items()})
+    assert not library.called
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+def test_all_tensors_on_another_gpu_than_the_current_one(library, call):
+    f, tensors = CALLS[call]
+    with pytest.raises(ValueError):
+        f({n: At(t, 1) for n, t in tensors.items()})
+    assert not library.called
+
+
+@pytest.mark.parametrize("call", ["matmul", "attention"])
+def test_a_workspace_with_gaps(library, call):
+    """Its elements would count for more bytes in a row than it has."""
+    f, tensors = CALLS[call]
+    with pytest.raises(ValueError):
+        f({n: At(u8(64, 2)[:, 0] if n == "ws" else t, 0) for n, t in tensors.items()})
+    assert not library.called
