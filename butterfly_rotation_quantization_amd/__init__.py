@@ -595,7 +595,7 @@ def _rows(t, dev) -> tuple:
     ld, one = t.stride()
     if one != 1 and n > 1:
         raise ValueError("expected a 2-D tensor with unit column stride")
-    return rows, n, (ld if rows > 1 and ld >= 0 else max(ld, n))
+    return rows, n, (ld if rows > 1 else n)  # one row: whatever its stride
 
 
 def _packed(t, dtype, shape, what, dev) -> int:
@@ -697,7 +697,7 @@ def _heads(t, D, what, dev) -> tuple:
         n, h, d = t.shape
         ld, sh, one = t.stride()
         if d == D and one == 1 and (h == 1 or sh == D):
-            return n, h, (ld if n > 1 and ld >= 0 else max(ld, h * D))
+            return n, h, (ld if n > 1 else h * D)
     raise ValueError(f"{what}: expected [tokens, heads, {D}] on the call's GPU with the heads of a token contiguous, "
                      f"got {tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
 

@@ -100,3 +100,24 @@ def test_a_workspace_with_gaps(library, call):
     with pytest.raises(ValueError):
         f({n: At(u8(64, 2)[:, 0] if n == "ws" else t, 0) for n, t in tensors.items()})
     assert not library.called
+
+
+def test_the_stride_of_a_single_row_does_not_matter(library, monkeypatch):
+    """A row of a tensor whose rows are no multiple of 16 bytes apart: the
+    library is told the row's own length, which it takes."""
+    seen = {}
+    for name in ("brq_mx_quantize", "brq_mx_dequantize", "brq_mx_matmul", "brq_kv_append", "brq_paged_attention"):
+        monkeypatch.setattr(library, name, lambda *a, name=name: seen.update({name: a}) or 0, raising=False)
+    wide = torch.zeros((3, 68))[1:2, :64]
+    heads = torch.zeros((3, 132))[1:2, :128].unflatten(1, (2, 64))
+    g = lambda t: At(t, 0)  # noqa: E731
+    codes, scales = g(u8(1, 32)), g(u8(1, 2))
+    brq.mx_quantize(None, g(wide), codes, scales)
+    brq.mx_dequantize(None, codes, scales, out=g(wide))
+    brq.mx_matmul(codes, scales, g(u8(64, 32)), g(u8(64, 2)), y=g(wide), ws=g(u8(64)))
+    brq.kv_append(None, g(heads), g(heads), g(torch.zeros(1, dtype=torch.int64)), g(CACHE()), 16)
+    brq.paged_attention(None, g(heads), g(CACHE()), g(torch.zeros((1, 2), dtype=torch.int32)),
+                        g(torch.zeros(1, dtype=torch.int32)), 16, out=g(heads), ws=g(u8(64)))
+    assert seen["brq_mx_quantize"][3] == 64 and seen["brq_mx_dequantize"][7] == 64 and seen["brq_mx_matmul"][9] == 64
+    assert seen["brq_kv_append"][2] == 128 and seen["brq_kv_append"][4] == 128
+    assert seen["brq_paged_attention"][2] == 128 and seen["brq_paged_attention"][17] == 128
