@@ -768,6 +768,7 @@ def paged_attention(plan: Optional[Plan], q, cache, table, lens, page: int, scal
     if ws is None:
         ws = _made(stream, lambda: paged_attention_workspace(B, hq, h, D, q.device))
     wp, wb = _ws_on(ws, dev)
+    window = max(-1, min(window, 2 ** 31 - 1))  # the call takes 32 bits, and would take those of a longer one
     check(lib().brq_paged_attention(
         _h(plan), q.data_ptr(), ldq, dtype_code(q), _cache_ptr(cache, h, D, page, dev),
         cache.shape[0], _packed(table, int32, (B, pages), "table", dev), pages, _packed(lens, int32, (B,), "lens", dev),

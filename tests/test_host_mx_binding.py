@@ -121,3 +121,17 @@ def test_the_stride_of_a_single_row_does_not_matter(library, monkeypatch):
     assert seen["brq_mx_quantize"][3] == 64 and seen["brq_mx_dequantize"][7] == 64 and seen["brq_mx_matmul"][9] == 64
     assert seen["brq_kv_append"][2] == 128 and seen["brq_kv_append"][4] == 128
     assert seen["brq_paged_attention"][2] == 128 and seen["brq_paged_attention"][17] == 128
+
+
+def test_a_window_beyond_32_bits(library, monkeypatch):
+    """The C call takes 32 bits: a longer window sees all there is, as its value
+    says, and a negative one stays negative (and is refused)."""
+    import ctypes
+    seen = []
+    monkeypatch.setattr(library, "brq_paged_attention", lambda *a: seen.append(ctypes.c_int32(a[15]).value) or 0,
+                        raising=False)
+    f, tensors = CALLS["attention"]
+    t = {n: At(x, 0) for n, x in tensors.items()}
+    for window in (0, 5, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 63 - 1, -1, -2 ** 32):
+        brq.paged_attention(None, t["q"], t["cache"], t["table"], t["lens"], 16, window=window, out=t["out"], ws=t["ws"])
+    assert seen == [0, 5] + [2 ** 31 - 1] * 4 + [-1] * 2
