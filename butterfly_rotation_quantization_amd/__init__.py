@@ -307,7 +307,10 @@ def dtype_code(t) -> int:
     if not _DTYPES:
         import torch
         _DTYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
-    return _DTYPES[t.dtype]
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"expected a float32, bfloat16 or float16 tensor, got {t.dtype}")
+    return code
 
 
 def _torch_dtype(code: int):

@@ -135,3 +135,13 @@ def test_a_window_beyond_32_bits(library, monkeypatch):
     for window in (0, 5, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 63 - 1, -1, -2 ** 32):
         brq.paged_attention(None, t["q"], t["cache"], t["table"], t["lens"], 16, window=window, out=t["out"], ws=t["ws"])
     assert seen == [0, 5] + [2 ** 31 - 1] * 4 + [-1] * 2
+
+
+@pytest.mark.parametrize("call,name", [("quantize", "x"), ("dequantize", "out"), ("matmul", "y"), ("append", "kv"),
+                                       ("read", "kv"), ("attention", "q out")])
+def test_other_types_are_refused_like_other_layouts(library, call, name):
+    f, tensors = CALLS[call]
+    names = ["k", "v"] if name == "kv" else name.split()
+    with pytest.raises(ValueError):
+        f({n: At(t.double() if n in names else t, 0) for n, t in tensors.items()})
+    assert not library.called
