@@ -14,13 +14,15 @@ static hipError_t bad(const char* fmt, long long a, long long b) {
   dry_violation(fmt, a, b);
   return hipErrorInvalidValue;
 }
+// A launch has fewer than 2^32 threads along a dimension.
+static bool launchable(int64_t workgroups, int64_t threads) { return workgroups * threads < (int64_t)1 << 32; }
 
 static hipError_t walk_mx(const MxArgs& a, int64_t ld) {
   dry_launch();
   const int64_t n = (int64_t)a.lpr * a.per;
   if ((a.per != 8 && a.per != 16) || n % kMxBlock || a.lanes != (uint64_t)a.rows * a.lpr || ld < n || (a.d && n % a.d))
     return bad("mx geometry (row of %lld, d %lld)", n, a.d);
-  if (a.lanes / kMxThreads >= ((uint64_t)1 << 31)) return bad("mx grid of %lld lanes", (long long)a.lanes, 0);
+  if (!launchable((int64_t)(a.lanes + kMxThreads - 1) / kMxThreads, kMxThreads)) return bad("mx grid of %lld lanes", (long long)a.lanes, 0);
   if (a.lanes > (1 << 22)) return hipSuccess;  // walked in full at test sizes
   std::vector<uint8_t> cover((size_t)(a.rows * n), 0);
   for (uint64_t li = 0; li < a.lanes; ++li) {
@@ -49,7 +51,8 @@ static hipError_t walk_tiles(const MmArgs& a) {
       reinterpret_cast<uint8_t*>(a.part) != a.ts + images ||
       (int64_t)bytes != images + (a.splits > 1 ? a.splits * a.T * a.m * 4 : 0))
     return bad("mx matmul workspace (%lld bytes, tile %lld)", (long long)bytes, R);
-  if (a.gt * R < a.T || a.go * R < a.m || (int64_t)a.stages * kMmK < a.n || 8 * a.per_xcd >= (int64_t)1 << 31)
+  if (a.gt * R < a.T || a.go * R < a.m || (int64_t)a.stages * kMmK < a.n || !launchable(8 * a.per_xcd, 256) ||
+      !launchable(a.gt + a.go, kMxThreads))
     return bad("mx matmul tiles (%lld x %lld)", a.gt, a.go);
   for (int p = 0; p < a.splits; ++p)
     if (a.stages - p * a.per < 1 || (p + 1 == a.splits && a.stages > (p + 1) * a.per))
@@ -102,9 +105,10 @@ hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t) {
   if (a.tile) return walk_tiles(a);
   if (a.T <= 64) {
     const int rows = mm_stream_rows(a);
-    if ((rows != 16 && rows != 32) || (a.m + rows - 1) / rows >= (int64_t)1 << 31)
+    const int64_t wgs = (a.m + rows - 1) / rows;
+    if ((rows != 16 && rows != 32) || !launchable(wgs, 64 * mm_stream_waves(wgs)))
       return bad("mx matmul stream of %lld rows", a.m, 0);
-  } else if (((a.T + 15) / 16) * ((a.m + 15) / 16) >= (int64_t)1 << 31) {
+  } else if (!launchable(((a.T + 15) / 16) * ((a.m + 15) / 16), 64)) {
     return bad("mx matmul grid (%lld x %lld)", a.T, a.m);
   }
   return hipSuccess;
@@ -140,7 +144,8 @@ static hipError_t walk_kv(const KvArgs& a) {
       (a.d && a.d != a.pg.D))
     return bad("cache geometry (page %lld, D %lld)", a.pg.P, a.pg.D);
   const int64_t rows = kv_rows(a.tokens, a.heads);
-  if (rows >= (int64_t)1 << 31) return bad("cache rows of %lld tokens", a.tokens, 0);
+  if (rows >= (int64_t)1 << 31 || !launchable(rows * (a.pg.D / kMxPerLane) / kMxThreads + 1, kMxThreads))
+    return bad("cache rows of %lld tokens", a.tokens, 0);
   if (rows <= 1 << 22) {  // every head of every token once
     std::vector<uint8_t> cover((size_t)(a.tokens * a.heads), 0);
     for (int64_t r = 0; r < rows; ++r) {
@@ -166,6 +171,10 @@ hipError_t launch_paged_attention(const AtArgs& a, hipStream_t) {
   if ((1 << a.lgP) != pg.P || a.group * a.heads != a.q_heads || a.ht * a.nt * kAtCols < a.group ||
       (int64_t)a.cap > a.ldt << a.lgP || a.cap > kAtMaxKeys || a.wgs < 0 || (a.wgs > 0 && !a.part))
     return bad("attention geometry (group %lld, workgroups %lld)", a.group, a.wgs);
+  const int64_t units = a.batch * a.heads * a.ht;
+  if (!launchable(a.wgs ? a.wgs : units, kAtThreads) ||
+      (a.wgs && !launchable(units * (kAtCols * a.nt / at_join_rows(units, a.nt, D)), kAtThreads)))
+    return bad("attention launch for %lld units", units, 0);
   // the deal of tiles to workgroups for some lengths: every part has a slot of
   // its own, and the join finds the workgroups that have one
   for (int seed = 0; a.wgs && a.batch <= 64 && seed < 6; ++seed) {

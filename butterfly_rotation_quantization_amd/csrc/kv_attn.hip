@@ -618,11 +618,8 @@ hipError_t at_launch(const AtArgs& a, hipStream_t s) {
   else at_kernel<D, 2><<<grid, kAtThreads, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.wgs) return e;
-  // few units: each has many parts, and a workgroup for every row; many: most
-  // were finished in one place, and a workgroup looks after several rows
-  const int H = kAtCols * a.nt, most = kAtThreads / (D / kMxPerLane);
-  const int rows = units * H <= 2048 ? 1 : (H < most ? H : most);
-  at_join_kernel<D><<<dim3((unsigned)(units * (H / rows))), kAtThreads, 0, s>>>(a, rows);
+  const int rows = at_join_rows(units, a.nt, D);
+  at_join_kernel<D><<<dim3((unsigned)(units * (kAtCols * a.nt / rows))), kAtThreads, 0, s>>>(a, rows);
   return hipGetLastError();
 }
 

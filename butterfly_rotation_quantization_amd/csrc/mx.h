@@ -293,6 +293,14 @@ struct AtArgs {
   int2* who;             // [batch][heads][ht]: a unit's first slot, workgroups after its first
 };
 
+// Rows of a workgroup of the join.  Few units: each has many parts, and a
+// workgroup for every row; many: most were finished in one place, and a
+// workgroup looks after several rows.
+inline int at_join_rows(int64_t units, int nt, int head_dim) {
+  const int rows = kAtCols * nt, most = kAtThreads / (head_dim / kMxPerLane);
+  return units * rows <= 2048 ? 1 : (rows < most ? rows : most);
+}
+
 // Workspace bytes with and without the units' records.
 inline size_t at_part_bytes(int head_dim, int nt) {
   return (size_t)2 * at_workgroups(head_dim, nt) * nt * kAtCols * (head_dim + 4) * sizeof(float);

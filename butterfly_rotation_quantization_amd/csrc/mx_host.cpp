@@ -307,8 +307,8 @@ brq_status brq_paged_attention(const brq_plan* plan, const void* q, int64_t ldq,
     return refuse(BRQ_ERR_INVALID_ARGUMENT, "leading dimension below q_heads * head_dim");
   if ((st = transform_of(plan, head_dim, &a.signs, &a.d, &a.rnorm)) != BRQ_OK) return st;
   if (batch == 0) return BRQ_OK;
-  if (batch > ((int64_t)1 << 24) / q_heads)
-    return refuse(BRQ_ERR_UNSUPPORTED, "more than 2^24 sequences times query heads");
+  if (batch > (((int64_t)1 << 24) - 1) / q_heads)  // up to one workgroup of 256 threads for each
+    return refuse(BRQ_ERR_UNSUPPORTED, "2^24 sequences times query heads or more");
   if (!q || !out || !lens || (ldt > 0 && !table) || (pages > 0 && !cache))
     return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL data pointer");
   if (rows_misaligned(q, ldq, qt) || rows_misaligned(out, ldo, qt))

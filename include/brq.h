@@ -488,8 +488,8 @@ brq_status brq_kv_read(const brq_plan* plan, const uint8_t* cache, const int64_t
  * 4-bit pieces, together within 2^-23 of the largest magnitude of its block of
  * 32 after the transform and the scale, and a probability has its 24 bits.
  * Errors: INVALID_ARGUMENT (q_heads not a multiple of heads, NULLs, scale not
- * finite, window < 0), UNSUPPORTED (head_dim, page, the plan; more than 2^24
- * sequences times query heads), ALIGNMENT, WORKSPACE, HIP.  batch == 0 is a no-op. */
+ * finite, window < 0), UNSUPPORTED (head_dim, page, the plan; 2^24
+ * sequences times query heads or more), ALIGNMENT, WORKSPACE, HIP.  batch == 0 is a no-op. */
 size_t brq_paged_attention_workspace_bytes(int64_t batch, int32_t q_heads, int32_t heads,
                                            int32_t head_dim);
 brq_status brq_paged_attention(const brq_plan* plan, const void* q, int64_t ldq, int32_t qt,

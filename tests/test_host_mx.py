@@ -159,3 +159,23 @@ def test_attention_refusals(dl):
     assert f(ws=None) == WORKSPACE
 
 
+
+
+@pytest.mark.parametrize("B,hq,H", [(4097, 64, 64), (4096, 4095, 4095), ((1 << 24) - 1, 1, 1), (1 << 23, 1, 1), (5000, 3355, 1),
+                                    (4096, 4080, 255), (100000, 160, 8)])
+def test_attention_walk_of_large_batches(dl, B, hq, H):
+    """Up to the largest number of sequences times query heads every launch has
+    fewer than 2^32 threads."""
+    nb = dl.brq_paged_attention_workspace_bytes(B, hq, H, 256)
+    for D in (64, 256):
+        dl.brq_dryrun_reset()
+        _ok(dl, dl.brq_paged_attention(None, X, hq * D, 1, CACHE, 100, TABLE, 4, LENS, B, hq, H, D, 16, 0.1, 0, Y, hq * D,
+                                       None, WS if nb else None, nb, None), f"attention {B}x{hq}/{H}")
+
+
+def test_attention_refuses_a_launch_that_cannot_be(dl):
+    for B, hq in ((1 << 24, 1), (1 << 20, 16), (4096, 4096), (1 << 23, 2)):
+        for D in (64, 128):
+            nb = dl.brq_paged_attention_workspace_bytes(B, hq, hq, D)
+            assert dl.brq_paged_attention(None, X, hq * D, 1, CACHE, 9, TABLE, 4, LENS, B, hq, hq, D, 64, 0.1, 0, Y, hq * D,
+                                          None, WS, nb, None) == UNSUPPORTED
