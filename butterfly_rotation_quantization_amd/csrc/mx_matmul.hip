@@ -179,7 +179,7 @@ hipError_t mm_rows(const MmArgs& a, hipStream_t s) {
 // a stage of 128 products of 16 x 16 x 128).  The hardware orders these among themselves and
 // after the loads of their operands; two wait states cover a move into an
 // operand just before (the matrix unit is busy longer than that with the
-// product before); mm_settle comes before other reads of c.
+// product before); mm_settle and mm_settled come before other reads of c.
 template <int SA, int SB>
 __device__ __forceinline__ void mm_mfma(mxi4 a, mxi4 b, mxf16& c, int sa, int sb) {
   asm volatile(
@@ -187,8 +187,11 @@ __device__ __forceinline__ void mm_mfma(mxi4 a, mxi4 b, mxf16& c, int sa, int sb
       : "+a"(c)
       : "v"(a), "v"(b), "v"(sa), "v"(sb), "n"(SA & 1), "n"(SB & 1), "n"(SA >> 1), "n"(SB >> 1));
 }
-// More wait states than any product needs until its result can be read.
+// More wait states than any product needs until its result can be read; then,
+// for each sum, a statement that passes it on, behind which its reads stay (they
+// are register moves, which a clobber of memory does not hold back).
 __device__ __forceinline__ void mm_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+__device__ __forceinline__ void mm_settled(mxf16& c) { asm volatile("" : "+a"(c)); }
 // byte ia of sa and byte ib of sb (constants once the loops are unrolled)
 __device__ __forceinline__ void mm_step(mxi4 a, mxi4 b, mxf16& c, int sa, int ia, int sb, int ib) {
   switch ((ia & 3) * 4 + (ib & 3)) {
@@ -238,13 +241,18 @@ __device__ const uint4 kMmZero = {0u, 0u, 0u, 0u};
 // read to depend on such a load, would wait for it before the next one; the
 // kernel waits for vmcnt(0) and a barrier before it reads what was brought.
 __device__ __forceinline__ void mm_to_lds(const void* p, uint32_t at) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(p) : "memory");
+  uint32_t m0;  // written, not read
+  asm volatile("s_mov_b32 %0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off"
+               : "=&{m0}"(m0)
+               : "s"(at), "v"(p)
+               : "memory");
 }
 // The same from base + (off + step), to byte at + to; off is left there.
 template <int TO>
 __device__ __forceinline__ void mm_to_lds(const void* base, uint32_t& off, uint32_t step, uint32_t at) {
-  asm volatile("s_add_u32 m0, %3, %4\n\tv_add_u32 %0, %2, %0\n\tglobal_load_lds_dwordx4 %0, %1"
-               : "+v"(off)
+  uint32_t m0;
+  asm volatile("s_add_u32 %1, %4, %5\n\tv_add_u32 %0, %3, %0\n\tglobal_load_lds_dwordx4 %0, %2"
+               : "+&v"(off), "=&{m0}"(m0)
                : "s"(base), "s"(step), "s"(at), "n"(TO)
                : "memory", "scc");
 }
@@ -546,6 +554,10 @@ struct MmTile {
       if (s + 1 < stages) stage<1>(s + 1, f0, f1, src);
     }
     mm_settle();
+#pragma unroll
+    for (int i = 0; i < TO; ++i)
+#pragma unroll
+      for (int j = 0; j < TT; ++j) mm_settled(acc[i][j]);
     // LDS is about to hold the sums: the last pieces, fetched for no stage,
     // have to be in it before, and every wavefront's reads done
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
