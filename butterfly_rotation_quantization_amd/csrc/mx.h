@@ -153,11 +153,14 @@ __host__ __device__ constexpr int mm_scale_at(int R, int c, int r) { return (c *
 // every compute unit one: the activations are read half as often (8192x28672:
 // 16 tokens 37 -> 30 us, 64 tokens 83 -> 53 us).
 inline int mm_stream_rows(const MmArgs& a) { return a.m >= 32 * 256 ? 32 : 16; }
-// Wavefronts of a workgroup of the stream.  Eight put only one workgroup on a
-// compute unit at a time; four where that still makes more than five
-// wavefronts a unit (16x11008x4000, 344 workgroups: 11.0 -> 9.6 us; 4x5120x5120,
-// 320: 7.1 us with eight, 7.5 with four).
-inline int mm_stream_waves(int64_t wgs) { return 4 * wgs > 5 * 256 ? 4 : 8; }
+// Wavefronts of a workgroup of the stream.  With one workgroup for each compute
+// unit or less, eight: more of a long row is in flight (one token at 4096x28672
+// 14.0 us, with four 16.9; at 4096x4096 4.1 both).  Beyond that four, or one
+// workgroup of eight keeps the next off its unit: 257 and more workgroups of 32
+// rows take 3 to 18% less with four at lengths of 512 to 28672 (16x9216x4000 9.8
+// us, with eight 11.3; 16x9216x5120 10.1 and 10.8), of 16 rows up to 25% less
+// above 16 tokens, otherwise the same within 4%.
+inline int mm_stream_waves(int64_t wgs) { return wgs > 256 ? 4 : 8; }
 
 hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t s);
 

@@ -11,9 +11,12 @@ __device__ __forceinline__ void mm_store(void* y, int yt, int64_t off, float v) 
   else static_cast<uint16_t*>(y)[off] = (uint16_t)mx_f16(v);
 }
 
-// For rows too short (or too long) for the kernels below.  One wavefront per
-// 16 x 16 outputs: lane l holds block l / 16 of a step of
-// 128 values of row l % 16, of both operands, with the block's scale.
+// For more than 64 tokens whose rows are too short (or too long) for the tiles
+// below.  One wavefront per 16 x 16 outputs: lane l holds block l / 16 of a step of
+// 128 values of row l % 16, of both operands, with the block's scale.  Bound by
+// the outputs where they are many (2048x4096x128 12 us, 8192x8192x224 80 us, 1.7
+// TB/s written two bytes a lane), by one wavefront's way through a row where that
+// is long (65x64 by 2^23 values: 32 ms).
 __global__ __launch_bounds__(64) void mm_simple_kernel(MmArgs a) {
   const int lane = threadIdx.x, lr = lane & 15, lg = lane >> 4;
   const uint32_t go = (uint32_t)((a.m + 15) / 16);
