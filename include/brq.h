@@ -481,7 +481,11 @@ brq_status brq_kv_read(const brq_plan* plan, const uint8_t* cache, const int64_t
  *   lens: device int32 [batch]; lse: device float32 [batch][q_heads], the
  *         natural logarithm of the sum of exp(s_j), or NULL.
  *   ws: device workspace of brq_paged_attention_workspace_bytes(...) bytes
- *       (16-byte aligned): partial results where a sequence's length is split.
+ *       (16-byte aligned; may be NULL if that is 0): partial results where a
+ *       sequence's length is split.  Up to 4096 sequences the work is dealt out
+ *       evenly whatever their lengths; of more, each group of query heads (of up
+ *       to 8 or 16 over one key-value head) is one workgroup's however long its
+ *       sequence, so a few long ones among them belong in a call of their own.
  * Lengths and tables are read on the device at each call, so a captured call
  * can be replayed while sequences grow.  Maxima, normalisers and sums are held
  * in float32.  Where they enter the matrix units, for every qt, a query is eight
