@@ -293,9 +293,12 @@ class Plan:
 def _h(plan: Optional[Plan]):
     """The handle of a plan, NULL (no transform) for None.  A closed plan's is
     NULL too, and would pass for none."""
-    if plan is not None and not plan.handle:
+    if plan is None:
+        return None
+    h = plan.handle
+    if not h:
         raise ValueError("the plan is closed")
-    return None if plan is None else plan.handle
+    return h
 
 
 # ---------------------------------------------------------------- torch marshalling
@@ -572,22 +575,25 @@ def _stream_of(stream, dev) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _made(stream, make):
-    """make(), a tensor the binding makes for a call, from the memory of the
-    call's stream.  Memory of the current stream's may still be in use by work
+def _maker(stream, make):
+    """`make`, a call that makes a tensor, for the call's stream: from that
+    stream's memory.  Memory of the current stream's may still be in use by work
     ahead on it, and once freed would be handed out there again with the call
     ahead on the other stream.  The current stream, where the caller goes on
     (once it waits for the call), may use the tensor too."""
     if stream is None:
-        return make()
+        return make
     import torch
     at = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
     here = torch.cuda.current_stream()
-    with torch.cuda.stream(at):
-        t = make()
-    if t is not None and here.cuda_stream != at.cuda_stream:
-        t.record_stream(here)
-    return t
+
+    def made(*args, **kw):
+        with torch.cuda.stream(at):
+            t = make(*args, **kw)
+        if t is not None and here.cuda_stream != at.cuda_stream:
+            t.record_stream(here)
+        return t
+    return made
 
 
 def _rows(t, dev) -> tuple:
@@ -611,9 +617,11 @@ def _packed(t, dtype, shape, what, dev) -> int:
 
 def _ws_on(ws, dev) -> tuple:
     """Address and bytes of a workspace on GPU dev."""
-    if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"the workspace: expected a contiguous tensor on the call's GPU, got one on {ws.device}")
-    return _ws_args(ws)
+    return ws.data_ptr(), ws.nbytes
 
 
 def mx_quantize(right: Optional[Plan], x, codes=None, scales=None, stream=None):
@@ -624,10 +632,10 @@ def mx_quantize(right: Optional[Plan], x, codes=None, scales=None, stream=None):
     from torch import uint8
     dev = x.get_device()
     rows, n, ld = _rows(x, dev)
-    if codes is None:
-        codes = _made(stream, lambda: x.new_empty((rows, n // 2), dtype=uint8))
-    if scales is None:
-        scales = _made(stream, lambda: x.new_empty((rows, n // 32), dtype=uint8))
+    if codes is None or scales is None:
+        new = _maker(stream, x.new_empty)
+        codes = new((rows, n // 2), dtype=uint8) if codes is None else codes
+        scales = new((rows, n // 32), dtype=uint8) if scales is None else scales
     check(lib().brq_mx_quantize(_h(right), x.data_ptr(), dtype_code(x), ld, rows, n,
                                 _packed(codes, uint8, (rows, n // 2), "codes", dev),
                                 _packed(scales, uint8, (rows, n // 32), "scales", dev), _stream_of(stream, dev)))
@@ -642,7 +650,7 @@ def mx_dequantize(right: Optional[Plan], codes, scales, out=None, out_dtype=None
     rows, n, _ = _rows(codes, dev)
     n *= 2
     if out is None:
-        out = _made(stream, lambda: codes.new_empty((rows, n), dtype=out_dtype or float32))
+        out = _maker(stream, codes.new_empty)((rows, n), dtype=out_dtype or float32)
     elif out.shape != (rows, n):
         raise ValueError(f"out: expected shape {(rows, n)}, got {tuple(out.shape)}")
     check(lib().brq_mx_dequantize(_h(right), _packed(codes, uint8, (rows, n // 2), "codes", dev),
@@ -668,11 +676,11 @@ def mx_matmul(a_codes, a_scales, b_codes, b_scales, y=None, out_dtype=None, ws=N
     n *= 2
     m = b_codes.shape[0]
     if y is None:
-        y = _made(stream, lambda: a_codes.new_empty((T, m), dtype=out_dtype or bfloat16))
+        y = _maker(stream, a_codes.new_empty)((T, m), dtype=out_dtype or bfloat16)
     elif y.shape != (T, m):
         raise ValueError(f"y: expected shape {(T, m)}, got {tuple(y.shape)}")
     if ws is None:
-        ws = _made(stream, lambda: mx_matmul_workspace(T, m, n, a_codes.device))
+        ws = _maker(stream, mx_matmul_workspace)(T, m, n, a_codes.device)
     wp, wb = _ws_on(ws, dev)
     check(lib().brq_mx_matmul(_packed(a_codes, uint8, (T, n // 2), "a_codes", dev),
                               _packed(a_scales, uint8, (T, n // 32), "a_scales", dev),
@@ -734,9 +742,9 @@ def kv_read(plan: Optional[Plan], cache, slots, head_dim: int, page: int, k=None
     from torch import bfloat16, int64
     n, h, D, dev = slots.shape[0], cache.shape[1], head_dim, cache.get_device()
     if k is None:
-        k = _made(stream, lambda: cache.new_empty((n, h, D), dtype=out_dtype or bfloat16))
+        k = _maker(stream, cache.new_empty)((n, h, D), dtype=out_dtype or bfloat16)
     if v is None:
-        v = _made(stream, lambda: k.new_empty((n, h, D)))
+        v = _maker(stream, k.new_empty)((n, h, D))
     if k.shape != (n, h, D) or v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError(f"k and v must have shape {(n, h, D)} and the same dtype")
     check(lib().brq_kv_read(_h(plan), _cache_ptr(cache, h, D, page, dev),
@@ -765,13 +773,14 @@ def paged_attention(plan: Optional[Plan], q, cache, table, lens, page: int, scal
     B, hq, ldq = _heads(q, D, "q", dev)
     h, pages = cache.shape[1], table.shape[-1]
     if out is None:
-        out = _made(stream, lambda: q.new_empty((B, hq, D)))
+        out = _maker(stream, q.new_empty)((B, hq, D))
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and dtype")
     if ws is None:
-        ws = _made(stream, lambda: paged_attention_workspace(B, hq, h, D, q.device))
+        ws = _maker(stream, paged_attention_workspace)(B, hq, h, D, q.device)
     wp, wb = _ws_on(ws, dev)
-    window = max(-1, min(window, 2 ** 31 - 1))  # the call takes 32 bits, and would take those of a longer one
+    if not 0 <= window < 2 ** 31:  # the call takes 32 bits, and would take those of a longer one
+        window = -1 if window < 0 else 2 ** 31 - 1
     check(lib().brq_paged_attention(
         _h(plan), q.data_ptr(), ldq, dtype_code(q), _cache_ptr(cache, h, D, page, dev),
         cache.shape[0], _packed(table, int32, (B, pages), "table", dev), pages, _packed(lens, int32, (B,), "lens", dev),
