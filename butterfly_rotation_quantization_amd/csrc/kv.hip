@@ -2,7 +2,10 @@
 // mx.h).  A row is one head of one token, its D values on D / 16 lanes (append)
 // or D / 8 (read); keys are the first half of the grid, values the second.
 // Memory-bound for prompts, latency for single tokens: 8190 tokens of 8 heads
-// of 128 are appended in 13.5 us and read in 11.4; 33 tokens in 3 us each.
+// of 128 are appended in 7.5 us without a transform and 11.6 with one, read in
+// 10.8 and, with it undone, 14.6 (one launch after the other; under the
+// profiler, like the figure of kv_rows, 13.5 with one and 11.4); 33 tokens in 3
+// us each.
 #include "mx_dev.h"
 
 namespace brq {

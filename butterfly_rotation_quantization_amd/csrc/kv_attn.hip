@@ -18,13 +18,17 @@
 //
 // A tile is 128 keys of one unit (workgroup: four wavefronts, 32 keys each);
 // which workgroup takes which tiles: kAtLead in mx.h.  64 query heads over 8
-// of 128: 4 sequences of 131072 tokens take 114 us, 5.0 TB/s of the cache,
-// bound by memory; 96 of 17 to 16384 tokens 67 us, 3.9 TB/s, the rest being
-// what beginning and joining 768 units takes.  The loads of the next 32 keys
-// are under way while these are worked on; that needs the queries in LDS
-// rather than in registers (in registers, with four workgroups a compute unit:
-// spilled, 132 and 88 us; without loads ahead 122 and 72).  With the keys
-// converted and the queries in pairs of bfloat16 the two took 139 and 84 us.
+// of 128: 4 sequences of 131072 tokens take 117 us, 4.9 TB/s of the cache,
+// bound by memory; 96 of 17 to 16384 tokens 68 us, 3.8 TB/s, the rest being
+// what beginning and joining 768 units takes; the same with float32 queries.
+// The loads of the next 32 keys are under way while these are worked on; that
+// needs the queries in LDS rather than in registers.  (Measured while a query
+// had 16 bits and a probability too, and the two took 114 and 67 us: queries in
+// registers, with four workgroups a compute unit, spilled, 132 and 88 us; no
+// loads ahead 122 and 72; keys converted and queries in pairs of bfloat16, then
+// without loads ahead, 139 and 84.)  A group of 16 heads takes 161 us for the four,
+// one of 128 over a single key-value head 146: 16 heads at a time, the products,
+// exponentials and the values' conversions of each pass bound it.
 #include <type_traits>
 
 #include "mx_dev.h"

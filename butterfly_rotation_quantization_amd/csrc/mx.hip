@@ -2,11 +2,13 @@
 //
 // Per block of 32: A = max |v|, scale 2^(floor(log2 A) - 2), codes of
 // v / scale.  One pass, each value read once, the transform ahead of it in
-// registers and lane exchanges.  Memory-bound: 8192x28672 bfloat16 in 124 us
-// without a transform (4.8 TB/s; back: 116 us), 124 us with one of 128 (with
-// eight values a lane, and so twice the exchanges, 193; with the size of the
-// transform not known to the compiler and the signs asked for after the values,
-// 129, and 9.2 us for 2048x4096, which now take 7.6).
+// registers and lane exchanges.  Memory-bound: 8192x28672 bfloat16 in 98 us
+// without a transform and 100 with one of 128, back in 116 and, with it undone
+// at eight values a lane, 146; 2048x4096 in 5.0 and 6.0, back in 5.7 and 7.0 (one
+// launch after the other).  Under the profiler, 124 us either way; with eight
+// values a lane, and so twice the exchanges, 193; with the size of the transform
+// not known to the compiler and the signs asked for after the values, 129, and
+// 9.2 us for 2048x4096, which then took 7.6.
 #include "mx_dev.h"
 
 namespace brq {

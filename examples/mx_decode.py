@@ -8,8 +8,9 @@ shared scale, rotated so that no value of a block stands out.
 A prompt's keys and values are projected (mx_quantize, mx_matmul) and appended
 to a paged cache (kv_append); a decoding step projects one token a sequence,
 appends it, attends over the cache (paged_attention) and projects back.  A step
-launches on the current stream, allocates nothing and reads its lengths on the
-device, so it is captured once and replayed while the sequences grow.  The
+launches on the current stream and reads its lengths on the device, so it is
+captured once and replayed while the sequences grow; the operators allocate
+nothing in it, since it gives them their outputs and workspaces.  The
 result is compared with the layer computed densely in float32, and each stage
 with the same stage in float32 on the stage's own 4-bit operands."""
 
