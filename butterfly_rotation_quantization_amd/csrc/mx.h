@@ -221,7 +221,7 @@ constexpr int kAtWaves = 4;       // wavefronts of an attention workgroup
 constexpr int kAtThreads = 64 * kAtWaves;
 constexpr int kAtKeys = 32;       // keys a wavefront takes at a time
 constexpr int kAtTile = kAtWaves * kAtKeys;
-constexpr int kAtCols = 8;        // query heads per 16 matrix columns (each as a high and a low part)
+constexpr int kAtCols = 8;        // query heads per 16 matrix columns (two pieces of each)
 
 constexpr int kAtMaxKeys = 1 << 30;
 
@@ -234,8 +234,8 @@ constexpr int kAtMaxBatch = 4096;  // sequences whose tiles are dealt out evenly
 // has kAtLead empty places, since beginning one (its queries, its join) takes
 // as long as some tiles: without them a workgroup got fourteen short sequences
 // where another got fourteen tiles of a long one, and 96 sequences of 17 to
-// 16384 tokens took 109 us (with 1, 2, 3 and 4 places 85, 72, 67 and 66.5; 64
-// sequences of 1000 tokens 26, 26, 27 and 28).  Workgroup w has places
+// 16384 tokens took 117 us (with 1, 2, 3 and 4 places 83, 75, 69 and 68; 64
+// sequences of 1000 tokens, none to 4 places, 26, 28, 28, 30 and 30).  Workgroup w has places
 // [at_start(w), at_start(w + 1)).  A unit whose tiles lie within one workgroup
 // is finished there; the parts of the others go to the workspace, two slots a
 // workgroup (a part from before its first place, one that it begins), and are
