@@ -40,7 +40,7 @@ EXPORTED = (
     "brq_qlinear_workspace_bytes", "brq_qlinear", "brq_orp_geo_quantize", "brq_orp_geo_dequant",
     "brq_qlinear_noalloc_limit", "brq_qlinear_noalloc", "brq_mx_quantize", "brq_mx_dequantize",
     "brq_mx_matmul_workspace_bytes", "brq_mx_matmul", "brq_kv_page_bytes", "brq_kv_append",
-    "brq_kv_read", "brq_paged_attention_workspace_bytes", "brq_paged_attention",
+    "brq_kv_read", "brq_paged_attention_workspace_bytes", "brq_paged_attention", "brq_mx_linear",
 )
 
 
@@ -59,6 +59,14 @@ class Quant(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("bits", ctypes.c_int32),
                 ("group", ctypes.c_int32), ("codebook", ctypes.c_float * 32)]
 
+
+class MxEpilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("mul", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("ldmul", ctypes.c_int64), ("ldresidual", ctypes.c_int64), ("act", ctypes.c_int32),
+                ("bias_type", ctypes.c_int32), ("mul_type", ctypes.c_int32), ("residual_type", ctypes.c_int32)]
+
+
+_ACTS = {None: 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 _lib = None
 
@@ -173,6 +181,9 @@ def bind(lib):
         lib.brq_mx_matmul_workspace_bytes.restype = sz
         lib.brq_mx_matmul.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, i32, i64, vp, sz, vp]
         lib.brq_mx_matmul.restype = i32
+        lib.brq_mx_linear.argtypes = [vp, vp, vp, vp, i64, i64, i64, ctypes.POINTER(MxEpilogue), vp, i32, i64, vp,
+                                      sz, vp]
+        lib.brq_mx_linear.restype = i32
         lib.brq_kv_page_bytes.argtypes = [i32, i32]
         lib.brq_kv_page_bytes.restype = sz
         lib.brq_kv_append.argtypes = [vp, vp, i64, vp, i64, i32, vp, i64, i32, i32, i32, i64, vp, vp]
@@ -687,6 +698,58 @@ def mx_matmul(a_codes, a_scales, b_codes, b_scales, y=None, out_dtype=None, ws=N
                               _packed(b_codes, uint8, (m, n // 2), "b_codes", dev),
                               _packed(b_scales, uint8, (m, n // 32), "b_scales", dev), T, m, n,
                               y.data_ptr(), dtype_code(y), _rows(y, dev)[2], wp, wb, _stream_of(stream, dev)))
+    return y
+
+
+def _like_y(t, T, m, what, dev) -> tuple:
+    """(address, dtype code, leading dimension) of a [T, m] operand of an epilogue."""
+    if t.shape != (T, m):
+        raise ValueError(f"{what}: expected shape {(T, m)}, got {tuple(t.shape)}")
+    return t.data_ptr(), dtype_code(t), _rows(t, dev)[2]
+
+
+def _epilogue(bias, act, mul, residual, T, m, bias_shape, dev):
+    """The brq_mx_epilogue of the given parts (None: no part)."""
+    if bias is None and act is None and mul is None and residual is None:
+        return None
+    if act not in _ACTS:
+        raise ValueError(f"act: expected one of {', '.join(str(a) for a in _ACTS)}, got {act!r}")
+    e = MxEpilogue(act=_ACTS[act])
+    if bias is not None:
+        e.bias_type = dtype_code(bias)
+        e.bias = _packed(bias, bias.dtype, bias_shape, "bias", dev)
+    if mul is not None:
+        e.mul, e.mul_type, e.ldmul = _like_y(mul, T, m, "mul", dev)
+    if residual is not None:
+        e.residual, e.residual_type, e.ldresidual = _like_y(residual, T, m, "residual", dev)
+    return ctypes.byref(e)
+
+
+def mx_linear(a_codes, a_scales, b_codes, b_scales, bias=None, act=None, mul=None, residual=None, y=None,
+              out_dtype=None, ws=None, stream=None):
+    """act(a b^T + bias) * mul + residual of two microscaled 4-bit matrices
+    (brq_mx_linear): mx_matmul with what follows it in a layer done on its
+    float32 sums.  act: None, "relu", "gelu", "gelu_tanh" or "silu"; bias [m],
+    mul and residual [T, m] (f32, bf16 or f16 each); y may be mul or residual.
+    Returns y [T, m] (bfloat16 by default).  Workspace: mx_matmul_workspace."""
+    from torch import bfloat16, uint8
+    dev = a_codes.get_device()
+    T, n, _ = _rows(a_codes, dev)
+    n *= 2
+    m = b_codes.shape[0]
+    if y is None:
+        y = _maker(stream, a_codes.new_empty)((T, m), dtype=out_dtype or bfloat16)
+    elif y.shape != (T, m):
+        raise ValueError(f"y: expected shape {(T, m)}, got {tuple(y.shape)}")
+    if ws is None:
+        ws = _maker(stream, mx_matmul_workspace)(T, m, n, a_codes.device)
+    wp, wb = _ws_on(ws, dev)
+    check(lib().brq_mx_linear(_packed(a_codes, uint8, (T, n // 2), "a_codes", dev),
+                              _packed(a_scales, uint8, (T, n // 32), "a_scales", dev),
+                              _packed(b_codes, uint8, (m, n // 2), "b_codes", dev),
+                              _packed(b_scales, uint8, (m, n // 32), "b_scales", dev), T, m, n,
+                              _epilogue(bias, act, mul, residual, T, m, (m,), dev), y.data_ptr(), dtype_code(y),
+                              _rows(y, dev)[2], wp, wb, _stream_of(stream, dev)))
     return y
 
 

@@ -114,6 +114,12 @@ hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t) {
   return hipSuccess;
 }
 
+hipError_t launch_mx_linear(const MmArgs& a, const MmEpi& e, hipStream_t s) {
+  if ((e.mul && e.ldm < a.m) || (e.res && e.ldr < a.m) || (e.wide && ((e.mul && a.T > 1 && e.ldm % 4) || (e.res && a.T > 1 && e.ldr % 4))))
+    return bad("mx linear epilogue (%lld, %lld)", e.ldm, e.ldr);
+  return launch_mx_matmul(a, s);
+}
+
 // Every byte of a page is written by exactly one lane of one token, and every
 // access is aligned to its width.
 static hipError_t walk_page(const KvPage& pg) {

@@ -73,6 +73,22 @@ struct MmArgs {
 
 constexpr int kMmK = 256;  // values of a row per stage
 
+// What follows a product's sums: y = act(sum + bias) * mul + res, each part
+// where its pointer is not null; in float32, rounded once to y's type.
+struct MmEpi {
+  int act;               // brq_act
+  const void* bias;      // [m], or [groups][m]
+  int bt;
+  const void* mul;       // [T][ldm]
+  int mt;
+  int64_t ldm;
+  const void* res;       // [T][ldr]
+  int rt;
+  int64_t ldr;
+  int wide;              // four consecutive values of each may be read at once
+};
+struct MmNoEpi {};       // the plain product
+
 // Launches within 2^32 threads (at most 64 per 16 x 16 outputs, 32 per row).
 inline bool mm_supported(int64_t T, int64_t m, int64_t n) {
   const int64_t most = (int64_t)1 << 28;
@@ -163,6 +179,7 @@ inline int mm_stream_rows(const MmArgs& a) { return a.m >= 32 * 256 ? 32 : 16; }
 inline int mm_stream_waves(int64_t wgs) { return wgs > 256 ? 4 : 8; }
 
 hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t s);
+hipError_t launch_mx_linear(const MmArgs& a, const MmEpi& e, hipStream_t s);
 
 // ---- paged cache (kv.hip) and attention (kv_attn.hip)
 

@@ -31,6 +31,13 @@ brq_status launched(hipError_t e, const char* what) {
   return e == hipSuccess ? BRQ_OK : refuse(BRQ_ERR_HIP, "%s launch: %s", what, hipGetErrorString(e));
 }
 
+brq_status workspace_ok(const void* ws, size_t bytes, size_t need) {
+  if (need && (!ws || bytes < need))
+    return refuse(BRQ_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? bytes : (size_t)0, need);
+  if (need && misaligned(ws, 16)) return refuse(BRQ_ERR_ALIGNMENT, "the workspace must be 16-byte aligned");
+  return BRQ_OK;
+}
+
 // The transform of a plan these kernels apply in registers: Hadamard, d in
 // 32..256 (want > 0: exactly that d).
 brq_status transform_of(const brq_plan* plan, int want, const float** signs, int* d, float* rnorm) {
@@ -90,6 +97,38 @@ brq_status mx_setup(MxArgs& a, const brq_plan* right, int64_t rows, int64_t n, c
   return BRQ_OK;
 }
 
+// The epilogue of a product of T x m outputs (`groups` rows of bias).
+brq_status epilogue_of(const brq_mx_epilogue* ep, int64_t T, int64_t m, int64_t groups, MmEpi* e) {
+  std::memset(e, 0, sizeof *e);
+  if (!ep) return BRQ_OK;
+  if (ep->act < BRQ_ACT_NONE || ep->act > BRQ_ACT_SILU)
+    return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad activation %d", ep->act);
+  if ((ep->bias && !dtype_ok(ep->bias_type)) || (ep->mul && !dtype_ok(ep->mul_type)) ||
+      (ep->residual && !dtype_ok(ep->residual_type)))
+    return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad dtype in the epilogue");
+  if ((ep->mul && ep->ldmul < m) || (ep->residual && ep->ldresidual < m))
+    return refuse(BRQ_ERR_INVALID_ARGUMENT, "leading dimension of mul or residual below m");
+  if ((ep->bias && misaligned(ep->bias, dtype_size(ep->bias_type))) ||
+      (ep->mul && misaligned(ep->mul, dtype_size(ep->mul_type))) ||
+      (ep->residual && misaligned(ep->residual, dtype_size(ep->residual_type))))
+    return refuse(BRQ_ERR_ALIGNMENT, "bias, mul and residual must be aligned to their types");
+  auto wide = [](const void* p, int32_t t, int64_t ld, int64_t rows) {
+    return !p || (!misaligned(p, 4 * dtype_size(t)) && (ld % 4 == 0 || rows == 1));
+  };
+  e->act = ep->act;
+  e->bias = ep->bias;
+  e->bt = ep->bias_type;
+  e->mul = ep->mul;
+  e->mt = ep->mul_type;
+  e->ldm = ep->ldmul;
+  e->res = ep->residual;
+  e->rt = ep->residual_type;
+  e->ldr = ep->ldresidual;
+  e->wide = wide(ep->bias, ep->bias_type, m, groups) && wide(ep->mul, ep->mul_type, ep->ldmul, T) &&
+            wide(ep->residual, ep->residual_type, ep->ldresidual, T);
+  return BRQ_OK;
+}
+
 }  // namespace
 }  // namespace brq
 
@@ -142,7 +181,16 @@ size_t brq_mx_matmul_workspace_bytes(int64_t T, int64_t m, int64_t n) {
 brq_status brq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
                          const uint8_t* b_scales, int64_t T, int64_t m, int64_t n, void* y, int32_t yt, int64_t ldy,
                          void* ws, size_t ws_bytes, void* stream) {
+  return brq_mx_linear(a_codes, a_scales, b_codes, b_scales, T, m, n, nullptr, y, yt, ldy, ws, ws_bytes, stream);
+}
+
+brq_status brq_mx_linear(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                         const uint8_t* b_scales, int64_t T, int64_t m, int64_t n, const brq_mx_epilogue* ep, void* y,
+                         int32_t yt, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
   clear_error();
+  MmEpi e;
+  brq_status st = epilogue_of(ep, T, m, 1, &e);
+  if (st != BRQ_OK) return st;
   if (!dtype_ok(yt)) return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad output dtype %d", yt);
   if (T < 0 || m < 0 || n < 0 || ldy < m)
     return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad shape or leading dimension");
@@ -156,9 +204,7 @@ brq_status brq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const 
     return refuse(BRQ_ERR_ALIGNMENT, "codes must be 16-byte and scales 4-byte aligned");
   if (misaligned(y, dtype_size(yt))) return refuse(BRQ_ERR_ALIGNMENT, "the output must be aligned to its type");
   const size_t need = brq_mx_matmul_workspace_bytes(T, m, n);
-  if (need && (!ws || ws_bytes < need))
-    return refuse(BRQ_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
-  if (need && misaligned(ws, 16)) return refuse(BRQ_ERR_ALIGNMENT, "the workspace must be 16-byte aligned");
+  if ((st = workspace_ok(ws, ws_bytes, need)) != BRQ_OK) return st;
   MmArgs a;
   std::memset(&a, 0, sizeof a);
   a.a = a_codes;
@@ -175,9 +221,9 @@ brq_status brq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const 
   a.wide = ldy % 4 == 0 && !misaligned(y, 4 * dtype_size(yt));
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int tok = prof_begin("mx matmul", s);
-  const hipError_t e = launch_mx_matmul(a, s);
+  const hipError_t err = ep ? launch_mx_linear(a, e, s) : launch_mx_matmul(a, s);
   prof_end(tok, s);
-  return launched(e, "mx matmul");
+  return launched(err, "mx matmul");
 }
 
 }  // extern "C"

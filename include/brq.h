@@ -429,6 +429,34 @@ brq_status brq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const 
                          int32_t yt, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * The same product with what follows it in a layer done on the sums:
+ *   y[t][o] = act(sum_k a[t][k] b[o][k] + bias[o]) * mul[t][o] + residual[t][o],
+ * each part where its pointer is not NULL, in float32, rounded once to yt.
+ *   act: BRQ_ACT_NONE; RELU, max(x, 0); GELU, x times the normal distribution
+ *     function; GELU_TANH, x / 2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))); SILU,
+ *     x / (1 + exp(-x)).
+ *   bias: device [m] of bias_type; mul: device [T][ldmul] of mul_type; residual:
+ *     device [T][ldresidual] of residual_type; each aligned to its type.  y may be
+ *     mul or residual if it has its type and leading dimension.
+ * Everything else as brq_mx_matmul, the workspace too (ep NULL: the plain
+ * product).  Errors: also INVALID_ARGUMENT (act, the types and leading
+ * dimensions of ep), ALIGNMENT (its operands). */
+typedef enum {
+  BRQ_ACT_NONE = 0, BRQ_ACT_RELU = 1, BRQ_ACT_GELU = 2, BRQ_ACT_GELU_TANH = 3, BRQ_ACT_SILU = 4
+} brq_act;
+typedef struct {
+  const void* bias;
+  const void* mul;
+  const void* residual;
+  int64_t ldmul, ldresidual;
+  int32_t act, bias_type, mul_type, residual_type;
+} brq_mx_epilogue;
+brq_status brq_mx_linear(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                         const uint8_t* b_scales, int64_t T, int64_t m, int64_t n,
+                         const brq_mx_epilogue* ep, void* y, int32_t yt, int64_t ldy, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/*
  * A paged key-value cache in MX4.  The cache is a device array of `pages` pages
  * of `page` tokens; a page holds, for each of `heads` key-value heads, the keys
  * and values of its tokens in brq_kv_page_bytes(head_dim, page) bytes:

@@ -148,3 +148,46 @@ def attention(q, cache: Cache, table, lens, scale, window=0, M=None):
             lse[b, i] = top + np.log(total)
             terms[b, i] = abs(scale) * (np.abs(k) @ np.abs(x)).max()
     return out, lse, (spread, terms)
+
+
+# ------------------------------------------------------------------ epilogue of a product
+
+def _erfc(z):
+    from scipy.special import erfc
+    return erfc(z)
+
+
+def activation(x: np.ndarray, act):
+    """(act(x), bound of a float32 evaluation's error in units of 2^-24): a
+    probability of tail z = x / sqrt 2 or of logit g is off by the rounding of
+    its argument times the logarithm's derivative (2 z, 1) besides a few units of its own."""
+    one = np.ones_like(x)
+    with np.errstate(over="ignore", invalid="ignore"):
+        if act is None:
+            return x, 0 * one
+        if act == "relu":
+            return np.where(x < 0, 0.0, x), 0 * one
+        if act == "gelu":
+            y = 0.5 * x * _erfc(-x / np.sqrt(2))
+            return y, np.abs(y) * (20 + 4 * np.minimum(x, 0) ** 2) + 1e-30
+        g = x if act == "silu" else np.sqrt(8 / np.pi) * (x + 0.044715 * x ** 3)
+        y = np.where(g < -700, 0.0, x / (1 + np.exp(-np.maximum(g, -700))))
+        return y, np.abs(y) * (12 + 6 * np.abs(np.minimum(g, 0))) + 1e-30
+
+
+def epilogue(s: np.ndarray, bias=None, act=None, mul=None, residual=None):
+    """(act(s + bias) * mul + residual, bound of the error of a float32
+    evaluation from exact sums s, before the output's own rounding)."""
+    half = 2.0 ** -24
+    x = s if bias is None else s + bias
+    err = 0 * x if bias is None else half * np.abs(x)
+    y, own = activation(x, act)
+    slope = 1.0 if act in (None, "relu") else 1.2  # the largest of any activation
+    err = slope * err + half * own
+    if mul is not None:
+        y = y * mul
+        err = err * np.abs(mul) + half * np.abs(y)
+    if residual is not None:
+        y = y + residual
+        err = err + half * np.abs(y)
+    return y, err
