@@ -41,6 +41,9 @@ EXPORTED = (
     "brq_qlinear_noalloc_limit", "brq_qlinear_noalloc", "brq_mx_quantize", "brq_mx_dequantize",
     "brq_mx_matmul_workspace_bytes", "brq_mx_matmul", "brq_kv_page_bytes", "brq_kv_append",
     "brq_kv_read", "brq_paged_attention_workspace_bytes", "brq_paged_attention", "brq_mx_linear",
+    "brq_mx_grouped_matmul_workspace_bytes", "brq_mx_grouped_matmul", "brq_kv_move_workspace_bytes",
+    "brq_kv_move", "brq_kv_fork", "brq_kv_reserve_workspace_bytes", "brq_kv_reserve", "brq_kv_free",
+    "brq_tree_attention_workspace_bytes", "brq_tree_attention",
 )
 
 
@@ -184,6 +187,11 @@ def bind(lib):
         lib.brq_mx_linear.argtypes = [vp, vp, vp, vp, i64, i64, i64, ctypes.POINTER(MxEpilogue), vp, i32, i64, vp,
                                       sz, vp]
         lib.brq_mx_linear.restype = i32
+        lib.brq_mx_grouped_matmul_workspace_bytes.argtypes = [i64, i64, i64, i64]
+        lib.brq_mx_grouped_matmul_workspace_bytes.restype = sz
+        lib.brq_mx_grouped_matmul.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, ctypes.POINTER(MxEpilogue), vp,
+                                              i32, i64, vp, sz, vp]
+        lib.brq_mx_grouped_matmul.restype = i32
         lib.brq_kv_page_bytes.argtypes = [i32, i32]
         lib.brq_kv_page_bytes.restype = sz
         lib.brq_kv_append.argtypes = [vp, vp, i64, vp, i64, i32, vp, i64, i32, i32, i32, i64, vp, vp]
@@ -195,6 +203,23 @@ def bind(lib):
         lib.brq_paged_attention.argtypes = [vp, vp, i64, i32, vp, i64, vp, i64, vp, i64, i32, i32, i32,
                                             i32, ctypes.c_float, i32, vp, i64, vp, vp, sz, vp]
         lib.brq_paged_attention.restype = i32
+        lib.brq_kv_move_workspace_bytes.argtypes = [i64, i32, i32]
+        lib.brq_kv_move_workspace_bytes.restype = sz
+        lib.brq_kv_move.argtypes = [vp, vp, vp, i64, i32, i32, i32, i64, vp, sz, vp]
+        lib.brq_kv_move.restype = i32
+        lib.brq_kv_fork.argtypes = [vp, vp, i64, i64, vp, i64, vp, i64, vp, vp, vp]
+        lib.brq_kv_fork.restype = i32
+        lib.brq_kv_reserve_workspace_bytes.argtypes = [i64, i64, i32, i64]
+        lib.brq_kv_reserve_workspace_bytes.restype = sz
+        lib.brq_kv_reserve.argtypes = [vp, vp, vp, i64, i64, vp, i64, i64, i32, i32, i32, vp, vp, sz, vp]
+        lib.brq_kv_reserve.restype = i32
+        lib.brq_kv_free.argtypes = [vp, i64, i64, vp, i64, vp, i64, vp]
+        lib.brq_kv_free.restype = i32
+        lib.brq_tree_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i32]
+        lib.brq_tree_attention_workspace_bytes.restype = sz
+        lib.brq_tree_attention.argtypes = [vp, vp, i64, i32, vp, i64, vp, i64, vp, vp, i64, i32, i32, i32, i32, i32,
+                                           ctypes.c_float, i32, vp, i64, vp, vp, sz, vp]
+        lib.brq_tree_attention.restype = i32
     if hasattr(lib, "brq_set_path"):  # libraries built before the path switch lack it
         lib.brq_set_path.argtypes = [i32]
         lib.brq_set_path.restype = i32
@@ -753,6 +778,45 @@ def mx_linear(a_codes, a_scales, b_codes, b_scales, bias=None, act=None, mul=Non
     return y
 
 
+def mx_grouped_matmul_workspace(T: int, groups: int, m: int, n: int, device="cuda"):
+    """A device workspace for mx_grouped_matmul of these sizes (None if it needs none)."""
+    import torch
+    nb = lib().brq_mx_grouped_matmul_workspace_bytes(int(T), int(groups), int(m), int(n))
+    return torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+
+
+def mx_grouped_matmul(a_codes, a_scales, b_codes, b_scales, offsets, bias=None, act=None, mul=None, residual=None,
+                      y=None, out_dtype=None, ws=None, stream=None):
+    """Rows grouped by expert times their experts' weights
+    (brq_mx_grouped_matmul): activations [T, n], row t of group g if offsets[g] <=
+    t < offsets[g + 1] (int32 [groups + 1] on the device), weights codes [groups,
+    m, n/2] and scales [groups, m, n/32]; the epilogue as of mx_linear, with a
+    bias [groups, m].  Rows of no group are left as they were (in a y made here:
+    whatever its memory held).  Returns y [T, m] (bfloat16 by default)."""
+    from torch import bfloat16, int32, uint8
+    dev = a_codes.get_device()
+    T, n, _ = _rows(a_codes, dev)
+    n *= 2
+    if b_codes.dim() != 3:
+        raise ValueError(f"b_codes: expected [groups, m, n/2], got {tuple(b_codes.shape)}")
+    groups, m, _ = b_codes.shape
+    if y is None:
+        y = _maker(stream, a_codes.new_empty)((T, m), dtype=out_dtype or bfloat16)
+    elif y.shape != (T, m):
+        raise ValueError(f"y: expected shape {(T, m)}, got {tuple(y.shape)}")
+    if ws is None:
+        ws = _maker(stream, mx_grouped_matmul_workspace)(T, groups, m, n, a_codes.device)
+    wp, wb = _ws_on(ws, dev)
+    check(lib().brq_mx_grouped_matmul(
+        _packed(a_codes, uint8, (T, n // 2), "a_codes", dev), _packed(a_scales, uint8, (T, n // 32), "a_scales", dev),
+        _packed(b_codes, uint8, (groups, m, n // 2), "b_codes", dev),
+        _packed(b_scales, uint8, (groups, m, n // 32), "b_scales", dev),
+        _packed(offsets, int32, (groups + 1,), "offsets", dev), T, groups, m, n,
+        _epilogue(bias, act, mul, residual, T, m, (groups, m), dev), y.data_ptr(), dtype_code(y), _rows(y, dev)[2],
+        wp, wb, _stream_of(stream, dev)))
+    return y
+
+
 # ---------------------------------------------------------------- paged 4-bit key-value cache
 
 def kv_cache(pages: int, heads: int, head_dim: int, page: int, device="cuda"):
@@ -851,6 +915,147 @@ def paged_attention(plan: Optional[Plan], q, cache, table, lens, page: int, scal
         _heads(out, D, "out", dev)[2], None if lse is None else _packed(lse, float32, (B, hq), "lse", dev),
         wp, wb, _stream_of(stream, dev)))
     return out
+
+
+def tree_attention_workspace(batch: int, tokens: int, q_heads: int, heads: int, head_dim: int, device="cuda"):
+    """A device workspace for tree_attention of these sizes (None if it needs none)."""
+    import torch
+    nb = lib().brq_tree_attention_workspace_bytes(int(batch), int(tokens), int(q_heads), int(heads), int(head_dim))
+    return torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+
+
+def _flat(t, shape, what):
+    """[batch * tokens, ...] of a [batch, tokens, ...] tensor whose rows are evenly spaced."""
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    B, N = t.shape[:2]
+    if B > 1 and N > 1 and t.stride(0) != N * t.stride(1):
+        raise ValueError(f"{what}: expected rows of [batch, tokens] evenly spaced, got strides {tuple(t.stride())}")
+    return t.flatten(0, 1) if N != 1 else t[:, 0]
+
+
+def tree_attention(plan: Optional[Plan], q, cache, table, lens, mask, page: int, scale=None, window: int = 0,
+                   out=None, lse=None, ws=None, stream=None):
+    """Attention of a tree of drafted tokens per sequence over the paged 4-bit
+    cache (brq_tree_attention): q [batch, tokens, q_heads, D] (f32, bf16 or f16;
+    up to 64 tokens), table int32 [batch, pages of a sequence], lens int32 [batch]
+    tokens of context, behind which the drafts are cached; mask int64 [batch,
+    tokens], bit j of a row: it sees draft j (no bit: padding, its output zero).
+    scale defaults to 1/sqrt(D), window 0 sees every token; lse, if given, is a
+    float32 [batch, tokens, q_heads] output.  Returns out, like q."""
+    from torch import float32, int32, int64
+    if q.dim() != 4:
+        raise ValueError(f"q: expected [batch, tokens, q_heads, D], got {tuple(q.shape)}")
+    (B, N, hq, D), dev = q.shape, q.get_device()
+    ldq = _heads(_flat(q, q.shape, "q"), D, "q", dev)[2]
+    h, pages = cache.shape[1], table.shape[-1]
+    if out is None:
+        out = _maker(stream, q.new_empty)((B, N, hq, D))
+    elif out.dtype != q.dtype:
+        raise ValueError("out must have q's dtype")
+    ldo = _heads(_flat(out, q.shape, "out"), D, "out", dev)[2]
+    if ws is None:
+        ws = _maker(stream, tree_attention_workspace)(B, N, hq, h, D, q.device)
+    wp, wb = _ws_on(ws, dev)
+    if not 0 <= window < 2 ** 31:  # the call takes 32 bits, and would take those of a longer one
+        window = -1 if window < 0 else 2 ** 31 - 1
+    check(lib().brq_tree_attention(
+        _h(plan), q.data_ptr(), ldq, dtype_code(q), _cache_ptr(cache, h, D, page, dev),
+        cache.shape[0], _packed(table, int32, (B, pages), "table", dev), pages, _packed(lens, int32, (B,), "lens", dev),
+        _packed(mask, int64, (B, N), "mask", dev), B, N, hq, h, D, page, D ** -0.5 if scale is None else scale, window,
+        out.data_ptr(), ldo, None if lse is None else _packed(lse, float32, (B, N, hq), "lse", dev),
+        wp, wb, _stream_of(stream, dev)))
+    return out
+
+
+# ---------------------------------------------------------------- tokens and pages of the cache moved and shared
+
+def kv_move_workspace(tokens: int, heads: int, head_dim: int, device="cuda"):
+    """A device workspace for kv_move of these sizes (None if it needs none)."""
+    import torch
+    nb = lib().brq_kv_move_workspace_bytes(int(tokens), int(heads), int(head_dim))
+    return torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+
+
+def kv_move(cache, src, dst, head_dim: int, page: int, ws=None, stream=None):
+    """Tokens of cache slots src to slots dst, each int64 [tokens], bits unchanged
+    and all read before any is written (brq_kv_move; a pair with a slot outside
+    the cache is skipped).  Returns cache."""
+    from torch import int64
+    dev, n, h = cache.get_device(), src.shape[0], cache.shape[1]
+    if ws is None:
+        ws = _maker(stream, kv_move_workspace)(n, h, head_dim, cache.device)
+    wp, wb = _ws_on(ws, dev)
+    check(lib().brq_kv_move(_cache_ptr(cache, h, head_dim, page, dev), _packed(src, int64, (n,), "src", dev),
+                            _packed(dst, int64, (n,), "dst", dev), n, h, head_dim, page, cache.shape[0], wp, wb,
+                            _stream_of(stream, dev)))
+    return cache
+
+
+def kv_fork(table, lens, parents, refs, out_table=None, out_lens=None, stream=None):
+    """Rows for new sequences that share their parents' pages (brq_kv_fork): table
+    int32 [batch, width], lens int32 [batch], parents int32 [children], refs
+    int32 [pages], the number of rows that hold a page.  Returns (out_table
+    [children, width], out_lens [children])."""
+    from torch import int32
+    dev = table.get_device()
+    if table.dim() != 2:
+        raise ValueError(f"table: expected [batch, width], got {tuple(table.shape)}")
+    (B, W), F = table.shape, parents.shape[0]
+    if out_table is None:
+        out_table = _maker(stream, table.new_empty)((F, W))
+    if out_lens is None:
+        out_lens = _maker(stream, lens.new_empty)((F,))
+    check(lib().brq_kv_fork(_packed(table, int32, (B, W), "table", dev), _packed(lens, int32, (B,), "lens", dev), B, W,
+                            _packed(parents, int32, (F,), "parents", dev), F,
+                            _packed(refs, int32, (refs.shape[0],), "refs", dev), refs.shape[0],
+                            _packed(out_table, int32, (F, W), "out_table", dev),
+                            _packed(out_lens, int32, (F,), "out_lens", dev), _stream_of(stream, dev)))
+    return out_table, out_lens
+
+
+def kv_reserve_workspace(batch: int, tokens: int, page: int, pages: int, device="cuda"):
+    """A device workspace for kv_reserve of these sizes (None if it needs none)."""
+    import torch
+    nb = lib().brq_kv_reserve_workspace_bytes(int(batch), int(tokens), int(page), int(pages))
+    return torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+
+
+def kv_reserve(cache, table, lens, refs, tokens: int, head_dim: int, page: int, slots=None, ws=None, stream=None):
+    """Pages for the next `tokens` tokens of every sequence, which no other row
+    of the table holds: free ones, with what a shared page holds of the sequence
+    copied (brq_kv_reserve).  table, refs and cache are updated.  Returns the new
+    tokens' slots int64 [batch, tokens], -1 where there was no page."""
+    from torch import int32, int64
+    dev = cache.get_device()
+    if table.dim() != 2:
+        raise ValueError(f"table: expected [batch, width], got {tuple(table.shape)}")
+    (B, W), (pages, h) = table.shape, cache.shape[:2]
+    if slots is None:
+        slots = _maker(stream, table.new_empty)((B, tokens), dtype=int64)
+    if ws is None:
+        ws = _maker(stream, kv_reserve_workspace)(B, tokens, page, pages, cache.device)
+    wp, wb = _ws_on(ws, dev)
+    check(lib().brq_kv_reserve(_cache_ptr(cache, h, head_dim, page, dev), _packed(table, int32, (B, W), "table", dev),
+                               _packed(lens, int32, (B,), "lens", dev), B, W,
+                               _packed(refs, int32, (pages,), "refs", dev), pages, tokens, h, head_dim, page,
+                               _packed(slots, int64, (B, tokens), "slots", dev), wp, wb, _stream_of(stream, dev)))
+    return slots
+
+
+def kv_free(table, refs, rows=None, stream=None):
+    """Give back the pages of the table's rows `rows` (int32; None: of all), whose
+    entries become -1 (brq_kv_free).  Returns refs."""
+    from torch import int32
+    dev = table.get_device()
+    if table.dim() != 2:
+        raise ValueError(f"table: expected [batch, width], got {tuple(table.shape)}")
+    (B, W), n = table.shape, table.shape[0] if rows is None else rows.shape[0]
+    check(lib().brq_kv_free(_packed(table, int32, (B, W), "table", dev), B, W,
+                            _packed(refs, int32, (refs.shape[0],), "refs", dev), refs.shape[0],
+                            None if rows is None else _packed(rows, int32, (n,), "rows", dev), n,
+                            _stream_of(stream, dev)))
+    return refs
 
 
 def profile_enable(on: bool = True):

@@ -120,6 +120,34 @@ hipError_t launch_mx_linear(const MmArgs& a, const MmEpi& e, hipStream_t s) {
   return launch_mx_matmul(a, s);
 }
 
+hipError_t launch_mx_grouped(const GmArgs& g, const MmEpi& e, hipStream_t) {
+  dry_launch();
+  const MmArgs& a = g.mm;
+  if (a.T < 1 || a.m < 1 || a.n % kMxBlock || a.ldy < a.m || g.groups < 1 || (e.mul && e.ldm < a.m) ||
+      (e.res && e.ldr < a.m))
+    return bad("mx grouped geometry (%lld x %lld)", a.T, a.m);
+  if (!launchable(gm_units(a.T, g.groups, 16) * ((a.m + 15) / 16), 64))
+    return bad("mx grouped grid (%lld x %lld)", a.T, a.m);
+  // groups of every kind have no more units than the grid has places, and no
+  // row beyond the last
+  for (int seed = 0; seed < 6 && a.T <= 1 << 20; ++seed)
+    for (int R : {16, 32, 64, 128, 256}) {
+      int64_t units = 0, at = 0;
+      for (int64_t e = 0; e < g.groups; ++e) {
+        const int64_t left = a.T - at, share = a.T / g.groups;
+        const int64_t n = seed == 0 ? share : seed == 1 ? (e ? 0 : a.T) : seed == 2 ? (left ? 1 : 0)
+                          : seed == 3 ? (e * 7919 + 13) % (2 * share + 2) : seed == 4 ? R + 1 : (e + 1 == g.groups ? left : 1);
+        int b, end;
+        gm_rows((int)at - (seed == 3 && e == 0 ? 5 : 0), (int)(at + n), (int)a.T, &b, &end);
+        if (b < 0 || end < b || end > a.T) return bad("mx grouped rows [%lld, %lld)", b, end);
+        units += (end - b + R - 1) / R;
+        at = end;
+      }
+      if (units > gm_units(a.T, g.groups, R)) return bad("mx grouped units %lld of %lld rows", units, R);
+    }
+  return hipSuccess;
+}
+
 // Every byte of a page is written by exactly one lane of one token, and every
 // access is aligned to its width.
 static hipError_t walk_page(const KvPage& pg) {
@@ -170,50 +198,38 @@ static hipError_t walk_kv(const KvArgs& a) {
 hipError_t launch_kv_append(const KvArgs& a, hipStream_t) { return walk_kv(a); }
 hipError_t launch_kv_read(const KvArgs& a, hipStream_t) { return walk_kv(a); }
 
-hipError_t launch_paged_attention(const AtArgs& a, hipStream_t) {
-  dry_launch();
-  const KvPage& pg = a.pg;
-  const int D = pg.D;
-  if ((1 << a.lgP) != pg.P || a.group * a.heads != a.q_heads || a.ht * a.nt * kAtCols < a.group ||
-      (int64_t)a.cap > a.ldt << a.lgP || a.cap > kAtMaxKeys || a.wgs < 0 || (a.wgs > 0 && !a.part))
-    return bad("attention geometry (group %lld, workgroups %lld)", a.group, a.wgs);
-  const int64_t units = a.batch * a.heads * a.ht;
-  if (!launchable(a.wgs ? a.wgs : units, kAtThreads) ||
-      (a.wgs && !launchable(units * (kAtCols * a.nt / at_join_rows(units, a.nt, D)), kAtThreads)))
-    return bad("attention launch for %lld units", units, 0);
-  // the deal of tiles to workgroups for some lengths: every part has a slot of
-  // its own, and the join finds the workgroups that have one
-  for (int seed = 0; a.wgs && a.batch <= 64 && seed < 6; ++seed) {
-    std::vector<int> tiles;
-    int64_t total = 0, units = (int64_t)a.heads * a.ht;
-    for (int64_t b = 0; b < a.batch; ++b) {
-      const int64_t n = seed == 0 ? 0 : seed == 1 ? a.cap : (b * 7919 + seed * 104729) % (a.cap + 1) >> (seed * b % 5);
-      tiles.push_back(at_tiles((int)n, seed == 3 ? 100 : 0));
-      total += at_cost(tiles.back()) * units;
+// The deal of a batch's tiles to workgroups: every part has a slot of its own, and
+// the join finds the workgroups that have one.
+static hipError_t walk_deal(const std::vector<int>& tiles, int64_t units, int of) {
+  int64_t total = 0;
+  for (int t : tiles) total += at_cost(t) * units;
+  if (!total) return hipSuccess;
+  const int wgs = at_dealt(total, of);
+  std::vector<int> owner, uses(2 * (size_t)wgs, 0);
+  for (int w = 0; w < wgs; ++w)
+    for (int64_t g = at_start(w, total, wgs); g < at_start(w + 1, total, wgs); ++g) owner.push_back(w);
+  if ((int64_t)owner.size() != total || at_start(wgs, total, wgs) != total)
+    return bad("attention deal of %lld tiles covers %lld", total, owner.size());
+  int64_t g0 = 0;
+  for (size_t b = 0; b < tiles.size(); ++b)
+    for (int64_t u = 0; u < units && tiles[b]; ++u, g0 += tiles[b]) {
+      g0 += kAtLead;  // the lead's places come before the first tile
+      const int64_t g1 = g0 + tiles[b] - 1;
+      if (at_owner(g0, total, wgs) != owner[(size_t)g0] || at_owner(g1, total, wgs) != owner[(size_t)g1])
+        return bad("attention owner of tile %lld of %lld", g0, total);
+      int last = -1;
+      for (int64_t g = g0; owner[(size_t)g0] != owner[(size_t)g1] && g <= g1; ++g)
+        if (owner[(size_t)g] != last) {
+          last = owner[(size_t)g];
+          if (uses[(size_t)at_slot(last, g0, total, wgs)]++)
+            return bad("attention slot of workgroup %lld used twice (tile %lld)", last, g);
+        }
     }
-    if (!total) continue;
-    const int wgs = at_dealt(total, a.wgs);
-    std::vector<int> owner, uses(2 * (size_t)wgs, 0);
-    for (int w = 0; w < wgs; ++w)
-      for (int64_t g = at_start(w, total, wgs); g < at_start(w + 1, total, wgs); ++g) owner.push_back(w);
-    if ((int64_t)owner.size() != total || at_start(wgs, total, wgs) != total)
-      return bad("attention deal of %lld tiles covers %lld", total, owner.size());
-    int64_t g0 = 0;
-    for (int64_t b = 0; b < a.batch; ++b)
-      for (int64_t u = 0; u < units && tiles[(size_t)b]; ++u, g0 += tiles[(size_t)b]) {
-        g0 += kAtLead;  // the lead's places come before the first tile
-        const int64_t g1 = g0 + tiles[(size_t)b] - 1;
-        if (at_owner(g0, total, wgs) != owner[(size_t)g0] || at_owner(g1, total, wgs) != owner[(size_t)g1])
-          return bad("attention owner of tile %lld of %lld", g0, total);
-        int last = -1;
-        for (int64_t g = g0; owner[(size_t)g0] != owner[(size_t)g1] && g <= g1; ++g)
-          if (owner[(size_t)g] != last) {
-            last = owner[(size_t)g];
-            if (uses[(size_t)at_slot(last, g0, total, wgs)]++)
-              return bad("attention slot of workgroup %lld used twice (tile %lld)", last, g);
-          }
-      }
-  }
+  return hipSuccess;
+}
+
+static hipError_t walk_loads(const KvPage& pg) {
+  const int D = pg.D;
   // the wide loads of 16 keys at every place of a page
   for (int p = 0; p < pg.P; p += 16)
     for (int lane = 0; lane < 64; ++lane) {
@@ -230,6 +246,137 @@ hipError_t launch_paged_attention(const AtArgs& a, hipStream_t) {
         if (pg.vcode(p + 4 * g + i, c) != vc + i * (D / 32) || pg.vscale(p + 4 * g + i, c * D / 512) != vs + i)
           return bad("attention values of lane %lld, key %lld", lane, i);
     }
+  return walk_page(pg);
+}
+
+hipError_t launch_paged_attention(const AtArgs& a, hipStream_t) {
+  dry_launch();
+  const KvPage& pg = a.pg;
+  const int D = pg.D;
+  if ((1 << a.lgP) != pg.P || a.group * a.heads != a.q_heads || a.ht * a.nt * kAtCols < a.group ||
+      (int64_t)a.cap > a.ldt << a.lgP || a.cap > kAtMaxKeys || a.wgs < 0 || (a.wgs > 0 && !a.part))
+    return bad("attention geometry (group %lld, workgroups %lld)", a.group, a.wgs);
+  const int64_t units = a.batch * a.heads * a.ht;
+  if (!launchable(a.wgs ? a.wgs : units, kAtThreads) ||
+      (a.wgs && !launchable(units * (kAtCols * a.nt / at_join_rows(units, a.nt, D)), kAtThreads)))
+    return bad("attention launch for %lld units", units, 0);
+  for (int seed = 0; a.wgs && a.batch <= 64 && seed < 6; ++seed) {  // some lengths
+    std::vector<int> tiles;
+    for (int64_t b = 0; b < a.batch; ++b) {
+      const int64_t n = seed == 0 ? 0 : seed == 1 ? a.cap : (b * 7919 + seed * 104729) % (a.cap + 1) >> (seed * b % 5);
+      tiles.push_back(at_tiles((int)n, seed == 3 ? 100 : 0));
+    }
+    const hipError_t e = walk_deal(tiles, (int64_t)a.heads * a.ht, a.wgs);
+    if (e != hipSuccess) return e;
+  }
+  return walk_loads(pg);
+}
+
+hipError_t launch_tree_attention(const TrArgs& t, hipStream_t) {
+  dry_launch();
+  const AtArgs& a = t.at;
+  const int D = a.pg.D, H = 16 * a.nt;
+  const int64_t rows = (int64_t)t.tokens * a.group, units = a.batch * a.heads * a.ht;
+  if ((1 << a.lgP) != a.pg.P || a.group * a.heads != a.q_heads || (int64_t)a.ht * H < rows || (int64_t)(a.ht - 1) * H >= rows ||
+      (a.nt != 1 && a.nt != 2 && (a.nt != 4 || D == 256)) || (int64_t)a.cap > a.ldt << a.lgP || a.cap > kAtMaxKeys ||
+      t.tokens < 1 || t.tokens > kTrTokens || a.wgs < 0 || a.wgs % 8 || (a.wgs > 0 && !a.part))
+    return bad("tree attention geometry (group %lld, tokens %lld)", a.group, t.tokens);
+  const int join = tr_join_rows(units, a.nt, D);
+  if (H % join || kAtThreads % (D / kMxPerLane * join) || !launchable(a.wgs ? a.wgs : units, kAtThreads) ||
+      (a.wgs && !launchable(units * (H / join), kAtThreads)))
+    return bad("tree attention launch for %lld units", units, 0);
+  // every number of the deal is one workgroup's
+  for (int n : {0, 1, 7, 8, 9, 100, a.wgs}) {
+    std::vector<int> uses((size_t)n, 0);
+    for (int x = 0; x < a.wgs && n <= a.wgs; ++x)
+      if (tr_number((uint32_t)x, n) < n) uses[(size_t)tr_number((uint32_t)x, n)]++;
+    for (int i = 0; a.wgs && n <= a.wgs && i < n; ++i)
+      if (uses[(size_t)i] != 1) return bad("tree attention number %lld of %lld", i, n);
+  }
+  for (int seed = 0; a.wgs && a.batch <= 64 && seed < 6; ++seed) {  // some lengths, windows too
+    std::vector<int> tiles;
+    for (int64_t b = 0; b < a.batch; ++b) {
+      const int64_t ctx = seed == 0 ? 0 : seed == 1 ? a.cap : (b * 7919 + seed * 104729) % (a.cap + 1) >> (seed * b % 5);
+      const int n = (int)(ctx + t.tokens < a.cap ? ctx + t.tokens : a.cap), window = seed == 3 ? 100 : seed == 4 ? 1 : 0;
+      const int skip = tr_skip((int)ctx, window);
+      if (skip < 0 || skip % kAtKeys || (window && skip > (ctx + 1 > window ? ctx + 1 - window : 0)))
+        return bad("tree attention skips %lld of %lld keys", skip, ctx);
+      tiles.push_back(tr_tiles(n, skip));
+    }
+    const hipError_t e = walk_deal(tiles, (int64_t)a.heads * a.ht, a.wgs);
+    if (e != hipSuccess) return e;
+  }
+  return walk_loads(a.pg);
+}
+
+// A row of a move's workspace, byte by byte; the pieces that a reservation
+// copies of a page, against the places of the tokens it copies.
+hipError_t launch_kv_move(const KpMove& a, hipStream_t) {
+  dry_launch();
+  const int D = a.pg.D;
+  if ((1 << a.lgP) != a.pg.P || a.tokens < 1 || !launchable((a.tokens * a.heads + 15) / 16, kMxThreads))
+    return bad("cache move of %lld tokens", a.tokens, 0);
+  std::vector<uint8_t> cover((size_t)kp_row_bytes(D), 0);
+  for (int r = 0; r < 16; ++r)
+    for (int i = 0; i < D / 32; ++i) {
+      cover[(size_t)(r * (D / 32) + i)]++;
+      cover[(size_t)(D / 2 + r * (D / 32) + i)]++;
+      if (r == 0) cover[(size_t)(D + i)]++, cover[(size_t)(D + D / 32 + i)]++;
+    }
+  for (size_t i = 0; i < cover.size(); ++i)
+    if (cover[i] != 1) return bad("cache move byte %lld written %lld times", (long long)i, cover[i]);
+  return walk_page(a.pg);
+}
+hipError_t launch_kv_fork(const KpFork& a, hipStream_t) {
+  dry_launch();
+  const int64_t n = a.children * (a.width > 0 ? a.width : 1);
+  return launchable((n + kMxThreads - 1) / kMxThreads, kMxThreads) ? hipSuccess : bad("cache fork of %lld", n, 0);
+}
+hipError_t launch_kv_free(const KpFree& a, hipStream_t) {
+  dry_launch();
+  return launchable((a.n * a.width + kMxThreads - 1) / kMxThreads, kMxThreads) ? hipSuccess
+                                                                             : bad("cache free of %lld", a.n, 0);
+}
+hipError_t launch_kv_reserve(const KpReserve& a, hipStream_t) {
+  dry_launch();
+  const KvPage& pg = a.pg;
+  const int P = pg.P, D = pg.D;
+  if ((1 << a.lgP) != P || a.per != kp_per(a.tokens, P) || !launchable(a.batch, kMxThreads) || a.heads > 65535)
+    return bad("cache reservation geometry (%lld tokens)", a.tokens, 0);
+  for (int used = 16; used <= P; used += 16) {
+    std::vector<uint8_t> cover((size_t)pg.bytes(), 0);
+    const int codes = used * (D / 32), scales = used * D / 512;
+    for (int i = 0; i < 2 * (codes + scales); ++i) {
+      const int64_t at = (int64_t)kp_piece(pg, codes, scales, i) * 16;
+      if (at < 0 || at + 16 > pg.bytes()) return bad("cache reservation piece %lld of %lld tokens", i, used);
+      for (int e = 0; e < 16; ++e) cover[(size_t)(at + e)]++;
+    }
+    for (int t = 0; t < P; ++t) {  // the first tokens' bytes once, no other's
+      bool ok = true;
+      for (int r = 0; r < 16; ++r)
+        for (int e = 0; e < D / 32; ++e)
+          ok = ok && cover[(size_t)(pg.kcode(t) + r * (D / 32) + e)] == (t < used) &&
+               cover[(size_t)(pg.vcode(t, r) + e)] == (t < used);
+      for (int e = 0; e < D / 32; ++e)
+        ok = ok && cover[(size_t)(pg.kscale(t) + e)] == (t < used) && cover[(size_t)pg.vscale(t, e)] == (t < used);
+      if (!ok) return bad("cache reservation copy of token %lld of %lld", t, used);
+    }
+  }
+  // the entries that new tokens lie in, for lengths around page and table ends
+  std::vector<int32_t> lens;
+  for (int64_t n : {(int64_t)-1, (int64_t)0, (int64_t)1, (int64_t)P - 1, (int64_t)P, a.width * P - 1, a.width * P, a.width * P + 5})
+    if (n < (int64_t)1 << 31) lens.push_back((int32_t)n);
+  KpReserve b = a;
+  b.lens = lens.data();
+  b.batch = (int64_t)lens.size();
+  for (int64_t i = 0; i < b.batch * b.per && b.per < 1 << 16; ++i) {
+    KpItem it;
+    if (!kp_item(b, i, it)) continue;
+    const int64_t n = lens[(size_t)it.row];
+    if (it.entry < 0 || it.entry >= a.width || it.entry < n / P || it.entry > (n + a.tokens - 1) / P ||
+        it.used != (it.entry == n / P ? n % P : 0))
+      return bad("cache reservation entry %lld of a row of %lld tokens", it.entry, n);
+  }
   return walk_page(pg);
 }
 

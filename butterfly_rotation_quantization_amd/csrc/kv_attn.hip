@@ -29,133 +29,15 @@
 // without loads ahead, 139 and 84.)  A group of 16 heads takes 161 us for the four,
 // one of 128 over a single key-value head 146: 16 heads at a time, the products,
 // exponentials and the values' conversions of each pass bound it.
-#include <type_traits>
-
-#include "mx_dev.h"
+#include "at_dev.h"
 
 namespace brq {
 namespace {
-
-__device__ __forceinline__ mxb2 at_pair(uint32_t w, float s, int byte) {
-  switch (byte & 3) {
-    case 0: return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
-    case 1: return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
-    case 2: return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
-    default: return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
-  }
-}
-__device__ __forceinline__ uint32_t at_bits(mxb2 x) { return __builtin_bit_cast(uint32_t, x); }
-
-__device__ __forceinline__ float at_ror8(float x) { return __uint_as_float(mx_dpp<0x128>(__float_as_uint(x))); }
-// maximum / sum over the four lanes of a column
-__device__ __forceinline__ float at_colmax(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-  const auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
-}
-__device__ __forceinline__ float at_colsum(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  const auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
-}
-
-__device__ __forceinline__ void at_load8(int t, const void* p, int64_t off, float (&v)[8]) {
-  if (t == BRQ_F32) mx_load8<BRQ_F32>(p, off, v);
-  else if (t == BRQ_BF16) mx_load8<BRQ_BF16>(p, off, v);
-  else mx_load8<BRQ_F16>(p, off, v);
-}
-__device__ __forceinline__ void at_store8(int t, void* p, int64_t off, const float (&v)[8]) {
-  if (t == BRQ_F32) mx_store8<BRQ_F32>(p, off, v);
-  else if (t == BRQ_BF16) mx_store8<BRQ_BF16>(p, off, v);
-  else mx_store8<BRQ_F16>(p, off, v);
-}
-
-// Eight values of a head's finished output: normalise, undo the transform,
-// store (m in units of log2).
-template <int D>
-__device__ __forceinline__ void at_finish(const AtArgs& a, int64_t b, int head, int c, int lane, float (&o)[8],
-                                          float m, float l) {
-  const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // a NaN sum stays one
-#pragma unroll
-  for (int e = 0; e < 8; ++e) o[e] = l != 0.0f ? o[e] * inv : 0.0f;
-  if (a.d) {
-    float sign[8];
-    mx_signs(a.signs, c, sign);
-    mx_unrotate<D>(o, sign, a.rnorm, lane);
-  }
-  at_store8(a.qt, a.out, b * a.ldo + (int64_t)head * D + c, o);
-  if (a.lse && c == 0)
-    a.lse[b * a.q_heads + head] = l != 0.0f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
-}
-
-// A query enters the scores as eight 4-bit floating-point pieces, each the
-// rounding of what the ones before it left.  The first has half the scale of
-// the largest exponent of its block of 32, so that it lies below 4, where the
-// format's steps are 1/2 and less, or 1: half of that is left, 4 of the next
-// piece, whose scale is an eighth.  Together the pieces are within 2^-23 of the
-// block's largest magnitude.  Products of 4-bit values lose nothing that a
-// float32 sum would keep; those of 8-bit ones, which would need four pieces for
-// 16 bits, drop what lies 14 bits below the largest of a block (a key's code of
-// 6 beside one of 1/2: scores 2^-14 of the sum of magnitudes off).
-// The eight values of a lane (its block is four lanes): the pieces' codes and
-// scale bytes.
-__device__ __forceinline__ void at_pieces(float (&v)[8], uint32_t (&piece)[8], uint32_t (&byte)[8]) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
-  top = max(top, mx_xor<1>(top));
-  top = max(top, mx_xor<2>(top));
-  const int ex = (int)(top >> 23);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int x = ex - 1 - 3 * k;
-    byte[k] = ex == 255 ? 255u : x > 0 ? (uint32_t)x : 0u;  // an infinity or a NaN: a NaN scale
-    const float sc = mx_scale(byte[k]);
-    uint32_t w = 0;
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], sc, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], sc, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], sc, 2);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], sc, 3);
-    piece[k] = w;
-    if (k < 7) {
-      float back[8];
-      mx_values8(w, byte[k], back);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] -= back[e];  // exact
-    }
-  }
-}
-
-// c += K Q, both 4-bit; the queries' scale is byte w of qs.
-__device__ __forceinline__ mxf4 at_score(mxi8 K, mxi8 Q, mxf4 c, int ks, int qs, int w) {
-  switch (w & 3) {
-    case 0: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(K, Q, c, 4, 4, 0, ks, 0, qs);
-    case 1: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(K, Q, c, 4, 4, 0, ks, 1, qs);
-    case 2: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(K, Q, c, 4, 4, 0, ks, 2, qs);
-    default: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(K, Q, c, 4, 4, 0, ks, 3, qs);
-  }
-}
 
 // Tokens of sequence b that the table has room for.
 __device__ __forceinline__ int at_length(const AtArgs& a, int64_t b) {
   const int n = a.lens[b];
   return n < 0 ? 0 : (n < a.cap ? n : a.cap);
-}
-
-// Sum over the workgroup's threads (every thread gets it); scratch: one value
-// per wavefront.
-__device__ __forceinline__ int64_t at_block_sum(int64_t x, int64_t* scratch) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = x;
-  __syncthreads();
-  int64_t s = 0;
-#pragma unroll
-  for (int w = 0; w < kAtWaves; ++w) s += scratch[w];
-  return s;
 }
 
 // One workgroup: its share of the tiles of all units (or, without a deal, the
@@ -171,9 +53,7 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
   constexpr int LPH = D / kMxPerLane; // lanes of a head's row
   __shared__ __align__(16) float os[kAtWaves][H][LD];
   __shared__ float ms[kAtWaves][H], ls[kAtWaves][H];
-  __shared__ int64_t sums[kAtWaves];
-  __shared__ int found[1];
-  __shared__ int64_t found_base[1];
+  __shared__ AtShareLds share;
   // The queries' pieces in the order of the operands, 16 columns of 16 bytes for
   // each column tile, product and block: a read's lanes find column c at place c
   // of the banks' 256 bytes, whatever their block (four sequences of 131072:
@@ -193,47 +73,17 @@ __global__ __launch_bounds__(kAtThreads, at_workgroups(D, NT) / 256) void at_ker
   int64_t b = 0;
   int wgs = 0;
   if (a.wgs) {
-    // all tiles; with more sequences than threads, by a pass of its own
-    if (a.batch > kAtThreads) {
-      int64_t mine = 0;
-      for (int64_t i = tid; i < a.batch; i += kAtThreads) mine += at_cost(at_tiles(at_length(a, i), a.window));
-      total = at_block_sum(mine, sums) * units;
-    }
-    for (int64_t i0 = 0;; i0 += kAtThreads) {
-      const int64_t i = i0 + tid;
-      const int64_t n = i < a.batch ? (int64_t)at_cost(at_tiles(at_length(a, i), a.window)) * units : 0;
-      int64_t x = n;  // inclusive sum over the threads before
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const int64_t y = __shfl_up(x, d);
-        if (lane >= d) x += y;
-      }
-      __syncthreads();
-      if (lane == 63) sums[wave] = x;
-      __syncthreads();
-      int64_t all = 0;
-#pragma unroll
-      for (int w = 0; w < kAtWaves; ++w) {
-        if (w < wave) x += sums[w];
-        all += sums[w];
-      }
-      if (i0 == 0) {
-        if (a.batch <= kAtThreads) total = all;
-        wgs = at_dealt(total, a.wgs);
-        if ((int)blockIdx.x >= wgs) return;
-        pos = at_start(blockIdx.x, total, wgs);
-        end = at_start((int64_t)blockIdx.x + 1, total, wgs);
-      }
-      if (pos >= base + x - n && pos < base + x) {  // the sequence that has place pos
-        found[0] = (int)i;
-        found_base[0] = base + x - n;
-      }
-      __syncthreads();
-      if (pos < base + all) break;  // it is one of these: pos < total
-      base += all;
-    }
-    b = found[0];
-    base = found_base[0];
+    AtShare s;
+    if (!at_share(a.batch, a.wgs, units, share,
+                  [&](int64_t i) { return at_cost(at_tiles(at_length(a, i), a.window)); },
+                  [](int) { return (int)blockIdx.x; }, s))
+      return;
+    total = s.total;
+    pos = s.pos;
+    end = s.end;
+    base = s.base;
+    b = s.b;
+    wgs = s.wgs;
   } else {
     b = blockIdx.x / (uint32_t)units;
     const int cost = at_cost(at_tiles(at_length(a, b), a.window));

@@ -1,0 +1,598 @@
+// Attention of a tree of drafted tokens per sequence over the paged 4-bit cache
+// (layout: KvPage in mx.h; what it shares with the attention of one token:
+// at_dev.h).
+//
+// The rows of a unit are 16 nt of the (draft, query head) pairs over one
+// key-value head of one sequence, in columns of the matrix products: the scores
+// S^T = K Q^T from the codes as they lie in the cache and the queries in eight
+// 4-bit pieces, a column a row, one product after the other into the same sums;
+// the output O^T = V^T P^T with the values in bfloat16 (exact) and a probability
+// in PP pieces of 8 bits: three for float32 rows, so that it has its 24 bits; two
+// for 16-bit ones, off by 2^-17 of it at most (their output's half step is 2^-12
+// or 2^-9 of a value).
+//
+// Which keys a row sees differs only among the drafts, and at a window's far
+// end: a step of 32 keys that lies clear of both is computed without a mask.
+#include "at_dev.h"
+
+namespace brq {
+namespace {
+
+// Keys of sequence b: context and drafts, as many as the table has room for.
+__device__ __forceinline__ int tr_keys(const TrArgs& a, int64_t b) {
+  const int64_t n = a.at.lens[b];
+  return n < 0 ? 0 : n + a.tokens < a.at.cap ? (int)n + a.tokens : a.at.cap;
+}
+__device__ __forceinline__ int tr_tiles_of(const TrArgs& a, int64_t b) {
+  return tr_tiles(tr_keys(a, b), tr_skip(a.at.lens[b], a.at.window));
+}
+
+// What a row sees: context from position `from` on, and drafts by their bits.
+// Of a window, drafts come last: bits below the last `window` set ones go.
+struct TrSeen {
+  int from;
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ TrSeen tr_seen(int64_t mask, int ctx, int window) {
+  TrSeen s;
+  uint64_t m = (uint64_t)mask;
+  const int ones = __popcll(m);
+  s.from = 0;
+  if (window > 0) {
+    const int64_t from = (int64_t)ctx + ones - window;
+    s.from = from > 0 ? (int)from : 0;
+    for (int drop = ones - window; drop > 0; --drop) m &= m - 1;  // the lowest set bit
+  }
+  s.lo = (uint32_t)m;
+  s.hi = (uint32_t)(m >> 32);
+  return s;
+}
+
+// The value of a code of a block with a scale's byte.
+__device__ __forceinline__ float tr_value(uint32_t code, uint32_t byte) {
+  const uint32_t m = code & 7u;
+  const float v = m < 4 ? 0.5f * (float)m : m < 6 ? (float)m - 2.f : m == 6 ? 4.f : 6.f;
+  const float s = byte == 255u ? __uint_as_float(0x7fc00000u) : mx_scale(byte);
+  return (code & 8u ? -v : v) * s;
+}
+
+// A unit's row: its row of the batch's and its query head; false past the last.
+__device__ __forceinline__ bool tr_row(const TrArgs& a, int64_t b, int h, int r, int64_t* row, int* head) {
+  const int group = a.at.group, i = r / group;
+  *row = b * a.tokens + i;
+  *head = h * group + (r - i * group);
+  return i < a.tokens;
+}
+// A row of the output, with nothing seen where its mask is 0.
+template <int D>
+__device__ __forceinline__ void tr_finish(const TrArgs& a, int64_t row, int head, int c, int lane, float (&o)[8],
+                                          float m, float l) {
+  const bool there = a.mask[row] != 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = there ? o[e] : 0.f;
+  at_finish<D>(a.at, row, head, c, lane, o, m, there ? l : 0.f);
+}
+
+template <int D, int NT, int PP>
+__global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_kernel(TrArgs t) {
+  const AtArgs& a = t.at;
+  constexpr int KW = D / 32;            // words of codes a lane holds per key (of the scores) or four keys (values)
+  constexpr int NQ = D == 256 ? 2 : 1;  // matrix steps of 128 values of a score
+  constexpr int NP = D == 64 ? 4 : 8;   // products of a step: a piece each (D = 64: two)
+  constexpr int R = D / 16;             // dimensions of a run = output tiles
+  constexpr int H = 16 * NT;            // rows
+  constexpr int LD = D + 4;
+  constexpr int LPH = D / kMxPerLane;   // lanes of a row
+  constexpr int NB = D == 64 ? 4 : D / 32;
+  // the queries' pieces in the order of the operands (16 columns of 16 bytes for
+  // each column tile, product and block); later the wavefronts' sums of a column tile
+  constexpr int kPieces = NT * NP * NB * 256, kSums = kAtWaves * 16 * LD * 4;
+  __shared__ __align__(16) uint8_t lds[kPieces > kSums ? kPieces : kSums];
+  __shared__ __align__(8) uint8_t qb[H][D / 32][8];  // the pieces' scales
+  __shared__ TrSeen seen[H];
+  __shared__ float ms[kAtWaves][16], ls[kAtWaves][16];
+  __shared__ AtShareLds share;
+  __shared__ int far[1];  // the first position that every row's window has reached
+  uint8_t* qs = lds;
+  float (*os)[16][LD] = reinterpret_cast<float (*)[16][LD]>(lds);
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int units = a.heads * a.ht;  // of a sequence
+  int64_t total = 0, pos = 0, end = 0, base = 0, b = 0;
+  int wgs = 0, number = 0;
+  if (a.wgs) {
+    AtShare s;
+    // neighbours in the deal, which read the same keys, on one XCD
+    if (!at_share(a.batch, a.wgs, units, share, [&](int64_t i) { return at_cost(tr_tiles_of(t, i)); },
+                  [](int n) { return tr_number(blockIdx.x, n); }, s))
+      return;
+    total = s.total;
+    pos = s.pos;
+    end = s.end;
+    base = s.base;
+    b = s.b;
+    wgs = s.wgs;
+    number = s.w;
+  } else {
+    b = blockIdx.x / (uint32_t)units;
+    const int cost = at_cost(tr_tiles_of(t, b)), u = (int)(blockIdx.x - (uint32_t)b * (uint32_t)units);
+    pos = (int64_t)u * cost;
+    end = pos + cost;
+    if (pos == end) {  // no key: the unit's rows get what an empty sum gives
+      for (int r = tid / LPH; r < H; r += kAtThreads / LPH) {
+        int64_t row;
+        int head;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (tr_row(t, b, u / a.ht, u % a.ht * H + r, &row, &head))
+          tr_finish<D>(t, row, head, (tid % LPH) * kMxPerLane, lane, v, 0.f, 0.f);
+      }
+      return;
+    }
+  }
+  while (pos < end) {
+  // the part's keys: tiles [tb, te) of unit u of sequence b
+  const int ctx = a.lens[b], n = tr_keys(t, b);
+  const int s0 = tr_skip(ctx, a.window), tiles = tr_tiles(n, s0);
+  const int cost = at_cost(tiles);
+  if (pos >= base + (int64_t)cost * units) {  // on to the next sequence (one without keys has no place)
+    base += (int64_t)cost * units;
+    ++b;
+    continue;
+  }
+  const int u = (int)((pos - base) / cost);
+  const int64_t g0 = base + (int64_t)u * cost + kAtLead;  // place of the unit's first tile
+  const int tb = pos > g0 ? (int)(pos - g0) : 0;
+  const int te = end - g0 < tiles ? (int)(end - g0) : tiles;
+  pos = g0 + tiles < end ? g0 + tiles : end;
+  if (te <= tb) continue;  // only of the unit's lead
+  const int h = u / a.ht, r0 = (u - h * a.ht) * H;  // key-value head; the unit's first row
+  if (wgs && tb == 0 && tid == 0)  // who has the unit's parts, and the first one's slot, for the join
+    a.who[b * units + u] = make_int2((int)at_slot(number, g0, total, wgs),
+                                     te == tiles ? 0 : at_owner(g0 + tiles - 1, total, wgs) - number);
+
+  const int64_t pbytes = a.pg.bytes();
+  const int32_t* table = a.table + b * a.ldt;
+  int k0 = s0 + tb * kAtTile + wave * kAtKeys;
+  const int kend = s0 + te * kAtTile < n ? s0 + te * kAtTile : n;
+  // Operands of 32 keys, 16 of them from one page, fetched a step ahead as in
+  // the attention of one token.  Where there is no key, or no page, page 0 is read and
+  // masked below.
+  int page[2], pg[2];
+  bool ok[2];
+  mxi4 kw[2][NQ];
+  uint32_t vw[2][KW], vs[2];
+  int ks[2][NQ];
+  auto look_up = [&](int k) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) page[t] = table[(k + 16 * t < n ? k + 16 * t : n - 1) >> a.lgP];
+  };
+  auto fetch_keys = [&](int k) {  // looked up before; looks up the next
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      pg[t] = __builtin_amdgcn_readfirstlane(page[t]);
+      ok[t] = pg[t] >= 0 && pg[t] < a.pages && k + 16 * t < n;
+      pg[t] = ok[t] ? pg[t] : 0;
+      const uint8_t* pb = a.cache + ((int64_t)pg[t] * a.heads + h) * pbytes;
+      const int p = (k + 16 * t) & (a.pg.P - 1);
+#pragma unroll
+      for (int e = 0; e < NQ; ++e) {
+        const int blk = D == 64 ? (g & 1) : 4 * e + g;  // D = 64: both halves of the lanes hold the 64 values
+        kw[t][e] = *reinterpret_cast<const mxi4*>(pb + a.pg.kcode(p) + (uint32_t)(c * (D / 2) + 16 * blk));
+        ks[t][e] = pb[a.pg.kscale(p) + (uint32_t)(c * (D / 32) + blk)];
+      }
+    }
+    look_up(k + kAtTile);
+  };
+  auto fetch_values = [&](int k) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint8_t* pb = a.cache + ((int64_t)pg[t] * a.heads + h) * pbytes;
+      const int p = (k + 16 * t) & (a.pg.P - 1);
+      const uint8_t* vp = pb + a.pg.vcode(p, 0) + (uint32_t)(g * (2 * D) + c * (D / 8));
+      if constexpr (D == 64) {
+        const uint2 y = *reinterpret_cast<const uint2*>(vp);
+        vw[t][0] = y.x; vw[t][1] = y.y;
+      } else {
+#pragma unroll
+        for (int q = 0; q < KW / 4; ++q) {
+          const uint4 y = reinterpret_cast<const uint4*>(vp)[q];
+          vw[t][4 * q] = y.x; vw[t][4 * q + 1] = y.y; vw[t][4 * q + 2] = y.z; vw[t][4 * q + 3] = y.w;
+        }
+      }
+      vs[t] = *reinterpret_cast<const uint32_t*>(pb + a.pg.vscale(p, 0) + (uint32_t)(g * (D / 8) + (c * D / 512) * 4));
+    }
+  };
+  if (k0 < kend) {
+    look_up(k0);
+    fetch_keys(k0);
+    fetch_values(k0);
+  }
+  // what the rows see; one that sees nothing is given all here and cleared at the end
+  if (tid == 0) far[0] = 0;
+  __syncthreads();
+  if (tid < H) {
+    int64_t row;
+    int head;
+    TrSeen s = {0, 0u, 0u};
+    if (tr_row(t, b, h, r0 + tid, &row, &head)) {
+      const int64_t m = t.mask[row];
+      s = tr_seen(m, ctx, a.window);
+      if (m == 0) s.from = 0;
+    }
+    seen[tid] = s;
+    if (s.from > 0) atomicMax(&far[0], s.from);
+  }
+  // queries: rotated, times the scale, in pieces
+  const float sl = a.scale * 1.44269504088896341f;  // scores in units of log2
+  for (int r = tid / LPH; r < H; r += kAtThreads / LPH) {
+    const int e0 = (tid % LPH) * kMxPerLane;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    int64_t row;
+    int head;
+    if (tr_row(t, b, h, r0 + r, &row, &head)) {
+      at_load8(a.qt, a.q, row * a.ldq + (int64_t)head * D + e0, v);
+      if (a.d) {
+        if (a.signs)  // after the query: registers are short here
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] *= a.signs[e0 + e];
+        mx_hadamard<D>(v, lane);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= a.rnorm;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= sl;
+    uint32_t piece[8], byte[8];
+    at_pieces(v, piece, byte);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int w = D == 64 ? k >> 1 : k;
+      const int chunk = (r / 16 * NP + w) * NB + e0 / 32 + (D == 64 ? 2 * (k & 1) : 0);
+      *reinterpret_cast<uint32_t*>(qs + chunk * 256 + r % 16 * 16 + e0 % 32 / 2) = piece[k];
+      // D = 64: the even pieces' scales, then the odd ones'
+      if ((e0 & 31) == 0) qb[r][e0 / 32][D == 64 ? (k & 1) * 4 + w : k] = (uint8_t)byte[k];
+    }
+  }
+  __syncthreads();
+  // scales of a column's pieces, four to a word
+  int qsc[NT][NQ][NP / 4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < NQ; ++e)
+#pragma unroll
+      for (int q = 0; q < NP / 4; ++q)
+        qsc[t][e][q] = D == 64 ? *reinterpret_cast<const int*>(&qb[16 * t + c][g & 1][4 * (g >> 1)])
+                               : *reinterpret_cast<const int*>(&qb[16 * t + c][4 * e + g][4 * q]);
+  const uint8_t* ql = qs + lane * 16;  // g * 256 + c * 16
+  auto query = [&](int t, int e, int w) {
+    const mxi4 x = *reinterpret_cast<const mxi4*>(ql + ((t * NP + w) * NB + 4 * e) * 256);
+    return mxi8{x[0], x[1], x[2], x[3], 0, 0, 0, 0};
+  };
+  const int reach = far[0];  // from here to the context's end nothing is masked
+
+  mxf4 o[NT][R];
+  float m[NT], l[NT];  // l: of the lane's keys
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    m[t] = -INFINITY;
+    l[t] = 0.f;
+#pragma unroll
+    for (int j = 0; j < R; ++j) o[t][j] = mxf4{0.f, 0.f, 0.f, 0.f};
+  }
+  // One step of 32 keys.  The last one fetches nothing (and is code of its own:
+  // under a condition in the loop, the fetches would be waited for at once).
+  auto step = [&](auto last) {
+    constexpr bool more = !decltype(last)::value;
+    asm volatile("" ::: "memory");  // the queries stay in LDS
+    // scores: column c, keys 16 t + 4 g + i
+    float s[NT][2][4];
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      mxf4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int e = 0; e < NQ; ++e)
+#pragma unroll
+        for (int w = 0; w < NP; ++w) {
+          const mxi8 Q = query(u, e, w);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const mxi8 K = {kw[t][e][0], kw[t][e][1], kw[t][e][2], kw[t][e][3], 0, 0, 0, 0};
+            acc[t] = at_score(K, Q, acc[t], ks[t][e], qsc[u][e][w / 4], w);
+          }
+        }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[u][t][i] = acc[t][i];
+    }
+    // Masked keys: scores to -infinity, values that no row sees to zero.  A value that
+    // some rows see and others do not is multiplied by their zeros too, so one
+    // that is not finite (its scale's byte 253 or more can be) is taken out and
+    // added below to the rows that see it.
+    uint32_t odd[2] = {0u, 0u};  // such values' scales, else 0
+    uint64_t keys = 0;           // of the step that have one
+    if (k0 < reach || k0 + kAtKeys > ctx || !ok[0] || !ok[1]) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = k0 + 16 * t + 4 * g + i;
+          const bool none = key >= n || !ok[t];
+#pragma unroll
+          for (int u = 0; u < NT; ++u) {
+            const TrSeen z = seen[16 * u + c];
+            const int j = key - ctx;
+            const bool sees = key < ctx ? key >= z.from : ((j < 32 ? z.lo >> (j & 31) : z.hi >> (j & 31)) & 1) != 0;
+            if (none || !sees) s[u][t][i] = -INFINITY;
+          }
+          const uint32_t byte = vs[t] >> (8 * i) & 255u;
+          if (none || byte >= 253u) {
+            if (!none) odd[t] |= byte << (8 * i);
+            vs[t] = (vs[t] & ~(255u << (8 * i))) | 127u << (8 * i);
+          }
+          if (none) {
+            if constexpr (D == 64) {
+              vw[t][i / 2] &= ~(0xffffu << (16 * (i & 1)));
+            } else {
+#pragma unroll
+              for (int q = 0; q < KW / 4; ++q) vw[t][i * (KW / 4) + q] = 0u;
+            }
+          }
+        }
+      keys = __builtin_amdgcn_ballot_w64((odd[0] | odd[1]) != 0);
+    }
+    if constexpr (more) fetch_keys(k0 + kAtTile);
+    // values: keys in pairs, one run of dimensions per lane (of a scale the
+    // conversion reads the exponent, so byte 0 is 2^-127 and 255 NaN)
+    float vsc[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) vsc[t][i] = __uint_as_float(i == 3 ? vs[t] >> 24 << 23 : (vs[t] >> (8 * i) & 255u) << 23);
+    mxb8 va[R];
+#pragma unroll
+    for (int q = 0; q < R / 2; ++q) {  // dimensions 2 q and 2 q + 1 of the run
+      uint32_t lo[4], hi[4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const int ba = i * (R / 2) + q, bb = (i + 1) * (R / 2) + q;  // bytes of the lane's words
+          uint32_t x = at_bits(at_pair(vw[t][ba / 4], vsc[t][i], ba));
+          uint32_t y = at_bits(at_pair(vw[t][bb / 4], vsc[t][i + 1], bb));
+          if (keys) {  // not the values that are taken out
+            if (odd[t] >> (8 * i) & 255u) x = 0u;
+            if (odd[t] >> (8 * i + 8) & 255u) y = 0u;
+          }
+          lo[2 * t + i / 2] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+          hi[2 * t + i / 2] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+        }
+      va[2 * q] = __builtin_bit_cast(mxb8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      va[2 * q + 1] = __builtin_bit_cast(mxb8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+    }
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      float mx = fmaxf(fmaxf(s[u][0][0], s[u][0][1]), fmaxf(s[u][0][2], s[u][0][3]));
+      mx = fmaxf(mx, fmaxf(fmaxf(s[u][1][0], s[u][1][1]), fmaxf(s[u][1][2], s[u][1][3])));
+      mx = fmaxf(at_colmax(mx), m[u]);
+      const float base = mx == -INFINITY ? 0.f : mx;
+      if (__builtin_amdgcn_ballot_w64(mx != m[u])) {  // seldom after the first tiles
+        const float f = __builtin_amdgcn_exp2f(m[u] - base);
+        m[u] = mx;
+        l[u] *= f;
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[u][j][i] *= f;
+      }
+      // A probability's first 8 bits, the next ones, the last ones
+      uint32_t w[PP][4];
+      float sum = 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float x[PP][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float p = __builtin_amdgcn_exp2f(s[u][q / 2][2 * (q & 1) + e] - base);
+          sum += p;
+#pragma unroll
+          for (int z = 0; z < PP; ++z) {
+            x[z][e] = p;
+            p -= __uint_as_float(__float_as_uint(p) & 0xffff0000u);
+          }
+        }
+#pragma unroll
+        for (int z = 0; z < PP; ++z)
+          w[z][q] = z == 1 && PP == 2 ? mx_bf16(x[z][0]) | mx_bf16(x[z][1]) << 16  // the last piece is rounded
+                                      : __builtin_amdgcn_perm(__float_as_uint(x[z][1]), __float_as_uint(x[z][0]), 0x07060302u);
+      }
+      l[u] += sum;
+#pragma unroll
+      for (int z = 0; z < PP; ++z) {
+        const mxb8 pf = __builtin_bit_cast(mxb8, make_uint4(w[z][0], w[z][1], w[z][2], w[z][3]));
+#pragma unroll
+        for (int j = 0; j < R; ++j) o[u][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va[j], pf, o[u][j], 0, 0, 0);
+      }
+      if (keys) {
+        // One such key at a time: its values to the lanes of its products, times
+        // its probabilities, added where the row sees it.
+        for (int kk = 0; kk < 32; ++kk) {
+          const int tt = kk >> 4, gg = kk >> 2 & 3, i = kk & 3;
+          const bool mine = g == gg && ((tt ? odd[1] : odd[0]) >> (8 * i) & 255u) != 0;
+          if (!__builtin_amdgcn_ballot_w64(mine)) continue;
+          float p = 0.f;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (t == tt && e == i) p = s[u][t][e];
+          p = __shfl(p, 16 * gg + c);
+          const bool sees = p != -INFINITY;
+          p = __builtin_amdgcn_exp2f(p - base);
+          uint32_t run[KW / 4 + 1] = {};  // the lane's run of the key, eight codes a word
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (t == tt && e == i) {
+                if constexpr (D == 64) run[0] = vw[t][e / 2] >> (16 * (e & 1));
+#pragma unroll
+                for (int q = 0; q < KW / 4; ++q) run[q] = vw[t][e * (KW / 4) + q];
+              }
+          // output (row c, dimension (4 g + e) R + j) wants run 4 g + e, which lane 16 gg + 4 g + e has
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int from = 16 * gg + 4 * g + e;
+            const uint32_t byte = __shfl(tt ? odd[1] : odd[0], from) >> (8 * i) & 255u;
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+              const float v = tr_value(__shfl(run[j / 8], from) >> (4 * (j & 7)) & 15u, byte);
+              if (sees && byte) o[u][j][e] += p * v;
+            }
+          }
+        }
+      }
+    }
+    if constexpr (more) fetch_values(k0 + kAtTile);
+  };
+  for (; k0 + kAtTile < kend; k0 += kAtTile) step(std::false_type{});
+  if (k0 < kend) step(std::true_type{});
+
+  // join the wavefronts, a column tile at a time: all parts to the common
+  // maximum, summed in order
+#pragma unroll
+  for (int u16 = 0; u16 < NT; ++u16) {
+    __syncthreads();  // the sums go where the queries were, or the tile before
+    const float sum = at_colsum(l[u16]);
+    if (lane < 16) {
+      ms[wave][lane] = m[u16];
+      ls[wave][lane] = sum;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < R; ++j) os[wave][c][(4 * g + i) * R + j] = o[u16][j][i];
+    __syncthreads();
+    for (int r = tid / LPH; r < 16; r += kAtThreads / LPH) {
+      int64_t row;
+      int head;
+      if (!tr_row(t, b, h, r0 + 16 * u16 + r, &row, &head)) continue;  // uniform over the row's lanes
+      const int e0 = (tid % LPH) * kMxPerLane;
+      float M = ms[0][r];
+#pragma unroll
+      for (int w = 1; w < kAtWaves; ++w) M = fmaxf(M, ms[w][r]);
+      const float base = M == -INFINITY ? 0.f : M;
+      float L = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kAtWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(ms[w][r] - base);
+        L += ls[w][r] * f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += os[w][r][e0 + e] * f;
+      }
+      if (tb == 0 && te == tiles) {
+        tr_finish<D>(t, row, head, e0, lane, v, M, L);
+      } else {
+        float* p = a.part + (at_slot(number, g0, total, wgs) * H + 16 * u16 + r) * (D + 4);
+        mx_store8<BRQ_F32>(p, e0, v);
+        if (e0 == 0) *reinterpret_cast<float2*>(p + D) = make_float2(M, L);
+      }
+    }
+  }
+  __syncthreads();  // the next part's queries go where these sums were
+  }
+}
+
+// Joins the parts of units that span workgroups and writes the rows of
+// sequences without keys, as at_join_kernel; `rows` rows of one unit to a workgroup.
+template <int D>
+__global__ __launch_bounds__(kAtThreads) void tr_join_kernel(TrArgs t, int rows) {
+  const AtArgs& a = t.at;
+  constexpr int LPH = D / kMxPerLane;
+  constexpr int LD = D + 4;
+  __shared__ float os[kAtThreads / LPH][LD];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int H = 16 * a.nt, units = a.heads * a.ht, per = H / rows;
+  const int64_t ub = blockIdx.x / (uint32_t)per;
+  const int64_t b = ub / units;
+  const int u = (int)(ub - b * units);
+  const int tiles = tr_tiles_of(t, b);
+  const int r = (int)(blockIdx.x - (uint32_t)ub * (uint32_t)per) * rows + tid / LPH % rows;
+  const int grp = tid / (LPH * rows), groups = kAtThreads / (LPH * rows);
+  const int e0 = (tid % LPH) * kMxPerLane;
+  int64_t row;
+  int head;
+  const bool mine = tr_row(t, b, u / a.ht, u % a.ht * H + r, &row, &head);
+  float M = -INFINITY, L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (tiles > 0) {
+    const int2 who = a.who[ub];
+    if (who.y == 0) return;  // finished by its workgroup
+    // part s (of who.y + 1) is the first of workgroup who.x / 2 + s
+    const float* p0 = a.part + r * (int64_t)LD;
+#pragma unroll 2
+    for (int s = grp; s <= who.y && mine; s += groups) {
+      const float* p = p0 + (s == 0 ? who.x : (who.x / 2 + s) * 2) * (int64_t)(H * LD);
+      const float2 ml = *reinterpret_cast<const float2*>(p + D);
+      float v[8];
+      mx_load8<BRQ_F32>(p, e0, v);
+      const float m = fmaxf(M, ml.x), base = m == -INFINITY ? 0.f : m;
+      const float f = __builtin_amdgcn_exp2f(M - base), q = __builtin_amdgcn_exp2f(ml.x - base);
+      M = m;
+      L = L * f + ml.y * q;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = o[e] * f + v[e] * q;
+    }
+  }
+  mx_store8<BRQ_F32>(&os[tid / LPH][0], e0, o);
+  if (e0 == 0) *reinterpret_cast<float2*>(&os[tid / LPH][D]) = make_float2(M, L);
+  __syncthreads();
+  if (grp != 0 || !mine) return;
+  const float own = M;
+#pragma unroll 4
+  for (int s = 1; s < groups; ++s) M = fmaxf(M, os[tid / LPH + s * rows][D]);
+  const float base = M == -INFINITY ? 0.f : M, f = __builtin_amdgcn_exp2f(own - base);
+  L *= f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] *= f;
+#pragma unroll 4
+  for (int s = 1; s < groups; ++s) {
+    const float* p = os[tid / LPH + s * rows];
+    const float q = __builtin_amdgcn_exp2f(p[D] - base);
+    L += p[D + 1] * q;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] += p[e0 + e] * q;
+  }
+  tr_finish<D>(t, row, head, e0, lane, o, M, L);
+}
+
+template <int D, int NT>
+void tr_launch(const TrArgs& t, dim3 grid, hipStream_t s) {
+  if (t.at.qt == BRQ_F32) tr_kernel<D, NT, 3><<<grid, kAtThreads, 0, s>>>(t);
+  else tr_kernel<D, NT, 2><<<grid, kAtThreads, 0, s>>>(t);
+}
+template <int D>
+hipError_t tr_launch(const TrArgs& t, hipStream_t s) {
+  const AtArgs& a = t.at;
+  const int64_t units = a.batch * a.heads * a.ht;
+  const dim3 grid((unsigned)(a.wgs ? a.wgs : units));
+  if (a.nt == 1) tr_launch<D, 1>(t, grid, s);
+  else if (a.nt == 2 || D == 256) tr_launch<D, 2>(t, grid, s);
+  else if constexpr (D != 256) tr_launch<D, 4>(t, grid, s);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.wgs) return e;
+  const int rows = tr_join_rows(units, a.nt, D);
+  tr_join_kernel<D><<<dim3((unsigned)(units * (16 * a.nt / rows))), kAtThreads, 0, s>>>(t, rows);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_tree_attention(const TrArgs& t, hipStream_t s) {
+  if (t.at.pg.D == 64) return tr_launch<64>(t, s);
+  if (t.at.pg.D == 128) return tr_launch<128>(t, s);
+  return tr_launch<256>(t, s);
+}
+
+}  // namespace brq

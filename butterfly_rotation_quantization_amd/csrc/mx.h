@@ -181,6 +181,34 @@ inline int mm_stream_waves(int64_t wgs) { return wgs > 256 ? 4 : 8; }
 hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t s);
 hipError_t launch_mx_linear(const MmArgs& a, const MmEpi& e, hipStream_t s);
 
+// ---- products grouped by expert (mx_grouped.hip)
+
+struct GmArgs {
+  MmArgs mm;             // T rows, m outputs; b, bs: of group 0, the others' behind
+  const int32_t* offs;   // [groups + 1]
+  int groups;
+};
+
+// Rows [b, end) of a group from its two offsets: within the T rows there are.
+__host__ __device__ inline void gm_rows(int from, int to, int T, int* b, int* end) {
+  *b = from < 0 ? 0 : from < T ? from : T;
+  *end = to < *b ? *b : to < T ? to : T;
+}
+// The most units of R rows that the groups can have: each begins at most one
+// that is not whole.
+inline int64_t gm_units(int64_t T, int64_t groups, int64_t R) { return T / R + (groups < T ? groups : T); }
+__host__ __device__ inline const void* gm_bias(const MmEpi& e, int64_t group, int64_t m) {
+  if (!e.bias) return nullptr;
+  return static_cast<const char*>(e.bias) + group * m * (e.bt == BRQ_F32 ? 4 : 2);
+}
+// Launches within 2^32 threads (64 per 16 x 16 outputs at most).
+inline bool gm_supported(int64_t T, int64_t groups, int64_t m, int64_t n) {
+  if (!mm_supported(T, m, n) || groups > 1 << 20) return false;
+  return m == 0 || gm_units(T, groups, 16) + 1 <= ((int64_t)1 << 32) / 64 / ((m + 15) / 16);
+}
+
+hipError_t launch_mx_grouped(const GmArgs& g, const MmEpi& e, hipStream_t s);
+
 // ---- paged cache (kv.hip) and attention (kv_attn.hip)
 
 constexpr int kKvQuad = 4;        // tokens whose value codes are interleaved
@@ -233,6 +261,89 @@ __host__ __device__ inline void kv_row(uint32_t row, int heads, int64_t* tok, in
 }
 hipError_t launch_kv_append(const KvArgs& a, hipStream_t s);
 hipError_t launch_kv_read(const KvArgs& a, hipStream_t s);
+
+// ---- tokens and pages moved, shared, taken, given back (kv_pages.hip)
+
+struct KpMove {
+  const int64_t *src, *dst;  // slots
+  int64_t tokens;
+  int heads;
+  KvPage pg;
+  int lgP;
+  int64_t pages;
+  uint8_t* cache;
+  uint8_t* ws;           // [tokens * heads] rows
+};
+// Bytes of a row of the workspace: the codes and scales of a token's head.
+__host__ __device__ constexpr int64_t kp_row_bytes(int D) { return D + D / 16; }
+constexpr int64_t kKpTokens = (int64_t)1 << 27;  // heads of tokens of a move: within 2^31 threads
+
+struct KpFork {
+  const int32_t *table, *lens, *parents;
+  int64_t batch, width, children, pages;
+  int32_t *refs, *out_table, *out_lens;
+};
+struct KpFree {
+  int32_t* table;
+  int64_t batch, width, pages, n;
+  int32_t* refs;
+  const int32_t* rows;   // [n], or null: all rows
+};
+
+constexpr int kKpThreads = 1024;  // of the workgroup that decides a reservation
+
+struct KpReserve {
+  uint8_t* cache;
+  int32_t* table;
+  const int32_t* lens;
+  int64_t batch, width;
+  int32_t* refs;
+  int64_t pages, tokens;
+  int heads;
+  KvPage pg;
+  int lgP;
+  int64_t* slots;        // [batch][tokens]
+  int64_t per;           // table entries that a row's new tokens can lie in
+  // in the workspace
+  int4* copy;            // [batch]: page to copy from and to, its tokens
+  int32_t* item;         // [batch * per]: the page of an entry, or -1
+  int32_t* fresh;        // free pages
+};
+// Entries that `tokens` tokens can lie in, from any place of a page on.
+__host__ __device__ inline int64_t kp_per(int64_t tokens, int64_t page) { return (tokens + page - 2) / page + 1; }
+inline size_t kp_bytes(int64_t batch, int64_t tokens, int64_t page, int64_t pages) {
+  const int64_t items = batch * kp_per(tokens, page);
+  return (size_t)(16 * batch + 4 * items + 4 * (items < pages ? items : pages) + 15) / 16 * 16;
+}
+
+struct KpItem {
+  int64_t row, entry;    // of the table
+  int used;              // tokens that the entry's page holds already
+};
+// Item i of a reservation; false: no entry, since the row's new tokens end
+// before it, its table does, or its length is negative.
+__host__ __device__ inline bool kp_item(const KpReserve& a, int64_t i, KpItem& it) {
+  it.row = i / a.per;
+  const int64_t k = i - it.row * a.per, n = a.lens[it.row];
+  if (n < 0) return false;
+  const int64_t first = n >> a.lgP;
+  it.entry = first + k;
+  it.used = k == 0 ? (int)(n & (a.pg.P - 1)) : 0;
+  return it.entry < a.width && it.entry <= (n + a.tokens - 1) >> a.lgP;
+}
+// Place in a page, in 16-byte pieces, of piece i of the first tokens' codes (keys',
+// then values') and scales (keys', then values'), of `codes` and `scales` pieces each.
+__host__ __device__ inline int kp_piece(const KvPage& pg, int codes, int scales, int i) {
+  if (i < 2 * codes) return i < codes ? i : pg.P * (pg.D / 32) + i - codes;
+  i -= 2 * codes;
+  const int base = pg.P * (pg.D / 16);
+  return i < scales ? base + i : base + pg.P * pg.D / 512 + i - scales;
+}
+
+hipError_t launch_kv_move(const KpMove& a, hipStream_t s);
+hipError_t launch_kv_fork(const KpFork& a, hipStream_t s);
+hipError_t launch_kv_free(const KpFree& a, hipStream_t s);
+hipError_t launch_kv_reserve(const KpReserve& a, hipStream_t s);
 
 constexpr int kAtWaves = 4;       // wavefronts of an attention workgroup
 constexpr int kAtThreads = 64 * kAtWaves;
@@ -330,5 +441,45 @@ inline size_t at_bytes(int head_dim, int nt, int64_t units) {
 }
 
 hipError_t launch_paged_attention(const AtArgs& a, hipStream_t s);
+
+// ---- attention of a tree of drafted tokens (kv_tree.hip)
+
+constexpr int kTrTokens = 64;     // drafted tokens of a sequence: a mask's bits
+
+// A unit is 16 nt rows (pairs of a draft and a query head over one key-value
+// head) over one sequence's keys; the deal of their tiles as above.
+struct TrArgs {
+  AtArgs at;             // q, out: a row for each draft; group, q_heads: of one
+  const int64_t* mask;   // [batch][tokens]
+  int tokens;
+};
+inline int64_t tr_rows(int tokens, int q_heads, int heads) { return (int64_t)tokens * (q_heads / heads); }
+// Column tiles of 16 rows of a workgroup.
+inline int tr_nt(int64_t rows, int head_dim) { return rows <= 16 ? 1 : rows <= 32 || head_dim == 256 ? 2 : 4; }
+// Workgroups that the chip holds at once, by the registers of their kernel.
+constexpr int tr_workgroups(int, int) { return 512; }
+// Keys before the first tile of a context of ctx tokens with a window (a row sees
+// one draft at least), and the tiles of n keys after them.
+__host__ __device__ inline int tr_skip(int ctx, int window) {
+  const int64_t first = (int64_t)ctx + 1 - window;
+  return window > 0 && first > 0 ? (int)(first & ~(int64_t)(kAtKeys - 1)) : 0;
+}
+__host__ __device__ inline int tr_tiles(int n, int skip) { return n > skip ? (n - skip + kAtTile - 1) / kAtTile : 0; }
+// The number in the deal of workgroup `block` of n that have places: blocks go
+// to the XCDs in turn, so those of one remainder by 8 take neighbouring numbers.
+// n or more: none.
+__host__ __device__ inline int tr_number(uint32_t block, int n) {
+  const int per = (n + 7) / 8, i = (int)(block >> 3);
+  return i < per ? (int)(block & 7) * per + i : n;
+}
+inline int tr_join_rows(int64_t units, int nt, int head_dim) {
+  const int rows = 16 * nt, most = kAtThreads / (head_dim / kMxPerLane);
+  return units * rows <= 2048 ? 1 : (rows < most ? rows : most);
+}
+inline size_t tr_part_bytes(int head_dim, int nt) {
+  return (size_t)2 * tr_workgroups(head_dim, nt) * nt * 16 * (head_dim + 4) * sizeof(float);
+}
+
+hipError_t launch_tree_attention(const TrArgs& t, hipStream_t s);
 
 }  // namespace brq

@@ -129,6 +129,43 @@ brq_status epilogue_of(const brq_mx_epilogue* ep, int64_t T, int64_t m, int64_t 
   return BRQ_OK;
 }
 
+// Shared checks of the products; *done set when there is nothing to do.
+brq_status mm_setup(MmArgs& a, MmEpi& e, const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                    const uint8_t* b_scales, int64_t T, int64_t m, int64_t n, int64_t groups, const brq_mx_epilogue* ep,
+                    void* y, int32_t yt, int64_t ldy, bool* done) {
+  *done = false;
+  std::memset(&a, 0, sizeof a);
+  if (!dtype_ok(yt)) return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad output dtype %d", yt);
+  if (T < 0 || m < 0 || n < 0 || ldy < m)
+    return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad shape or leading dimension");
+  if (n % kMxBlock)
+    return refuse(BRQ_ERR_INVALID_ARGUMENT, "n = %lld must be a multiple of %d", (long long)n, kMxBlock);
+  if (!mm_supported(T, m, n)) return refuse(BRQ_ERR_UNSUPPORTED, "T, m or n above 2^28, or more than 2^33 outputs");
+  const brq_status st = epilogue_of(ep, T, m, groups, &e);
+  if (st != BRQ_OK) return st;
+  if (T == 0 || m == 0 || groups == 0) {
+    *done = true;
+    return BRQ_OK;
+  }
+  if (!y || (n > 0 && (!a_codes || !a_scales || !b_codes || !b_scales)))
+    return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL data pointer");
+  if (misaligned(a_codes, 16) || misaligned(b_codes, 16) || misaligned(a_scales, 4) || misaligned(b_scales, 4))
+    return refuse(BRQ_ERR_ALIGNMENT, "codes must be 16-byte and scales 4-byte aligned");
+  if (misaligned(y, dtype_size(yt))) return refuse(BRQ_ERR_ALIGNMENT, "the output must be aligned to its type");
+  a.a = a_codes;
+  a.as = a_scales;
+  a.b = b_codes;
+  a.bs = b_scales;
+  a.T = T;
+  a.m = m;
+  a.n = n;
+  a.y = y;
+  a.yt = yt;
+  a.ldy = ldy;
+  a.wide = ldy % 4 == 0 && !misaligned(y, 4 * dtype_size(yt));
+  return BRQ_OK;
+}
+
 }  // namespace
 }  // namespace brq
 
@@ -188,42 +225,51 @@ brq_status brq_mx_linear(const uint8_t* a_codes, const uint8_t* a_scales, const 
                          const uint8_t* b_scales, int64_t T, int64_t m, int64_t n, const brq_mx_epilogue* ep, void* y,
                          int32_t yt, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
   clear_error();
+  MmArgs a;
   MmEpi e;
-  brq_status st = epilogue_of(ep, T, m, 1, &e);
-  if (st != BRQ_OK) return st;
-  if (!dtype_ok(yt)) return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad output dtype %d", yt);
-  if (T < 0 || m < 0 || n < 0 || ldy < m)
-    return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad shape or leading dimension");
-  if (n % kMxBlock)
-    return refuse(BRQ_ERR_INVALID_ARGUMENT, "n = %lld must be a multiple of %d", (long long)n, kMxBlock);
-  if (!mm_supported(T, m, n)) return refuse(BRQ_ERR_UNSUPPORTED, "T, m or n above 2^28, or more than 2^33 outputs");
-  if (T == 0 || m == 0) return BRQ_OK;
-  if (!y || (n > 0 && (!a_codes || !a_scales || !b_codes || !b_scales)))
-    return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL data pointer");
-  if (misaligned(a_codes, 16) || misaligned(b_codes, 16) || misaligned(a_scales, 4) || misaligned(b_scales, 4))
-    return refuse(BRQ_ERR_ALIGNMENT, "codes must be 16-byte and scales 4-byte aligned");
-  if (misaligned(y, dtype_size(yt))) return refuse(BRQ_ERR_ALIGNMENT, "the output must be aligned to its type");
+  bool done;
+  brq_status st = mm_setup(a, e, a_codes, a_scales, b_codes, b_scales, T, m, n, 1, ep, y, yt, ldy, &done);
+  if (st != BRQ_OK || done) return st;
   const size_t need = brq_mx_matmul_workspace_bytes(T, m, n);
   if ((st = workspace_ok(ws, ws_bytes, need)) != BRQ_OK) return st;
-  MmArgs a;
-  std::memset(&a, 0, sizeof a);
-  a.a = a_codes;
-  a.as = a_scales;
-  a.b = b_codes;
-  a.bs = b_scales;
-  a.T = T;
-  a.m = m;
-  a.n = n;
-  a.y = y;
-  a.yt = yt;
-  a.ldy = ldy;
   mm_plan(a, static_cast<uint8_t*>(ws));
-  a.wide = ldy % 4 == 0 && !misaligned(y, 4 * dtype_size(yt));
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int tok = prof_begin("mx matmul", s);
   const hipError_t err = ep ? launch_mx_linear(a, e, s) : launch_mx_matmul(a, s);
   prof_end(tok, s);
   return launched(err, "mx matmul");
+}
+
+size_t brq_mx_grouped_matmul_workspace_bytes(int64_t T, int64_t groups, int64_t m, int64_t n) {
+  if (T <= 0 || groups <= 0 || m <= 0 || n <= 0 || n % kMxBlock || !gm_supported(T, groups, m, n)) return 0;
+  return 0;
+}
+
+brq_status brq_mx_grouped_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                                 const uint8_t* b_scales, const int32_t* offsets, int64_t T, int64_t groups, int64_t m,
+                                 int64_t n, const brq_mx_epilogue* ep, void* y, int32_t yt, int64_t ldy, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  clear_error();
+  GmArgs g;
+  std::memset(&g, 0, sizeof g);
+  MmEpi e;
+  bool done;
+  if (groups < 0) return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad number of groups");
+  if (T > 0 && m > 0 && n >= 0 && !gm_supported(T, groups, m, n))
+    return refuse(BRQ_ERR_UNSUPPORTED, "T, m or n above 2^28, more than 2^33 outputs, 2^20 groups or 2^32 threads");
+  brq_status st = mm_setup(g.mm, e, a_codes, a_scales, b_codes, b_scales, T, m, n, groups, ep, y, yt, ldy, &done);
+  if (st != BRQ_OK || done) return st;
+  if (!offsets) return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL offsets");
+  if (misaligned(offsets, 4)) return refuse(BRQ_ERR_ALIGNMENT, "offsets must be 4-byte aligned");
+  const size_t need = brq_mx_grouped_matmul_workspace_bytes(T, groups, m, n);
+  if ((st = workspace_ok(ws, ws_bytes, need)) != BRQ_OK) return st;
+  g.offs = offsets;
+  g.groups = (int)groups;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int tok = prof_begin("mx grouped matmul", s);
+  const hipError_t err = launch_mx_grouped(g, e, s);
+  prof_end(tok, s);
+  return launched(err, "mx grouped matmul");
 }
 
 }  // extern "C"
@@ -277,11 +323,75 @@ brq_status kv_setup(KvArgs& a, const brq_plan* plan, const void* k, int64_t ldk,
   return BRQ_OK;
 }
 
+constexpr int64_t kKpMost = ((int64_t)1 << 31) - 1;
+// A table whose entries a launch of a thread for each can have.
+bool entries_ok(int64_t rows, int64_t width) { return rows <= kKpMost && (width == 0 || rows <= kKpMost / width); }
+// A reservation whose entries have ranks in 32 bits and whose sequences a launch can have.
+bool reserve_ok(int64_t batch, int64_t tokens, int64_t page) {
+  return batch < (int64_t)1 << 24 && tokens <= kKpMost && batch <= kKpMost / kp_per(tokens, page);
+}
+
 // Query heads per workgroup and their number of workgroups (AtArgs::nt, ht).
 void at_shape(int32_t q_heads, int32_t heads, int* nt, int* ht) {
   const int group = q_heads / heads;
   *nt = group > kAtCols ? 2 : 1;
   *ht = (group + kAtCols * *nt - 1) / (kAtCols * *nt);
+}
+
+// Shared checks of the attentions, `tokens` rows a sequence; *done set when
+// there is nothing to do.
+brq_status at_setup(AtArgs& a, const brq_plan* plan, const void* q, int64_t ldq, int32_t qt, const uint8_t* cache,
+                    int64_t pages, const int32_t* table, int64_t ldt, const int32_t* lens, int64_t batch,
+                    int32_t tokens, int32_t q_heads, int32_t heads, int32_t head_dim, int32_t page, float scale,
+                    int32_t window, void* out, int64_t ldo, float* lse, bool* done) {
+  *done = false;
+  std::memset(&a, 0, sizeof a);
+  if (!dtype_ok(qt)) return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad dtype %d", qt);
+  if (batch < 0 || heads < 1 || q_heads < 1 || pages < 0 || ldt < 0 || window < 0)
+    return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad shape or window");
+  if (q_heads % heads)
+    return refuse(BRQ_ERR_INVALID_ARGUMENT, "%d query heads are not a multiple of %d key-value heads", q_heads, heads);
+  if (!std::isfinite(scale)) return refuse(BRQ_ERR_INVALID_ARGUMENT, "scale must be finite");
+  brq_status st = page_ok(head_dim, page);
+  if (st != BRQ_OK) return st;
+  const int64_t row = (int64_t)q_heads * head_dim;
+  if (ldq < row || ldo < row)
+    return refuse(BRQ_ERR_INVALID_ARGUMENT, "leading dimension below q_heads * head_dim");
+  if ((st = transform_of(plan, head_dim, &a.signs, &a.d, &a.rnorm)) != BRQ_OK) return st;
+  if (batch == 0 || tokens == 0) {
+    *done = true;
+    return BRQ_OK;
+  }
+  if (batch > (((int64_t)1 << 24) - 1) / q_heads / tokens)  // up to one workgroup of 256 threads for each
+    return refuse(BRQ_ERR_UNSUPPORTED, "2^24 rows times query heads or more");
+  if (!q || !out || !lens || (ldt > 0 && !table) || (pages > 0 && !cache))
+    return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL data pointer");
+  if (rows_misaligned(q, ldq, qt) || rows_misaligned(out, ldo, qt))
+    return refuse(BRQ_ERR_ALIGNMENT, "query and output rows must be 16-byte aligned");
+  if (misaligned(cache, 16) || misaligned(table, 4) || misaligned(lens, 4) || misaligned(lse, 4))
+    return refuse(BRQ_ERR_ALIGNMENT, "the cache must be 16-byte, table, lens and lse 4-byte aligned");
+  a.q = q;
+  a.ldq = ldq;
+  a.out = out;
+  a.ldo = ldo;
+  a.qt = qt;
+  a.cache = cache;
+  a.pages = pages;
+  a.pg = KvPage{head_dim, page};
+  a.lgP = log2_of(page);
+  a.table = table;
+  a.ldt = ldt;
+  a.lens = lens;
+  // without a page there is no visible token (and none to read where there is no other)
+  a.cap = pages == 0 ? 0 : (int)(ldt < (kAtMaxKeys >> a.lgP) ? ldt << a.lgP : kAtMaxKeys);
+  a.batch = batch;
+  a.q_heads = q_heads;
+  a.heads = heads;
+  a.group = q_heads / heads;
+  a.scale = scale;
+  a.window = window;
+  a.lse = lse;
+  return BRQ_OK;
 }
 
 }  // namespace
@@ -324,6 +434,121 @@ brq_status brq_kv_read(const brq_plan* plan, const uint8_t* cache, const int64_t
   return launched(e, "kv read");
 }
 
+size_t brq_kv_move_workspace_bytes(int64_t tokens, int32_t heads, int32_t head_dim) {
+  if (tokens <= 0 || heads < 1 || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+      tokens > kKpTokens / heads)
+    return 0;
+  return (size_t)(tokens * heads * kp_row_bytes(head_dim) + 15) / 16 * 16;
+}
+
+brq_status brq_kv_move(uint8_t* cache, const int64_t* src, const int64_t* dst, int64_t tokens, int32_t heads,
+                       int32_t head_dim, int32_t page, int64_t pages, void* ws, size_t ws_bytes, void* stream) {
+  clear_error();
+  if (tokens < 0 || heads < 1 || pages < 0) return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad shape");
+  brq_status st = page_ok(head_dim, page);
+  if (st != BRQ_OK) return st;
+  if (tokens == 0 || pages == 0) return BRQ_OK;
+  if (tokens > kKpTokens / heads) return refuse(BRQ_ERR_UNSUPPORTED, "more than 2^27 tokens times heads");
+  if (!cache || !src || !dst) return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL data pointer");
+  if (misaligned(cache, 16) || misaligned(src, 8) || misaligned(dst, 8))
+    return refuse(BRQ_ERR_ALIGNMENT, "the cache must be 16-byte and slots 8-byte aligned");
+  if ((st = workspace_ok(ws, ws_bytes, brq_kv_move_workspace_bytes(tokens, heads, head_dim))) != BRQ_OK) return st;
+  const KpMove a = {src, dst, tokens, heads, KvPage{head_dim, page}, log2_of(page), pages, cache,
+                    static_cast<uint8_t*>(ws)};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int tok = prof_begin("kv move", s);
+  const hipError_t e = launch_kv_move(a, s);
+  prof_end(tok, s);
+  return launched(e, "kv move");
+}
+
+brq_status brq_kv_fork(const int32_t* table, const int32_t* lens, int64_t batch, int64_t width, const int32_t* parents,
+                       int64_t children, int32_t* refs, int64_t pages, int32_t* out_table, int32_t* out_lens,
+                       void* stream) {
+  clear_error();
+  if (batch < 0 || width < 0 || children < 0 || pages < 0) return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad shape");
+  if (children == 0) return BRQ_OK;
+  if (!entries_ok(batch, width) || !entries_ok(children, width) || pages > kKpMost)
+    return refuse(BRQ_ERR_UNSUPPORTED, "2^31 entries or pages or more");
+  if (!parents || !out_lens || (batch > 0 && !lens) || (width > 0 && (!out_table || (batch > 0 && !table))) ||
+      (pages > 0 && !refs))
+    return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL data pointer");
+  if (misaligned(table, 4) || misaligned(lens, 4) || misaligned(parents, 4) || misaligned(refs, 4) ||
+      misaligned(out_table, 4) || misaligned(out_lens, 4))
+    return refuse(BRQ_ERR_ALIGNMENT, "tables, lengths, parents and refs must be 4-byte aligned");
+  const KpFork a = {table, lens, parents, batch, width, children, pages, refs, out_table, out_lens};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int tok = prof_begin("kv fork", s);
+  const hipError_t e = launch_kv_fork(a, s);
+  prof_end(tok, s);
+  return launched(e, "kv fork");
+}
+
+size_t brq_kv_reserve_workspace_bytes(int64_t batch, int64_t tokens, int32_t page, int64_t pages) {
+  if (batch <= 0 || tokens <= 0 || pages < 0 || page_ok(64, page) != BRQ_OK || !reserve_ok(batch, tokens, page)) return 0;
+  return kp_bytes(batch, tokens, page, pages);
+}
+
+brq_status brq_kv_reserve(uint8_t* cache, int32_t* table, const int32_t* lens, int64_t batch, int64_t width,
+                          int32_t* refs, int64_t pages, int64_t tokens, int32_t heads, int32_t head_dim, int32_t page,
+                          int64_t* slots, void* ws, size_t ws_bytes, void* stream) {
+  clear_error();
+  if (batch < 0 || width < 0 || pages < 0 || tokens < 0 || heads < 1)
+    return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad shape");
+  brq_status st = page_ok(head_dim, page);
+  if (st != BRQ_OK) return st;
+  if (batch == 0 || tokens == 0) return BRQ_OK;
+  if (!entries_ok(batch, width) || !reserve_ok(batch, tokens, page) || pages > kKpMost || heads > 65535)
+    return refuse(BRQ_ERR_UNSUPPORTED, "2^31 entries or pages or more, 2^24 sequences or more, or above 65535 heads");
+  if (!lens || !slots || (width > 0 && !table) || (pages > 0 && (!cache || !refs)))
+    return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL data pointer");
+  if (misaligned(cache, 16) || misaligned(slots, 8) || misaligned(table, 4) || misaligned(lens, 4) || misaligned(refs, 4))
+    return refuse(BRQ_ERR_ALIGNMENT, "the cache must be 16-byte, slots 8-byte, table, lens and refs 4-byte aligned");
+  if ((st = workspace_ok(ws, ws_bytes, kp_bytes(batch, tokens, page, pages))) != BRQ_OK) return st;
+  KpReserve a;
+  std::memset(&a, 0, sizeof a);
+  a.cache = cache;
+  a.table = table;
+  a.lens = lens;
+  a.batch = batch;
+  a.width = width;
+  a.refs = refs;
+  a.pages = pages;
+  a.tokens = tokens;
+  a.heads = heads;
+  a.pg = KvPage{head_dim, page};
+  a.lgP = log2_of(page);
+  a.slots = slots;
+  a.per = kp_per(tokens, page);
+  a.copy = static_cast<int4*>(ws);
+  a.item = reinterpret_cast<int32_t*>(a.copy + batch);
+  a.fresh = a.item + batch * a.per;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int tok = prof_begin("kv reserve", s);
+  const hipError_t e = launch_kv_reserve(a, s);
+  prof_end(tok, s);
+  return launched(e, "kv reserve");
+}
+
+brq_status brq_kv_free(int32_t* table, int64_t batch, int64_t width, int32_t* refs, int64_t pages, const int32_t* rows,
+                       int64_t n, void* stream) {
+  clear_error();
+  if (batch < 0 || width < 0 || pages < 0 || n < 0 || (!rows && n > batch))
+    return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad shape");
+  if (batch == 0 || width == 0 || n == 0) return BRQ_OK;
+  if (!entries_ok(batch, width) || !entries_ok(n, width) || pages > kKpMost)
+    return refuse(BRQ_ERR_UNSUPPORTED, "2^31 entries or pages or more");
+  if (!table || (pages > 0 && !refs)) return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL data pointer");
+  if (misaligned(table, 4) || misaligned(refs, 4) || misaligned(rows, 4))
+    return refuse(BRQ_ERR_ALIGNMENT, "table, refs and rows must be 4-byte aligned");
+  const KpFree a = {table, batch, width, pages, n, refs, rows};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int tok = prof_begin("kv free", s);
+  const hipError_t e = launch_kv_free(a, s);
+  prof_end(tok, s);
+  return launched(e, "kv free");
+}
+
 size_t brq_paged_attention_workspace_bytes(int64_t batch, int32_t q_heads, int32_t heads, int32_t head_dim) {
   if (batch <= 0 || heads < 1 || q_heads < heads || q_heads % heads || head_dim < 1) return 0;
   int nt, ht;
@@ -339,54 +564,13 @@ brq_status brq_paged_attention(const brq_plan* plan, const void* q, int64_t ldq,
                                void* stream) {
   clear_error();
   AtArgs a;
-  std::memset(&a, 0, sizeof a);
-  if (!dtype_ok(qt)) return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad dtype %d", qt);
-  if (batch < 0 || heads < 1 || q_heads < 1 || pages < 0 || ldt < 0 || window < 0)
-    return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad shape or window");
-  if (q_heads % heads)
-    return refuse(BRQ_ERR_INVALID_ARGUMENT, "%d query heads are not a multiple of %d key-value heads", q_heads, heads);
-  if (!std::isfinite(scale)) return refuse(BRQ_ERR_INVALID_ARGUMENT, "scale must be finite");
-  brq_status st = page_ok(head_dim, page);
-  if (st != BRQ_OK) return st;
-  const int64_t row = (int64_t)q_heads * head_dim;
-  if (ldq < row || ldo < row)
-    return refuse(BRQ_ERR_INVALID_ARGUMENT, "leading dimension below q_heads * head_dim");
-  if ((st = transform_of(plan, head_dim, &a.signs, &a.d, &a.rnorm)) != BRQ_OK) return st;
-  if (batch == 0) return BRQ_OK;
-  if (batch > (((int64_t)1 << 24) - 1) / q_heads)  // up to one workgroup of 256 threads for each
-    return refuse(BRQ_ERR_UNSUPPORTED, "2^24 sequences times query heads or more");
-  if (!q || !out || !lens || (ldt > 0 && !table) || (pages > 0 && !cache))
-    return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL data pointer");
-  if (rows_misaligned(q, ldq, qt) || rows_misaligned(out, ldo, qt))
-    return refuse(BRQ_ERR_ALIGNMENT, "query and output rows must be 16-byte aligned");
-  if (misaligned(cache, 16) || misaligned(table, 4) || misaligned(lens, 4) || misaligned(lse, 4))
-    return refuse(BRQ_ERR_ALIGNMENT, "the cache must be 16-byte, table, lens and lse 4-byte aligned");
-  const size_t need = brq_paged_attention_workspace_bytes(batch, q_heads, heads, head_dim);
-  if (need && (!ws || ws_bytes < need))
-    return refuse(BRQ_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
-  if (need && misaligned(ws, 16)) return refuse(BRQ_ERR_ALIGNMENT, "the workspace must be 16-byte aligned");
-  a.q = q;
-  a.ldq = ldq;
-  a.out = out;
-  a.ldo = ldo;
-  a.qt = qt;
-  a.cache = cache;
-  a.pages = pages;
-  a.pg = KvPage{head_dim, page};
-  a.lgP = log2_of(page);
-  a.table = table;
-  a.ldt = ldt;
-  a.lens = lens;
-  // without a page there is no visible token (and none to read where there is no other)
-  a.cap = pages == 0 ? 0 : (int)(ldt < (kAtMaxKeys >> a.lgP) ? ldt << a.lgP : kAtMaxKeys);
-  a.batch = batch;
-  a.q_heads = q_heads;
-  a.heads = heads;
-  a.group = q_heads / heads;
+  bool done;
+  brq_status st = at_setup(a, plan, q, ldq, qt, cache, pages, table, ldt, lens, batch, 1, q_heads, heads, head_dim, page,
+                           scale, window, out, ldo, lse, &done);
+  if (st != BRQ_OK || done) return st;
+  if ((st = workspace_ok(ws, ws_bytes, brq_paged_attention_workspace_bytes(batch, q_heads, heads, head_dim))) != BRQ_OK)
+    return st;
   at_shape(q_heads, heads, &a.nt, &a.ht);
-  a.scale = scale;
-  a.window = window;
-  a.lse = lse;
   a.wgs = batch <= kAtMaxBatch ? at_workgroups(head_dim, a.nt) : 0;
   a.part = static_cast<float*>(ws);
   a.who = a.wgs ? reinterpret_cast<int2*>(static_cast<char*>(ws) + at_part_bytes(head_dim, a.nt)) : nullptr;
@@ -395,6 +579,51 @@ brq_status brq_paged_attention(const brq_plan* plan, const void* q, int64_t ldq,
   const hipError_t e = launch_paged_attention(a, s);
   prof_end(tok, s);
   return launched(e, "paged attention");
+}
+
+size_t brq_tree_attention_workspace_bytes(int64_t batch, int32_t tokens, int32_t q_heads, int32_t heads,
+                                          int32_t head_dim) {
+  if (batch <= 0 || batch > kAtMaxBatch || tokens < 1 || tokens > kTrTokens || heads < 1 || q_heads < heads ||
+      q_heads % heads || (head_dim != 64 && head_dim != 128 && head_dim != 256))
+    return 0;
+  const int64_t rows = tr_rows(tokens, q_heads, heads);
+  const int nt = tr_nt(rows, head_dim);
+  return tr_part_bytes(head_dim, nt) + (size_t)(batch * heads * ((rows + 16 * nt - 1) / (16 * nt))) * sizeof(int2);
+}
+
+brq_status brq_tree_attention(const brq_plan* plan, const void* q, int64_t ldq, int32_t qt, const uint8_t* cache,
+                              int64_t pages, const int32_t* table, int64_t ldt, const int32_t* lens,
+                              const int64_t* mask, int64_t batch, int32_t tokens, int32_t q_heads, int32_t heads,
+                              int32_t head_dim, int32_t page, float scale, int32_t window, void* out, int64_t ldo,
+                              float* lse, void* ws, size_t ws_bytes, void* stream) {
+  clear_error();
+  TrArgs t;
+  bool done;
+  if (tokens < 0) return refuse(BRQ_ERR_INVALID_ARGUMENT, "bad shape");
+  if (tokens > kTrTokens)
+    return refuse(BRQ_ERR_UNSUPPORTED, "%d drafted tokens, a mask has %d bits", tokens, kTrTokens);
+  brq_status st = at_setup(t.at, plan, q, ldq, qt, cache, pages, table, ldt, lens, batch, tokens, q_heads, heads,
+                           head_dim, page, scale, window, out, ldo, lse, &done);
+  if (st != BRQ_OK || done) return st;
+  if (!mask) return refuse(BRQ_ERR_INVALID_ARGUMENT, "NULL data pointer");
+  if (misaligned(mask, 8)) return refuse(BRQ_ERR_ALIGNMENT, "the mask must be 8-byte aligned");
+  if ((st = workspace_ok(ws, ws_bytes,
+                         brq_tree_attention_workspace_bytes(batch, tokens, q_heads, heads, head_dim))) != BRQ_OK)
+    return st;
+  t.mask = mask;
+  t.tokens = tokens;
+  const int64_t rows = tr_rows(tokens, q_heads, heads);
+  t.at.nt = tr_nt(rows, head_dim);
+  t.at.ht = (int)((rows + 16 * t.at.nt - 1) / (16 * t.at.nt));
+  t.at.wgs = batch <= kAtMaxBatch ? tr_workgroups(head_dim, t.at.nt) : 0;
+  t.at.part = static_cast<float*>(ws);
+  t.at.who =
+      t.at.wgs ? reinterpret_cast<int2*>(static_cast<char*>(ws) + tr_part_bytes(head_dim, t.at.nt)) : nullptr;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int tok = prof_begin("tree attention", s);
+  const hipError_t e = launch_tree_attention(t, s);
+  prof_end(tok, s);
+  return launched(e, "tree attention");
 }
 
 }  // extern "C"

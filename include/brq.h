@@ -457,6 +457,27 @@ brq_status brq_mx_linear(const uint8_t* a_codes, const uint8_t* a_scales, const 
                          size_t ws_bytes, void* stream);
 
 /*
+ * Products grouped by expert: for group g the rows t with offsets[g] <= t <
+ * offsets[g + 1] times weight g,
+ *   y[t][o] = act(sum_k a[t][k] b[g][o][k] + bias[g][o]) * mul[t][o] + residual[t][o].
+ *   b_codes [groups][m][n/2], b_scales [groups][m][n/32]; bias: device [groups][m].
+ *   offsets: device int32 [groups + 1], not decreasing, read at each call (a
+ *     captured call can be replayed with other groups); what lies outside [0, T]
+ *     counts as the nearer end.  A group may be empty; rows of no group are left as
+ *     they were.  Offsets that decrease give some rows to several groups: which of
+ *     them a row's outputs come from is not said.
+ *   ws: device workspace of brq_mx_grouped_matmul_workspace_bytes(...) bytes
+ *     (16-byte aligned; may be NULL if that is 0).
+ * Everything else as brq_mx_linear (ep NULL: the sums alone).  Errors: also
+ * UNSUPPORTED (more than 2^20 groups; T / 16 + groups times m / 16 above 2^26). */
+size_t brq_mx_grouped_matmul_workspace_bytes(int64_t T, int64_t groups, int64_t m, int64_t n);
+brq_status brq_mx_grouped_matmul(const uint8_t* a_codes, const uint8_t* a_scales,
+                                 const uint8_t* b_codes, const uint8_t* b_scales,
+                                 const int32_t* offsets, int64_t T, int64_t groups, int64_t m,
+                                 int64_t n, const brq_mx_epilogue* ep, void* y, int32_t yt,
+                                 int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * A paged key-value cache in MX4.  The cache is a device array of `pages` pages
  * of `page` tokens; a page holds, for each of `heads` key-value heads, the keys
  * and values of its tokens in brq_kv_page_bytes(head_dim, page) bytes:
@@ -492,6 +513,63 @@ brq_status brq_kv_read(const brq_plan* plan, const uint8_t* cache, const int64_t
                        int64_t tokens, int32_t heads, int32_t head_dim, int32_t page,
                        int64_t pages, void* k, int64_t ldk, void* v, int64_t ldv, int32_t ot,
                        void* stream);
+
+/*
+ * Tokens moved between slots of the cache, bits unchanged, all heads: what slot
+ * src[i] held when the call began is in slot dst[i] when it ends (everything is
+ * read before anything is written, so lists may overlap, as when accepted drafts
+ * move to the front).  A pair with a slot outside the cache is skipped
+ * (padding).  Two pairs must not share a dst.
+ *   src, dst: device int64 [tokens]; ws: device workspace of
+ *   brq_kv_move_workspace_bytes(...) bytes (16-byte aligned).
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (head_dim, page; more than 2^27 tokens
+ * times heads), ALIGNMENT, WORKSPACE, HIP.  tokens == 0 is a no-op. */
+size_t brq_kv_move_workspace_bytes(int64_t tokens, int32_t heads, int32_t head_dim);
+brq_status brq_kv_move(uint8_t* cache, const int64_t* src, const int64_t* dst, int64_t tokens,
+                       int32_t heads, int32_t head_dim, int32_t page, int64_t pages, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/*
+ * Pages shared by several sequences.  refs: device int32 [pages], for each page
+ * the number of table rows that hold it; a page with none is free.  table:
+ * device int32 [batch][width]; entries outside [0, pages) hold no page.  All three calls
+ * read and write device memory only, so a loop of them can be captured.
+ *
+ * brq_kv_fork makes `children` rows of a table: out_table[f] gets the pages of row
+ * parents[f] (-1 where that holds none), each then held once more, and
+ * out_lens[f] its length; a parent outside [0, batch): no page, length 0.
+ *   out_table: device int32 [children][width], out_lens: device int32 [children],
+ *   neither of them overlapping what is read.
+ *
+ * brq_kv_reserve makes room for the next `tokens` tokens of every sequence, at
+ * positions lens[b] .. lens[b] + tokens - 1: each entry of the table that these
+ * lie in gets a page that no other row holds, unless it has one (a page with refs
+ * 1).  In the order of rows and positions they get the lowest free pages.  If the
+ * entry held a shared page, that is held once less, and where it holds tokens
+ * before position lens[b] these are copied (whole sixteens of them; the rest of
+ * the new page stays as it was).  What is free, shared or not is decided by refs
+ * as the call finds them.
+ *   slots: device int64 [batch][tokens], the slot of every new token as
+ *     brq_kv_append takes it; -1 where the table ends or no page was left (that
+ *     entry stays as it was), and for a row with a negative length (padding).
+ *   ws: device workspace of brq_kv_reserve_workspace_bytes(...) bytes (16-byte aligned).
+ *
+ * brq_kv_free gives back the pages of rows rows[0 .. n) of the table (device
+ * int32 [n]; NULL: of the first n rows): each is held once less, its entry becomes
+ * -1.  A row outside [0, batch) is skipped; one that is named twice is given back once.
+ * Errors: INVALID_ARGUMENT (shapes, NULLs), UNSUPPORTED (head_dim, page; 2^31
+ * entries or pages or more), ALIGNMENT, WORKSPACE, HIP.  Nothing to do (no
+ * children, tokens, rows or width): a no-op. */
+brq_status brq_kv_fork(const int32_t* table, const int32_t* lens, int64_t batch, int64_t width,
+                       const int32_t* parents, int64_t children, int32_t* refs, int64_t pages,
+                       int32_t* out_table, int32_t* out_lens, void* stream);
+size_t brq_kv_reserve_workspace_bytes(int64_t batch, int64_t tokens, int32_t page, int64_t pages);
+brq_status brq_kv_reserve(uint8_t* cache, int32_t* table, const int32_t* lens, int64_t batch,
+                          int64_t width, int32_t* refs, int64_t pages, int64_t tokens,
+                          int32_t heads, int32_t head_dim, int32_t page, int64_t* slots, void* ws,
+                          size_t ws_bytes, void* stream);
+brq_status brq_kv_free(int32_t* table, int64_t batch, int64_t width, int32_t* refs, int64_t pages,
+                       const int32_t* rows, int64_t n, void* stream);
 
 /*
  * Attention of one new token per sequence over the paged cache: for sequence b
@@ -530,6 +608,33 @@ brq_status brq_paged_attention(const brq_plan* plan, const void* q, int64_t ldq,
                                int32_t heads, int32_t head_dim, int32_t page, float scale,
                                int32_t window, void* out, int64_t ldo, float* lse, void* ws,
                                size_t ws_bytes, void* stream);
+
+/*
+ * Attention of a tree of drafted tokens per sequence over the paged cache: for
+ * sequence b with lens[b] tokens of context, its `tokens` drafted ones are cached
+ * behind them, draft j at position lens[b] + j.  Row i of the sequence sees the
+ * context and the drafts j whose bit is set in mask[b][i] (its ancestors and, as
+ * a rule, itself): over these keys, in the order of positions, or over the last
+ * `window` of them if window > 0, what brq_paged_attention computes.  One draft
+ * with mask 1 is a sequence's next token there.  A row whose mask is 0 is padding
+ * and sees nothing, as does every row of a sequence with a negative length; of
+ * drafts whose bit no row has set, nothing is seen.
+ *   q, out: device [batch * tokens][ldq], [batch * tokens][ldo] of type qt, rows of a
+ *           sequence one after the other, head i at element i * head_dim of its row;
+ *           16-byte aligned rows.  out may be q.
+ *   mask: device int64 [batch][tokens]; tokens at most 64.
+ *   lse: device float32 [batch][tokens][q_heads] or NULL.
+ *   ws: device workspace of brq_tree_attention_workspace_bytes(...) bytes.
+ * Everything else, and the errors, as brq_paged_attention; also UNSUPPORTED
+ * (tokens above 64; 2^24 rows times heads or more). */
+size_t brq_tree_attention_workspace_bytes(int64_t batch, int32_t tokens, int32_t q_heads,
+                                          int32_t heads, int32_t head_dim);
+brq_status brq_tree_attention(const brq_plan* plan, const void* q, int64_t ldq, int32_t qt,
+                              const uint8_t* cache, int64_t pages, const int32_t* table,
+                              int64_t ldt, const int32_t* lens, const int64_t* mask, int64_t batch,
+                              int32_t tokens, int32_t q_heads, int32_t heads, int32_t head_dim,
+                              int32_t page, float scale, int32_t window, void* out, int64_t ldo,
+                              float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Host helper: the 2^bits Lloyd-Max centroids for N(0,1), ascending, rounded

@@ -191,3 +191,111 @@ def epilogue(s: np.ndarray, bias=None, act=None, mul=None, residual=None):
         y = y + residual
         err = err + half * np.abs(y)
     return y, err
+
+
+# ------------------------------------------------------------------ trees of drafts; tokens and pages moved and shared
+
+def tree_attention(q, cache: Cache, table, lens, mask, scale, window=0, M=None):
+    """attention() for q [batch, drafts, q_heads, D]: row i of sequence b sees the
+    positions below lens[b] and lens[b] + j for the bits j of mask[b, i], of these the
+    last `window`; nothing if mask[b, i] is 0 or lens[b] negative."""
+    B, N, hq, D = q.shape
+    pages, heads, P = cache.shape
+    K, V = cache.keys_values()
+    out, lse = np.zeros(q.shape), np.full((B, N, hq), -np.inf)
+    spread, terms = np.zeros(q.shape), np.zeros((B, N, hq))
+    for b in range(B):
+        n = int(lens[b])
+        for i in range(N):
+            m = int(mask[b, i]) & (2 ** 64 - 1)
+            if n < 0 or m == 0:
+                continue
+            at = np.concatenate((np.arange(min(n, table.shape[1] * P)), [n + j for j in range(64) if m >> j & 1])).astype(int)
+            if window:
+                first = n + bin(m).count("1") - window  # how many positions are passed over
+                drafts = at[at >= n]
+                at = np.concatenate((at[(at < n) & (at >= first)], drafts[max(0, len(drafts) - window):]))
+            at = at[at < table.shape[1] * P]
+            page = table[b, at // P]
+            at, page = at[(page >= 0) & (page < pages)], page[(page >= 0) & (page < pages)]
+            if not len(at):
+                continue
+            g = hq // heads
+            x = q[b, i] if M is None else q[b, i] @ M.T
+            for h in range(heads):
+                k, v, xh = K[page, h, at % P], V[page, h, at % P], x[h * g:(h + 1) * g]
+                s = scale * (xh @ k.T)
+                top = s.max(1, keepdims=True)
+                p = np.exp(s - top)
+                total = p.sum(1, keepdims=True)
+                o, w = p @ v / total, p @ np.abs(v) / total
+                r = slice(h * g, (h + 1) * g)
+                out[b, i, r] = o if M is None else o @ M
+                spread[b, i, r] = w if M is None else w @ np.abs(M)
+                lse[b, i, r] = (top + np.log(total))[:, 0]
+                terms[b, i, r] = abs(scale) * (np.abs(xh) @ np.abs(k).T).max(1)
+    return out, lse, (spread, terms)
+
+
+def move(cache: Cache, src, dst):
+    """Tokens of slots src to slots dst, all read first; pairs outside the cache skipped."""
+    pages, _, P = cache.shape
+    pairs = [(int(a), int(b)) for a, b in zip(src, dst) if 0 <= a < pages * P and 0 <= b < pages * P]
+    for x in (cache.kc, cache.ks, cache.vc, cache.vs):
+        old = x.copy()
+        for a, b in pairs:
+            x[b // P, :, b % P] = old[a // P, :, a % P]
+
+
+def fork(table, lens, parents, refs):
+    """(table, lens) of the children; refs updated."""
+    out, n = np.full((len(parents), table.shape[1]), -1, np.int32), np.zeros(len(parents), np.int32)
+    for f, p in enumerate(parents):
+        if 0 <= p < len(table):
+            n[f] = lens[p]
+            for c, page in enumerate(table[p]):
+                if 0 <= page < len(refs):
+                    out[f, c] = page
+                    refs[page] += 1
+    return out, n
+
+
+def reserve(cache: Cache, table, lens, refs, tokens):
+    """Slots [batch, tokens] of the next tokens; cache, table and refs updated."""
+    pages, _, P = cache.shape
+    before = refs.copy()
+    free = [p for p in range(pages) if before[p] <= 0]
+    slots = np.full((len(lens), tokens), -1, np.int64)
+    src, dst = [], []
+    for b, n in enumerate(int(x) for x in lens):
+        if n < 0:
+            continue
+        for c in range(n // P, min(table.shape[1], (n + tokens - 1) // P + 1)):
+            old = int(table[b, c])
+            valid = 0 <= old < pages
+            page = old
+            if not (valid and before[old] == 1):
+                if not free:
+                    continue
+                page = free.pop(0)
+                table[b, c] = page
+                refs[page] = 1
+                if valid:
+                    refs[old] -= 1
+                    if c == n // P:
+                        used = (n % P + 15) // 16 * 16
+                        src += [old * P + t for t in range(used)]
+                        dst += [page * P + t for t in range(used)]
+            for t in range(max(n, c * P), min(n + tokens, (c + 1) * P)):
+                slots[b, t - n] = page * P + t % P
+    move(cache, src, dst)
+    return slots
+
+
+def free(table, refs, rows):
+    for r in rows:
+        if 0 <= r < len(table):
+            for c, page in enumerate(table[r]):
+                if 0 <= page < len(refs):
+                    refs[page] -= 1
+                table[r, c] = -1

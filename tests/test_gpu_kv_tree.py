@@ -1,0 +1,345 @@
+"""GPU parity of the attention of a tree of drafted tokens over the paged 4-bit
+cache, against the formula in 64 bits (oracle/mx.py).
+
+The bound counts as test_gpu_kv.py does: a score is off by e = (2^-16 + 2 D
+2^-23) times its sum of |q_i k_i| at most, a probability by a factor of exp(2 e),
+by 2^-17 of itself where it enters in 16 bits and by a few 2^-22 of its
+exponential; sums run over n / 32 + 96 additions of 2^-23; the output adds its
+rounding."""
+
+import numpy as np
+import pytest
+
+from gpu_util import announce, from_dev, to_dev, torch_dtype
+from oracle import mx as X
+from test_gpu_kv import build, rht, tokens
+
+pytestmark = pytest.mark.gpu
+
+HALF_ULP = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+
+
+def tree(rng, N, there=None):
+    """Ancestor bits of N drafts: each follows an earlier one or the context; those from `there` on are padding."""
+    masks = []
+    for j in range(N):
+        p = int(rng.integers(-1, j)) if j else -1
+        masks.append((masks[p] if p >= 0 else 0) | 1 << j)
+    return [m if there is None or j < there else 0 for j, m in enumerate(masks)]
+
+
+def to_mask(rows):
+    return np.array(rows, dtype=np.uint64).view(np.int64)
+
+
+def check(got, lse, want, wlse, slack, lens, D, dtype):
+    spread, terms = slack
+    e = (2.0 ** -16 + 2 * D * 2.0 ** -23) * terms  # [B, N, hq]
+    rel = 2 * e + 2.0 ** -16 + (np.maximum(0, np.asarray(lens, dtype=np.int64)) / 32 + 98)[:, None, None] * 2.0 ** -23
+    bound = 2 * rel[..., None] * spread + HALF_ULP[dtype] * np.abs(want) + 2.0 ** -25
+    over = ~(np.abs(got - want) <= bound)
+    assert not over.any(), (f"{int(over.sum())} outputs beyond the bound, first {np.argwhere(over)[:3].tolist()}, "
+                            f"largest error {np.abs(got - want).max():.3g}")
+    fine = np.isfinite(wlse)
+    assert np.array_equal(np.isneginf(lse), np.isneginf(wlse))
+    assert (np.abs(lse[fine] - wlse[fine]) <= (2 * rel + 2.0 ** -22 * (1 + np.abs(np.where(fine, wlse, 0))))[fine]).all()
+
+
+def attend(ctx, N, hq, H, D, P, rot, dtype, window=0, scale=None, hot=False, seed=0, mask=None, edit=None):
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce(f"tree ctx={list(ctx)[:6]} N={N} hq={hq} H={H} D={D} P={P} rot={rot} {dtype} window={window}")
+    rng = np.random.default_rng(seed + D + P + hq + N)
+    B = len(ctx)
+    cache, ref, table, plan, M, _ = build(rng, [c + N if c >= 0 else 0 for c in ctx], H, D, P, rot, hot=hot)
+    if mask is None:
+        mask = [tree(rng, N, int(rng.integers(1, N + 1))) for _ in range(B)]
+    mask = to_mask(mask)
+    lens = np.asarray(ctx, dtype=np.int32)
+    if edit:
+        cache, ref, table = edit(cache, ref, table)
+    q, qh = tokens(rng, B * N, hq, D, dtype, 32)
+    q, qh = q.unflatten(0, (B, N)), qh.reshape(B, N, hq, D)
+    lse = torch.full((B, N, hq), 7.0, device="cuda")
+    args = (plan, q, cache, to_dev(table, "i32"), to_dev(lens, "i32"), to_dev(mask, "i64"), P)
+    out = brq.tree_attention(*args, scale=scale, window=window, lse=lse)
+    again = brq.tree_attention(*args, scale=scale, window=window)
+    bits = torch.int16 if dtype != "f32" else torch.int32
+    assert torch.equal(out.view(bits), again.view(bits)), "a second call differs"
+    want, wlse, slack = X.tree_attention(qh.astype(np.float64), ref, table, lens, mask,
+                                         D ** -0.5 if scale is None else scale, window, M)
+    check(from_dev(out), from_dev(lse), want, wlse, slack, lens, D, dtype)
+    return out
+
+
+# context lengths around the 16 and 32 keys of a step, the 128 of a workgroup, a page
+EDGES = [0, 1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 257, 500]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("P,rot,N", [(16, True, 5), (64, False, 33), (32, True, 64)])
+def test_context_lengths(D, P, rot, N):
+    attend(EDGES, N, 4, 2, D, P, rot, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N,hq,H", [(1, 1, 1), (1, 16, 1), (2, 8, 8), (3, 9, 1), (7, 32, 8), (11, 5, 1), (16, 1, 1),
+                                    (17, 4, 2), (64, 1, 1), (64, 8, 1), (9, 33, 1)])
+def test_rows_of_every_number(N, hq, H, dtype):
+    attend([77, 0, 300, 1], N, hq, H, 128, 32, True, dtype)
+
+
+@pytest.mark.parametrize("D,N,hq", [(64, 13, 12), (256, 13, 12), (256, 2, 5), (64, 1, 3)])
+def test_rows_of_other_dimensions(D, N, hq):
+    attend([130, 3, 45], N, hq, 1, D, 16, True, "bf16")
+
+
+@pytest.mark.parametrize("window", [1, 2, 5, 16, 31, 40, 100, 1000])
+def test_windows(window):
+    attend(EDGES, 11, 6, 2, 128, 16, False, "f32", window=window)
+
+
+def test_masks_of_every_kind():
+    """No bit, one, all, the last only, bits ahead of the row, a row that does not see itself."""
+    N = 64
+    rows = [0, 1, 2 ** 64 - 1, 1 << 63, 1 << 31, 1 << 32, 0x5555555555555555, 0] + [0] * 55 + [2 ** 63]
+    attend([40, 0, 129, 33], N, 2, 1, 128, 16, False, "f32", mask=[rows, rows[::-1], [0] * N, rows])
+    attend([40, 0, 129, 33], N, 2, 1, 64, 16, True, "f32", mask=[rows, rows[::-1], [0] * N, rows], window=20)
+
+
+def test_long_and_ragged():
+    attend([20011, 1, 4099, 0, 777], 6, 8, 2, 128, 64, True, "bf16")
+
+
+def test_a_long_context_is_split():
+    attend([33333], 9, 4, 1, 128, 128, False, "f32")
+    attend([9001], 40, 8, 1, 256, 128, True, "f16")
+
+
+def test_more_sequences_than_are_dealt_out():
+    """Above 4096 sequences each unit has a workgroup of its own."""
+    rng = np.random.default_rng(1)
+    ctx = rng.integers(-1, 40, 4100)
+    ctx[77] = 700
+    attend(ctx, 2, 2, 1, 64, 16, True, "f32")
+
+
+def test_many_sequences():
+    rng = np.random.default_rng(0)
+    attend(rng.integers(-2, 120, 300), 3, 8, 4, 64, 16, True, "f16")
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
+def test_scales_and_peaked_softmax(scale):
+    attend([400, 33], 5, 8, 2, 128, 64, True, "f32", scale=scale, hot=True)
+
+
+def test_pages_outside_the_cache_are_invisible():
+    def edit(cache, ref, table):
+        t = table.copy()
+        t[0, 1], t[1, 0], t[1, 1], t[2, 0] = -1, cache.shape[0], -5, 2 ** 30
+        return cache, ref, t
+    out = attend([90, 40, 20], 6, 4, 2, 128, 32, True, "f32", edit=edit, mask=[[1, 3, 7, 15, 31, 63]] * 3)
+    assert not out[2].any()
+
+
+def test_a_chain_is_what_single_tokens_give():
+    """Row i of a chain sees what the attention of one token sees of i + 1 drafts."""
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce("tree chain")
+    rng = np.random.default_rng(3)
+    N, D, P, H = 6, 128, 32, 2
+    for ctx, window in (([100, 3, 700], 0), ([100, 3, 700], 50)):
+        cache, _, table, plan, _, _ = build(rng, [c + N for c in ctx], H, D, P, True)
+        q = torch.randn((3, N, 8, D), device="cuda")
+        t, lens = to_dev(table, "i32"), torch.tensor(ctx, dtype=torch.int32, device="cuda")
+        mask = to_dev(to_mask([[2 ** (i + 1) - 1 for i in range(N)]] * 3), "i64")
+        out = brq.tree_attention(plan, q, cache, t, lens, mask, P, window=window)
+        for i in range(N):
+            one = brq.paged_attention(plan, q[:, i].contiguous(), cache, t, lens + i + 1, P, window=window)
+            # both are within a few 2^-21 of the formula's in the norm
+            assert (out[:, i] - one).norm() <= 2.0 ** -17 * one.norm()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_what_is_not_finite_reaches_only_rows_that_see_it(D, dtype):
+    """A draft whose key or value is NaN, whose value is too large for the
+    format's conversion, or infinite: rows that see it show it, in its block
+    alone, the others do not change by a bit."""
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce(f"tree not finite D={D} {dtype}")
+    rng = np.random.default_rng(D)
+    P, H, N, ctx = 16, 2, 9, [50, 7]
+    cache, ref, table, _, _, slots = build(rng, [c + N for c in ctx], H, D, P, False)
+    rows = [tree(rng, N)] * 2
+    sees = np.array([[bool(m >> 4 & 1) for m in r] for r in rows])
+    assert sees[0].any() and not sees[0].all()
+    q = torch.randn((2, N, 4, D), device="cuda").to(torch_dtype(dtype))
+    t, lens, mask = to_dev(table, "i32"), torch.tensor(ctx, dtype=torch.int32, device="cuda"), to_dev(to_mask(rows), "i64")
+    run = lambda raw, **kw: brq.tree_attention(None, q, raw, t, lens, mask, P, **kw)  # noqa: E731
+    before = run(cache)
+    assert torch.isfinite(before).all()
+    s = int(slots[ctx[0] + 4])  # draft 4 of sequence 0, head 1, block 1
+    for part, byte in (("k", 255), ("v", 255), ("v", 254), ("v", 253)):
+        c = X.Cache.from_bytes(cache.cpu().numpy(), D, P)
+        (c.ks if part == "k" else c.vs)[s // P, 1, s % P, 1] = byte
+        if part == "v":
+            c.vc[s // P, 1, s % P, 16:32] = 0x73  # 3/2 and 6 in turn
+        out = run(to_dev(c.to_bytes(), "u8"))
+        assert torch.equal(out[1], before[1]) and torch.equal(out[0, :, :2], before[0, :, :2])
+        blind = torch.from_numpy(~sees[0]).cuda()
+        assert torch.equal(out[0, blind], before[0, blind])
+        mine = out[0, ~blind, 2:].float()
+        if part == "k":
+            assert torch.isnan(mine).all()
+        elif byte == 255:
+            assert torch.isnan(mine[..., 32:64]).all()
+            assert not torch.isnan(mine[..., :32]).any() and not torch.isnan(mine[..., 64:]).any()
+        else:  # 6 times 2^126 or 2^127 is beyond float32, 3/2 times is not
+            assert not torch.isnan(mine).any()
+            big = mine[..., 32:64].abs()
+            assert (big > 1e30).all() and torch.isfinite(mine[..., :32]).all() and torch.isfinite(mine[..., 64:]).all()
+    # a NaN query is its own row's
+    q[0, 2, 1, 5] = float("nan")
+    out = run(cache)
+    nan = torch.isnan(out)
+    assert nan[0, 2, 1].all() and nan.sum() == D
+
+
+def test_rows_of_padding_and_negative_lengths():
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce("tree padding")
+    rng = np.random.default_rng(6)
+    D, P, N = 64, 16, 4
+    cache, ref, table, plan, M, _ = build(rng, [32 + N, 32 + N], 1, D, P, True)
+    q = torch.randn((2, N, 2, D), device="cuda")
+    q[:, 2:] = float("nan")  # what padding holds does not matter
+    t = to_dev(np.ascontiguousarray(table[:, :3]), "i32")
+    mask = to_dev(to_mask([[1, 3, 0, 0]] * 2), "i64")
+    lse = torch.zeros((2, N, 2), device="cuda")
+    f = lambda lens, **kw: brq.tree_attention(plan, q, cache, t, torch.tensor(lens, dtype=torch.int32, device="cuda"),  # noqa: E731
+                                              mask, P, **kw)
+    full = f([32, 32], lse=lse)
+    assert torch.isfinite(full).all() and not full[:, 2:].any() and full[:, :2].any()
+    assert torch.isneginf(lse[:, 2:]).all() and torch.isfinite(lse[:, :2]).all()
+    neg = f([-3, 32], lse=lse)
+    assert not neg[0].any() and torch.isneginf(lse[0]).all() and torch.equal(neg[1], full[1])
+    # a length beyond the table: what it holds is context, the drafts lie beyond it
+    q = torch.randn((2, N, 2, D), device="cuda")
+    rows = to_mask([[1, 3, 0, 0]] * 2)
+    for width, n in ((3, 48), (2, 32)):  # of 48 tokens the last 12 were never written: NaN
+        t = to_dev(np.ascontiguousarray(table[:, :width]), "i32")
+        far = from_dev(f([2 ** 31 - 1, n]))
+        want, _, _ = X.tree_attention(from_dev(q), ref, table[:, :width], [n, n], rows, D ** -0.5, 0, M)
+        assert np.allclose(far, want, rtol=0, atol=1e-4, equal_nan=True) and np.isnan(want).any() == (n == 48)
+    assert not f([2 ** 31 - 1, 2 ** 30], window=5).any()  # all that the window holds lies beyond the table
+
+
+def test_other_layouts_of_queries_and_outputs():
+    """Heads inside a wider projection, a single sequence or draft of any stride, the output in the queries' place."""
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce("tree layouts")
+    rng = np.random.default_rng(7)
+    for B, N, n in ((1, 5, 3000), (3, 1, 40), (60, 8, 40)):
+        cache, _, table, plan, _, _ = build(rng, [n + N] * B, 4, 128, 32, True)
+        wide = torch.randn((B, N, 12, 128), device="cuda").to(torch.bfloat16)
+        t, lens = to_dev(table, "i32"), torch.full((B,), n, dtype=torch.int32, device="cuda")
+        mask = to_dev(to_mask([tree(rng, N) for _ in range(B)]), "i64")
+        q = wide[:, :, :8]
+        want = brq.tree_attention(plan, q.contiguous(), cache, t, lens, mask, 32)
+        assert torch.equal(brq.tree_attention(plan, q, cache, t, lens, mask, 32), want)
+        before = wide[:, :, 8:].clone()
+        brq.tree_attention(plan, q, cache, t, lens, mask, 32, out=q)
+        assert torch.equal(q, want) and torch.equal(wide[:, :, 8:], before)
+
+
+@pytest.mark.parametrize("D,hq,rot", [(64, 8, True), (128, 8, True), (128, 40, False), (256, 3, True)])
+def test_float32_keeps_float32(D, hq, rot):
+    """As for single tokens: 2^-18 of the norm leaves a factor of four; 16 bits anywhere would be at 2^-17."""
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce(f"tree float32 D={D} hq={hq} rot={rot}")
+    rng = np.random.default_rng(D + hq)
+    ctx, N = [150, 700], 7
+    cache, ref, table, plan, M, _ = build(rng, [c + N for c in ctx], 1, D, 64, rot)
+    rows = to_mask([tree(rng, N)] * 2)
+    q = torch.from_numpy(rng.standard_normal((2, N, hq, D)).astype(np.float32)).cuda()
+    out = brq.tree_attention(plan, q, cache, to_dev(table, "i32"), torch.tensor(ctx, dtype=torch.int32).cuda(),
+                             to_dev(rows, "i64"), 64)
+    want, _, _ = X.tree_attention(q.cpu().numpy().astype(np.float64), ref, table, ctx, rows, D ** -0.5, 0, M)
+    assert np.linalg.norm(from_dev(out) - want) < 2.0 ** -18 * np.linalg.norm(want)
+
+
+def test_tree_without_drafts_sequences_or_pages():
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce("tree of nothing")
+    cache = brq.kv_cache(0, 2, 128, 32)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    i64 = lambda *s: torch.ones(s, dtype=torch.int64, device="cuda")  # noqa: E731
+    q = torch.randn((3, 4, 4, 128), device="cuda")
+    lse = torch.zeros((3, 4, 4), device="cuda")
+    out = brq.tree_attention(None, q, cache, i32(3, 2), i32(3) + 40, i64(3, 4), 32, lse=lse)
+    assert not out.any() and torch.isneginf(lse).all()
+    assert brq.tree_attention(None, q[:0], cache, i32(0, 2), i32(0), i64(0, 4), 32).shape == (0, 4, 4, 128)
+    assert brq.tree_attention(None, q[:, :0], cache, i32(3, 2), i32(3), i64(3, 0), 32).shape == (3, 0, 4, 128)
+    out = brq.tree_attention(None, q, brq.kv_cache(2, 2, 128, 32), i32(3, 0), i32(3) + 40, i64(3, 4), 32)
+    assert not out.any()
+
+
+def test_a_captured_tree_follows_growing_sequences():
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce("tree graph")
+    rng = np.random.default_rng(9)
+    H, D, P, B, N = 2, 128, 16, 3, 5
+    cache, _, table, plan, _, _ = build(rng, [150] * B, H, D, P, True)
+    t = to_dev(table, "i32")
+    lens, mask = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros((B, N), dtype=torch.int64, device="cuda")
+    q = torch.randn((B, N, 8, D), device="cuda")
+    out, ws = torch.empty_like(q), brq.tree_attention_workspace(B, N, 8, H, D)
+    step = lambda: brq.tree_attention(plan, q, cache, t, lens, mask, P, out=out, ws=ws)  # noqa: E731
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        step()
+    for i in range(6):
+        lens.copy_(torch.tensor(rng.integers(-1, 146, B), dtype=torch.int32))
+        mask.copy_(to_dev(to_mask([tree(rng, N, int(rng.integers(0, N + 1))) for _ in range(B)]), "i64"))
+        q.normal_()
+        ws.fill_(255)
+        want = brq.tree_attention(plan, q, cache, t, lens, mask, P)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), f"replay {i} differs"
+
+
+def test_tree_refusals():
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce("tree refusals")
+    z = lambda *s, t=torch.float32: torch.zeros(s, dtype=t, device="cuda")  # noqa: E731
+    full = dict(plan=None, q=z(2, 3, 4, 64), cache=brq.kv_cache(4, 2, 64, 16), table=z(2, 2, t=torch.int32),
+                lens=z(2, t=torch.int32), mask=z(2, 3, t=torch.int64), page=16)
+    brq.tree_attention(**full)
+    for bad in (dict(q=z(6, 4, 64)), dict(mask=z(2, 4, t=torch.int64)), dict(mask=z(2, 3, t=torch.int32)),
+                dict(lens=z(3, t=torch.int32)), dict(table=z(3, 2, t=torch.int32)), dict(page=32),
+                dict(out=z(2, 3, 4, 64).half()), dict(out=z(2, 3, 5, 64)), dict(q=z(2, 3, 4, 64).double()),
+                dict(q=z(2, 5, 4, 64)[:, :3]), dict(q=z(2, 3, 64, 4).transpose(2, 3)), dict(lse=z(2, 3)),
+                dict(mask=z(2, 3, t=torch.int64).cpu())):
+        with pytest.raises(ValueError):
+            brq.tree_attention(**{**full, **bad})
+    for bad in (dict(q=z(2, 3, 5, 64)), dict(window=-1), dict(scale=float("nan")),
+                dict(q=z(2, 65, 4, 64), mask=z(2, 65, t=torch.int64))):
+        with pytest.raises(brq.BrqError):
+            brq.tree_attention(**{**full, **bad})
