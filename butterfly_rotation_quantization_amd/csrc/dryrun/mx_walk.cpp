@@ -42,9 +42,9 @@ hipError_t launch_mx_quant(const MxArgs& a, hipStream_t) { return walk_mx(a, a.l
 hipError_t launch_mx_dequant(const MxArgs& a, hipStream_t) { return walk_mx(a, a.ldy); }
 
 // Tiles, parts, scale images and LDS places of the tile kernels of a matmul.
-static hipError_t walk_tiles(const MmArgs& a) {
+static hipError_t walk_tiles(const MmArgs& a, bool epilogue) {
   MmArgs b = a;
-  const size_t bytes = mm_plan(b, a.ts);
+  const size_t bytes = mm_plan(b, a.ts, epilogue);
   const int R = a.tile;
   const int64_t image = (int64_t)a.stages * 8 * R, images = (a.gt + a.go) * image;
   if (b.os != a.os || b.part != a.part || b.splits != a.splits || (R != 128 && R != 256) || a.os != a.ts + a.gt * image ||
@@ -99,10 +99,10 @@ static hipError_t walk_tiles(const MmArgs& a) {
   return hipSuccess;
 }
 
-hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t) {
+static hipError_t walk_matmul(const MmArgs& a, bool epilogue) {
   dry_launch();
   if (a.T < 1 || a.m < 1 || a.n % kMxBlock || a.ldy < a.m) return bad("mx matmul geometry (%lld x %lld)", a.T, a.m);
-  if (a.tile) return walk_tiles(a);
+  if (a.tile) return walk_tiles(a, epilogue);
   if (a.T <= 64) {
     const int rows = mm_stream_rows(a);
     const int64_t wgs = (a.m + rows - 1) / rows;
@@ -114,10 +114,11 @@ hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t) {
   return hipSuccess;
 }
 
-hipError_t launch_mx_linear(const MmArgs& a, const MmEpi& e, hipStream_t s) {
+hipError_t launch_mx_matmul(const MmArgs& a, hipStream_t) { return walk_matmul(a, false); }
+hipError_t launch_mx_linear(const MmArgs& a, const MmEpi& e, hipStream_t) {
   if ((e.mul && e.ldm < a.m) || (e.res && e.ldr < a.m) || (e.wide && ((e.mul && a.T > 1 && e.ldm % 4) || (e.res && a.T > 1 && e.ldr % 4))))
     return bad("mx linear epilogue (%lld, %lld)", e.ldm, e.ldr);
-  return launch_mx_matmul(a, s);
+  return walk_matmul(a, true);
 }
 
 hipError_t launch_mx_grouped(const GmArgs& g, const MmEpi& e, hipStream_t) {
@@ -126,8 +127,29 @@ hipError_t launch_mx_grouped(const GmArgs& g, const MmEpi& e, hipStream_t) {
   if (a.T < 1 || a.m < 1 || a.n % kMxBlock || a.ldy < a.m || g.groups < 1 || (e.mul && e.ldm < a.m) ||
       (e.res && e.ldr < a.m))
     return bad("mx grouped geometry (%lld x %lld)", a.T, a.m);
-  if (!launchable(gm_units(a.T, g.groups, 16) * ((a.m + 15) / 16), 64))
-    return bad("mx grouped grid (%lld x %lld)", a.T, a.m);
+  const int64_t units = gm_units(a.T, g.groups, g.rows);
+  if (!a.tile) {
+    if ((g.rows != 16 && g.rows != 32 && g.rows != 64) || !launchable(units * ((a.m + 15) / 16), 256))
+      return bad("mx grouped stream (%lld units of %lld rows)", units, g.rows);
+  } else {
+    GmArgs h = g;
+    const size_t bytes = gm_plan(h, a.ts);
+    const int64_t image = (int64_t)a.stages * 8 * a.tile;
+    if (g.rows != a.tile || (a.tile != 128 && a.tile != 256) || a.gt != units || a.go * a.tile < a.m || a.os != a.ts + units * image ||
+        (int64_t)bytes != (units + g.groups * a.go) * image || (int64_t)a.stages * kMmK < a.n || a.per != a.stages ||
+        !launchable(units * a.go + 7, 256) || !launchable(units + g.groups * a.go, kMxThreads) || a.tile * (a.n / 2) >= (int64_t)1 << 31)
+      return bad("mx grouped tiles (%lld units, %lld bytes)", units, (long long)bytes);
+    // every tile of a group of some units once
+    for (int64_t gt : {1, 2, 4, 5, 11}) {
+      std::vector<uint8_t> cover((size_t)(gt * a.go), 0);
+      for (int64_t p = 0; p < gt * a.go && a.go < 1 << 16; ++p) {
+        MmWhere w;
+        mm_place(p, gt, a.go, a.band, w);
+        if (w.tt < 0 || w.tt >= gt || w.to < 0 || w.to >= a.go || cover[(size_t)(w.tt * a.go + w.to)]++)
+          return bad("mx grouped tile (%lld, %lld)", w.tt, w.to);
+      }
+    }
+  }
   // groups of every kind have no more units than the grid has places, and no
   // row beyond the last
   for (int seed = 0; seed < 6 && a.T <= 1 << 20; ++seed)

@@ -4,6 +4,8 @@
 // through LDS, the epilogue.  Format: mx.h.
 #pragma once
 
+#include <type_traits>
+
 #include "mx_dev.h"
 
 namespace brq {
@@ -13,6 +15,23 @@ __device__ __forceinline__ void mm_store(void* y, int yt, int64_t off, float v) 
   if (yt == BRQ_F32) static_cast<float*>(y)[off] = v;
   else if (yt == BRQ_BF16) static_cast<uint16_t*>(y)[off] = (uint16_t)mx_bf16(v);
   else static_cast<uint16_t*>(y)[off] = (uint16_t)mx_f16(v);
+}
+
+__device__ __forceinline__ void mm_store4(void* y, int yt, int64_t off, mxf4 v, int valid, bool wide) {
+  if (wide && valid >= 4) {
+    if (yt == BRQ_F32) {
+      *reinterpret_cast<mxf4*>(static_cast<float*>(y) + off) = v;
+    } else {
+      uint2 w;
+      w.x = yt == BRQ_BF16 ? (mx_bf16(v[0]) | mx_bf16(v[1]) << 16) : (mx_f16(v[0]) | mx_f16(v[1]) << 16);
+      w.y = yt == BRQ_BF16 ? (mx_bf16(v[2]) | mx_bf16(v[3]) << 16) : (mx_f16(v[2]) | mx_f16(v[3]) << 16);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + off) = w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < valid) mm_store(y, yt, off + i, v[i]);
 }
 
 // ---- the epilogue
@@ -42,35 +61,167 @@ __device__ __forceinline__ mxf4 mm_read4(const void* p, int t, int64_t i, int va
   return v;
 }
 
-// Both forms of gelu by their tails, x times a probability, so that large
-// negative x lose no digits to 1 - 1.
-__device__ __forceinline__ float mm_act(int act, float x) {
+// x times the logistic function of g, by its tail, which keeps the digits of
+// large negative g; the exponential enters as two factors of half the exponent,
+// since a single one would be zero below 2^-126, where the product is not yet.
+__device__ __forceinline__ float mm_logistic(float x, float g) {
+  const float h = __builtin_amdgcn_exp2f(-0.72134752044448170f * fabsf(g)), r = __builtin_amdgcn_rcpf(fmaf(h, h, 1.f));
+  return g < 0.f ? x * r * h * h : x * r;
+}
+// x times the normal distribution function of x, by its tail too: erfc(z) exp(z^2)
+// is t times a polynomial of degree 8 in t = 1 / (1 + z / 2), fitted over z >= 0 to
+// within 0.75 2^-24 of its value.  (The library's erfcf took more than twice the
+// time: 2048x28672x8192 with bias and gelu 478 us, with this 349.)
+__device__ __forceinline__ float mm_gelu(float x) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(x), 0.35355339059327373f, 1.f));
+  float p = -0.059385716915130615f;
+  p = fmaf(p, t, 0.28612077236175537f);
+  p = fmaf(p, t, -0.49040067195892334f);
+  p = fmaf(p, t, 0.28172776103019714f);
+  p = fmaf(p, t, -0.029145410284399986f);
+  p = fmaf(p, t, 0.20375148952007294f);
+  p = fmaf(p, t, 0.24283531308174133f);
+  p = fmaf(p, t, 0.2824120819568634f);
+  p = fmaf(p, t, 0.2820843458175659f);
+  const float h = __builtin_amdgcn_exp2f(-0.36067376022224085f * (x * x)), q = 0.5f * p * t;
+  return x < 0.f ? q * x * h * h : x * (1.f - q * h * h);
+}
+template <int N>
+__device__ __forceinline__ void mm_act(int act, float (&v)[N]) {
   switch (act) {
-    case BRQ_ACT_RELU: return x < 0.f ? 0.f : x;  // a NaN stays one
-    case BRQ_ACT_GELU: return 0.5f * x * erfcf(-0.70710678118654752f * x);
-    case BRQ_ACT_GELU_TANH: return x / (1.f + expf(-1.5957691216057308f * (x + 0.044715f * x * x * x)));
-    case BRQ_ACT_SILU: return x / (1.f + expf(-x));
-    default: return x;
+    case BRQ_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];  // a NaN stays one
+      return;
+    case BRQ_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = mm_gelu(v[i]);
+      return;
+    case BRQ_ACT_GELU_TANH:  // (1 + tanh(g)) / 2 is the logistic function of 2 g
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = mm_logistic(v[i], 1.5957691216057308f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
+      return;
+    case BRQ_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = mm_logistic(v[i], v[i]);
+      return;
+    default: return;
   }
 }
 // The output of row t, column o from its sum.
 __device__ __forceinline__ float mm_finish(const MmNoEpi&, int64_t, int64_t, float v) { return v; }
 __device__ __forceinline__ float mm_finish(const MmEpi& e, int64_t t, int64_t o, float v) {
-  if (e.bias) v += mm_read(e.bias, e.bt, o);
-  v = mm_act(e.act, v);
-  if (e.mul) v *= mm_read(e.mul, e.mt, t * e.ldm + o);
-  if (e.res) v += mm_read(e.res, e.rt, t * e.ldr + o);
-  return v;
+  const float mul = e.mul ? mm_read(e.mul, e.mt, t * e.ldm + o) : 1.f;  // asked for before what they wait for
+  const float res = e.res ? mm_read(e.res, e.rt, t * e.ldr + o) : 0.f;
+  float x[1] = {e.bias ? v + mm_read(e.bias, e.bt, o) : v};
+  mm_act(e.act, x);
+  if (e.mul) x[0] *= mul;
+  return e.res ? x[0] + res : x[0];
 }
+// Four consecutive values of each of N rows `step` apart, those below T (past it the
+// last one again); one decision on the type for all of them.
+template <int N, class F>
+__device__ __forceinline__ void mm_each(int64_t t, int step, int64_t T, F f) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) f(i, t + i * step < T ? t + i * step : T - 1);
+}
+template <int N>
+__device__ __forceinline__ void mm_read_rows(const void* p, int type, int64_t ld, int64_t t, int step, int64_t T, int64_t o,
+                                             int valid, bool wide, mxf4 (&v)[N]) {
+  if (!wide || valid < 4) {
+    mm_each<N>(t, step, T, [&](int i, int64_t row) { v[i] = mm_read4(p, type, row * ld + o, valid, false); });
+  } else if (type == BRQ_F32) {
+    mm_each<N>(t, step, T, [&](int i, int64_t row) {
+      v[i] = *reinterpret_cast<const mxf4*>(static_cast<const float*>(p) + row * ld + o);
+    });
+  } else {
+    uint2 w[N];
+    mm_each<N>(t, step, T, [&](int i, int64_t row) {
+      w[i] = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + row * ld + o);
+    });
+    if (type == BRQ_BF16) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        v[i] = mxf4{__uint_as_float(w[i].x << 16), __uint_as_float(w[i].x & 0xffff0000u), __uint_as_float(w[i].y << 16),
+                    __uint_as_float(w[i].y & 0xffff0000u)};
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        v[i] = mxf4{(float)__builtin_bit_cast(_Float16, (uint16_t)(w[i].x & 0xffffu)),
+                    (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i].x >> 16)),
+                    (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i].y & 0xffffu)),
+                    (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i].y >> 16))};
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void mm_store_rows(void* y, int yt, int64_t ldy, int64_t t, int step, int64_t T, int64_t o,
+                                              int valid, bool wide, const mxf4 (&v)[N]) {
+  if (!wide || valid < 4) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (t + i * step < T) mm_store4(y, yt, (t + i * step) * ldy + o, v[i], valid, false);
+  } else if (yt == BRQ_F32) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (t + i * step < T) *reinterpret_cast<mxf4*>(static_cast<float*>(y) + (t + i * step) * ldy + o) = v[i];
+  } else {
+    uint2 w[N];
+    if (yt == BRQ_BF16) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        w[i] = make_uint2(mx_bf16(v[i][0]) | mx_bf16(v[i][1]) << 16, mx_bf16(v[i][2]) | mx_bf16(v[i][3]) << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        w[i] = make_uint2(mx_f16(v[i][0]) | mx_f16(v[i][1]) << 16, mx_f16(v[i][2]) | mx_f16(v[i][3]) << 16);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (t + i * step < T) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + (t + i * step) * ldy + o) = w[i];
+  }
+}
+// Such rows' epilogue: what they take from memory is asked for before anything
+// waits for it, and every part is done for all of them under one condition.
+template <int N, class EP>
+struct MmFinish;
+template <int N>
+struct MmFinish<N, MmNoEpi> {
+  __device__ __forceinline__ void ask(const MmNoEpi&, int64_t, int, int64_t, int64_t, int) {}
+  __device__ __forceinline__ void apply(const MmNoEpi&, mxf4, mxf4 (&)[N]) const {}
+};
+template <int N>
+struct MmFinish<N, MmEpi> {
+  mxf4 mul[N], res[N];
+
+  // rows below T, the first `valid` of four columns
+  __device__ __forceinline__ void ask(const MmEpi& e, int64_t t, int step, int64_t T, int64_t o, int valid) {
+    if (e.mul) mm_read_rows<N>(e.mul, e.mt, e.ldm, t, step, T, o, valid, e.wide, mul);
+    if (e.res) mm_read_rows<N>(e.res, e.rt, e.ldr, t, step, T, o, valid, e.wide, res);
+  }
+  __device__ __forceinline__ void apply(const MmEpi& e, mxf4 bias, mxf4 (&v)[N]) const {
+    float x[4 * N];
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) x[i] = v[i / 4][i & 3] + bias[i & 3];  // without one, -0
+    mm_act(e.act, x);
+    if (e.mul)
+#pragma unroll
+      for (int i = 0; i < 4 * N; ++i) x[i] *= mul[i / 4][i & 3];
+    if (e.res)
+#pragma unroll
+      for (int i = 0; i < 4 * N; ++i) x[i] += res[i / 4][i & 3];
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) v[i / 4][i & 3] = x[i];
+  }
+};
+constexpr float kMmNoBias = -0.f;  // adds nothing, not even to a zero's sign
 __device__ __forceinline__ mxf4 mm_finish4(const MmNoEpi&, int64_t, int64_t, mxf4 v, int) { return v; }
 __device__ __forceinline__ mxf4 mm_finish4(const MmEpi& e, int64_t t, int64_t o, mxf4 v, int valid) {
-  if (e.bias) v += mm_read4(e.bias, e.bt, o, valid, e.wide);
-  if (e.act != BRQ_ACT_NONE)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = mm_act(e.act, v[i]);
-  if (e.mul) v *= mm_read4(e.mul, e.mt, t * e.ldm + o, valid, e.wide);
-  if (e.res) v += mm_read4(e.res, e.rt, t * e.ldr + o, valid, e.wide);
-  return v;
+  MmFinish<1, MmEpi> f;
+  f.ask(e, t, 0, t + 1, o, valid);
+  mxf4 x[1] = {v};
+  f.apply(e, e.bias ? mm_read4(e.bias, e.bt, o, valid, e.wide) : mxf4{kMmNoBias, kMmNoBias, kMmNoBias, kMmNoBias}, x);
+  return x[0];
 }
 
 // ---- few tokens: a stream over the weight
@@ -109,6 +260,97 @@ __device__ __forceinline__ int mm_scale_of(const uint4& v, int s, int sh) {
   const uint32_t w = s == 0 ? v.x : s == 1 ? v.y : s == 2 ? v.z : v.w;
   return (int)(w >> sh);
 }
+
+// 16 RT outputs, up to 16 TT tokens: outputs from o0 on, tokens t0 .. t0 + 16 TT - 1
+// as far as there are a.T.  The workgroup's W wavefronts take chunks of the weight's
+// rows in turn, 2 KB of each row in flight at a time, and join their sums in LDS:
+// the weight is read once, in one launch.  Bound by memory: one token at
+// 8192x28672 23 us, 5.4 TB/s of the weight.
+template <int TT, int RT, int W>
+struct MmRows {
+  static constexpr int B = kMmChunk / kMxBlock;
+  typedef float Sums[W][RT][TT][16][17];
+  int lane, wave, lr, lg;
+  const uint8_t *wrow[RT], *wsrow[RT];
+  MmChunk w[RT];
+
+  __device__ __forceinline__ MmRows() : lane(threadIdx.x & 63), wave(threadIdx.x >> 6), lr(lane & 15), lg(lane >> 4) {}
+
+  // the first chunk of the weight's rows
+  __device__ __forceinline__ void begin(const uint8_t* b, const uint8_t* bs, int64_t m, int64_t nb, int64_t o0) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {  // rows past the end: the last one, not stored
+      const int64_t o = o0 + 16 * i + lr < m ? o0 + 16 * i + lr : m - 1;
+      wrow[i] = b + (o * nb + lg) * 16;
+      wsrow[i] = bs + o * nb;
+    }
+    const int64_t k = (int64_t)wave * B;
+    if (k < nb)
+#pragma unroll
+      for (int i = 0; i < RT; ++i) mm_chunk(w[i], wrow[i], wsrow[i], k, nb, lg);
+  }
+  // the sums of rows begun before, into LDS
+  __device__ __forceinline__ void sum(const MmArgs& a, int64_t T, int64_t t0, Sums& sums) {
+    const int sh = 8 * lg;
+    const int64_t nb = a.n / kMxBlock;
+    const uint8_t *xrow[TT], *xsrow[TT];
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+      const int64_t t = t0 + 16 * j + lr < T ? t0 + 16 * j + lr : T - 1;
+      xrow[j] = a.a + (t * nb + lg) * 16;
+      xsrow[j] = a.as + t * nb;
+    }
+    mxf4 acc[RT][TT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < TT; ++j) acc[i][j] = mxf4{0.f, 0.f, 0.f, 0.f};
+    int64_t k = (int64_t)wave * B;
+    while (k < nb) {
+      const int64_t next = k + W * B;
+      MmChunk wn[RT], x[TT];
+#pragma unroll
+      for (int j = 0; j < TT; ++j) mm_chunk(x[j], xrow[j], xsrow[j], k, nb, lg);
+      if (next < nb)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) mm_chunk(wn[i], wrow[i], wsrow[i], next, nb, lg);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+          const mxi8 A8 = {x[j].c[s][0], x[j].c[s][1], x[j].c[s][2], x[j].c[s][3], 0, 0, 0, 0};
+          const int sx = mm_scale_of(x[j].s, s, sh);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            const mxi8 B8 = {w[i].c[s][0], w[i].c[s][1], w[i].c[s][2], w[i].c[s][3], 0, 0, 0, 0};
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(B8, A8, acc[i][j], 4, 4, 0,
+                                                                         mm_scale_of(w[i].s, s, sh), 0, sx);
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < RT; ++i) w[i] = wn[i];
+      k = next;
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < TT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sums[wave][i][j][lr][4 * lg + e] = acc[i][j][e];  // token lr, output 4 lg + e
+  }
+  // the wavefronts' sums joined and stored
+  template <class E>
+  __device__ __forceinline__ void finish(const MmArgs& a, const E& ep, int64_t T, int64_t t0, int64_t o0, const Sums& sums) {
+    for (int e = threadIdx.x; e < 256 * TT * RT; e += 64 * W) {
+      const int c = e & 15, i = (e >> 4) % RT, t = (e >> 4) / RT, j = t >> 4;  // a token's outputs on consecutive lanes
+      float v = sums[0][i][j][t & 15][c];
+#pragma unroll
+      for (int u = 1; u < W; ++u) v += sums[u][i][j][t & 15][c];
+      const int64_t o = o0 + 16 * i + c;
+      if (t0 + t < T && o < a.m) mm_store(a.y, a.yt, (t0 + t) * a.ldy + o, mm_finish(ep, t0 + t, o, v));
+    }
+  }
+};
 
 // ---- tiles through LDS
 
@@ -153,23 +395,6 @@ __device__ __forceinline__ void mm_step(mxi4 a, mxi4 b, mxf16& c, int sa, int ia
   }
 }
 
-__device__ __forceinline__ void mm_store4(void* y, int yt, int64_t off, mxf4 v, int valid, bool wide) {
-  if (wide && valid >= 4) {
-    if (yt == BRQ_F32) {
-      *reinterpret_cast<mxf4*>(static_cast<float*>(y) + off) = v;
-    } else {
-      uint2 w;
-      w.x = yt == BRQ_BF16 ? (mx_bf16(v[0]) | mx_bf16(v[1]) << 16) : (mx_f16(v[0]) | mx_f16(v[1]) << 16);
-      w.y = yt == BRQ_BF16 ? (mx_bf16(v[2]) | mx_bf16(v[3]) << 16) : (mx_f16(v[2]) | mx_f16(v[3]) << 16);
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + off) = w;
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < valid) mm_store(y, yt, off + i, v[i]);
-}
-
 constexpr int kMmKB = kMmK / 2;     // code bytes of a row in a stage
 constexpr int kMmKS = kMmK / kMxBlock;
 
@@ -205,8 +430,9 @@ __device__ __forceinline__ void mm_to_lds(const void* base, uint32_t& off, uint3
 // get zeros (2^-127, times codes of zero).  One workgroup: a tile, kMmRun
 // stages.
 constexpr int kMmRun = 4;
+// Of rows row0 .. of a tile; `out`: the tile's image.
 template <int R>
-__device__ __forceinline__ void mm_scale_tile(const uint8_t* src, int64_t rows, int64_t nb, int stages, int64_t tile,
+__device__ __forceinline__ void mm_scale_tile(const uint8_t* src, int64_t row0, int64_t rows, int64_t nb, int stages,
                                               int s0, uint8_t* out) {
   constexpr int W = kMmRun * kMmKS, LD = W + 4;
   __shared__ uint8_t lds[R][LD];
@@ -215,14 +441,14 @@ __device__ __forceinline__ void mm_scale_tile(const uint8_t* src, int64_t rows, 
   if (nb % 4 == 0) {  // whole words (the base is aligned)
     for (int e = tid; e < R * (W / 4); e += kMxThreads) {
       const int r = e / (W / 4), c = 4 * (e % (W / 4));
-      const int64_t row = tile * R + r;
+      const int64_t row = row0 + r;
       *reinterpret_cast<uint32_t*>(&lds[r][c]) =
           row < rows && k0 + c < nb ? *reinterpret_cast<const uint32_t*>(src + row * nb + k0 + c) : 0u;
     }
   } else {
     for (int e = tid; e < R * W; e += kMxThreads) {
       const int r = e / W, c = e % W;
-      const int64_t row = tile * R + r;
+      const int64_t row = row0 + r;
       lds[r][c] = row < rows && k0 + c < nb ? src[row * nb + k0 + c] : 0;
     }
   }
@@ -230,7 +456,7 @@ __device__ __forceinline__ void mm_scale_tile(const uint8_t* src, int64_t rows, 
   for (int e = tid; e < kMmRun * kMmKS * 32; e += kMxThreads) {
     const int r = e & 31, c = e >> 5, s = s0 + c / kMmKS;  // block c of the run
     if (s >= stages) break;
-    uint8_t* d = out + (tile * stages + s) * (8 * R) + mm_scale_at(R, c % kMmKS, r);
+    uint8_t* d = out + (int64_t)s * (8 * R) + mm_scale_at(R, c % kMmKS, r);
 #pragma unroll
     for (int q = 0; q < R / 128; ++q) {
       uint32_t w = 0;
@@ -240,6 +466,34 @@ __device__ __forceinline__ void mm_scale_tile(const uint8_t* src, int64_t rows, 
     }
   }
 }
+// A kernel's epilogue, its second argument after ARGS, read from where the
+// arguments are when it is wanted: taken at the kernel's beginning, as arguments
+// are, it would hold registers that the addresses of the main loop need.
+template <class EP>
+struct MmLate;
+template <>
+struct MmLate<MmNoEpi> {
+};
+template <>
+struct MmLate<MmEpi> {
+  typedef const __attribute__((address_space(4))) char* Ptr;
+  Ptr p;
+  int64_t group;  // of a bias for each
+
+  template <class ARGS>
+  static __device__ __forceinline__ MmLate after(int64_t group = 0) {
+    return {(Ptr)__builtin_amdgcn_kernarg_segment_ptr() + (sizeof(ARGS) + 7) / 8 * 8, group};
+  }
+  __device__ __forceinline__ MmEpi get(int64_t m) const {
+    Ptr q = p;
+    asm volatile("" : "+s"(q));
+    MmEpi e;
+    __builtin_memcpy(&e, (const void*)q, sizeof e);
+    e.bias = gm_bias(e, group, m);
+    return e;
+  }
+};
+
 // Operands of a step of 128 values: two of 64, and the scales of the tiles.
 template <int TT, int TO>
 struct MmFrag {
@@ -268,10 +522,11 @@ struct MmTile {
   };
 
   const MmArgs& a;
-  const EP& ep;
+  const MmLate<EP> late;
   Lds& lds;
   const int tid, lane, wave, lr, lg, wt, wo;
   const int64_t t0, o0, nb, ld;
+  const uint8_t *ts, *os;   // the tile's images of scales
   const int first, stages;  // the part's first stage, its number of stages
   // where the sums go: the output, or the part's float32 partial sums
   const bool whole;
@@ -286,10 +541,13 @@ struct MmTile {
   const uint32_t base, at;  // LDS addresses: of the workgroup, of the wavefront's first piece
   uint32_t off0;
   mxf16 acc[TO][TT];
+  mxf4 bias;  // of the lane's four outputs
 
-  __device__ __forceinline__ MmTile(const MmArgs& a_, const EP& e, Lds& l, int64_t t0_, int64_t o0_, int part)
-      : a(a_), ep(e), lds(l), tid(threadIdx.x), lane(tid & 63), wave(tid >> 6), lr(lane & 31), lg(lane >> 5), wt(wave % WT),
+  __device__ __forceinline__ MmTile(const MmArgs& a_, const MmLate<EP>& e, Lds& l, int64_t t0_, int64_t o0_, int part,
+                                    const uint8_t* ts_, const uint8_t* os_)
+      : a(a_), late(e), lds(l), tid(threadIdx.x), lane(tid & 63), wave(tid >> 6), lr(lane & 31), lg(lane >> 5), wt(wave % WT),
         wo(wave / WT), t0(t0_), o0(o0_), nb(a_.n / kMxBlock), ld(a_.n / 2),
+        ts(ts_), os(os_),
         first(part * a_.per), stages(a_.stages - first < a_.per ? a_.stages - first : a_.per), whole(a_.splits == 1), pr(tid >> 3), pc((tid & 7) ^ (pr >> 1 & 7)),
         lt((int)(a_.T - t0_ < BT ? a_.T - t0_ : BT) - 1), lo((int)(a_.m - o0_ < BO ? a_.m - o0_ : BO) - 1),
         base((uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)&l)),
@@ -350,8 +608,7 @@ struct MmTile {
     constexpr int from = (int)sizeof(lds.codes) + BUF * (int)sizeof(lds.scales[0]);
     const int piece = __builtin_amdgcn_readfirstlane(wave % (8 * ROWS / 1024)) * 1024;
     const int64_t st = first + (s < stages ? s : stages - 1);
-    const uint8_t* g = piece < 8 * BT ? a.ts + (t0 / BT * a.stages + st) * (8 * BT) + piece
-                                      : a.os + (o0 / BO * a.stages + st) * (8 * BO) + (piece - 8 * BT);
+    const uint8_t* g = piece < 8 * BT ? ts + st * (8 * BT) + piece : os + st * (8 * BO) + (piece - 8 * BT);
     mm_to_lds(g + 16 * lane, base + from + piece);
   }
   template <int E>  // operand E of step k2: the first 64 values, tokens first, then the second
@@ -494,7 +751,14 @@ struct MmTile {
     // have to be in it before, and every wavefront's reads done
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    store<0>();
+    EP ep;
+    if constexpr (!std::is_same<EP, MmNoEpi>::value) {
+      ep = late.get(a.m);
+      const int64_t o = o0 + 32 * TO * wo + 4 * (lane % (8 * TO)), left = a.m - o;
+      bias = mxf4{kMmNoBias, kMmNoBias, kMmNoBias, kMmNoBias};
+      if (ep.bias && left > 0) bias = mm_read4(ep.bias, ep.bt, o, left < 4 ? (int)left : 4, ep.wide);
+    }
+    store<0>(ep);
   }
 
   // The sums of 32 tokens at a time through the wavefront's part of LDS, so
@@ -502,7 +766,7 @@ struct MmTile {
   // enough to stay in the instruction cache (one store a register, unrolled,
   // cost 25 us of fetching instructions).
   template <int J>
-  __device__ __forceinline__ void store() {
+  __device__ __forceinline__ void store(const EP& ep) {
     if constexpr (J < TT) {
       constexpr int LD = 32 * TO + 4, LPR = 8 * TO;  // floats a row, lanes a row
       static_assert(32 * LD * 4 * WT * WO <= (int)sizeof(Lds), "sums of 32 tokens of every wavefront");
@@ -516,15 +780,22 @@ struct MmTile {
       __builtin_amdgcn_wave_barrier();
       const int64_t o = o0 + 32 * TO * wo + 4 * (lane % LPR), left = a.m - o;
       const int64_t tj = t0 + 32 * (TT * wt + J);
+      const int valid = left < 4 ? (int)left : 4;
+      // four rows at a time, whose operands travel together
+      constexpr int N = 4, S = 64 / LPR;
 #pragma unroll 1
-      for (int r = lane / LPR; r < 32; r += 64 / LPR) {
-        mxf4 v = *reinterpret_cast<const mxf4*>(&my[r * LD + 4 * (lane % LPR)]);
-        if (tj + r >= a.T || left <= 0) continue;
-        if (whole) v = mm_finish4(ep, tj + r, o, v, left < 4 ? (int)left : 4);
-        mm_store4(y, yt, (tj + r) * ldy + o, v, left < 4 ? (int)left : 4, wide);
+      for (int r = lane / LPR; r < 32; r += N * S) {
+        if (tj + r >= a.T || left <= 0) break;
+        MmFinish<N, EP> f;
+        if (whole) f.ask(ep, tj + r, S, a.T, o, valid);
+        mxf4 v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const mxf4*>(&my[(r + i * S) * LD + 4 * (lane % LPR)]);
+        if (whole) f.apply(ep, bias, v);
+        mm_store_rows<N>(y, yt, ldy, tj + r, S, a.T, o, valid, wide, v);
       }
       __builtin_amdgcn_wave_barrier();
-      store<J + 1>();
+      store<J + 1>(ep);
     }
   }
 };

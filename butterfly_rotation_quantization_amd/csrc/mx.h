@@ -95,9 +95,9 @@ inline bool mm_supported(int64_t T, int64_t m, int64_t n) {
   return T <= most && m <= most && n <= most && (m == 0 || T <= kMxMost / 2 / m);
 }
 
-// Kernel and workspace of a product (a.T, a.m, a.n set): returns the
-// workspace bytes.
-inline size_t mm_plan(MmArgs& a, uint8_t* ws) {
+// Kernel and workspace of a product (a.T, a.m, a.n set), with an epilogue or
+// without: returns the workspace bytes.
+inline size_t mm_plan(MmArgs& a, uint8_t* ws, bool epilogue) {
   a.tile = 0;
   a.splits = 1;
   if (a.n < kMmK || a.n > (1 << 23)) return 0;
@@ -108,9 +108,13 @@ inline size_t mm_plan(MmArgs& a, uint8_t* ws) {
   auto tiles = [&](int64_t t) { return ((a.T + t - 1) / t) * ((a.m + t - 1) / t); };
   // One 256 x 256 tile per compute unit at a time, two of 128 x 128; such a
   // pair takes about 2/3 of a large tile's time for half its work.
-  const int64_t large = (tiles(256) + 255) / 256 * 3, small = (tiles(128) + 511) / 512 * 2;
-  a.tile = large <= small ? 256 : 128;
+  // An epilogue's operands and activations are worked on while the other tile of a pair
+  // is multiplied, but by a large tile alone, for as long as 11 stages take it
+  // (2048x28672x8192 with bias and gelu: large 318 us, small 299; with factor and
+  // residual too 396 and 348; 4096x8192x8192 169 and 173, 186 and 180).
   a.stages = (int)((a.n + kMmK - 1) / kMmK);
+  const int64_t large = (tiles(256) + 255) / 256 * 3, small = (tiles(128) + 511) / 512 * 2;
+  a.tile = (epilogue ? large * (a.stages + 11) <= small * (a.stages + 3) : large <= small) ? 256 : 128;
   a.gt = (a.T + a.tile - 1) / a.tile;
   a.go = (a.m + a.tile - 1) / a.tile;
   // Too few tiles for the chip: the long axis in parts, of eight stages or more
@@ -145,16 +149,17 @@ struct MmWhere {
   int64_t tt, to;  // the tile, along tokens and outputs
   int part;
 };
+__host__ __device__ inline void mm_place(int64_t p, int64_t gt, int64_t go, int rows, MmWhere& w) {
+  const int64_t band = p / (rows * go), q = p - band * rows * go;
+  const int64_t h = gt - band * rows < rows ? gt - band * rows : rows;  // rows of tiles in this band
+  w.tt = band * rows + q % h;
+  w.to = q / h;
+}
 __host__ __device__ inline bool mm_where(const MmArgs& a, uint32_t block, MmWhere& w) {
   int64_t p = (int64_t)(block & 7) * a.per_xcd + (block >> 3);
   if (p >= a.gt * a.go * a.splits) return false;
   w.part = (int)(p / (a.gt * a.go));
-  p -= w.part * (a.gt * a.go);
-  const int64_t band = p / ((int64_t)a.band * a.go);
-  const int64_t q = p - band * a.band * a.go;
-  const int64_t h = a.gt - band * a.band < a.band ? a.gt - band * a.band : a.band;  // rows of tiles in this band
-  w.tt = band * a.band + q % h;
-  w.to = q / h;
+  mm_place(p - w.part * (a.gt * a.go), a.gt, a.go, a.band, w);
   return true;
 }
 // Place in LDS of 16-byte piece c of row r, in pieces: the pieces c of sixteen
@@ -187,6 +192,7 @@ struct GmArgs {
   MmArgs mm;             // T rows, m outputs; b, bs: of group 0, the others' behind
   const int32_t* offs;   // [groups + 1]
   int groups;
+  int rows;              // of a unit: 16, 32 or 64 of the stream, a tile's 128 or 256
 };
 
 // Rows [b, end) of a group from its two offsets: within the T rows there are.
@@ -201,10 +207,49 @@ __host__ __device__ inline const void* gm_bias(const MmEpi& e, int64_t group, in
   if (!e.bias) return nullptr;
   return static_cast<const char*>(e.bias) + group * m * (e.bt == BRQ_F32 ? 4 : 2);
 }
-// Launches within 2^32 threads (64 per 16 x 16 outputs at most).
+// Kernel and workspace of a grouped product (g.mm.T, m, n and g.groups set): a
+// group's units are taken by the stream over its weight, or by tiles through LDS, whose
+// images of scales (of every unit, and of every group's weight) are in the workspace.
+inline size_t gm_plan(GmArgs& g, uint8_t* ws) {
+  MmArgs& a = g.mm;
+  a.tile = 0;
+  a.splits = 1;
+  g.rows = 16;
+  if (a.n > (1 << 23) || a.n < kMmK) return 0;
+  // Rows a group in the mean, up to which the stream takes less time than tiles
+  // (8 groups of 11008x4096, 16, 32 and 40 rows: 46, 61 and 103 us, tiles of 128 66, 66 and 69).
+  const int64_t mean = a.T / g.groups;
+  if (mean <= 32) {
+    g.rows = mean <= 16 ? 16 : 32;
+    return 0;
+  }
+  // as many units as are to be expected: half of a group's last one is empty, none all of it
+  const int64_t some = g.groups < a.T ? g.groups : a.T;
+  auto tiles = [&](int64_t t) {
+    const int64_t units = a.T / t + some / 2;
+    return (units > some ? units : some) * ((a.m + t - 1) / t);
+  };
+  // As for one product (mm_plan), what follows the stages for an epilogue and without one
+  // alike, and rounds in fractions, since the groups' sizes are not known.
+  auto most = [](int64_t x, int64_t y) { return x > y ? x : y; };
+  a.stages = (int)((a.n + kMmK - 1) / kMmK);
+  const int64_t large = most(tiles(256), 256) * 2 * (3 * a.stages + 16), small = most(tiles(128), 512) * (2 * a.stages + 4);
+  a.tile = large <= small ? 256 : 128;
+  g.rows = a.tile;
+  a.per = a.stages;
+  a.gt = gm_units(a.T, g.groups, a.tile);
+  a.go = (a.m + a.tile - 1) / a.tile;
+  a.band = 4;
+  const int64_t image = (int64_t)a.stages * (kMmK / kMxBlock) * a.tile;
+  a.ts = ws;
+  a.os = ws + a.gt * image;
+  return (size_t)((a.gt + g.groups * a.go) * image);
+}
+// Launches within 2^32 threads: of the stream 256 for each unit and 16 outputs,
+// where units of 16 rows are taken up to 8 rows a group in the mean, of 32 up to 24.
 inline bool gm_supported(int64_t T, int64_t groups, int64_t m, int64_t n) {
   if (!mm_supported(T, m, n) || groups > 1 << 20) return false;
-  return m == 0 || gm_units(T, groups, 16) + 1 <= ((int64_t)1 << 32) / 64 / ((m + 15) / 16);
+  return m == 0 || T / 64 + 2 * (groups < T ? groups : T) < ((int64_t)1 << 24) / ((m + 15) / 16);
 }
 
 hipError_t launch_mx_grouped(const GmArgs& g, const MmEpi& e, hipStream_t s);

@@ -212,7 +212,8 @@ size_t brq_mx_matmul_workspace_bytes(int64_t T, int64_t m, int64_t n) {
   a.T = T;
   a.m = m;
   a.n = n;
-  return mm_plan(a, nullptr);
+  const size_t plain = mm_plan(a, nullptr, false), with = mm_plan(a, nullptr, true);
+  return plain > with ? plain : with;
 }
 
 brq_status brq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
@@ -232,7 +233,7 @@ brq_status brq_mx_linear(const uint8_t* a_codes, const uint8_t* a_scales, const 
   if (st != BRQ_OK || done) return st;
   const size_t need = brq_mx_matmul_workspace_bytes(T, m, n);
   if ((st = workspace_ok(ws, ws_bytes, need)) != BRQ_OK) return st;
-  mm_plan(a, static_cast<uint8_t*>(ws));
+  mm_plan(a, static_cast<uint8_t*>(ws), ep != nullptr);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int tok = prof_begin("mx matmul", s);
   const hipError_t err = ep ? launch_mx_linear(a, e, s) : launch_mx_matmul(a, s);
@@ -242,7 +243,13 @@ brq_status brq_mx_linear(const uint8_t* a_codes, const uint8_t* a_scales, const 
 
 size_t brq_mx_grouped_matmul_workspace_bytes(int64_t T, int64_t groups, int64_t m, int64_t n) {
   if (T <= 0 || groups <= 0 || m <= 0 || n <= 0 || n % kMxBlock || !gm_supported(T, groups, m, n)) return 0;
-  return 0;
+  GmArgs g;
+  std::memset(&g, 0, sizeof g);
+  g.mm.T = T;
+  g.mm.m = m;
+  g.mm.n = n;
+  g.groups = (int)groups;
+  return gm_plan(g, nullptr);
 }
 
 brq_status brq_mx_grouped_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
@@ -265,6 +272,7 @@ brq_status brq_mx_grouped_matmul(const uint8_t* a_codes, const uint8_t* a_scales
   if ((st = workspace_ok(ws, ws_bytes, need)) != BRQ_OK) return st;
   g.offs = offsets;
   g.groups = (int)groups;
+  gm_plan(g, static_cast<uint8_t*>(ws));
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int tok = prof_begin("mx grouped matmul", s);
   const hipError_t err = launch_mx_grouped(g, e, s);

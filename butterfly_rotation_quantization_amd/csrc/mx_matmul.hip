@@ -43,80 +43,15 @@ __global__ __launch_bounds__(64) void mm_simple_kernel(MmArgs a, E ep) {
 }
 
 
-// 16 RT outputs, up to 16 TT tokens.  The workgroup's W wavefronts take chunks
-// of its weight rows in turn, 2 KB of each row in flight at a time, and join
-// their sums in LDS: the weight is read once, in one launch.  Bound by memory:
-// one token at 8192x28672 23 us, 5.4 TB/s of the weight.
 template <int TT, int RT, int W, class E>
 __global__ __launch_bounds__(64 * W) void mm_rows_kernel(MmArgs a, E ep) {
-  __shared__ float sums[W][RT][TT][16][17];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int lr = lane & 15, lg = lane >> 4, sh = 8 * lg;
-  const int64_t o0 = (int64_t)blockIdx.x * (16 * RT), nb = a.n / kMxBlock;
-  const uint8_t *wrow[RT], *wsrow[RT], *xrow[TT], *xsrow[TT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {  // rows past the end: the last one, not stored
-    const int64_t o = o0 + 16 * i + lr < a.m ? o0 + 16 * i + lr : a.m - 1;
-    wrow[i] = a.b + (o * nb + lg) * 16;
-    wsrow[i] = a.bs + o * nb;
-  }
-#pragma unroll
-  for (int j = 0; j < TT; ++j) {
-    const int64_t t = 16 * j + lr < a.T ? 16 * j + lr : a.T - 1;
-    xrow[j] = a.a + (t * nb + lg) * 16;
-    xsrow[j] = a.as + t * nb;
-  }
-  mxf4 acc[RT][TT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < TT; ++j) acc[i][j] = mxf4{0.f, 0.f, 0.f, 0.f};
-  constexpr int B = kMmChunk / kMxBlock;
-  MmChunk w[RT], x[TT];
-  int64_t k = (int64_t)wave * B;
-  if (k < nb)
-#pragma unroll
-    for (int i = 0; i < RT; ++i) mm_chunk(w[i], wrow[i], wsrow[i], k, nb, lg);
-  while (k < nb) {
-    const int64_t next = k + W * B;
-    MmChunk wn[RT];
-#pragma unroll
-    for (int j = 0; j < TT; ++j) mm_chunk(x[j], xrow[j], xsrow[j], k, nb, lg);
-    if (next < nb)
-#pragma unroll
-      for (int i = 0; i < RT; ++i) mm_chunk(wn[i], wrow[i], wsrow[i], next, nb, lg);
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int j = 0; j < TT; ++j) {
-        const mxi8 A8 = {x[j].c[s][0], x[j].c[s][1], x[j].c[s][2], x[j].c[s][3], 0, 0, 0, 0};
-        const int sx = mm_scale_of(x[j].s, s, sh);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const mxi8 B8 = {w[i].c[s][0], w[i].c[s][1], w[i].c[s][2], w[i].c[s][3], 0, 0, 0, 0};
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(B8, A8, acc[i][j], 4, 4, 0,
-                                                                       mm_scale_of(w[i].s, s, sh), 0, sx);
-        }
-      }
-#pragma unroll
-    for (int i = 0; i < RT; ++i) w[i] = wn[i];
-    k = next;
-  }
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < TT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sums[wave][i][j][lr][4 * lg + e] = acc[i][j][e];  // token lr, output 4 lg + e
+  __shared__ typename MmRows<TT, RT, W>::Sums sums;
+  const int64_t o0 = (int64_t)blockIdx.x * (16 * RT);
+  MmRows<TT, RT, W> r;
+  r.begin(a.b, a.bs, a.m, a.n / kMxBlock, o0);
+  r.sum(a, a.T, 0, sums);
   __syncthreads();
-  for (int e = tid; e < 256 * TT * RT; e += 64 * W) {
-    const int c = e & 15, i = (e >> 4) % RT, t = (e >> 4) / RT, j = t >> 4;  // a token's outputs on consecutive lanes
-    float v = sums[0][i][j][t & 15][c];
-#pragma unroll
-    for (int u = 1; u < W; ++u) v += sums[u][i][j][t & 15][c];
-    const int64_t o = o0 + 16 * i + c;
-    if (t < a.T && o < a.m) mm_store(a.y, a.yt, t * a.ldy + o, mm_finish(ep, t, o, v));
-  }
+  r.finish(a, ep, a.T, 0, o0, sums);
 }
 
 template <int TT, int RT, class E>
@@ -136,20 +71,24 @@ template <int BT, int BO>
 __global__ __launch_bounds__(kMxThreads) void mm_scales_kernel(MmArgs a) {
   const int64_t nb = a.n / kMxBlock;
   const int stages = (int)((nb + kMmKS - 1) / kMmKS), s0 = (int)blockIdx.y * kMmRun;
-  if ((int64_t)blockIdx.x < a.gt) mm_scale_tile<BT>(a.as, a.T, nb, stages, blockIdx.x, s0, a.ts);
-  else mm_scale_tile<BO>(a.bs, a.m, nb, stages, (int64_t)blockIdx.x - a.gt, s0, a.os);
+  const int64_t t = blockIdx.x, o = t - a.gt;
+  if (t < a.gt) mm_scale_tile<BT>(a.as, t * BT, a.T, nb, stages, s0, a.ts + t * stages * (8 * BT));
+  else mm_scale_tile<BO>(a.bs, o * BO, a.m, nb, stages, s0, a.os + o * stages * (8 * BO));
 }
 
 template <int WT, int WO, int TT, int TO, int NB, class E>
-__global__ __launch_bounds__(64 * WT * WO, 1) void mm_tile_kernel(MmArgs a, E ep) {
+__global__ __launch_bounds__(64 * WT * WO, 1) void mm_tile_kernel(MmArgs a, E) {
   using Full = MmTile<WT, WO, TT, TO, NB, true, E>;
   using Any = MmTile<WT, WO, TT, TO, NB, false, E>;
   __shared__ typename Full::Lds lds;
   MmWhere w;
   if (!mm_where(a, blockIdx.x, w)) return;
   const int64_t t0 = w.tt * Full::BT, o0 = w.to * Full::BO;
-  if (t0 + Full::BT <= a.T && o0 + Full::BO <= a.m && a.n % kMmK == 0) Full(a, ep, lds, t0, o0, w.part).run();
-  else Any(a, ep, reinterpret_cast<typename Any::Lds&>(lds), t0, o0, w.part).run();
+  MmLate<E> late;
+  if constexpr (!std::is_same<E, MmNoEpi>::value) late = MmLate<E>::template after<MmArgs>();
+  const uint8_t *ts = a.ts + w.tt * a.stages * (8 * Full::BT), *os = a.os + w.to * a.stages * (8 * Full::BO);
+  if (t0 + Full::BT <= a.T && o0 + Full::BO <= a.m && a.n % kMmK == 0) Full(a, late, lds, t0, o0, w.part, ts, os).run();
+  else Any(a, late, reinterpret_cast<typename Any::Lds&>(lds), t0, o0, w.part, ts, os).run();
 }
 
 // Parts of the long axis, added in order.  W: outputs per thread.
