@@ -300,7 +300,7 @@ hipError_t launch_tree_attention(const TrArgs& t, hipStream_t) {
   const int D = a.pg.D, H = 16 * a.nt;
   const int64_t rows = (int64_t)t.tokens * a.group, units = a.batch * a.heads * a.ht;
   if ((1 << a.lgP) != a.pg.P || a.group * a.heads != a.q_heads || (int64_t)a.ht * H < rows || (int64_t)(a.ht - 1) * H >= rows ||
-      (a.nt != 1 && a.nt != 2 && (a.nt != 4 || D == 256)) || (int64_t)a.cap > a.ldt << a.lgP || a.cap > kAtMaxKeys ||
+      (a.nt != 1 && (a.nt != 2 || D == 256)) || (int64_t)a.cap > a.ldt << a.lgP || a.cap > kAtMaxKeys ||
       t.tokens < 1 || t.tokens > kTrTokens || a.wgs < 0 || a.wgs % 8 || (a.wgs > 0 && !a.part))
     return bad("tree attention geometry (group %lld, tokens %lld)", a.group, t.tokens);
   const int join = tr_join_rows(units, a.nt, D);

@@ -48,12 +48,9 @@ __device__ __forceinline__ TrSeen tr_seen(int64_t mask, int ctx, int window) {
   return s;
 }
 
-// The value of a code of a block with a scale's byte.
-__device__ __forceinline__ float tr_value(uint32_t code, uint32_t byte) {
-  const uint32_t m = code & 7u;
-  const float v = m < 4 ? 0.5f * (float)m : m < 6 ? (float)m - 2.f : m == 6 ? 4.f : 6.f;
-  const float s = byte == 255u ? __uint_as_float(0x7fc00000u) : mx_scale(byte);
-  return (code & 8u ? -v : v) * s;
+__device__ __forceinline__ bool tr_sees(const TrSeen& z, int key, int ctx) {
+  const int j = key - ctx;
+  return j < 0 ? key >= z.from : ((j < 32 ? z.lo >> (j & 31) : z.hi >> (j & 31)) & 1u) != 0;
 }
 
 // A unit's row: its row of the batch's and its query head; false past the last.
@@ -151,62 +148,72 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
     a.who[b * units + u] = make_int2((int)at_slot(number, g0, total, wgs),
                                      te == tiles ? 0 : at_owner(g0 + tiles - 1, total, wgs) - number);
 
-  const int64_t pbytes = a.pg.bytes();
-  const int32_t* table = a.table + b * a.ldt;
+  // Places in a page, with the dimension known; of the 16 tokens from p on, keys and
+  // values of either kind lie p times as many bytes into their part of it.
+  const KvPage pp{D, a.pg.P};
+  const int64_t pbytes = pp.bytes(), stride = a.heads * pbytes;
+  const uint8_t* head = a.cache + h * pbytes;
+  typedef const __attribute__((address_space(4))) int32_t* Table;  // not written while this runs: scalar loads
+  const Table table = (Table)(a.table + b * a.ldt);
+  const uint32_t pages = (uint32_t)(a.pages < kAtMaxKeys ? a.pages : kAtMaxKeys);
   int k0 = s0 + tb * kAtTile + wave * kAtKeys;
   const int kend = s0 + te * kAtTile < n ? s0 + te * kAtTile : n;
   // Operands of 32 keys, 16 of them from one page, fetched a step ahead as in
   // the attention of one token.  Where there is no key, or no page, page 0 is read and
   // masked below.
-  int page[2], pg[2];
+  int page[2];
   bool ok[2];
+  const uint8_t *code[2], *scale[2];  // of the 16 keys: in the keys' codes; from the page's beginning on in scales
   mxi4 kw[2][NQ];
   uint32_t vw[2][KW], vs[2];
   int ks[2][NQ];
+  const int blk0 = D == 64 ? (g & 1) : g;  // D = 64: both halves of the lanes hold the 64 values
+  uint32_t kc_at = c * (D / 2) + 16 * blk0, ks_at = (uint32_t)pp.kscale(0) + c * (D / 32) + blk0;
+  uint32_t vc_at = (uint32_t)pp.vcode(0, 0) + g * (2 * D) + c * (D / 8);
+  uint32_t vs_at = (uint32_t)pp.vscale(0, 0) + g * (D / 8) + (c * D / 512) * 4;
   auto look_up = [&](int k) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) page[t] = table[(k + 16 * t < n ? k + 16 * t : n - 1) >> a.lgP];
   };
   auto fetch_keys = [&](int k) {  // looked up before; looks up the next
+    asm volatile("" : "+v"(kc_at), "+v"(ks_at));  // offsets of 32 bits stay such
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      pg[t] = __builtin_amdgcn_readfirstlane(page[t]);
-      ok[t] = pg[t] >= 0 && pg[t] < a.pages && k + 16 * t < n;
-      pg[t] = ok[t] ? pg[t] : 0;
-      const uint8_t* pb = a.cache + ((int64_t)pg[t] * a.heads + h) * pbytes;
-      const int p = (k + 16 * t) & (a.pg.P - 1);
+      const int pg = __builtin_amdgcn_readfirstlane(page[t]);
+      ok[t] = (uint32_t)pg < pages && k + 16 * t < n;
+      const uint8_t* pb = head + (uint64_t)(uint32_t)(ok[t] ? pg : 0) * stride;
+      const uint32_t p = (uint32_t)(k + 16 * t) & (uint32_t)(a.pg.P - 1);
+      code[t] = pb + p * (D / 2);
+      scale[t] = pb + p * (D / 32);
 #pragma unroll
       for (int e = 0; e < NQ; ++e) {
-        const int blk = D == 64 ? (g & 1) : 4 * e + g;  // D = 64: both halves of the lanes hold the 64 values
-        kw[t][e] = *reinterpret_cast<const mxi4*>(pb + a.pg.kcode(p) + (uint32_t)(c * (D / 2) + 16 * blk));
-        ks[t][e] = pb[a.pg.kscale(p) + (uint32_t)(c * (D / 32) + blk)];
+        kw[t][e] = *reinterpret_cast<const mxi4*>(code[t] + 64 * e + kc_at);
+        ks[t][e] = *(scale[t] + 4 * e + ks_at);
       }
     }
     look_up(k + kAtTile);
   };
-  auto fetch_values = [&](int k) {
+  auto fetch_values = [&]() {  // of the keys fetched last
+    asm volatile("" : "+v"(vc_at), "+v"(vs_at));
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const uint8_t* pb = a.cache + ((int64_t)pg[t] * a.heads + h) * pbytes;
-      const int p = (k + 16 * t) & (a.pg.P - 1);
-      const uint8_t* vp = pb + a.pg.vcode(p, 0) + (uint32_t)(g * (2 * D) + c * (D / 8));
       if constexpr (D == 64) {
-        const uint2 y = *reinterpret_cast<const uint2*>(vp);
+        const uint2 y = *reinterpret_cast<const uint2*>(code[t] + vc_at);
         vw[t][0] = y.x; vw[t][1] = y.y;
       } else {
 #pragma unroll
         for (int q = 0; q < KW / 4; ++q) {
-          const uint4 y = reinterpret_cast<const uint4*>(vp)[q];
+          const uint4 y = *reinterpret_cast<const uint4*>(code[t] + 16 * q + vc_at);
           vw[t][4 * q] = y.x; vw[t][4 * q + 1] = y.y; vw[t][4 * q + 2] = y.z; vw[t][4 * q + 3] = y.w;
         }
       }
-      vs[t] = *reinterpret_cast<const uint32_t*>(pb + a.pg.vscale(p, 0) + (uint32_t)(g * (D / 8) + (c * D / 512) * 4));
+      vs[t] = *reinterpret_cast<const uint32_t*>(scale[t] + vs_at);
     }
   };
   if (k0 < kend) {
     look_up(k0);
     fetch_keys(k0);
-    fetch_values(k0);
+    fetch_values();
   }
   // what the rows see; one that sees nothing is given all here and cleared at the end
   if (tid == 0) far[0] = 0;
@@ -267,16 +274,17 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
                                : *reinterpret_cast<const int*>(&qb[16 * t + c][4 * e + g][4 * q]);
   const uint8_t* ql = qs + lane * 16;  // g * 256 + c * 16
   auto query = [&](int t, int e, int w) {
-    const mxi4 x = *reinterpret_cast<const mxi4*>(ql + ((t * NP + w) * NB + 4 * e) * 256);
-    return mxi8{x[0], x[1], x[2], x[3], 0, 0, 0, 0};
+    return *reinterpret_cast<const mxi4*>(ql + ((t * NP + w) * NB + 4 * e) * 256);
   };
   const int reach = far[0];  // from here to the context's end nothing is masked
 
   mxf4 o[NT][R];
-  float m[NT], l[NT];  // l: of the lane's keys
+  // m: the maximum, 0 while no key was seen; then least is -infinity, afterwards 0; l: of the lane's keys
+  float m[NT], least[NT], l[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    m[t] = -INFINITY;
+    m[t] = 0.f;
+    least[t] = -INFINITY;
     l[t] = 0.f;
 #pragma unroll
     for (int j = 0; j < R; ++j) o[t][j] = mxf4{0.f, 0.f, 0.f, 0.f};
@@ -288,31 +296,42 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
     asm volatile("" ::: "memory");  // the queries stay in LDS
     // scores: column c, keys 16 t + 4 g + i
     float s[NT][2][4];
+    // A piece takes as long to come from LDS as six of these products take, so
+    // four are on their way ahead (left to itself, the compiler waits for each: four
+    // sequences of 32768 tokens and 64 drafts took 646 us, so 584).
+    mxf4 acc[NT][2];
 #pragma unroll
-    for (int u = 0; u < NT; ++u) {
-      mxf4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    for (int u = 0; u < NT; ++u) acc[u][0] = acc[u][1] = mxf4{0.f, 0.f, 0.f, 0.f};
+    constexpr int kAhead = 4, kReads = NQ * NP * NT;
+    mxi4 Q[kReads];  // piece i: column tile i % NT, product i / NT of them
 #pragma unroll
-      for (int e = 0; e < NQ; ++e)
+    for (int i = 0; i < kAhead; ++i) Q[i] = query(i % NT, i / NT / NP, i / NT % NP);
 #pragma unroll
-        for (int w = 0; w < NP; ++w) {
-          const mxi8 Q = query(u, e, w);
+    for (int i = 0; i < kReads; ++i) {
+      const int j = i + kAhead, u = i % NT, e = i / NT / NP, w = i / NT % NP;
+      __builtin_amdgcn_sched_barrier(0);
+      if (j < kReads) Q[j] = query(j % NT, j / NT / NP, j / NT % NP);
+      __builtin_amdgcn_sched_barrier(0);
+      const mxi8 B = {Q[i][0], Q[i][1], Q[i][2], Q[i][3], 0, 0, 0, 0};
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const mxi8 K = {kw[t][e][0], kw[t][e][1], kw[t][e][2], kw[t][e][3], 0, 0, 0, 0};
-            acc[t] = at_score(K, Q, acc[t], ks[t][e], qsc[u][e][w / 4], w);
-          }
-        }
+      for (int t = 0; t < 2; ++t) {
+        const mxi8 K = {kw[t][e][0], kw[t][e][1], kw[t][e][2], kw[t][e][3], 0, 0, 0, 0};
+        acc[u][t] = at_score(K, B, acc[u][t], ks[t][e], qsc[u][e][w / 4], w);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[u][t][i] = acc[t][i];
-    }
+        for (int i = 0; i < 4; ++i) s[u][t][i] = acc[u][t][i];
     // Masked keys: scores to -infinity, values that no row sees to zero.  A value that
     // some rows see and others do not is multiplied by their zeros too, so one
     // that is not finite (its scale's byte 253 or more can be) is taken out and
     // added below to the rows that see it.
-    uint32_t odd[2] = {0u, 0u};  // such values' scales, else 0
-    uint64_t keys = 0;           // of the step that have one
+    uint32_t odd = 0u;  // such keys of the lane's block: bit 4 t + i
+    bool any = false;   // of the step's
     if (k0 < reach || k0 + kAtKeys > ctx || !ok[0] || !ok[1]) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -322,17 +341,12 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
           const bool none = key >= n || !ok[t];
 #pragma unroll
           for (int u = 0; u < NT; ++u) {
-            const TrSeen z = seen[16 * u + c];
-            const int j = key - ctx;
-            const bool sees = key < ctx ? key >= z.from : ((j < 32 ? z.lo >> (j & 31) : z.hi >> (j & 31)) & 1) != 0;
-            if (none || !sees) s[u][t][i] = -INFINITY;
+            if (none || !tr_sees(seen[16 * u + c], key, ctx)) s[u][t][i] = -INFINITY;
           }
           const uint32_t byte = vs[t] >> (8 * i) & 255u;
           if (none || byte >= 253u) {
-            if (!none) odd[t] |= byte << (8 * i);
+            if (!none) odd |= 1u << (4 * t + i);
             vs[t] = (vs[t] & ~(255u << (8 * i))) | 127u << (8 * i);
-          }
-          if (none) {
             if constexpr (D == 64) {
               vw[t][i / 2] &= ~(0xffffu << (16 * (i & 1)));
             } else {
@@ -341,9 +355,79 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
             }
           }
         }
-      keys = __builtin_amdgcn_ballot_w64((odd[0] | odd[1]) != 0);
+      any = __builtin_amdgcn_ballot_w64(odd != 0) != 0;
     }
     if constexpr (more) fetch_keys(k0 + kAtTile);
+    // Scores relative to the rows' maxima so far.  Seldom after the first tiles is one
+    // larger; only then are the four lanes of a column compared and the sums rescaled.
+    bool moved = false;
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[u][t][i] -= m[u];
+          top = fmaxf(top, s[u][t][i]);
+        }
+      moved |= top > least[u];
+    }
+    if (__builtin_amdgcn_ballot_w64(moved)) {
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
+        float top = least[u];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, s[u][t][i]);
+        top = at_colmax(top);
+        if (top > -INFINITY) {
+          const float f = __builtin_amdgcn_exp2f(-top);  // where nothing was seen, the sums are 0
+          m[u] += top;
+          least[u] = 0.f;
+          l[u] *= f;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[u][t][i] -= top;
+#pragma unroll
+          for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[u][j][i] *= f;
+        }
+      }
+    }
+    // A probability's first 8 bits, the next ones, the last ones; the last piece is
+    // rounded (of three there is nothing left to round).
+    mxb8 pf[NT][PP];
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      uint32_t w[PP][4];
+      float sum = 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float x[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[e] = __builtin_amdgcn_exp2f(s[u][q / 2][2 * (q & 1) + e]);
+          sum += x[e];
+        }
+#pragma unroll
+        for (int z = 0; z < PP; ++z) {
+          if (z + 1 == PP) {
+            w[z][q] = __builtin_bit_cast(uint32_t, __builtin_convertvector((mxf2{x[0], x[1]}), mxb2));
+          } else {
+            w[z][q] = __builtin_amdgcn_perm(__float_as_uint(x[1]), __float_as_uint(x[0]), 0x07060302u);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x[e] -= __uint_as_float(__float_as_uint(x[e]) & 0xffff0000u);
+          }
+        }
+      }
+      l[u] += sum;
+#pragma unroll
+      for (int z = 0; z < PP; ++z) pf[u][z] = __builtin_bit_cast(mxb8, make_uint4(w[z][0], w[z][1], w[z][2], w[z][3]));
+    }
     // values: keys in pairs, one run of dimensions per lane (of a scale the
     // conversion reads the exponent, so byte 0 is 2^-127 and 255 NaN)
     float vsc[2][4];
@@ -351,7 +435,6 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) vsc[t][i] = __uint_as_float(i == 3 ? vs[t] >> 24 << 23 : (vs[t] >> (8 * i) & 255u) << 23);
-    mxb8 va[R];
 #pragma unroll
     for (int q = 0; q < R / 2; ++q) {  // dimensions 2 q and 2 q + 1 of the run
       uint32_t lo[4], hi[4];
@@ -360,102 +443,73 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
           const int ba = i * (R / 2) + q, bb = (i + 1) * (R / 2) + q;  // bytes of the lane's words
-          uint32_t x = at_bits(at_pair(vw[t][ba / 4], vsc[t][i], ba));
-          uint32_t y = at_bits(at_pair(vw[t][bb / 4], vsc[t][i + 1], bb));
-          if (keys) {  // not the values that are taken out
-            if (odd[t] >> (8 * i) & 255u) x = 0u;
-            if (odd[t] >> (8 * i + 8) & 255u) y = 0u;
-          }
+          const uint32_t x = at_bits(at_pair(vw[t][ba / 4], vsc[t][i], ba));
+          const uint32_t y = at_bits(at_pair(vw[t][bb / 4], vsc[t][i + 1], bb));
           lo[2 * t + i / 2] = __builtin_amdgcn_perm(y, x, 0x05040100u);
           hi[2 * t + i / 2] = __builtin_amdgcn_perm(y, x, 0x07060302u);
         }
-      va[2 * q] = __builtin_bit_cast(mxb8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-      va[2 * q + 1] = __builtin_bit_cast(mxb8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-    }
+      const mxb8 va = __builtin_bit_cast(mxb8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      const mxb8 vb = __builtin_bit_cast(mxb8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
 #pragma unroll
-    for (int u = 0; u < NT; ++u) {
-      float mx = fmaxf(fmaxf(s[u][0][0], s[u][0][1]), fmaxf(s[u][0][2], s[u][0][3]));
-      mx = fmaxf(mx, fmaxf(fmaxf(s[u][1][0], s[u][1][1]), fmaxf(s[u][1][2], s[u][1][3])));
-      mx = fmaxf(at_colmax(mx), m[u]);
-      const float base = mx == -INFINITY ? 0.f : mx;
-      if (__builtin_amdgcn_ballot_w64(mx != m[u])) {  // seldom after the first tiles
-        const float f = __builtin_amdgcn_exp2f(m[u] - base);
-        m[u] = mx;
-        l[u] *= f;
+      for (int z = 0; z < PP; ++z)
 #pragma unroll
-        for (int j = 0; j < R; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[u][j][i] *= f;
-      }
-      // A probability's first 8 bits, the next ones, the last ones
-      uint32_t w[PP][4];
-      float sum = 0.f;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float x[PP][2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float p = __builtin_amdgcn_exp2f(s[u][q / 2][2 * (q & 1) + e] - base);
-          sum += p;
-#pragma unroll
-          for (int z = 0; z < PP; ++z) {
-            x[z][e] = p;
-            p -= __uint_as_float(__float_as_uint(p) & 0xffff0000u);
-          }
+        for (int u = 0; u < NT; ++u) {
+          o[u][2 * q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, pf[u][z], o[u][2 * q], 0, 0, 0);
+          o[u][2 * q + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, pf[u][z], o[u][2 * q + 1], 0, 0, 0);
         }
+    }
+    if (any) {
+      // The values that were taken out, a key at a time, from the cache again: a
+      // product of that key alone, added where the row sees it.
+#pragma unroll 1
+      for (int kk = 0; kk < 32; ++kk) {
+        const int tt = kk >> 4, gg = kk >> 2 & 3, i = kk & 3, key = k0 + kk;
+        if (!__builtin_amdgcn_ballot_w64(g == gg && (odd >> (4 * tt + i) & 1u) != 0)) continue;
+        const uint8_t* pb = head + (uint64_t)(uint32_t)table[key >> a.lgP] * stride;
+        const int p = key & (a.pg.P - 1);
+        const uint32_t byte = pb[pp.vscale(p, c * D / 512)];
+        const bool keep = g == gg && byte >= 253u;
+        uint32_t run[KW / 4 + 1] = {};  // the lane's run of the key, eight codes a word
+        if (keep) {
+          const uint8_t* vp = pb + pp.vcode(p, c);
+          if constexpr (D == 64) run[0] = *reinterpret_cast<const uint16_t*>(vp);
 #pragma unroll
-        for (int z = 0; z < PP; ++z)
-          w[z][q] = z == 1 && PP == 2 ? mx_bf16(x[z][0]) | mx_bf16(x[z][1]) << 16  // the last piece is rounded
-                                      : __builtin_amdgcn_perm(__float_as_uint(x[z][1]), __float_as_uint(x[z][0]), 0x07060302u);
-      }
-      l[u] += sum;
+          for (int q = 0; q < KW / 4; ++q) run[q] = reinterpret_cast<const uint32_t*>(vp)[q];
+        }
+        const float scale = __uint_as_float(byte << 23);
+        const uint32_t half = keep ? (i & 1 ? 0xffff0000u : 0x0000ffffu) : 0u;  // of the pair of keys
+        const int pair = 2 * tt + i / 2;
+        bool sees[NT];
 #pragma unroll
-      for (int z = 0; z < PP; ++z) {
-        const mxb8 pf = __builtin_bit_cast(mxb8, make_uint4(w[z][0], w[z][1], w[z][2], w[z][3]));
+        for (int u = 0; u < NT; ++u) sees[u] = tr_sees(seen[16 * u + c], key, ctx);
 #pragma unroll
-        for (int j = 0; j < R; ++j) o[u][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va[j], pf, o[u][j], 0, 0, 0);
-      }
-      if (keys) {
-        // One such key at a time: its values to the lanes of its products, times
-        // its probabilities, added where the row sees it.
-        for (int kk = 0; kk < 32; ++kk) {
-          const int tt = kk >> 4, gg = kk >> 2 & 3, i = kk & 3;
-          const bool mine = g == gg && ((tt ? odd[1] : odd[0]) >> (8 * i) & 255u) != 0;
-          if (!__builtin_amdgcn_ballot_w64(mine)) continue;
-          float p = 0.f;
+        for (int q = 0; q < R / 2; ++q) {
+          const uint32_t x = at_bits(at_pair(run[q / 4], scale, q));
+          const uint32_t xl = __builtin_amdgcn_perm(x, x, 0x01000100u) & half, xh = __builtin_amdgcn_perm(x, x, 0x03020302u) & half;
+          // an infinity times a piece that is 0 would be NaN: only the first piece, which is not, meets it
+          auto place = [&](uint32_t y, bool first) {
+            const uint32_t inf = 0x7f807f80u & half;
+            y = !first && (y & inf) == inf ? 0u : y;
+            return __builtin_bit_cast(mxb8, make_uint4(pair == 0 ? y : 0u, pair == 1 ? y : 0u, pair == 2 ? y : 0u, pair == 3 ? y : 0u));
+          };
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int u = 0; u < NT; ++u) {
+            mxf4 x0 = {0.f, 0.f, 0.f, 0.f}, x1 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (t == tt && e == i) p = s[u][t][e];
-          p = __shfl(p, 16 * gg + c);
-          const bool sees = p != -INFINITY;
-          p = __builtin_amdgcn_exp2f(p - base);
-          uint32_t run[KW / 4 + 1] = {};  // the lane's run of the key, eight codes a word
+            for (int z = 0; z < PP; ++z) {
+              x0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(place(xl, z == 0), pf[u][z], x0, 0, 0, 0);
+              x1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(place(xh, z == 0), pf[u][z], x1, 0, 0, 0);
+            }
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (t == tt && e == i) {
-                if constexpr (D == 64) run[0] = vw[t][e / 2] >> (16 * (e & 1));
-#pragma unroll
-                for (int q = 0; q < KW / 4; ++q) run[q] = vw[t][e * (KW / 4) + q];
-              }
-          // output (row c, dimension (4 g + e) R + j) wants run 4 g + e, which lane 16 gg + 4 g + e has
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int from = 16 * gg + 4 * g + e;
-            const uint32_t byte = __shfl(tt ? odd[1] : odd[0], from) >> (8 * i) & 255u;
-#pragma unroll
-            for (int j = 0; j < R; ++j) {
-              const float v = tr_value(__shfl(run[j / 8], from) >> (4 * (j & 7)) & 15u, byte);
-              if (sees && byte) o[u][j][e] += p * v;
+            for (int e = 0; e < 4; ++e) {
+              o[u][2 * q][e] += sees[u] ? x0[e] : 0.f;
+              o[u][2 * q + 1][e] += sees[u] ? x1[e] : 0.f;
             }
           }
         }
       }
     }
-    if constexpr (more) fetch_values(k0 + kAtTile);
+    if constexpr (more) fetch_values();
   };
   for (; k0 + kAtTile < kend; k0 += kAtTile) step(std::false_type{});
   if (k0 < kend) step(std::true_type{});
@@ -467,7 +521,7 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
     __syncthreads();  // the sums go where the queries were, or the tile before
     const float sum = at_colsum(l[u16]);
     if (lane < 16) {
-      ms[wave][lane] = m[u16];
+      ms[wave][lane] = least[u16] == 0.f ? m[u16] : -INFINITY;
       ls[wave][lane] = sum;
     }
 #pragma unroll
@@ -577,9 +631,8 @@ hipError_t tr_launch(const TrArgs& t, hipStream_t s) {
   const AtArgs& a = t.at;
   const int64_t units = a.batch * a.heads * a.ht;
   const dim3 grid((unsigned)(a.wgs ? a.wgs : units));
-  if (a.nt == 1) tr_launch<D, 1>(t, grid, s);
-  else if (a.nt == 2 || D == 256) tr_launch<D, 2>(t, grid, s);
-  else if constexpr (D != 256) tr_launch<D, 4>(t, grid, s);
+  if (D == 256 || a.nt == 1) tr_launch<D, 1>(t, grid, s);
+  else if constexpr (D != 256) tr_launch<D, 2>(t, grid, s);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.wgs) return e;
   const int rows = tr_join_rows(units, a.nt, D);

@@ -499,10 +499,16 @@ struct TrArgs {
   int tokens;
 };
 inline int64_t tr_rows(int tokens, int q_heads, int heads) { return (int64_t)tokens * (q_heads / heads); }
-// Column tiles of 16 rows of a workgroup.
-inline int tr_nt(int64_t rows, int head_dim) { return rows <= 16 ? 1 : rows <= 32 || head_dim == 256 ? 2 : 4; }
+// Column tiles of 16 rows of a workgroup: one where a second would be empty.  Two share
+// the conversion of the values and take 0.82 of one's time each, so three rather go
+// one by one (64 rows over 20000 tokens, eight sequences: two at a time 108 us, one
+// 113; 40 rows, sixteen of 300 to 3000: 33 and 30).  A head of 256 has registers for one.
+inline int tr_nt(int64_t rows, int head_dim) {
+  const int64_t tiles = (rows + 15) / 16;
+  return tiles == 1 || tiles == 3 || head_dim == 256 ? 1 : 2;
+}
 // Workgroups that the chip holds at once, by the registers of their kernel.
-constexpr int tr_workgroups(int, int) { return 512; }
+constexpr int tr_workgroups(int head_dim, int nt) { return nt == 1 && head_dim != 256 ? 768 : 512; }
 // Keys before the first tile of a context of ctx tokens with a window (a row sees
 // one draft at least), and the tiles of n keys after them.
 __host__ __device__ inline int tr_skip(int ctx, int window) {
