@@ -222,9 +222,9 @@ hipError_t launch_kv_read(const KvArgs& a, hipStream_t) { return walk_kv(a); }
 
 // The deal of a batch's tiles to workgroups: every part has a slot of its own, and
 // the join finds the workgroups that have one.
-static hipError_t walk_deal(const std::vector<int>& tiles, int64_t units, int of) {
+static hipError_t walk_deal(const std::vector<int>& tiles, int64_t units, int of, int lead) {
   int64_t total = 0;
-  for (int t : tiles) total += at_cost(t) * units;
+  for (int t : tiles) total += (t > 0 ? t + lead : 0) * units;
   if (!total) return hipSuccess;
   const int wgs = at_dealt(total, of);
   std::vector<int> owner, uses(2 * (size_t)wgs, 0);
@@ -235,7 +235,7 @@ static hipError_t walk_deal(const std::vector<int>& tiles, int64_t units, int of
   int64_t g0 = 0;
   for (size_t b = 0; b < tiles.size(); ++b)
     for (int64_t u = 0; u < units && tiles[b]; ++u, g0 += tiles[b]) {
-      g0 += kAtLead;  // the lead's places come before the first tile
+      g0 += lead;  // the lead's places come before the first tile
       const int64_t g1 = g0 + tiles[b] - 1;
       if (at_owner(g0, total, wgs) != owner[(size_t)g0] || at_owner(g1, total, wgs) != owner[(size_t)g1])
         return bad("attention owner of tile %lld of %lld", g0, total);
@@ -288,7 +288,7 @@ hipError_t launch_paged_attention(const AtArgs& a, hipStream_t) {
       const int64_t n = seed == 0 ? 0 : seed == 1 ? a.cap : (b * 7919 + seed * 104729) % (a.cap + 1) >> (seed * b % 5);
       tiles.push_back(at_tiles((int)n, seed == 3 ? 100 : 0));
     }
-    const hipError_t e = walk_deal(tiles, (int64_t)a.heads * a.ht, a.wgs);
+    const hipError_t e = walk_deal(tiles, (int64_t)a.heads * a.ht, a.wgs, kAtLead);
     if (e != hipSuccess) return e;
   }
   return walk_loads(pg);
@@ -325,7 +325,7 @@ hipError_t launch_tree_attention(const TrArgs& t, hipStream_t) {
         return bad("tree attention skips %lld of %lld keys", skip, ctx);
       tiles.push_back(tr_tiles(n, skip));
     }
-    const hipError_t e = walk_deal(tiles, (int64_t)a.heads * a.ht, a.wgs);
+    const hipError_t e = walk_deal(tiles, (int64_t)a.heads * a.ht, a.wgs, kTrLead);
     if (e != hipSuccess) return e;
   }
   return walk_loads(a.pg);
@@ -336,8 +336,15 @@ hipError_t launch_tree_attention(const TrArgs& t, hipStream_t) {
 hipError_t launch_kv_move(const KpMove& a, hipStream_t) {
   dry_launch();
   const int D = a.pg.D;
-  if ((1 << a.lgP) != a.pg.P || a.tokens < 1 || !launchable((a.tokens * a.heads + 15) / 16, kMxThreads))
+  const int64_t rows = kp_runs(a.tokens) * a.heads;
+  if ((1 << a.lgP) != a.pg.P || a.tokens < 1 || kKpFew % (kKpThreads / 16) || !launchable(a.heads, kKpThreads) ||
+      !launchable(rows / (kMxThreads / 16) + 1, kMxThreads))
     return bad("cache move of %lld tokens", a.tokens, 0);
+  if (a.tokens > kKpFew) {  // rows past the last run stay in the workspace only if they move nothing
+    const int64_t last = (rows - 1) * kKpRun * kp_row_bytes(D) + kKpRun * kp_row_bytes(D);
+    if (!a.ws || last > (int64_t)kp_move_bytes(a.tokens, a.heads, D) || rows >= (int64_t)1 << 32)
+      return bad("cache move workspace of %lld bytes", last, 0);
+  }
   std::vector<uint8_t> cover((size_t)kp_row_bytes(D), 0);
   for (int r = 0; r < 16; ++r)
     for (int i = 0; i < D / 32; ++i) {

@@ -55,32 +55,83 @@ struct KpWord {
   }
 };
 
-__device__ __forceinline__ bool kp_in(const KpMove& a, int64_t slot) { return slot >= 0 && (slot >> a.lgP) < a.pages; }
+// The slots of a pair, or one outside the cache: not moved.
+__device__ __forceinline__ bool kp_pair(const KpMove& a, int64_t tok, int64_t* src, int64_t* dst) {
+  if (tok >= a.tokens) return false;
+  *src = a.src[tok];
+  *dst = a.dst[tok];
+  return *src >= 0 && (*src >> a.lgP) < a.pages && *dst >= 0 && (*dst >> a.lgP) < a.pages;
+}
+template <int D>
+__device__ __forceinline__ uint8_t* kp_head(const KpMove& a, int64_t slot, int h, int* t) {
+  *t = (int)(slot & (a.pg.P - 1));
+  return a.cache + ((slot >> a.lgP) * a.heads + h) * KvPage{D, a.pg.P}.bytes();
+}
 
-// Tokens to the workspace and from it, one launch each: everything is read
-// before anything is written.
+// Up to kKpFew tokens: a workgroup for each head reads them all into registers, then
+// writes them.
+template <int D>
+__global__ __launch_bounds__(kKpThreads) void kp_few_kernel(KpMove a) {
+  constexpr int N = kKpFew / (kKpThreads / 16);
+  const int h = blockIdx.x, r = threadIdx.x & 15;
+  const KvPage pg{D, a.pg.P};
+  KpWord<D> w[N];
+  int64_t src, dst[N];
+  bool ok[N];
+  int t;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    ok[i] = kp_pair(a, i * (kKpThreads / 16) + threadIdx.x / 16, &src, &dst[i]);
+    if (ok[i]) {
+      const uint8_t* head = kp_head<D>(a, src, h, &t);
+      w[i].load(head, pg, t, r);
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // every wavefront has what it read
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (ok[i]) {
+      uint8_t* head = kp_head<D>(a, dst[i], h, &t);
+      w[i].store(head, pg, t, r);
+    }
+}
+
+// More: tokens to the workspace and from it, one launch each, so that everything is
+// read before anything is written; 16 lanes take kKpRun tokens of a head, whose loads
+// travel together (15000 tokens of 8 heads of 128, one at a time 14.7 and 12.6 us).
 template <int D, bool OUT>
 __global__ __launch_bounds__(kMxThreads) void kp_move_kernel(KpMove a) {
-  const int64_t row = (int64_t)blockIdx.x * (kMxThreads / 16) + threadIdx.x / 16;
-  const int r = threadIdx.x & 15;
-  const int64_t tok = row / a.heads;
-  if (tok >= a.tokens) return;
-  const int h = (int)(row - tok * a.heads);
-  const int64_t src = a.src[tok], dst = a.dst[tok];
-  if (!kp_in(a, src) || !kp_in(a, dst)) return;
+  const uint32_t row = blockIdx.x * (kMxThreads / 16) + threadIdx.x / 16, run = row / (uint32_t)a.heads;
+  const int h = (int)(row - run * (uint32_t)a.heads), r = threadIdx.x & 15;
   const KvPage pg{D, a.pg.P};
-  const int64_t slot = OUT ? dst : src;
-  uint8_t* head = a.cache + ((slot >> a.lgP) * a.heads + h) * pg.bytes();
-  const int t = (int)(slot & (a.pg.P - 1));
-  uint8_t* keep = a.ws + row * kp_row_bytes(D);
-  KpWord<D> w;
-  if constexpr (OUT) {
-    w.load(keep, r);
-    w.store(head, pg, t, r);
-  } else {
-    w.load(head, pg, t, r);
-    w.store(keep, r);
-  }
+  KpWord<D> w[kKpRun];
+  int64_t src[kKpRun], dst[kKpRun];
+  bool ok[kKpRun];
+  int t;
+#pragma unroll
+  for (int i = 0; i < kKpRun; ++i) ok[i] = kp_pair(a, (int64_t)run * kKpRun + i, &src[i], &dst[i]);
+  uint8_t* keep = a.ws + (int64_t)row * kKpRun * kp_row_bytes(D);
+#pragma unroll
+  for (int i = 0; i < kKpRun; ++i)
+    if (ok[i]) {
+      if constexpr (OUT) {
+        w[i].load(keep + i * kp_row_bytes(D), r);
+      } else {
+        const uint8_t* head = kp_head<D>(a, src[i], h, &t);
+        w[i].load(head, pg, t, r);
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < kKpRun; ++i)
+    if (ok[i]) {
+      if constexpr (OUT) {
+        uint8_t* head = kp_head<D>(a, dst[i], h, &t);
+        w[i].store(head, pg, t, r);
+      } else {
+        w[i].store(keep + i * kp_row_bytes(D), r);
+      }
+    }
 }
 
 // A row of the table for each child: its parent's pages, which it holds too.
@@ -226,7 +277,12 @@ __global__ __launch_bounds__(kMxThreads) void kp_copy_kernel(KpReserve a) {
 
 template <int D>
 void kp_move(const KpMove& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.tokens * a.heads + kMxThreads / 16 - 1) / (kMxThreads / 16)));
+  if (a.tokens <= kKpFew) {
+    kp_few_kernel<D><<<dim3((unsigned)a.heads), kKpThreads, 0, s>>>(a);
+    return;
+  }
+  const int64_t rows = kp_runs(a.tokens) * a.heads;
+  const dim3 grid((unsigned)((rows + kMxThreads / 16 - 1) / (kMxThreads / 16)));
   kp_move_kernel<D, false><<<grid, kMxThreads, 0, s>>>(a);
   kp_move_kernel<D, true><<<grid, kMxThreads, 0, s>>>(a);
 }

@@ -101,7 +101,7 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
   if (a.wgs) {
     AtShare s;
     // neighbours in the deal, which read the same keys, on one XCD
-    if (!at_share(a.batch, a.wgs, units, share, [&](int64_t i) { return at_cost(tr_tiles_of(t, i)); },
+    if (!at_share(a.batch, a.wgs, units, share, [&](int64_t i) { return tr_cost(tr_tiles_of(t, i)); },
                   [](int n) { return tr_number(blockIdx.x, n); }, s))
       return;
     total = s.total;
@@ -113,7 +113,7 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
     number = s.w;
   } else {
     b = blockIdx.x / (uint32_t)units;
-    const int cost = at_cost(tr_tiles_of(t, b)), u = (int)(blockIdx.x - (uint32_t)b * (uint32_t)units);
+    const int cost = tr_cost(tr_tiles_of(t, b)), u = (int)(blockIdx.x - (uint32_t)b * (uint32_t)units);
     pos = (int64_t)u * cost;
     end = pos + cost;
     if (pos == end) {  // no key: the unit's rows get what an empty sum gives
@@ -131,14 +131,14 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
   // the part's keys: tiles [tb, te) of unit u of sequence b
   const int ctx = a.lens[b], n = tr_keys(t, b);
   const int s0 = tr_skip(ctx, a.window), tiles = tr_tiles(n, s0);
-  const int cost = at_cost(tiles);
+  const int cost = tr_cost(tiles);
   if (pos >= base + (int64_t)cost * units) {  // on to the next sequence (one without keys has no place)
     base += (int64_t)cost * units;
     ++b;
     continue;
   }
   const int u = (int)((pos - base) / cost);
-  const int64_t g0 = base + (int64_t)u * cost + kAtLead;  // place of the unit's first tile
+  const int64_t g0 = base + (int64_t)u * cost + kTrLead;  // place of the unit's first tile
   const int tb = pos > g0 ? (int)(pos - g0) : 0;
   const int te = end - g0 < tiles ? (int)(end - g0) : tiles;
   pos = g0 + tiles < end ? g0 + tiles : end;
@@ -232,21 +232,30 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
   }
   // queries: rotated, times the scale, in pieces
   const float sl = a.scale * 1.44269504088896341f;  // scores in units of log2
-  for (int r = tid / LPH; r < H; r += kAtThreads / LPH) {
-    const int e0 = (tid % LPH) * kMxPerLane;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  constexpr int kPass = kAtThreads / LPH, kRows = H < kPass ? 1 : H / kPass;  // rows of a pass, passes
+  const int e0 = (tid % LPH) * kMxPerLane;
+  float qv[kRows][8];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {  // all on their way before the first is waited for
     int64_t row;
     int head;
-    if (tr_row(t, b, h, r0 + r, &row, &head)) {
-      at_load8(a.qt, a.q, row * a.ldq + (int64_t)head * D + e0, v);
-      if (a.d) {
-        if (a.signs)  // after the query: registers are short here
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] *= a.signs[e0 + e];
-        mx_hadamard<D>(v, lane);
+    for (int e = 0; e < 8; ++e) qv[i][e] = 0.f;
+    if (tid / LPH < H && tr_row(t, b, h, r0 + tid / LPH + i * kPass, &row, &head))
+      at_load8(a.qt, a.q, row * a.ldq + (int64_t)head * D + e0, qv[i]);
+  }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= a.rnorm;
-      }
+  for (int i = 0; i < kRows; ++i) {
+    const int r = tid / LPH + i * kPass;
+    if (r >= H) break;  // uniform over the row's lanes
+    float (&v)[8] = qv[i];
+    if (a.d) {
+      if (a.signs)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= a.signs[e0 + e];
+      mx_hadamard<D>(v, lane);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= a.rnorm;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= sl;

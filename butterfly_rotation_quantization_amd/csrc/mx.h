@@ -317,11 +317,19 @@ struct KpMove {
   int lgP;
   int64_t pages;
   uint8_t* cache;
-  uint8_t* ws;           // [tokens * heads] rows
+  uint8_t* ws;           // rows: runs of kKpRun tokens of a head, the heads, then the next run
 };
 // Bytes of a row of the workspace: the codes and scales of a token's head.
 __host__ __device__ constexpr int64_t kp_row_bytes(int D) { return D + D / 16; }
 constexpr int64_t kKpTokens = (int64_t)1 << 27;  // heads of tokens of a move: within 2^31 threads
+constexpr int kKpThreads = 1024;  // of a workgroup that does by itself what has an order: a move, a reservation
+constexpr int kKpFew = 512;       // tokens that such a workgroup holds in registers, of one head
+constexpr int kKpRun = 4;         // tokens of a head that 16 lanes move at a time
+inline int64_t kp_runs(int64_t tokens) { return (tokens + kKpRun - 1) / kKpRun; }
+// Bytes of a move's workspace.
+inline size_t kp_move_bytes(int64_t tokens, int64_t heads, int D) {
+  return tokens <= kKpFew ? 0 : (size_t)(kp_runs(tokens) * kKpRun * heads * kp_row_bytes(D) + 15) / 16 * 16;
+}
 
 struct KpFork {
   const int32_t *table, *lens, *parents;
@@ -334,8 +342,6 @@ struct KpFree {
   int32_t* refs;
   const int32_t* rows;   // [n], or null: all rows
 };
-
-constexpr int kKpThreads = 1024;  // of the workgroup that decides a reservation
 
 struct KpReserve {
   uint8_t* cache;
@@ -509,6 +515,10 @@ inline int tr_nt(int64_t rows, int head_dim) {
 }
 // Workgroups that the chip holds at once, by the registers of their kernel.
 constexpr int tr_workgroups(int head_dim, int nt) { return nt == 1 && head_dim != 256 ? 768 : 512; }
+// Empty places ahead of a unit's tiles (kAtLead): beginning one takes longer here, with
+// more queries to bring in and more sums to hand on.
+constexpr int kTrLead = 7;
+__host__ __device__ inline int tr_cost(int tiles) { return tiles > 0 ? tiles + kTrLead : 0; }
 // Keys before the first tile of a context of ctx tokens with a window (a row sees
 // one draft at least), and the tiles of n keys after them.
 __host__ __device__ inline int tr_skip(int ctx, int window) {

@@ -446,7 +446,7 @@ size_t brq_kv_move_workspace_bytes(int64_t tokens, int32_t heads, int32_t head_d
   if (tokens <= 0 || heads < 1 || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
       tokens > kKpTokens / heads)
     return 0;
-  return (size_t)(tokens * heads * kp_row_bytes(head_dim) + 15) / 16 * 16;
+  return kp_move_bytes(tokens, heads, head_dim);
 }
 
 brq_status brq_kv_move(uint8_t* cache, const int64_t* src, const int64_t* dst, int64_t tokens, int32_t heads,
