@@ -161,8 +161,8 @@ hipError_t launch_mx_grouped(const GmArgs& g, const MmEpi& e, hipStream_t) {
                           : seed == 3 ? (e * 7919 + 13) % (2 * share + 2) : seed == 4 ? R + 1 : (e + 1 == g.groups ? left : 1);
         int b, end;
         gm_rows((int)at - (seed == 3 && e == 0 ? 5 : 0), (int)(at + n), (int)a.T, &b, &end);
-        if (b < 0 || end < b || end > a.T) return bad("mx grouped rows [%lld, %lld)", b, end);
-        units += (end - b + R - 1) / R;
+        if (b < 0 || b > a.T || end < 0 || end > a.T || (seed != 3 && end < b)) return bad("mx grouped rows [%lld, %lld)", b, end);
+        units += end > b ? (end - b + R - 1) / R : 0;
         at = end;
       }
       if (units > gm_units(a.T, g.groups, R)) return bad("mx grouped units %lld of %lld rows", units, R);

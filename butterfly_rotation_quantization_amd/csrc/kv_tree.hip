@@ -40,7 +40,7 @@ __device__ __forceinline__ TrSeen tr_seen(int64_t mask, int ctx, int window) {
   s.from = 0;
   if (window > 0) {
     const int64_t from = (int64_t)ctx + ones - window;
-    s.from = from > 0 ? (int)from : 0;
+    s.from = from <= 0 ? 0 : from < INT32_MAX ? (int)from : INT32_MAX;
     for (int drop = ones - window; drop > 0; --drop) m &= m - 1;  // the lowest set bit
   }
   s.lo = (uint32_t)m;

@@ -195,10 +195,11 @@ struct GmArgs {
   int rows;              // of a unit: 16, 32 or 64 of the stream, a tile's 128 or 256
 };
 
-// Rows [b, end) of a group from its two offsets: within the T rows there are.
+// Rows [b, end) of a group from its two offsets, within the T rows there are; of
+// offsets that do not decrease.
 __host__ __device__ inline void gm_rows(int from, int to, int T, int* b, int* end) {
   *b = from < 0 ? 0 : from < T ? from : T;
-  *end = to < *b ? *b : to < T ? to : T;
+  *end = to < 0 ? 0 : to < T ? to : T;
 }
 // The most units of R rows that the groups can have: each begins at most one
 // that is not whole.

@@ -19,18 +19,38 @@ struct GmUnit {
   int unit;        // the one, of the group's
 };
 // The groups, one to a lane and 64 at a time: their rows, their units and the
-// inclusive sum of these.  Every lane of a wavefront makes the same calls.
+// inclusive sum of these.  Every lane of a wavefront makes the same calls.  No row
+// is in two groups, whatever the offsets are, so there are never more units than
+// the grid and the workspace have places for.
 struct GmGroups {
-  int at, base;  // of the 64: the first group, the units before it
+  int at, base, low;  // of the 64: the first group, the units before it, the rows that earlier ones end at
   int b, end, n, x;
 
-  __device__ __forceinline__ explicit GmGroups(const GmArgs& g) { load(g, 0, 0); }
-  __device__ __forceinline__ void load(const GmArgs& g, int e0, int before) {
-    const int lane = threadIdx.x & 63;
+  __device__ __forceinline__ explicit GmGroups(const GmArgs& g) { load(g, 0, 0, 0); }
+  __device__ __forceinline__ void next(const GmArgs& g) {
+    load(g, at + 64, base + __builtin_amdgcn_readlane(x, 63), __builtin_amdgcn_readlane(end, 63));
+  }
+  __device__ __forceinline__ void load(const GmArgs& g, int e0, int before, int rows) {
+    const int lane = threadIdx.x & 63, last = g.groups - e0 < 64 ? g.groups - e0 : 64;
     at = e0;
     base = before;
-    b = end = 0;
-    if (e0 + lane < g.groups) gm_rows(g.offs[e0 + lane], g.offs[e0 + lane + 1], (int)g.mm.T, &b, &end);
+    low = rows;
+    const int e = e0 + (lane < last ? lane : last - 1);
+    gm_rows(g.offs[e], g.offs[e + 1], (int)g.mm.T, &b, &end);
+    if (lane >= last) b = end;
+    if (__builtin_amdgcn_ballot_w64(b < low || end < b)) {  // an offset below an earlier one: the greatest so far
+      int top = b > end ? b : end;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int y = __shfl_up(top, d);
+        if (lane >= d && y > top) top = y;
+      }
+      const int y = __shfl_up(top, 1);
+      if (lane > 0 && y > b) b = y;
+      b = b > low ? b : low;
+      end = top > low ? top : low;
+      if (lane >= last) b = end;
+    }
     n = (end - b + g.rows - 1) / g.rows;
     x = n;
 #pragma unroll
@@ -41,15 +61,14 @@ struct GmGroups {
   }
   // all groups' units
   __device__ __forceinline__ int64_t all(const GmArgs& g) {
-    while (at + 64 < g.groups) load(g, at + 64, base + __builtin_amdgcn_readlane(x, 63));
+    while (at + 64 < g.groups) next(g);
     return base + __builtin_amdgcn_readlane(x, 63);
   }
   // The group that has place p, of `places` a unit; there is one.
   __device__ __forceinline__ void find(const GmArgs& g, int64_t p, int64_t places, GmUnit& u) {
-    if (p < base * places) load(g, 0, 0);
+    if (p < base * places) load(g, 0, 0, 0);
     uint64_t past;
-    while (!(past = __builtin_amdgcn_ballot_w64(p < (int64_t)(base + x) * places)))
-      load(g, at + 64, base + __builtin_amdgcn_readlane(x, 63));
+    while (!(past = __builtin_amdgcn_ballot_w64(p < (int64_t)(base + x) * places))) next(g);
     const int l = __builtin_ctzll(past);
     u.e = at + l;
     u.begin = __builtin_amdgcn_readlane(b, l);
@@ -105,7 +124,7 @@ __global__ __launch_bounds__(kMxThreads) void gm_scales_kernel(GmArgs g) {
     const int64_t i = t - a.gt, e = i / a.go, o = i - e * a.go;
     int b, end;
     gm_rows(g.offs[e], g.offs[e + 1], (int)a.T, &b, &end);
-    if (b == end) return;
+    if (end <= b) return;
     mm_scale_tile<R>(a.bs + e * a.m * nb, o * R, a.m, nb, a.stages, s0, a.os + i * a.stages * (8 * R));
   }
 }

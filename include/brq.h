@@ -463,9 +463,8 @@ brq_status brq_mx_linear(const uint8_t* a_codes, const uint8_t* a_scales, const 
  *   b_codes [groups][m][n/2], b_scales [groups][m][n/32]; bias: device [groups][m].
  *   offsets: device int32 [groups + 1], not decreasing, read at each call (a
  *     captured call can be replayed with other groups); what lies outside [0, T]
- *     counts as the nearer end.  A group may be empty; rows of no group are left as
- *     they were.  Offsets that decrease give some rows to several groups: which of
- *     them a row's outputs come from is not said.
+ *     counts as the nearer end, an offset below an earlier one as that.  A group may
+ *     be empty; rows of no group are left as they were.
  *   ws: device workspace of brq_mx_grouped_matmul_workspace_bytes(...) bytes
  *     (16-byte aligned; may be NULL if that is 0).
  * Everything else as brq_mx_linear (ep NULL: the sums alone).  Errors: also

@@ -237,6 +237,8 @@ def test_rows_of_padding_and_negative_lengths():
         want, _, _ = X.tree_attention(from_dev(q), ref, table[:, :width], [n, n], rows, D ** -0.5, 0, M)
         assert np.allclose(far, want, rtol=0, atol=1e-4, equal_nan=True) and np.isnan(want).any() == (n == 48)
     assert not f([2 ** 31 - 1, 2 ** 30], window=5).any()  # all that the window holds lies beyond the table
+    mask = to_dev(to_mask([[1, 2 ** 64 - 1, 0, 0]] * 2), "i64")
+    assert not f([2 ** 31 - 1, 2 ** 31 - 40], window=1).any()  # where it begins, beyond 32 bits
 
 
 def test_other_layouts_of_queries_and_outputs():

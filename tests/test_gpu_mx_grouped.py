@@ -27,8 +27,9 @@ def experts(rng, E, T, m, n):
 def expected(a, b, offsets, T, m):
     """(sums [T, m], the group of each row, -1 for none)."""
     s, of = np.zeros((T, m)), np.full(T, -1)
+    offsets = np.maximum.accumulate(np.clip(np.asarray(offsets, dtype=np.int64), 0, T))
     for e in range(len(offsets) - 1):
-        lo, hi = (min(max(int(x), 0), T) for x in offsets[e:e + 2])
+        lo, hi = (int(x) for x in offsets[e:e + 2])
         if hi > lo:
             s[lo:hi] = sums([z[lo:hi] for z in a], [z[e] for z in b])
             of[lo:hi] = e
@@ -80,7 +81,7 @@ def test_grouped(counts, m, n):
 
 @pytest.mark.parametrize("T,m,n", [(40, 130, 288), (700, 300, 1376)])
 def test_offsets_beyond_the_rows(T, m, n):
-    """What lies outside [0, T] counts as the nearer end; decreasing offsets give no group a row it has not."""
+    """What lies outside [0, T] counts as the nearer end, an offset below an earlier one as that."""
     import butterfly_rotation_quantization_amd as brq
     import torch
     announce(f"mx grouped offsets outside {T}x{m}x{n}")
@@ -89,13 +90,35 @@ def test_offsets_beyond_the_rows(T, m, n):
     ad, bd = on_gpu(a), on_gpu(b)
     third = T // 3
     for offsets in ([-5, third, 2 * third, T + 9], [-2 ** 31, 0, third, 2 ** 31 - 1], [T, T, T, T], [0, T, T, T],
-                    [third, third, third, third], [T + 1, T + 2, T + 3, T + 4], [5, 3, 4, 4]):
+                    [third, third, third, third], [T + 1, T + 2, T + 3, T + 4], [5, 3, 4, 4], [0, T, 0, T],
+                    [third, 0, T, 0], [T, 0, T, 0], [0, T, -1, -2 ** 31]):
         off = np.array(offsets, dtype=np.int32)
         y = torch.full((T, m), 7.0, device="cuda")
         brq.mx_grouped_matmul(*ad, *bd, to_dev(off, "i32"), y=y)
         s, of = expected(a, b, offsets, T, m)
         got = from_dev(y)
         assert np.array_equal(got[of >= 0], s[of >= 0].astype(np.float32)) and (got[of < 0] == 7).all(), offsets
+
+
+@pytest.mark.parametrize("E", [70, 200])
+def test_many_offsets_in_disorder(E):
+    """Offsets at random, as of a table that was never written: every row once at most, whichever wavefront's 64 it falls to."""
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce(f"mx grouped offsets in disorder E={E}")
+    rng = np.random.default_rng(E)
+    for T, m, n in ((60, 40, 96), (40 * E, 130, 256)):
+        a, b = experts(rng, E, T, m, n)
+        ad, bd = on_gpu(a), on_gpu(b)
+        for lo, hi in ((0, T + 1), (-2 ** 31, 2 ** 31 - 1), (T // 2, T // 2 + 9)):
+            off = rng.integers(lo, hi, E + 1).astype(np.int32)
+            if hi == T + 1:
+                off[:E // 2] = np.sort(off[:E // 2]) // 4
+            y = torch.full((T, m), 7.0, device="cuda")
+            brq.mx_grouped_matmul(*ad, *bd, to_dev(off, "i32"), y=y)
+            s, of = expected(a, b, off, T, m)
+            got = from_dev(y)
+            assert np.array_equal(got[of >= 0], s[of >= 0].astype(np.float32)) and (got[of < 0] == 7).all()
 
 
 @pytest.mark.parametrize("counts", [[5, 7, 4], [70, 3, 200], [300, 290, 310]])
