@@ -99,7 +99,8 @@ __global__ __launch_bounds__(kKpThreads) void kp_few_kernel(KpMove a) {
 
 // More: tokens to the workspace and from it, one launch each, so that everything is
 // read before anything is written; 16 lanes take kKpRun tokens of a head, whose loads
-// travel together (15000 tokens of 8 heads of 128, one at a time 14.7 and 12.6 us).
+// travel together (15000 tokens of 8 heads of 128, one at a time 14.7 and 12.6 us, so
+// 12.8 and 10.4: bound by the number of pieces, a run of values being 4 bytes).
 template <int D, bool OUT>
 __global__ __launch_bounds__(kMxThreads) void kp_move_kernel(KpMove a) {
   const uint32_t row = blockIdx.x * (kMxThreads / 16) + threadIdx.x / 16, run = row / (uint32_t)a.heads;
@@ -186,7 +187,8 @@ __device__ __forceinline__ int kp_scan(int n, int* scratch, int* all) {
 
 // One workgroup decides: which entries need a page, in order (their ranks); as
 // many free pages, the lowest first; then who gets which.  Counts are read
-// before any is changed.
+// before any is changed.  (128 sequences over 5000 pages 5 us, of which most is waiting for
+// one read after the other; a search through all of a pool takes 1 us for some 4000 pages.)
 __global__ __launch_bounds__(kKpThreads) void kp_reserve_kernel(KpReserve a) {
   __shared__ int scratch[kKpThreads / 64];
   const int tid = threadIdx.x;
@@ -246,8 +248,9 @@ __global__ __launch_bounds__(kKpThreads) void kp_reserve_kernel(KpReserve a) {
   }
 }
 
-// The slots of the new tokens, and the first tokens of shared pages, whole
-// sixteens of them: of each of a page's four parts the first bytes, 16 at a time.
+// The slots of the new tokens, and the first tokens of shared pages (128 sequences with
+// 32 tokens of 8 heads of 128 each in the mean 4 us):
+// whole sixteens of them, of each of a page's four parts the first bytes, 16 at a time.
 __global__ __launch_bounds__(kMxThreads) void kp_copy_kernel(KpReserve a) {
   const int64_t b = blockIdx.x;
   const int part = blockIdx.y, tid = threadIdx.x;

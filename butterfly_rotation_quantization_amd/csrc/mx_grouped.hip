@@ -16,7 +16,6 @@ struct GmUnit {
   int begin, end;  // its rows
   int units;       // its units
   int first;       // the first one's number
-  int unit;        // the one, of the group's
 };
 // The groups, one to a lane and 64 at a time: their rows, their units and the
 // inclusive sum of these.  Every lane of a wavefront makes the same calls.  No row
@@ -87,7 +86,10 @@ __device__ __forceinline__ MmArgs gm_group(const GmArgs& g, const GmUnit& u) {
   return a;
 }
 
-// Few rows a group: the stream over its weight, once for each unit.
+// Few rows a group: the stream over its weight, once for each unit.  Bound by memory
+// where rows are long (32 rows, 8 groups of 11008x4096: 40 us, 4.8 TB/s), by finding the
+// unit, one way from memory and the join where they are short (64 groups of 1376x2048, a row
+// each 21 us, 12 each 25; 777 rows in shares that fall as the rank 32).
 template <int TT, int RT, int W>
 __global__ __launch_bounds__(64 * W) void gm_rows_kernel(GmArgs g, MmEpi ep) {
   __shared__ typename MmRows<TT, RT, W>::Sums sums;
