@@ -34,15 +34,19 @@ __device__ __forceinline__ int tr_tiles_of(const TrArgs& a, int64_t b) {
   return tr_tiles(tr_keys(a, b), tr_skip(a.at.lens[b], a.at.window));
 }
 
+// A row's mask, of the drafts that there are.
+__device__ __forceinline__ uint64_t tr_mask(const TrArgs& a, int64_t row) {
+  return (uint64_t)a.mask[row] & ~0ull >> (kTrTokens - a.tokens);
+}
+
 // What a row sees: context from position `from` on, and drafts by their bits.
 // Of a window, drafts come last: bits below the last `window` set ones go.
 struct TrSeen {
   int from;
   uint32_t lo, hi;
 };
-__device__ __forceinline__ TrSeen tr_seen(int64_t mask, int ctx, int window) {
+__device__ __forceinline__ TrSeen tr_seen(uint64_t m, int ctx, int window) {
   TrSeen s;
-  uint64_t m = (uint64_t)mask;
   const int ones = __popcll(m);
   s.from = 0;
   if (window > 0) {
@@ -71,7 +75,7 @@ __device__ __forceinline__ bool tr_row(const TrArgs& a, int64_t b, int h, int r,
 template <int D>
 __device__ __forceinline__ void tr_finish(const TrArgs& a, int64_t row, int head, int c, int lane, float (&o)[8],
                                           float m, float l) {
-  const bool there = a.mask[row] != 0;
+  const bool there = tr_mask(a, row) != 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) o[e] = there ? o[e] : 0.f;
   at_finish<D>(a.at, row, head, c, lane, o, m, there ? l : 0.f);
@@ -230,7 +234,7 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
     int head;
     TrSeen s = {0, 0u, 0u};
     if (tr_row(t, b, h, r0 + tid, &row, &head)) {
-      const int64_t m = t.mask[row];
+      const uint64_t m = tr_mask(t, row);
       s = tr_seen(m, ctx, a.window);
       if (m == 0) s.from = 0;
     }

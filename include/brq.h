@@ -622,7 +622,8 @@ brq_status brq_paged_attention(const brq_plan* plan, const void* q, int64_t ldq,
  *   q, out: device [batch * tokens][ldq], [batch * tokens][ldo] of type qt, rows of a
  *           sequence one after the other, head i at element i * head_dim of its row;
  *           16-byte aligned rows.  out may be q.
- *   mask: device int64 [batch][tokens]; tokens at most 64.
+ *   mask: device int64 [batch][tokens]; tokens at most 64, bits from there on are
+ *     not looked at.
  *   lse: device float32 [batch][tokens][q_heads] or NULL.
  *   ws: device workspace of brq_tree_attention_workspace_bytes(...) bytes.
  * With 16-bit rows a probability enters the matrix units within 2^-17 of itself, with

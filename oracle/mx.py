@@ -207,7 +207,7 @@ def tree_attention(q, cache: Cache, table, lens, mask, scale, window=0, M=None):
     for b in range(B):
         n = int(lens[b])
         for i in range(N):
-            m = int(mask[b, i]) & (2 ** 64 - 1)
+            m = int(mask[b, i]) & (2 ** N - 1)
             if n < 0 or m == 0:
                 continue
             at = np.concatenate((np.arange(min(n, table.shape[1] * P)), [n + j for j in range(64) if m >> j & 1])).astype(int)

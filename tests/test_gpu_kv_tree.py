@@ -107,6 +107,46 @@ def test_masks_of_every_kind():
     attend([40, 0, 129, 33], N, 2, 1, 64, 16, True, "f32", mask=[rows, rows[::-1], [0] * N, rows], window=20)
 
 
+def test_bits_of_drafts_that_are_not_there():
+    """They are not looked at, not by a window's count either; a row with no other is padding."""
+    rows = [1 | 2 ** 63, 2 ** 64 - 1, 2 ** 5 | 4 | 1, 2 ** 63, 2 ** 5]
+    attend([40, 0, 129, 33], 5, 2, 1, 128, 16, False, "f32", mask=[rows] * 4)
+    out = attend([40, 0, 129, 33], 5, 2, 1, 128, 16, False, "f32", mask=[rows] * 4, window=3)
+    assert not out[:, 3:].any()
+
+
+def test_cache_beyond_32_bit_offsets():
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce("tree over a cache of 4.7 GB")
+    H, D, P, pages, N, ctx = 8, 128, 64, 68000, 9, 70
+    rng = np.random.default_rng(8)
+    cache = brq.kv_cache(pages, H, D, P)
+    (k, kh), (v, vh) = tokens(rng, ctx + N, H, D, "bf16"), tokens(rng, ctx + N, H, D, "bf16")
+    table = np.array([[pages - 1, pages - 3]], dtype=np.int32)
+    slots = np.array([int(table[0, j // P]) * P + j % P for j in range(ctx + N)], dtype=np.int64)
+    brq.kv_append(None, k, v, to_dev(slots, "i64"), cache, P)
+    ref = X.Cache(3, H, D, P)
+    ref.append(kh, vh, slots - (pages - 3) * P)
+    q, qh = tokens(rng, N, 16, D, "f32")
+    rows = to_mask([tree(rng, N)])
+    lens, lse = torch.tensor([ctx], dtype=torch.int32, device="cuda"), torch.empty((1, N, 16), device="cuda")
+    out = brq.tree_attention(None, q[None], cache, to_dev(table, "i32"), lens, to_dev(rows, "i64"), P, lse=lse)
+    want, wlse, slack = X.tree_attention(qh[None].astype(np.float64), ref, table - (pages - 3), [ctx], rows, D ** -0.5)
+    check(from_dev(out), from_dev(lse), want, wlse, slack, [ctx], D, "f32")
+    # drafts 1 and 4 to the front of the tree, and a sample of the sequence, whose last page is copied
+    brq.kv_move(cache, to_dev(slots[[ctx + 1, ctx + 4]], "i64"), to_dev(slots[[ctx, ctx + 1]], "i64"), D, P)
+    X.move(ref, slots[[ctx + 1, ctx + 4]] - (pages - 3) * P, slots[[ctx, ctx + 1]] - (pages - 3) * P)
+    assert np.array_equal(cache[-3:].cpu().numpy(), ref.to_bytes())
+    refs = torch.ones(pages, dtype=torch.int32, device="cuda")
+    refs[pages - 2] = 0
+    kids, klens = brq.kv_fork(to_dev(table, "i32"), lens, torch.zeros(1, dtype=torch.int32, device="cuda"), refs)
+    at = brq.kv_reserve(cache, kids, klens, refs, 3, D, P)
+    assert at.tolist() == [[(pages - 2) * P + 6 + i for i in range(3)]]
+    assert torch.equal(*(brq.kv_read(None, cache, torch.arange(6, device="cuda") + p * P, D, P)[0] for p in (pages - 2, pages - 3)))
+    assert not cache[:-3].any()
+
+
 def test_long_and_ragged():
     attend([20011, 1, 4099, 0, 777], 6, 8, 2, 128, 64, True, "bf16")
 

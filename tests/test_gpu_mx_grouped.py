@@ -175,6 +175,29 @@ def test_grouped_graph_replays_with_other_groups(T, E):
         assert torch.equal(y, brq.mx_grouped_matmul(*ad, *bd, off, out_dtype=torch.float32)), seed
 
 
+@pytest.mark.parametrize("rows", [5, 100])
+def test_weights_beyond_32_bit_offsets(rows):
+    """Rows of the first and the last of 64 experts, whose weights take 4.6 GB, against each expert alone."""
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce(f"mx grouped 64 experts of 16384 x 8192, {rows} rows")
+    E, m, n = 64, 16384, 8192
+    rng = np.random.default_rng(rows)
+    (a, b), T = scaled(rng, 2 * rows, 2 * m, n), 2 * rows
+    (ac, asc), (bc, bsc) = on_gpu(a), on_gpu(b)
+    codes = torch.full((E, m, n // 2), 0x77, dtype=torch.uint8, device="cuda")
+    scales = torch.full((E, m, n // 32), 255, dtype=torch.uint8, device="cuda")
+    for e, i in ((0, 0), (E - 1, 1)):
+        codes[e], scales[e] = bc[i * m:(i + 1) * m], bsc[i * m:(i + 1) * m]
+    off = torch.full((E + 1,), rows, dtype=torch.int32, device="cuda")
+    off[0], off[E] = 0, T
+    y = brq.mx_grouped_matmul(ac, asc, codes, scales, off, out_dtype=torch.float32)
+    for i in range(2):
+        r, w = slice(i * rows, (i + 1) * rows), slice(i * m, (i + 1) * m)
+        assert torch.equal(y[r], brq.mx_matmul(ac[r].contiguous(), asc[r].contiguous(), bc[w].contiguous(), bsc[w].contiguous(),
+                                               out_dtype=torch.float32))
+
+
 def test_one_group_is_the_linear_product():
     import butterfly_rotation_quantization_amd as brq
     import torch
