@@ -521,7 +521,7 @@ brq_status brq_kv_read(const brq_plan* plan, const uint8_t* cache, const int64_t
  * move to the front).  A pair with a slot outside the cache is skipped
  * (padding).  Two pairs must not share a dst.
  *   src, dst: device int64 [tokens]; ws: device workspace of
- *   brq_kv_move_workspace_bytes(...) bytes (16-byte aligned).
+ *   brq_kv_move_workspace_bytes(...) bytes (16-byte aligned; may be NULL if that is 0).
  * Errors: INVALID_ARGUMENT, UNSUPPORTED (head_dim, page; more than 2^27 tokens
  * times heads), ALIGNMENT, WORKSPACE, HIP.  tokens == 0 is a no-op. */
 size_t brq_kv_move_workspace_bytes(int64_t tokens, int32_t heads, int32_t head_dim);

@@ -385,3 +385,19 @@ def test_tree_refusals():
                 dict(q=z(2, 65, 4, 64), mask=z(2, 65, t=torch.int64))):
         with pytest.raises(brq.BrqError):
             brq.tree_attention(**{**full, **bad})
+
+
+def test_a_closed_plan_is_refused():
+    """Not taken for no plan: the rows would be attended unrotated."""
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce("tree with a closed plan")
+    plan = brq.Plan(64, (2,) * 6, "hadamard", signs=np.ones(64, np.int8))
+    plan.close()
+    out = torch.full((1, 2, 1, 64), 3.0, device="cuda")
+    with pytest.raises(ValueError, match="closed"):
+        brq.tree_attention(plan, torch.zeros_like(out), brq.kv_cache(1, 1, 64, 16),
+                           torch.zeros((1, 1), dtype=torch.int32, device="cuda"),
+                           torch.ones(1, dtype=torch.int32, device="cuda"),
+                           torch.ones((1, 2), dtype=torch.int64, device="cuda"), 16, out=out)
+    assert (out == 3).all()
