@@ -300,6 +300,22 @@ def test_other_layouts_of_queries_and_outputs():
         assert torch.equal(q, want) and torch.equal(wide[:, :, 8:], before)
 
 
+def test_queries_and_outputs_beyond_32_bit_offsets():
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    from test_gpu_mx_linear import apart
+    announce("tree far apart")
+    rng, (B, N, n) = np.random.default_rng(3), (2, 5, 300)
+    cache, _, table, plan, _, _ = build(rng, [n + N] * B, 4, 128, 32, True)
+    t, lens = to_dev(table, "i32"), torch.full((B,), n, dtype=torch.int32, device="cuda")
+    mask = to_dev(to_mask([tree(rng, N) for _ in range(B)]), "i64")
+    q = torch.randn((B, N, 8, 128), device="cuda").to(torch.bfloat16)
+    far = [apart(B * N, 8 * 128, torch.bfloat16).unflatten(1, (8, 128)).unflatten(0, (B, N)) for _ in range(2)]
+    far[0].copy_(q), far[1].zero_()
+    want = brq.tree_attention(plan, q, cache, t, lens, mask, 32)
+    assert torch.equal(brq.tree_attention(plan, far[0], cache, t, lens, mask, 32, out=far[1]), want)
+
+
 @pytest.mark.parametrize("D,hq,rot", [(64, 8, True), (128, 8, True), (128, 40, False), (256, 3, True)])
 def test_float32_keeps_float32(D, hq, rot):
     """As for single tokens: 2^-18 of the norm leaves a factor of four; 16 bits anywhere would be at 2^-17."""

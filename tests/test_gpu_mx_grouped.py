@@ -8,7 +8,7 @@ import pytest
 from gpu_util import announce, from_dev, to_dev, torch_dtype
 from oracle import mx as X
 from test_gpu_mx import operands
-from test_gpu_mx_linear import check, operand, scaled, sums
+from test_gpu_mx_linear import apart, check, operand, scaled, sums
 from test_gpu_mx_products import on_gpu
 
 pytestmark = pytest.mark.gpu
@@ -196,6 +196,21 @@ def test_weights_beyond_32_bit_offsets(rows):
         r, w = slice(i * rows, (i + 1) * rows), slice(i * m, (i + 1) * m)
         assert torch.equal(y[r], brq.mx_matmul(ac[r].contiguous(), asc[r].contiguous(), bc[w].contiguous(), bsc[w].contiguous(),
                                                out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("counts,m,n", [([3, 0, 1, 2], 70, 160), ([300, 0, 513, 128], 770, 768), ([40, 41, 39], 130, 288)])
+def test_grouped_rows_beyond_32_bit_offsets(counts, m, n):
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce(f"mx grouped {counts} {m}x{n} far apart")
+    rng, T = np.random.default_rng(m), sum(counts)
+    a, b = experts(rng, len(counts), T, m, n)
+    off = to_dev(ends(counts), "i32")
+    mul, res = torch.randn((T, m), device="cuda").half(), torch.randn((T, m), device="cuda")
+    far = apart(T, m, torch.float16), apart(T, m, torch.float32), apart(T, m, torch.bfloat16)
+    far[0].copy_(mul), far[1].copy_(res), far[2].zero_()
+    want = brq.mx_grouped_matmul(*on_gpu(a), *on_gpu(b), off, act="silu", mul=mul, residual=res)
+    assert torch.equal(brq.mx_grouped_matmul(*on_gpu(a), *on_gpu(b), off, act="silu", mul=far[0], residual=far[1], y=far[2]), want)
 
 
 def test_one_group_is_the_linear_product():

@@ -122,6 +122,29 @@ def test_activations_over_their_range(act):
     assert np.isnan(y[m]) and np.isposinf(y[m + 1])
 
 
+def apart(rows, m, dtype, over=33):
+    """Rows so far apart that the last one's elements lie beyond 2^`over` bytes."""
+    import torch
+    size = torch.empty((), dtype=dtype).element_size()
+    ld = (2 ** over // size // max(rows - 1, 1) + m + 16) // 16 * 16
+    return torch.empty((rows - 1) * ld + m, dtype=dtype, device="cuda").as_strided((rows, m), (ld, 1))
+
+
+@pytest.mark.parametrize("T,m,n", [(20, 70, 160), (300, 384, 16640), (300, 520, 512), (2101, 4197, 768), (100, 70, 160)])
+def test_rows_beyond_32_bit_offsets(T, m, n):
+    """Output, factor and residual whose rows are gigabytes away, against rows next to each other."""
+    import butterfly_rotation_quantization_amd as brq
+    import torch
+    announce(f"mx linear {T}x{m}x{n} far apart")
+    rng = np.random.default_rng(m)
+    a, b = (on_gpu(z) for z in scaled(rng, T, m, n))
+    mul, res = torch.randn((T, m), device="cuda").half(), torch.randn((T, m), device="cuda")
+    far = apart(T, m, torch.float16), apart(T, m, torch.float32), apart(T, m, torch.bfloat16)
+    far[0].copy_(mul), far[1].copy_(res), far[2].zero_()
+    want = brq.mx_linear(*a, *b, act="silu", mul=mul, residual=res)
+    assert torch.equal(brq.mx_linear(*a, *b, act="silu", mul=far[0], residual=far[1], y=far[2]), want)
+
+
 def test_linear_empty_sizes():
     import butterfly_rotation_quantization_amd as brq
     import torch
