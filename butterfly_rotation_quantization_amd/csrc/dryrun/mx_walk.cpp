@@ -1,6 +1,7 @@
 // Dry-run walks of the microscaled 4-bit operators: every lane's reads and
 // writes of rows, codes, scales, cache pages and partial results, from the
 // index functions the kernels use.
+#include <cmath>
 #include <vector>
 
 #include "mx.h"
@@ -410,3 +411,28 @@ hipError_t launch_kv_reserve(const KpReserve& a, hipStream_t) {
 }
 
 }  // namespace brq
+
+// A row's maximum and sum over n scores (in units of log2, -infinity where masked), as a
+// wavefront of the tree attention holds them: `step` scores at a time, relative to
+// the maximum so far.
+extern "C" void brq_dryrun_tree_row(const float* scores, int n, int step, float* max, float* sum) {
+  float m = 0.f, least = -INFINITY, l = 0.f;
+  for (int k = 0; k < n; k += step) {
+    const int end = n < k + step ? n : k + step;
+    float top = least;
+    for (int i = k; i < end; ++i) top = std::fmax(top, scores[i] - m);
+    const bool moved = top > least;
+    float up = 0.f;
+    if (moved) {
+      l *= std::exp2(brq::tr_rescale(top));
+      up = top;
+    }
+    for (int i = k; i < end; ++i) l += std::exp2(scores[i] - m - up);
+    if (moved) {
+      m += top;
+      least = 0.f;
+    }
+  }
+  *max = least == 0.f ? m : -INFINITY;
+  *sum = l;
+}

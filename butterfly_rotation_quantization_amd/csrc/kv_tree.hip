@@ -403,7 +403,7 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
           for (int i = 0; i < 4; ++i) top = fmaxf(top, s[u][t][i]);
         top = at_colmax(top);
         if (top > -INFINITY) {
-          const float f = __builtin_amdgcn_exp2f(-top);  // where nothing was seen, the sums are 0
+          const float f = __builtin_amdgcn_exp2f(tr_rescale(top));
           m[u] += top;
           least[u] = 0.f;
           l[u] *= f;

@@ -528,6 +528,11 @@ __host__ __device__ inline int tr_skip(int ctx, int window) {
   return window > 0 && first > 0 ? (int)(first & ~(int64_t)(kAtKeys - 1)) : 0;
 }
 __host__ __device__ inline int tr_tiles(int n, int skip) { return n > skip ? (n - skip + kAtTile - 1) / kAtTile : 0; }
+// A row's running maximum goes up by `top`, the largest of a step's scores relative to it: the
+// exponent of the factor on the row's sums.  At the first keys that the row sees, top is relative
+// to 0 and can be far below it; the sums are 0 then, and stay so with any finite factor
+// (2^200 is not one: times 0 it is NaN), so the factor is never above 1.
+__host__ __device__ inline float tr_rescale(float top) { return top > 0.f ? -top : 0.f; }
 // The number in the deal of workgroup `block` of n that have places: blocks go
 // to the XCDs in turn, so those of one remainder by 8 take neighbouring numbers.
 // n or more: none.
