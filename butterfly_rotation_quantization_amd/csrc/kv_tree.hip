@@ -7,19 +7,19 @@
 // S^T = K Q^T from the codes as they lie in the cache and the queries in eight
 // 4-bit pieces, a column a row, one product after the other into the same sums;
 // the output O^T = V^T P^T with the values in bfloat16 (exact) and a probability
-// in PP pieces of 8 bits: three for float32 rows, so that it has its 24 bits; two
-// for 16-bit ones, off by 2^-17 of it at most (their output's half step is 2^-12
-// or 2^-9 of a value; a third piece takes 20% more of the largest call's time).
+// in three pieces of 8 bits, whatever the rows' type, so that it has its 24 bits, as in the
+// attention of one token (of 7 drafts over 1000 tokens, two pieces left 31 to 62 of 28672 bfloat16
+// outputs other than the formula's rounding, three 2 to 8, elementary float32 operations 10 to 14;
+// the third takes 16% of the largest call's time).
 //
 // Which keys a row sees differs only among the drafts, and at a window's far
 // end: a step of 32 keys that lies clear of both is computed without a mask.
 //
 // Four wavefronts of a workgroup take 32 keys each in turn over the same rows, of one
 // or two column tiles (tr_nt), and join at the part's end.  64 drafts over 8 key-value
-// heads of 128 and 64 query heads, four sequences of 32768 tokens: 500 us (float32 rows,
-// with three pieces, 620), bound by what two wavefronts a SIMD issue: 64 products and some 190
-// other instructions a step; the products are busy half of the time.  8 drafts, 32
-// sequences of 17 to 16384: 75 us, half of it 512 units' beginnings and ends.
+// heads of 128 and 64 query heads, four sequences of 32768 tokens: 608 us, bound by what two
+// wavefronts a SIMD issue: 80 products and some 200 other instructions a step.  8 drafts, 32
+// sequences of 17 to 16384: 84 us, half of it 512 units' beginnings and ends.
 #include "at_dev.h"
 
 namespace brq {
@@ -81,7 +81,7 @@ __device__ __forceinline__ void tr_finish(const TrArgs& a, int64_t row, int head
   at_finish<D>(a.at, row, head, c, lane, o, m, there ? l : 0.f);
 }
 
-template <int D, int NT, int PP>
+template <int D, int NT>
 __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_kernel(TrArgs t) {
   const AtArgs& a = t.at;
   constexpr int KW = D / 32;            // words of codes a lane holds per key (of the scores) or four keys (values)
@@ -91,6 +91,7 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
   constexpr int H = 16 * NT;            // rows
   constexpr int LD = D + 4;
   constexpr int LPH = D / kMxPerLane;   // lanes of a row
+  constexpr int PP = 3;                 // pieces of a probability
   constexpr int NB = D == 64 ? 4 : D / 32;
   // the queries' pieces in the order of the operands (16 columns of 16 bytes for
   // each column tile, product and block); later the wavefronts' sums of a column tile
@@ -418,8 +419,7 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
         }
       }
     }
-    // A probability's first 8 bits, the next ones, the last ones; the last piece is
-    // rounded (of three there is nothing left to round).
+    // A probability's first 8 bits, the next ones, the last ones.
     mxb8 pf[NT][PP];
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
@@ -435,13 +435,9 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
         }
 #pragma unroll
         for (int z = 0; z < PP; ++z) {
-          if (z + 1 == PP) {
-            w[z][q] = __builtin_bit_cast(uint32_t, __builtin_convertvector((mxf2{x[0], x[1]}), mxb2));
-          } else {
-            w[z][q] = __builtin_amdgcn_perm(__float_as_uint(x[1]), __float_as_uint(x[0]), 0x07060302u);
+          w[z][q] = __builtin_amdgcn_perm(__float_as_uint(x[1]), __float_as_uint(x[0]), 0x07060302u);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) x[e] -= __uint_as_float(__float_as_uint(x[e]) & 0xffff0000u);
-          }
+          for (int e = 0; e < 2; ++e) x[e] -= __uint_as_float(__float_as_uint(x[e]) & 0xffff0000u);
         }
       }
       l[u] += sum;
@@ -641,18 +637,13 @@ __global__ __launch_bounds__(kAtThreads) void tr_join_kernel(TrArgs t, int rows)
   tr_finish<D>(t, row, head, e0, lane, o, M, L);
 }
 
-template <int D, int NT>
-void tr_launch(const TrArgs& t, dim3 grid, hipStream_t s) {
-  if (t.at.qt == BRQ_F32) tr_kernel<D, NT, 3><<<grid, kAtThreads, 0, s>>>(t);
-  else tr_kernel<D, NT, 2><<<grid, kAtThreads, 0, s>>>(t);
-}
 template <int D>
 hipError_t tr_launch(const TrArgs& t, hipStream_t s) {
   const AtArgs& a = t.at;
   const int64_t units = a.batch * a.heads * a.ht;
   const dim3 grid((unsigned)(a.wgs ? a.wgs : units));
-  if (D == 256 || a.nt == 1) tr_launch<D, 1>(t, grid, s);
-  else if constexpr (D != 256) tr_launch<D, 2>(t, grid, s);
+  if (D == 256 || a.nt == 1) tr_kernel<D, 1><<<grid, kAtThreads, 0, s>>>(t);
+  else if constexpr (D != 256) tr_kernel<D, 2><<<grid, kAtThreads, 0, s>>>(t);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.wgs) return e;
   const int rows = tr_join_rows(units, a.nt, D);

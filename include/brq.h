@@ -626,9 +626,7 @@ brq_status brq_paged_attention(const brq_plan* plan, const void* q, int64_t ldq,
  *     not looked at.
  *   lse: device float32 [batch][tokens][q_heads] or NULL.
  *   ws: device workspace of brq_tree_attention_workspace_bytes(...) bytes.
- * With 16-bit rows a probability enters the matrix units within 2^-17 of itself, with
- * float32 rows it has its 24 bits.  A key or value that is not finite shows in the
- * rows that see it and in no other.
+ * A key or value that is not finite shows in the rows that see it and in no other.
  * Everything else, and the errors, as brq_paged_attention; also UNSUPPORTED
  * (tokens above 64; 2^24 rows times heads or more). */
 size_t brq_tree_attention_workspace_bytes(int64_t batch, int32_t tokens, int32_t q_heads,
