@@ -64,6 +64,10 @@ __device__ __forceinline__ bool tr_sees(const TrSeen& z, int key, int ctx) {
   return j < 0 ? key >= z.from : ((j < 32 ? z.lo >> (j & 31) : z.hi >> (j & 31)) & 1u) != 0;
 }
 
+// Not 0 if one of w's bytes is 253 or more: subtracted from 252 in every byte, the lowest such one
+// borrows and has its own highest bit (and no byte below it does).
+__device__ __forceinline__ uint32_t tr_large(uint32_t w) { return (0xfcfcfcfcu - w) & w & 0x80808080u; }
+
 // A unit's row: its row of the batch's and its query head; false past the last.
 __device__ __forceinline__ bool tr_row(const TrArgs& a, int64_t b, int h, int r, int64_t* row, int* head) {
   const int group = a.at.group, i = r / group;
@@ -310,6 +314,15 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
 #pragma unroll
     for (int j = 0; j < R; ++j) o[t][j] = mxf4{0.f, 0.f, 0.f, 0.f};
   }
+  auto no_value = [&](int t, int i) {  // key i of the lane's four: zero
+    vs[t] = (vs[t] & ~(255u << (8 * i))) | 127u << (8 * i);
+    if constexpr (D == 64) {
+      vw[t][i / 2] &= ~(0xffffu << (16 * (i & 1)));
+    } else {
+#pragma unroll
+      for (int q = 0; q < KW / 4; ++q) vw[t][i * (KW / 4) + q] = 0u;
+    }
+  };
   // One step of 32 keys.  The last one fetches nothing (and is code of its own:
   // under a condition in the loop, the fetches would be waited for at once).
   auto step = [&](auto last) {
@@ -347,12 +360,7 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[u][t][i] = acc[u][t][i];
-    // Masked keys: scores to -infinity, values that no row sees to zero.  A value that
-    // some rows see and others do not is multiplied by their zeros too, so one
-    // that is not finite (its scale's byte 253 or more can be) is taken out and
-    // added below to the rows that see it.
-    uint32_t odd = 0u;  // such keys of the lane's block: bit 4 t + i
-    bool any = false;   // of the step's
+    // masked keys: scores to -infinity, values that no row sees to zero
     if (k0 < reach || k0 + kAtKeys > ctx || !ok[0] || !ok[1]) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -364,19 +372,8 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
           for (int u = 0; u < NT; ++u) {
             if (none || !tr_sees(seen[16 * u + c], key, ctx)) s[u][t][i] = -INFINITY;
           }
-          const uint32_t byte = vs[t] >> (8 * i) & 255u;
-          if (none || byte >= 253u) {
-            if (!none) odd |= 1u << (4 * t + i);
-            vs[t] = (vs[t] & ~(255u << (8 * i))) | 127u << (8 * i);
-            if constexpr (D == 64) {
-              vw[t][i / 2] &= ~(0xffffu << (16 * (i & 1)));
-            } else {
-#pragma unroll
-              for (int q = 0; q < KW / 4; ++q) vw[t][i * (KW / 4) + q] = 0u;
-            }
-          }
+          if (none) no_value(t, i);
         }
-      any = __builtin_amdgcn_ballot_w64(odd != 0) != 0;
     }
     if constexpr (more) fetch_keys(k0 + kAtTile);
     // Scores relative to the rows' maxima so far.  Seldom after the first tiles is one
@@ -443,6 +440,21 @@ __global__ __launch_bounds__(kAtThreads, tr_workgroups(D, NT) / 256) void tr_ker
       l[u] += sum;
 #pragma unroll
       for (int z = 0; z < PP; ++z) pf[u][z] = __builtin_bit_cast(mxb8, make_uint4(w[z][0], w[z][1], w[z][2], w[z][3]));
+    }
+    // A value is multiplied by the zeros of rows that do not see it, and by those that a
+    // probability's lower pieces can be, so one that is not finite (its scale's byte
+    // is 253 or more) is taken out here and added below to the rows that see it.
+    uint32_t odd = 0u;  // such keys of the lane's block: bit 4 t + i
+    const bool any = __builtin_amdgcn_ballot_w64((tr_large(vs[0]) | tr_large(vs[1])) != 0u) != 0;  // of the step's
+    if (any) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((vs[t] >> (8 * i) & 255u) >= 253u) {
+            odd |= 1u << (4 * t + i);
+            no_value(t, i);
+          }
     }
     // values: keys in pairs, one run of dimensions per lane (of a scale the
     // conversion reads the exponent, so byte 0 is 2^-127 and 255 NaN)
