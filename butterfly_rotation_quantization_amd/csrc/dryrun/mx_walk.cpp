@@ -392,6 +392,12 @@ hipError_t launch_kv_reserve(const KpReserve& a, hipStream_t) {
       if (!ok) return bad("cache reservation copy of token %lld of %lld", t, used);
     }
   }
+  for (int rank : {0, 1, 1000, kKpRanks - 1, kKpRanks, INT32_MAX})  // what an entry wants is no page
+    for (bool shared : {false, true}) {
+      const int32_t w = kp_want(rank, shared);
+      if (w >= -1 || kp_shared(w) != shared || kp_rank(w) != (rank < kKpRanks ? rank : kKpRanks))
+        return bad("cache reservation rank %lld as %lld", rank, w);
+    }
   // the entries that new tokens lie in, for lengths around page and table ends
   std::vector<int32_t> lens;
   for (int64_t n : {(int64_t)-1, (int64_t)0, (int64_t)1, (int64_t)P - 1, (int64_t)P, a.width * P - 1, a.width * P, a.width * P + 5})

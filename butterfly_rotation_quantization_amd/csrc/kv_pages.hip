@@ -187,7 +187,8 @@ __device__ __forceinline__ int kp_scan(int n, int* scratch, int* all) {
 
 // One workgroup decides: which entries need a page, in order (their ranks); as
 // many free pages, the lowest first; then who gets which.  Counts are read
-// before any is changed.  (128 sequences over 5000 pages 5 us, of which most is waiting for
+// before any is changed, that of an entry's page too: one that nobody holds (refs below 1) is
+// free, may be another's a moment later, and is neither counted nor copied here.  (128 sequences over 5000 pages 5 us, of which most is waiting for
 // one read after the other; a search through all of a pool takes 1 us for some 4000 pages.)
 __global__ __launch_bounds__(kKpThreads) void kp_reserve_kernel(KpReserve a) {
   __shared__ int scratch[kKpThreads / 64];
@@ -200,11 +201,11 @@ __global__ __launch_bounds__(kKpThreads) void kp_reserve_kernel(KpReserve a) {
     const bool here = i < items && kp_item(a, i, it);
     int p = -1;
     if (here) p = a.table[it.row * a.width + it.entry];
-    const bool valid = here && p >= 0 && p < a.pages;
-    const bool need = here && !(valid && a.refs[p] == 1);
+    const int holders = here && p >= 0 && p < a.pages ? a.refs[p] : 0;
+    const bool need = here && holders != 1;
     int all;
     const int rank = total + kp_scan(need, scratch, &all) - 1;
-    if (i < items) a.item[i] = need ? -2 - rank : here ? p : -1;  // a page, none, or a rank
+    if (i < items) a.item[i] = need ? kp_want(rank, holders > 1) : here ? p : -1;
     total += all;
   }
   // free pages
@@ -229,15 +230,15 @@ __global__ __launch_bounds__(kKpThreads) void kp_reserve_kernel(KpReserve a) {
     }
     int4 copy = make_int4(-1, -1, 0, 0);
     if (r <= -2) {
-      const int rank = -2 - r;
+      const int rank = kp_rank(r);
       int page = -1;
-      if (rank < found) {
+      if (rank < found && rank < kKpRanks) {
         int* entry = &a.table[it.row * a.width + it.entry];
         const int old = *entry;
         page = a.fresh[rank];
         *entry = page;
         a.refs[page] = 1;
-        if (old >= 0 && old < a.pages) {
+        if (kp_shared(r)) {
           atomicSub(&a.refs[old], 1);
           if (it.used > 0) copy = make_int4(old, page, it.used, 0);
         }

@@ -358,7 +358,7 @@ struct KpReserve {
   int64_t per;           // table entries that a row's new tokens can lie in
   // in the workspace
   int4* copy;            // [batch]: page to copy from and to, its tokens
-  int32_t* item;         // [batch * per]: the page of an entry, or -1
+  int32_t* item;         // [batch * per]: the page of an entry, or -1; kp_want's while it has none
   int32_t* fresh;        // free pages
 };
 // Entries that `tokens` tokens can lie in, from any place of a page on.
@@ -383,6 +383,15 @@ __host__ __device__ inline bool kp_item(const KpReserve& a, int64_t i, KpItem& i
   it.used = k == 0 ? (int)(n & (a.pg.P - 1)) : 0;
   return it.entry < a.width && it.entry <= (n + a.tokens - 1) >> a.lgP;
 }
+// An entry that needs a page, before it has one: the how manieth such one it is, and whether
+// it leaves a page that others hold.  Below -1, in 32 bits: ranks from kKpRanks on (a pool
+// beyond a terabyte) count as that, and get none.
+constexpr int kKpRanks = (1 << 30) - 2;
+__host__ __device__ inline int32_t kp_want(int rank, bool shared) {
+  return -2 - (2 * (rank < kKpRanks ? rank : kKpRanks) + (shared ? 1 : 0));
+}
+__host__ __device__ inline int kp_rank(int32_t want) { return (-2 - want) >> 1; }
+__host__ __device__ inline bool kp_shared(int32_t want) { return ((-2 - want) & 1) != 0; }
 // Place in a page, in 16-byte pieces, of piece i of the first tokens' codes (keys',
 // then values') and scales (keys', then values'), of `codes` and `scales` pieces each.
 __host__ __device__ inline int kp_piece(const KvPage& pg, int codes, int scales, int i) {

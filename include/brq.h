@@ -547,7 +547,8 @@ brq_status brq_kv_move(uint8_t* cache, const int64_t* src, const int64_t* dst, i
  * 1).  In the order of rows and positions they get the lowest free pages.  If the
  * entry held a shared page, that is held once less, and where it holds tokens
  * before position lens[b] these are copied (whole sixteens of them; the rest of
- * the new page stays as it was).  What is free, shared or not is decided by refs
+ * the new page stays as it was).  An entry whose page has refs below 1 holds none: that
+ * page is free, for any row.  What is free, shared or not is decided by refs
  * as the call finds them.
  *   slots: device int64 [batch][tokens], the slot of every new token as
  *     brq_kv_append takes it; -1 where the table ends or no page was left (that

@@ -272,15 +272,15 @@ def reserve(cache: Cache, table, lens, refs, tokens):
             continue
         for c in range(n // P, min(table.shape[1], (n + tokens - 1) // P + 1)):
             old = int(table[b, c])
-            valid = 0 <= old < pages
+            holders = before[old] if 0 <= old < pages else 0  # below 1: a page that is free, whatever the entry says
             page = old
-            if not (valid and before[old] == 1):
+            if holders != 1:
                 if not free:
                     continue
                 page = free.pop(0)
                 table[b, c] = page
                 refs[page] = 1
-                if valid:
+                if holders > 1:
                     refs[old] -= 1
                     if c == n // P:
                         used = (n % P + 15) // 16 * 16
