@@ -553,6 +553,11 @@ inline int tr_join_rows(int64_t units, int nt, int head_dim) {
   const int rows = 16 * nt, most = kAtThreads / (head_dim / kMxPerLane);
   return units * rows <= 2048 ? 1 : (rows < most ? rows : most);
 }
+// Whether the tiles are dealt out evenly: not where the join's launch would have 2^32 threads
+// (from 2^23 units of a head of 256 on, two workgroups each), and enough units fill the chip.
+inline bool tr_dealt(int64_t batch, int64_t units, int nt, int head_dim) {
+  return batch <= kAtMaxBatch && units * (16 * nt / tr_join_rows(units, nt, head_dim)) < (int64_t)1 << 24;
+}
 inline size_t tr_part_bytes(int head_dim, int nt) {
   return (size_t)2 * tr_workgroups(head_dim, nt) * nt * 16 * (head_dim + 4) * sizeof(float);
 }

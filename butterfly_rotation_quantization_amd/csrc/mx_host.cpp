@@ -591,12 +591,14 @@ brq_status brq_paged_attention(const brq_plan* plan, const void* q, int64_t ldq,
 
 size_t brq_tree_attention_workspace_bytes(int64_t batch, int32_t tokens, int32_t q_heads, int32_t heads,
                                           int32_t head_dim) {
-  if (batch <= 0 || batch > kAtMaxBatch || tokens < 1 || tokens > kTrTokens || heads < 1 || q_heads < heads ||
+  if (batch <= 0 || tokens < 1 || tokens > kTrTokens || heads < 1 || q_heads < heads ||
       q_heads % heads || (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
   const int64_t rows = tr_rows(tokens, q_heads, heads);
   const int nt = tr_nt(rows, head_dim);
-  return tr_part_bytes(head_dim, nt) + (size_t)(batch * heads * ((rows + 16 * nt - 1) / (16 * nt))) * sizeof(int2);
+  if (batch > kAtMaxBatch) return 0;
+  const int64_t units = batch * heads * ((rows + 16 * nt - 1) / (16 * nt));
+  return tr_dealt(batch, units, nt, head_dim) ? tr_part_bytes(head_dim, nt) + (size_t)units * sizeof(int2) : 0;
 }
 
 brq_status brq_tree_attention(const brq_plan* plan, const void* q, int64_t ldq, int32_t qt, const uint8_t* cache,
@@ -623,7 +625,7 @@ brq_status brq_tree_attention(const brq_plan* plan, const void* q, int64_t ldq, 
   const int64_t rows = tr_rows(tokens, q_heads, heads);
   t.at.nt = tr_nt(rows, head_dim);
   t.at.ht = (int)((rows + 16 * t.at.nt - 1) / (16 * t.at.nt));
-  t.at.wgs = batch <= kAtMaxBatch ? tr_workgroups(head_dim, t.at.nt) : 0;
+  t.at.wgs = tr_dealt(batch, batch * heads * t.at.ht, t.at.nt, head_dim) ? tr_workgroups(head_dim, t.at.nt) : 0;
   t.at.part = static_cast<float*>(ws);
   t.at.who =
       t.at.wgs ? reinterpret_cast<int2*>(static_cast<char*>(ws) + tr_part_bytes(head_dim, t.at.nt)) : nullptr;
