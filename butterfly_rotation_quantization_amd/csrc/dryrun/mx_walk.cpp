@@ -338,10 +338,11 @@ hipError_t launch_kv_move(const KpMove& a, hipStream_t) {
   dry_launch();
   const int D = a.pg.D;
   const int64_t rows = kp_runs(a.tokens) * a.heads;
-  if ((1 << a.lgP) != a.pg.P || a.tokens < 1 || kKpFew % (kKpThreads / 16) || !launchable(a.heads, kKpThreads) ||
-      !launchable(rows / (kMxThreads / 16) + 1, kMxThreads))
+  const bool few = kp_few(a.tokens, a.heads);
+  if ((1 << a.lgP) != a.pg.P || a.tokens < 1 || (few && a.tokens > kKpFew) || kKpFew % (kKpThreads / 16) ||
+      !(few ? launchable(a.heads, kKpThreads) : launchable(rows / (kMxThreads / 16) + 1, kMxThreads)))
     return bad("cache move of %lld tokens", a.tokens, 0);
-  if (a.tokens > kKpFew) {  // rows past the last run stay in the workspace only if they move nothing
+  if (!few) {  // rows past the last run stay in the workspace only if they move nothing
     const int64_t last = (rows - 1) * kKpRun * kp_row_bytes(D) + kKpRun * kp_row_bytes(D);
     if (!a.ws || last > (int64_t)kp_move_bytes(a.tokens, a.heads, D) || rows >= (int64_t)1 << 32)
       return bad("cache move workspace of %lld bytes", last, 0);

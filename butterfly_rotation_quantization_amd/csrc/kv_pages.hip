@@ -281,7 +281,7 @@ __global__ __launch_bounds__(kMxThreads) void kp_copy_kernel(KpReserve a) {
 
 template <int D>
 void kp_move(const KpMove& a, hipStream_t s) {
-  if (a.tokens <= kKpFew) {
+  if (kp_few(a.tokens, a.heads)) {
     kp_few_kernel<D><<<dim3((unsigned)a.heads), kKpThreads, 0, s>>>(a);
     return;
   }

@@ -322,14 +322,16 @@ struct KpMove {
 };
 // Bytes of a row of the workspace: the codes and scales of a token's head.
 __host__ __device__ constexpr int64_t kp_row_bytes(int D) { return D + D / 16; }
-constexpr int64_t kKpTokens = (int64_t)1 << 27;  // heads of tokens of a move: within 2^31 threads
+constexpr int64_t kKpTokens = (int64_t)1 << 27;  // heads of tokens of a move: within 2^31 threads of 16 a token and head
 constexpr int kKpThreads = 1024;  // of a workgroup that does by itself what has an order: a move, a reservation
 constexpr int kKpFew = 512;       // tokens that such a workgroup holds in registers, of one head
 constexpr int kKpRun = 4;         // tokens of a head that 16 lanes move at a time
 inline int64_t kp_runs(int64_t tokens) { return (tokens + kKpRun - 1) / kKpRun; }
+// Whether a move is one launch, of a workgroup for each head: within 2^32 threads.
+inline bool kp_few(int64_t tokens, int64_t heads) { return tokens <= kKpFew && heads < ((int64_t)1 << 32) / kKpThreads; }
 // Bytes of a move's workspace.
 inline size_t kp_move_bytes(int64_t tokens, int64_t heads, int D) {
-  return tokens <= kKpFew ? 0 : (size_t)(kp_runs(tokens) * kKpRun * heads * kp_row_bytes(D) + 15) / 16 * 16;
+  return kp_few(tokens, heads) ? 0 : (size_t)(kp_runs(tokens) * kKpRun * heads * kp_row_bytes(D) + 15) / 16 * 16;
 }
 
 struct KpFork {
