@@ -130,7 +130,7 @@ hipError_t launch_mx_grouped(const GmArgs& g, const MmEpi& e, hipStream_t) {
     return bad("mx grouped geometry (%lld x %lld)", a.T, a.m);
   const int64_t units = gm_units(a.T, g.groups, g.rows);
   if (!a.tile) {
-    if ((g.rows != 16 && g.rows != 32 && g.rows != 64) || !launchable(units * ((a.m + 15) / 16), 256))
+    if ((g.rows != 16 && g.rows != 32) || !launchable(units * ((a.m + 15) / 16), 256))
       return bad("mx grouped stream (%lld units of %lld rows)", units, g.rows);
   } else {
     GmArgs h = g;
@@ -154,7 +154,7 @@ hipError_t launch_mx_grouped(const GmArgs& g, const MmEpi& e, hipStream_t) {
   // groups of every kind have no more units than the grid has places, and no
   // row beyond the last
   for (int seed = 0; seed < 6 && a.T <= 1 << 20; ++seed)
-    for (int R : {16, 32, 64, 128, 256}) {
+    for (int R : {16, 32, 128, 256}) {
       int64_t units = 0, at = 0;
       for (int64_t e = 0; e < g.groups; ++e) {
         const int64_t left = a.T - at, share = a.T / g.groups;

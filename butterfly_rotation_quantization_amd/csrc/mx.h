@@ -192,7 +192,7 @@ struct GmArgs {
   MmArgs mm;             // T rows, m outputs; b, bs: of group 0, the others' behind
   const int32_t* offs;   // [groups + 1]
   int groups;
-  int rows;              // of a unit: 16, 32 or 64 of the stream, a tile's 128 or 256
+  int rows;              // of a unit: 16 or 32 of the stream, a tile's 128 or 256
 };
 
 // Rows [b, end) of a group from its two offsets, within the T rows there are; of

@@ -185,7 +185,6 @@ hipError_t gm_tiles(const GmArgs& g, const MmEpi& ep, hipStream_t s) {
 hipError_t launch_mx_grouped(const GmArgs& g, const MmEpi& e, hipStream_t s) {
   if (g.mm.tile == 256) return gm_tiles<2, 2, 4, 4, 2>(g, e, s);
   if (g.mm.tile == 128) return gm_tiles<2, 2, 2, 2, 2>(g, e, s);
-  if (g.rows == 64) return gm_rows<4>(g, e, s);
   if (g.rows == 32) return gm_rows<2>(g, e, s);
   return gm_rows<1>(g, e, s);
 }
