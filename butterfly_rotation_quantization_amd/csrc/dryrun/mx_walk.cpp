@@ -130,7 +130,7 @@ hipError_t launch_mx_grouped(const GmArgs& g, const MmEpi& e, hipStream_t) {
     return bad("mx grouped geometry (%lld x %lld)", a.T, a.m);
   const int64_t units = gm_units(a.T, g.groups, g.rows);
   if (!a.tile) {
-    if ((g.rows != 16 && g.rows != 32) || !launchable(units * ((a.m + 15) / 16), 256))
+    if ((g.rows != 16 && g.rows != 32) || !launchable(gm_stream_workgroups(g), 64 * gm_stream_waves(a.n)))
       return bad("mx grouped stream (%lld units of %lld rows)", units, g.rows);
   } else {
     GmArgs h = g;

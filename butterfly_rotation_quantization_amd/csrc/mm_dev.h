@@ -226,8 +226,6 @@ __device__ __forceinline__ mxf4 mm_finish4(const MmEpi& e, int64_t t, int64_t o,
 
 // ---- few tokens: a stream over the weight
 
-constexpr int kMmChunk = 512;    // values of a row a wavefront takes at a time
-
 // 512 values of 16 rows: lane l holds blocks 4 s + l / 16 of row l % 16.
 struct MmChunk {
   mxi4 c[4];

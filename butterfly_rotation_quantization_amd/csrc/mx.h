@@ -71,7 +71,8 @@ struct MmArgs {
   float* part;           // [splits][T][m] partial sums, in the workspace
 };
 
-constexpr int kMmK = 256;  // values of a row per stage
+constexpr int kMmK = 256;      // values of a row per stage
+constexpr int kMmChunk = 512;  // values of a row that a wavefront of the stream takes at a time
 
 // What follows a product's sums: y = act(sum + bias) * mul + res, each part
 // where its pointer is not null; in float32, rounded once to y's type.
@@ -208,21 +209,20 @@ __host__ __device__ inline const void* gm_bias(const MmEpi& e, int64_t group, in
   if (!e.bias) return nullptr;
   return static_cast<const char*>(e.bias) + group * m * (e.bt == BRQ_F32 ? 4 : 2);
 }
-// Kernel and workspace of a grouped product (g.mm.T, m, n and g.groups set): a
-// group's units are taken by the stream over its weight, or by tiles through LDS, whose
-// images of scales (of every unit, and of every group's weight) are in the workspace.
-inline size_t gm_plan(GmArgs& g, uint8_t* ws) {
+// Kernel of a grouped product (g.mm.T, m, n and g.groups set, none of the first two and the
+// last 0): a group's units are taken by the stream over its weight, or by tiles through LDS.
+inline void gm_choose(GmArgs& g) {
   MmArgs& a = g.mm;
   a.tile = 0;
   a.splits = 1;
   g.rows = 16;
-  if (a.n > (1 << 23) || a.n < kMmK) return 0;
+  if (a.n > (1 << 23) || a.n < kMmK) return;
   // Rows a group in the mean, up to which the stream takes less time than tiles
   // (8 groups of 11008x4096, 16, 32 and 40 rows: 46, 61 and 103 us, tiles of 128 66, 66 and 69).
   const int64_t mean = a.T / g.groups;
   if (mean <= 32) {
     g.rows = mean <= 16 ? 16 : 32;
-    return 0;
+    return;
   }
   // as many units as are to be expected: half of a group's last one is empty, none all of it
   const int64_t some = g.groups < a.T ? g.groups : a.T;
@@ -241,16 +241,36 @@ inline size_t gm_plan(GmArgs& g, uint8_t* ws) {
   a.gt = gm_units(a.T, g.groups, a.tile);
   a.go = (a.m + a.tile - 1) / a.tile;
   a.band = 4;
+}
+// The same and the workspace's bytes: the tiles' images of scales, of every unit and of every
+// group's weight.
+inline size_t gm_plan(GmArgs& g, uint8_t* ws) {
+  gm_choose(g);
+  MmArgs& a = g.mm;
+  if (!a.tile) return 0;
   const int64_t image = (int64_t)a.stages * (kMmK / kMxBlock) * a.tile;
   a.ts = ws;
   a.os = ws + a.gt * image;
   return (size_t)((a.gt + g.groups * a.go) * image);
 }
-// Launches within 2^32 threads: of the stream 256 for each unit and 16 outputs,
-// where units of 16 rows are taken up to 8 rows a group in the mean, of 32 up to 24.
+// The stream's workgroups, 32 outputs of a unit each, and their wavefronts: rows of up to four
+// chunks take two, longer ones four.
+inline int64_t gm_stream_workgroups(const GmArgs& g) { return (g.mm.m + 31) / 32 * gm_units(g.mm.T, g.groups, g.rows); }
+inline int gm_stream_waves(int64_t n) { return n <= 4 * kMmChunk ? 2 : 4; }
+// Launches within 2^32 threads, of the kernel that is chosen: rows shorter than a stage, or longer
+// than 2^23, are the stream's however many a group has, in units of 16.
 inline bool gm_supported(int64_t T, int64_t groups, int64_t m, int64_t n) {
   if (!mm_supported(T, m, n) || groups > 1 << 20) return false;
-  return m == 0 || T / 64 + 2 * (groups < T ? groups : T) < ((int64_t)1 << 24) / ((m + 15) / 16);
+  if (T == 0 || groups == 0 || m == 0) return true;
+  GmArgs g = {};
+  g.mm.T = T;
+  g.mm.m = m;
+  g.mm.n = n;
+  g.groups = (int)groups;
+  gm_choose(g);
+  const int64_t most = (int64_t)1 << 32;
+  if (!g.mm.tile) return gm_stream_workgroups(g) * 64 * gm_stream_waves(n) < most;
+  return (g.mm.gt * g.mm.go + 7) * 256 < most && (g.mm.gt + groups * g.mm.go) * kMxThreads < most;
 }
 
 hipError_t launch_mx_grouped(const GmArgs& g, const MmEpi& e, hipStream_t s);

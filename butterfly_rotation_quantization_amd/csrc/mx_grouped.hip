@@ -157,12 +157,11 @@ __global__ __launch_bounds__(64 * WT * WO, 1) void gm_tile_kernel(GmArgs g, MmEp
 
 template <int TT, int W>
 void gm_rows(const GmArgs& g, const MmEpi& e, hipStream_t s) {
-  const int64_t wgs = (g.mm.m + 31) / 32 * gm_units(g.mm.T, g.groups, 16 * TT);
-  gm_rows_kernel<TT, 2, W><<<dim3((unsigned)wgs), 64 * W, 0, s>>>(g, e);
+  gm_rows_kernel<TT, 2, W><<<dim3((unsigned)gm_stream_workgroups(g)), 64 * W, 0, s>>>(g, e);
 }
 template <int TT>
 hipError_t gm_rows(const GmArgs& g, const MmEpi& e, hipStream_t s) {
-  if (g.mm.n <= 4 * kMmChunk) gm_rows<TT, 2>(g, e, s);
+  if (gm_stream_waves(g.mm.n) == 2) gm_rows<TT, 2>(g, e, s);
   else gm_rows<TT, 4>(g, e, s);
   return hipGetLastError();
 }

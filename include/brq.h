@@ -468,8 +468,8 @@ brq_status brq_mx_linear(const uint8_t* a_codes, const uint8_t* a_scales, const 
  *   ws: device workspace of brq_mx_grouped_matmul_workspace_bytes(...) bytes
  *     (16-byte aligned; may be NULL if that is 0).
  * Everything else as brq_mx_linear (ep NULL: the sums alone).  Errors: also
- * UNSUPPORTED (more than 2^20 groups; T / 64 + 2 groups times m / 16 at 2^24 or
- * more). */
+ * UNSUPPORTED (more than 2^20 groups; sizes whose launch would have 2^32 threads: none
+ * with (T / 16 + groups) times m / 32, both rounded up, below 2^24). */
 size_t brq_mx_grouped_matmul_workspace_bytes(int64_t T, int64_t groups, int64_t m, int64_t n);
 brq_status brq_mx_grouped_matmul(const uint8_t* a_codes, const uint8_t* a_scales,
                                  const uint8_t* b_codes, const uint8_t* b_scales,
