@@ -443,3 +443,9 @@ extern "C" void brq_dryrun_tree_row(const float* scores, int n, int step, float*
   *max = least == 0.f ? m : -INFINITY;
   *sum = l;
 }
+
+// gelu's polynomial for erfc(z) exp(z^2), with its own error alone.
+extern "C" double brq_dryrun_gelu_tail(double z) {
+  const double t = 1 / (1 + z / 2);
+  return t * brq::mm_gelu_tail(t);
+}

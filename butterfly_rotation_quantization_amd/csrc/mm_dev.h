@@ -68,21 +68,11 @@ __device__ __forceinline__ float mm_logistic(float x, float g) {
   const float h = __builtin_amdgcn_exp2f(-0.72134752044448170f * fabsf(g)), r = __builtin_amdgcn_rcpf(fmaf(h, h, 1.f));
   return g < 0.f ? x * r * h * h : x * r;
 }
-// x times the normal distribution function of x, by its tail too: erfc(z) exp(z^2)
-// is t times a polynomial of degree 8 in t = 1 / (1 + z / 2), fitted over z >= 0 to
-// within 0.75 2^-24 of its value.  (The library's erfcf took more than twice the
+// x times the normal distribution function of x, by its tail too, mm_gelu_tail.  (The library's erfcf took more than twice the
 // time: 2048x28672x8192 with bias and gelu 478 us, with this 349.)
 __device__ __forceinline__ float mm_gelu(float x) {
   const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(x), 0.35355339059327373f, 1.f));
-  float p = -0.059385716915130615f;
-  p = fmaf(p, t, 0.28612077236175537f);
-  p = fmaf(p, t, -0.49040067195892334f);
-  p = fmaf(p, t, 0.28172776103019714f);
-  p = fmaf(p, t, -0.029145410284399986f);
-  p = fmaf(p, t, 0.20375148952007294f);
-  p = fmaf(p, t, 0.24283531308174133f);
-  p = fmaf(p, t, 0.2824120819568634f);
-  p = fmaf(p, t, 0.2820843458175659f);
+  const float p = mm_gelu_tail(t);
   const float h = __builtin_amdgcn_exp2f(-0.36067376022224085f * (x * x)), q = 0.5f * p * t;
   return x < 0.f ? q * x * h * h : x * (1.f - q * h * h);
 }
