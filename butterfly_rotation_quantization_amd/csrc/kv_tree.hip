@@ -18,7 +18,7 @@
 // Four wavefronts of a workgroup take 32 keys each in turn over the same rows, of one
 // or two column tiles (tr_nt), and join at the part's end.  64 drafts over 8 key-value
 // heads of 128 and 64 query heads, four sequences of 32768 tokens: 608 us, bound by what two
-// wavefronts a SIMD issue: 80 products and some 200 other instructions a step.  8 drafts, 32
+// wavefronts a SIMD issue: 80 products and some 240 vector instructions a step.  8 drafts, 32
 // sequences of 17 to 16384: 84 us, half of it 512 units' beginnings and ends.
 #include "at_dev.h"
 

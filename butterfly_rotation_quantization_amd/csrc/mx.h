@@ -555,9 +555,10 @@ struct TrArgs {
 };
 inline int64_t tr_rows(int tokens, int q_heads, int heads) { return (int64_t)tokens * (q_heads / heads); }
 // Column tiles of 16 rows of a workgroup: one where a second would be empty.  Two share
-// the conversion of the values and take 0.82 of one's time each, so three rather go
-// one by one (64 rows over 20000 tokens, eight sequences: two at a time 108 us, one
-// 113; 40 rows, sixteen of 300 to 3000: 33 and 30).  A head of 256 has registers for one.
+// the conversion of the values, which saves less than a fourth, empty one would cost, so three
+// rather go one by one (64 rows over 20000 tokens, eight sequences: two at a time 125 us, one
+// 129; 32 rows over 130000, four: 207 and 227; 40 rows, sixteen of 300 to 3000: 39 and 32).
+// A head of 256 has registers for one.
 inline int tr_nt(int64_t rows, int head_dim) {
   const int64_t tiles = (rows + 15) / 16;
   return tiles == 1 || tiles == 3 || head_dim == 256 ? 1 : 2;
@@ -566,7 +567,8 @@ inline int tr_nt(int64_t rows, int head_dim) {
 constexpr int tr_workgroups(int head_dim, int nt) { return nt == 1 && head_dim != 256 ? 768 : 512; }
 // Empty places ahead of a unit's tiles (kAtLead): beginning one takes longer here, with
 // more queries to bring in and more sums to hand on (32 sequences of 17 to 16384 tokens, 8
-// drafts, 4, 7 and 10 places: 87, 81 and 87 us; sixteen of 300 to 3000, 5 drafts: 30, 31, 32).
+// drafts, in the mean of six such, 4, 5, 6 and 7 places: 93, 90, 90 and 92 us, with 10 6% more;
+// sixteen of 300 to 3000, 5 drafts: 31, 32, 32 and 33).
 constexpr int kTrLead = 7;
 __host__ __device__ inline int tr_cost(int tiles) { return tiles > 0 ? tiles + kTrLead : 0; }
 // Keys before the first tile of a context of ctx tokens with a window (a row sees

@@ -619,7 +619,8 @@ brq_status brq_paged_attention(const brq_plan* plan, const void* q, int64_t ldq,
  * `window` of them if window > 0, what brq_paged_attention computes.  One draft
  * with mask 1 is a sequence's next token there.  A row whose mask is 0 is padding
  * and sees nothing, as does every row of a sequence with a negative length; of
- * drafts whose bit no row has set, nothing is seen.
+ * drafts whose bit no row has set, nothing is seen.  A window counts the positions, also
+ * those past the table's end or on pages outside the cache, where there is nothing.
  *   q, out: device [batch * tokens][ldq], [batch * tokens][ldo] of type qt, rows of a
  *           sequence one after the other, head i at element i * head_dim of its row;
  *           16-byte aligned rows.  out may be q.
